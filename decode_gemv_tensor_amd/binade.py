@@ -36,7 +36,10 @@ EXPORTS = ["binade_status_str", "binade_last_hip_error", "binade_build_table",
            "binade_build_table_gpu", "binade_pack_gpu_workspace_bytes", "binade_pack_rice_gpu",
            "binade_huff_lengths", "binade_huff_pack", "binade_huff_workspace_bytes",
            "binade_huff_decode", "binade_rice_plan_bytes", "binade_rice_to_r4_plan",
-           "binade_rice_to_r4_run"]
+           "binade_rice_to_r4_run", "binade_moe_combine_grad", "binade_moe_route",
+           "binade_moe_route_workspace_bytes", "binade_moe_route_grad", "binade_lora_add",
+           "binade_lora_workspace_bytes", "binade_lora_grad",
+           "binade_lora_grad_workspace_bytes"]
 
 
 class Table(ctypes.Structure):
@@ -94,6 +97,12 @@ class R4Desc(ctypes.Structure):
                 ("n_esc", ctypes.c_uint64)]
 
 
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("rank", ctypes.c_int32),
+                ("n_adapters", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
 class BinadeError(RuntimeError):
     def __init__(self, fn: str, code: int, hip: int = 0):
         lib = _lib_or_none()
@@ -134,6 +143,12 @@ def lib() -> ctypes.CDLL:
             L.binade_huff_workspace_bytes.restype = I64
             L.binade_rice_plan_bytes.argtypes = [I32]
             L.binade_rice_plan_bytes.restype = I64
+            L.binade_moe_route_workspace_bytes.argtypes = [I64, I32]
+            L.binade_moe_route_workspace_bytes.restype = I64
+            L.binade_lora_workspace_bytes.argtypes = [I64, I64, I64, I32]
+            L.binade_lora_workspace_bytes.restype = I64
+            L.binade_lora_grad_workspace_bytes.argtypes = [I64, I64, I64, I32, I32]
+            L.binade_lora_grad_workspace_bytes.restype = I64
             sig = {
                 "binade_build_table": [P, I64, P],
                 "binade_sizes_of": [P, I64, I64, P],
@@ -166,6 +181,15 @@ def lib() -> ctypes.CDLL:
                 "binade_r4_moe_gemv": [P, I32, P, I32, P, I64, I32, P, I32, P, P],
                 "binade_bf16_moe_gemv": [P, I32, I64, I64, P, I32, P, I64, I32,
                                          P, I32, P, P],
+                "binade_moe_combine_grad": [P, P, P, I32, I64, I32, I64, P, I32, P, P],
+                "binade_moe_route": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, P, P, I64,
+                                     P],
+                "binade_moe_route_grad": [P, I32, I64, I64, I32, I32, I32, P, P, P, P, P, I32,
+                                          I64, P, P],
+                "binade_lora_add": [P, P, I64, I64, P, P, I64, I32, P, I64, I32, P, P, I64, P,
+                                    P],
+                "binade_lora_grad": [P, P, I64, I64, P, P, I64, P, P, I64, P, I64, P, P, I32, P,
+                                     I64, P, P],
             }
             for name, args in sig.items():
                 if hasattr(L, name):
@@ -912,3 +936,260 @@ def bf16_moe_gemv(experts: torch.Tensor, n_experts: int, x: torch.Tensor,
           1 if x_per_slot else 0, _ptr(idx), n_tokens, top_k, _ptr(y), code,
           _ptr(status), _stream(stream))
     return y
+
+
+# ------------------------------------------------------------------ router
+def _on_device(fn):
+    """Run a device binding on the device of its first argument: its tensors
+    are checked to be there, and kernels, temporaries and a default stream are
+    that device's even when another one is current."""
+    @functools.wraps(fn)
+    def wrapper(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError(f"{fn.__name__} takes device tensors")
+        index = first.device.index
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != index:
+            raise ValueError("stream of another device")
+        if index == torch.cuda.current_device():
+            return fn(first, *args, stream=stream, **kw)
+        with torch.cuda.device(index):
+            return fn(first, *args, stream=stream, **kw)
+    return wrapper
+
+
+def _arg(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
+    """t checked: one of dtypes, the shape, the device, and contiguous."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    return t.contiguous()
+
+
+def _out_arg(name: str, t: torch.Tensor | None, dtype, shape, device) -> torch.Tensor:
+    """An output: allocated, or the caller's, which has to fit as it is."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return _arg(name, t, (dtype,), shape, device)
+
+
+def _status_arg(status: torch.Tensor | None, device) -> torch.Tensor | None:
+    if status is not None and (status.device != device or status.element_size() != 4
+                               or status.numel() < 1):
+        raise ValueError("status: one 32-bit word on the device")
+    return status
+
+
+def _scratch(nbytes: int, workspace: torch.Tensor | None, device):
+    """(tensor, bytes) of a workspace: the caller's, or torch's allocator's."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+def _logits_arg(t: torch.Tensor) -> torch.Tensor:
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"logits: {t.dtype}, expected bf16 or fp32")
+    if t.dim() != 2:
+        raise ValueError("logits: [n_tokens, n_experts]")
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
+@dataclass
+class MoeRoute:
+    """What moe_route gives: the slots' experts and weights, and with stats
+    the counts (the last entry: rows that count), the summed probabilities
+    and the balance loss."""
+    idx: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor | None = None
+    prob_sum: torch.Tensor | None = None
+    loss: torch.Tensor | None = None
+
+
+@_on_device
+@_on_stream
+def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
+              valid: torch.Tensor | None = None, stats: bool = True,
+              workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
+    """binade_moe_route: each token's top_k experts (idx int32 [T, top_k], for
+    r4_moe_gemv) and their weights (fp32 [T, top_k], for moe_combine) from
+    logits [T, E]; valid: bool or uint8 [T], False for padding."""
+    logits = _logits_arg(logits)
+    dev = logits.device
+    T, E = logits.shape
+    if valid is not None:
+        valid = _arg("valid", valid, (torch.bool, torch.uint8), (T,), dev)
+    out = MoeRoute(torch.empty(T, top_k, dtype=torch.int32, device=dev),
+                   torch.empty(T, top_k, dtype=torch.float32, device=dev))
+    ws, nb = None, 0
+    if stats:
+        out.counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        out.prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
+        out.loss = torch.empty(1, dtype=torch.float32, device=dev)
+        ws, nb = _scratch(int(lib().binade_moe_route_workspace_bytes(T, E)), workspace, dev)
+    _call("binade_moe_route", _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E,
+          top_k, int(bool(renormalize)), _ptr(valid), _ptr(out.idx), _ptr(out.weights),
+          _ptr(out.counts), _ptr(out.prob_sum), _ptr(out.loss), _ptr(ws), nb, _stream(stream))
+    return out
+
+
+@_on_device
+@_on_stream
+def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
+                   dweights: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                   dloss: torch.Tensor | None = None, renormalize: bool = True, out_dtype=None,
+                   dlogits: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """binade_moe_route_grad: the gradient of the logits from that of the
+    weights and (counts and dloss together) of the balance loss."""
+    logits = _logits_arg(logits)
+    dev = logits.device
+    T, E = logits.shape
+    code = _dtype_code(logits.dtype if out_dtype is None else out_dtype)
+    if idx.dim() != 2:
+        raise ValueError("idx: [n_tokens, top_k]")
+    top_k = idx.shape[1]
+    idx = _arg("idx", idx, (torch.int32,), (T, top_k), dev)
+    if dweights is not None:
+        dweights = _arg("dweights", dweights, (torch.float32,), (T, top_k), dev)
+    if (counts is None) != (dloss is None):
+        raise ValueError("counts and dloss go together")
+    if counts is not None:
+        counts = _arg("counts", counts, (torch.int32,), (E + 1,), dev)
+        dloss = _arg("dloss", dloss.reshape(-1), (torch.float32,), (1,), dev)
+    dlogits = _out_arg("dlogits", dlogits, _TORCH_DTYPE[code], (T, E), dev)
+    _call("binade_moe_route_grad", _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E,
+          top_k, int(bool(renormalize)), _ptr(idx), _ptr(dweights), _ptr(counts), _ptr(dloss),
+          _ptr(dlogits), code, E, _ptr(_status_arg(status, dev)), _stream(stream))
+    return dlogits
+
+
+@_on_device
+@_on_stream
+def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor, top_k: int,
+                     out_dtype=torch.float32, need_dy: bool = True, stream=None):
+    """binade_moe_combine_grad: (dy [T*top_k, N] or None, dweights fp32
+    [T*top_k] in the shape of weights) of moe_combine(y, weights, top_k)."""
+    code = _dtype_code(out_dtype)
+    dev = y.device
+    if y.dim() != 2 or dout.dim() != 2:
+        raise ValueError("y: [n_tokens * top_k, N], dout: [n_tokens, N]")
+    T, N = dout.shape
+    y = _arg("y", y, (torch.float32,), (T * top_k, N), dev)
+    dout = _arg("dout", dout, _FLOATS, (T, N), dev)
+    if weights.numel() != T * top_k:
+        raise ValueError("weights: n_tokens * top_k")
+    w = _arg("weights", weights, (torch.float32,), weights.shape, dev)
+    dy = torch.empty(T * top_k, N, dtype=_TORCH_DTYPE[code], device=dev) if need_dy else None
+    dw = torch.empty(weights.shape, dtype=torch.float32, device=dev)
+    _call("binade_moe_combine_grad", _ptr(y), _ptr(w), _ptr(dout), _dtype_code(dout.dtype), T,
+          top_k, N, _ptr(dy), code, _ptr(dw), _stream(stream))
+    return dy, dw
+
+
+# ---------------------------------------------------------------- adapters
+def _rows16(name: str, t: torch.Tensor, cols: int, device, m: int | None = None) -> torch.Tensor:
+    """bf16 [m, cols] rows at a 16-byte aligned stride (copied otherwise)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: {t.dtype}, expected bf16")
+    if t.dim() != 2 or t.shape[1] != cols or (m is not None and t.shape[0] != m):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.stride(1) != 1 or t.stride(0) < cols or t.stride(0) % 8 or t.data_ptr() % 16:
+        t = t.contiguous()
+    return t
+
+
+def _lora_desc(a, b, scale, device):
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError("a: [n_adapters, rank, K], b: [n_adapters, N, rank]")
+    a = _arg("a", a, (torch.bfloat16,), a.shape, device)
+    b = _arg("b", b, (torch.bfloat16,), b.shape, device)
+    d = LoraDesc()
+    d.n_adapters, d.rank, d.k = a.shape
+    d.n = b.shape[1]
+    d.a, d.b = a.data_ptr(), b.data_ptr()
+    if scale is not None:
+        scale = _arg("scale", scale, (torch.float32,), (a.shape[0],), device)
+        d.scale = scale.data_ptr()
+    return d, (a, b, scale)
+
+
+def _lora_ids(ids, m, device):
+    return None if ids is None else _arg("ids", ids, (torch.int32,), (m,), device)
+
+
+@_on_device
+@_on_stream
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor | None = None,
+             base: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+             out_dtype=torch.float32, y: torch.Tensor | None = None, keep_h: bool = False,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             stream=None):
+    """binade_lora_add: base + scale * B (A x) with row t's adapter ids[t]
+    (None: adapter 0 for all; -1: none), beside r4_gemv_rows / r4_gemm of the
+    same x [m, K]. y may be base. With keep_h: (y, h), h fp32 [m, rank] for
+    lora_grad."""
+    code = _dtype_code(out_dtype)
+    dev = x.device
+    d, keep = _lora_desc(a, b, scale, dev)
+    x = _rows16("x", x, d.k, dev)
+    m = x.shape[0]
+    ids = _lora_ids(ids, m, dev)
+    if base is not None:
+        base = _arg("base", base, _FLOATS, (m, d.n), dev)
+    y = _out_arg("y", y, _TORCH_DTYPE[code], (m, d.n), dev)
+    h = torch.empty(m, d.rank, dtype=torch.float32, device=dev) if keep_h else None
+    ws, nb = _scratch(int(lib().binade_lora_workspace_bytes(m, d.n, d.k, d.rank)), workspace, dev)
+    _call("binade_lora_add", ctypes.byref(d), _ptr(x), m, x.stride(0), _ptr(ids), _ptr(base), d.n,
+          F32 if base is None else _dtype_code(base.dtype), _ptr(y), d.n, code, _ptr(h), _ptr(ws),
+          nb, _ptr(_status_arg(status, dev)), _stream(stream))
+    return (y, h) if keep_h else y
+
+
+@_on_device
+@_on_stream
+def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor | None,
+              dy: torch.Tensor, h: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+              dx_base: torch.Tensor | None = None, grad_dtype=torch.float32,
+              dx: torch.Tensor | None = None, need_dx: bool = True,
+              workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+              stream=None):
+    """binade_lora_grad: (dx bf16 [m, K] or None, da, db) of lora_add from dy
+    bf16 [m, N]; h as lora_add(keep_h=True) gave it (None: computed again);
+    dx_base: the projection's own input gradient, added; dx may be dx_base."""
+    code = _dtype_code(grad_dtype)
+    dev = x.device
+    d, keep = _lora_desc(a, b, scale, dev)
+    x = _rows16("x", x, d.k, dev)
+    m = x.shape[0]
+    ids = _lora_ids(ids, m, dev)
+    dy = _arg("dy", dy, (torch.bfloat16,), (m, d.n), dev)
+    if h is not None:
+        h = _arg("h", h, (torch.float32,), (m, d.rank), dev)
+    if dx_base is not None:
+        dx_base = _rows16("dx_base", dx_base, d.k, dev, m)
+    dx = _out_arg("dx", dx, torch.bfloat16, (m, d.k), dev) if need_dx or dx is not None else None
+    da = torch.empty(d.n_adapters, d.rank, d.k, dtype=_TORCH_DTYPE[code], device=dev)
+    db = torch.empty(d.n_adapters, d.n, d.rank, dtype=_TORCH_DTYPE[code], device=dev)
+    ws, nb = _scratch(int(lib().binade_lora_grad_workspace_bytes(m, d.n, d.k, d.rank,
+                                                                 d.n_adapters)), workspace, dev)
+    _call("binade_lora_grad", ctypes.byref(d), _ptr(x), m, x.stride(0), _ptr(ids), _ptr(dy), d.n,
+          _ptr(h), _ptr(dx_base), 0 if dx_base is None else dx_base.stride(0), _ptr(dx), d.k,
+          _ptr(da), _ptr(db), code, _ptr(ws), nb, _ptr(_status_arg(status, dev)),
+          _stream(stream))
+    return dx, da, db

@@ -83,7 +83,8 @@ typedef enum binade_dtype {
 #define BINADE_DEV_CORRUPT_STREAM 0x1u  /* a chunk's unary bits do not hold
                                             its weight count, or a rank is not
                                             in the table */
-#define BINADE_DEV_BAD_INDEX 0x2u       /* an expert index is out of range */
+#define BINADE_DEV_BAD_INDEX 0x2u       /* an expert or adapter index is out
+                                            of range */
 #define BINADE_DEV_CORRUPT_ESC 0x4u     /* escape prefix / entries disagree */
 
 /* Per-tensor exponent table. */
@@ -536,6 +537,154 @@ int32_t binade_moe_silu_mul(const float *gate, const float *up, int64_t n,
 int32_t binade_moe_combine(const float *y, const float *weights,
                            int64_t n_tokens, int32_t top_k, int64_t n,
                            void *out, int32_t out_dtype, void *stream);
+
+/* The combine's backward, for out[t, j] = sum_s w[t, s] y[t, s, j] with the
+ * gradient dout of out: dy[t, s, j] = w[t, s] * dout[t, j] (one fp32
+ * product, then bf16, nearest-even, when dy_dtype is BF16) and
+ * dweights[t, s] = sum_j dout[t, j] * y[t, s, j] in fp32 (an fma chain per
+ * thread, then a fixed tree; the order depends on n alone). y, weights: as
+ * binade_moe_combine takes them. dout: device fp32 or bf16 [n_tokens, n] per
+ * dout_dtype. dy: device [n_tokens*top_k, n] fp32 or bf16 per dy_dtype, or
+ * NULL (the experts are frozen and nothing below them learns). dweights:
+ * device fp32 [n_tokens*top_k]. EINVAL: top_k outside 1..64, sizes, null
+ * pointers. */
+int32_t binade_moe_combine_grad(const float *y, const float *weights,
+                                const void *dout, int32_t dout_dtype,
+                                int64_t n_tokens, int32_t top_k, int64_t n,
+                                void *dy, int32_t dy_dtype, float *dweights,
+                                void *stream);
+
+/* The router of a MoE layer: which experts each token's slots take, with
+ * what weight, how often each expert is taken, and the balance loss. For
+ * each row t of logits [n_tokens, n_experts] (device fp32 or bf16 per
+ * dtype, row stride ld elements):
+ *   p = softmax(logits[t]) in fp32;
+ *   idx[t, s] (device int32 [n_tokens, top_k]): the top_k largest logits in
+ *   falling order, equal ones by rising expert. An expert of logit -inf is
+ *   never taken: a slot with none left holds -1 and weight 0 (the expert
+ *   products leave such a slot's row zero and flag it). NaN ranks with -inf;
+ *   as in the formula, a NaN or +inf makes its row's weights NaN;
+ *   weights[t, s] (device fp32): p of the slot's expert, divided by the sum
+ *   of p over the row's taken experts if renormalize != 0.
+ * valid (device u8 [n_tokens] or NULL): rows of value 0 are padding; all
+ * their slots are -1 with weight 0. A row counts if it is valid and has a
+ * slot taken. With counts, prob_sum and loss (all three or none, NULL):
+ *   counts[e] (device int32 [n_experts + 1]): slots that took expert e;
+ *   counts[n_experts]: the rows R that count;
+ *   prob_sum[e] (device fp32 [n_experts]): sum of p[e] over these rows;
+ *   loss (device fp32 [1]) = n_experts * sum_e counts[e] / (top_k R)
+ *   * prob_sum[e] / R, 0 for R = 0 (1 for a balanced router).
+ * Sums run in a fixed order for given sizes: the same call gives the same
+ * bits. workspace: device, 16-byte aligned, binade_moe_route_workspace_bytes
+ * bytes (0 and NULL without counts); not read before written; calls that
+ * overlap need their own. n_experts in 1..1024, top_k in 1..min(64,
+ * n_experts), ld >= n_experts, else EINVAL; ENOSPACE: workspace_bytes. */
+int32_t binade_moe_route(const void *logits, int32_t dtype, int64_t ld,
+                         int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                         int32_t renormalize, const uint8_t *valid,
+                         int32_t *idx, float *weights, int32_t *counts,
+                         float *prob_sum, float *loss, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes binade_moe_route needs with counts (0 for sizes it
+ * refuses). Pure host function. */
+int64_t binade_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts);
+
+/* The router's backward: dlogits of sum(dweights * weights) + dloss * loss.
+ * logits, ld, renormalize: as in the forward call; idx: its choice. With
+ * u[e] = sum over the row's slots s that took e of dw'[s], plus
+ * dloss * n_experts * counts[e] / (top_k R R), where dw' = dweights, or
+ * (dweights - sum_s dweights[s] weights[s]) / (sum of p over the slots) if
+ * renormalised: dlogits[e] = p[e] (u[e] - sum_j p[j] u[j]), in fp32. Rows
+ * without a taken slot (idx[t, 0] < 0) get zeros. dweights: device fp32
+ * [n_tokens, top_k] or NULL (zeros). counts and dloss (device fp32 [1]):
+ * both or none (no balance term). dlogits: device fp32 or bf16 per
+ * dlogits_dtype, row stride ld_d >= n_experts, may be logits itself if type
+ * and stride agree. An index outside [-1, n_experts) sets
+ * BINADE_DEV_BAD_INDEX in dev_status (if not NULL) and counts as -1. */
+int32_t binade_moe_route_grad(const void *logits, int32_t dtype, int64_t ld,
+                              int64_t n_tokens, int32_t n_experts,
+                              int32_t top_k, int32_t renormalize,
+                              const int32_t *idx, const float *dweights,
+                              const int32_t *counts, const float *dloss,
+                              void *dlogits, int32_t dlogits_dtype,
+                              int64_t ld_d, uint32_t *dev_status,
+                              void *stream);
+
+/* Low-rank adapters of a projection with n outputs and k inputs (device
+ * pointers): n_adapters adapters stacked at one rank, those of a smaller
+ * rank padded with zeros.
+ *   a      bf16 [n_adapters, rank, k]
+ *   b      bf16 [n_adapters, n, rank]
+ *   scale  fp32 [n_adapters], or NULL for ones
+ * k % 32 == 0, rank a multiple of 8 in 8..128, n_adapters in 1..65535; a and
+ * b 16-byte aligned, else BINADE_EUNSUPPORTED. */
+typedef struct binade_lora {
+  int64_t n, k;
+  int32_t rank, n_adapters;
+  const uint16_t *a, *b;
+  const float *scale;
+} binade_lora;
+
+/* Adapters of many requests beside one shared projection: with base the
+ * projection's product (binade_r4_gemv, _rows or binade_r4_gemm of the same
+ * rows), y[t, :] = base[t, :] + scale[i] * B[i] (A[i] x[t]) for i = ids[t],
+ * for m rows of any mix of adapters. Rows of id -1 have no adapter (y =
+ * base); an id outside [-1, n_adapters) sets BINADE_DEV_BAD_INDEX in
+ * dev_status (if not NULL) and counts as -1. ids: device int32 [m], or NULL
+ * for adapter 0 on every row.
+ * x: device bf16, row t at x + t*ldx (ldx >= k, a multiple of 8; 16-byte
+ * aligned). base: device fp32 or bf16 per base_dtype, row stride ld_base >=
+ * n, or NULL for zeros; y: fp32 or bf16 per y_dtype, row stride ldy >= n; y
+ * may be base itself if type and stride agree. h: device fp32 [m, rank] or
+ * NULL; gets A[i] x[t] (zeros without adapter), which binade_lora_grad
+ * takes.
+ * Arithmetic: A x on bf16 MFMA in fp32, in a fixed order that depends on k
+ * alone; h stays fp32 through the second product (three bf16 terms whose
+ * sum is h to 2^-24); y is rounded once. A row's result does not depend on
+ * the other rows, on m or on its place.
+ * workspace: device, 16-byte aligned, binade_lora_workspace_bytes bytes; not
+ * read before written; calls that overlap need their own. ENOSPACE: too
+ * small. */
+int32_t binade_lora_add(const binade_lora *l, const uint16_t *x, int64_t m,
+                        int64_t ldx, const int32_t *ids, const void *base,
+                        int64_t ld_base, int32_t base_dtype, void *y,
+                        int64_t ldy, int32_t y_dtype, float *h,
+                        void *workspace, int64_t workspace_bytes,
+                        uint32_t *dev_status, void *stream);
+
+/* Workspace bytes of binade_lora_add (0 for sizes it refuses). Pure host
+ * function. */
+int64_t binade_lora_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                    int32_t rank);
+
+/* The adapters' backward. With dy (device bf16, row stride ld_dy >= n) the
+ * gradient of y and i = ids[t]: g[t] = scale[i] * B[i]^T dy[t];
+ *   dx[t, :] = dx_base[t, :] + A[i]^T g[t]      bf16, rounded once
+ *   da[i]    = sum over rows t of i of g[t] x[t]^T
+ *   db[i]    = sum over rows t of i of scale[i] * dy[t] h[t]^T
+ * da [n_adapters, rank, k] and db [n_adapters, n, rank]: fp32 or bf16 per
+ * grad_dtype, zeros for an adapter without rows. dx: row stride ld_dx >= k,
+ * or NULL (nothing below learns); dx_base: bf16, row stride ld_dx_base >= k
+ * (the projection's own input gradient), or NULL for zeros; dx may be
+ * dx_base itself if the strides agree. h: device fp32 [m, rank] as
+ * binade_lora_add leaves it, or NULL (computed again). Other arguments as
+ * in binade_lora_add; dy rows need no alignment, x, dx and dx_base rows are
+ * 16-byte aligned. Sums are fp32 in a fixed order for given sizes and ids:
+ * the same call gives the same bits. */
+int32_t binade_lora_grad(const binade_lora *l, const uint16_t *x, int64_t m,
+                         int64_t ldx, const int32_t *ids, const uint16_t *dy,
+                         int64_t ld_dy, const float *h,
+                         const uint16_t *dx_base, int64_t ld_dx_base,
+                         uint16_t *dx, int64_t ld_dx, void *da, void *db,
+                         int32_t grad_dtype, void *workspace,
+                         int64_t workspace_bytes, uint32_t *dev_status,
+                         void *stream);
+
+/* Workspace bytes of binade_lora_grad (0 for sizes it refuses). Pure host
+ * function. */
+int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                         int32_t rank, int32_t n_adapters);
 
 #ifdef __cplusplus
 }
