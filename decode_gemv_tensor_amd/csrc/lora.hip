@@ -81,6 +81,18 @@ __device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uin
   lo = static_cast<uint16_t>(__float_as_uint(rest - __uint_as_float(m)) >> 16);
 }
 
+// Blocks are dealt to the 8 XCDs round robin. This gives every XCD one run of
+// consecutive units of work, so that neighbours, which read the same
+// adapter, meet in one L2. Launched over xcd_grid(units) blocks; a unit of
+// units or more has no work.
+constexpr int64_t kXcds = 8;
+__device__ __forceinline__ int64_t xcd_unit() {
+  return static_cast<int64_t>(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+}
+dim3 xcd_grid(int64_t units) {
+  return dim3(static_cast<uint32_t>((units + kXcds - 1) / kXcds * kXcds));
+}
+
 // ---------------------------------------------------------------- forward
 // h[t] = A[i] x[t]. Order, fixed by k alone: columns are cut into slices of
 // 256; slice s is one MFMA chain c_s from +0.0 (step j: lane group g carries
@@ -94,47 +106,86 @@ __device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uin
 //  - slices: a block per tile and slice, for the fewest rows.
 // The two finer ones deal the tile's adapters to the block's waves and leave
 // partial sums [parts][m][rank] that the second product's kernel adds.
+// The whole grain also splits h into the second product's MFMA operands.
+//
+// MFMA wants 16 rows in consecutive lanes, and a load whose neighbouring lanes
+// sit in different rows costs the L1 one access a lane (64 of 16 bytes; that
+// bound the first version). So every operand is loaded with four lanes on 64
+// contiguous bytes of a row and turned round through 1 KB of LDS.
 struct ShrinkArgs {
   LoraArgs p;
   const uint16_t* x;
-  float* out;
+  float* out;              // streams, slices: partial sums [parts][m][rank]
+  float* h;                // whole: fp32 [m][rank] or NULL
+  uint4* frag;             // whole: [tiles][3][KS][64] operands (NULL otherwise)
   int64_t ldx;
   int32_t slices, parts;   // parts: 1 (whole), 8 (streams) or slices
 };
 
+// Orders a wave's LDS writes before its lanes' reads of each other's values
+// (the hardware keeps a wave's LDS operations in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// N operands as loaded (lane 4 row + octet) -> as MFMA takes them (lane row +
+// 16 octet), through N KB of the wave's own; the swizzle spreads the reads of
+// 8 lanes over all banks.
+template <int N>
+__device__ __forceinline__ void turn(uint4 (&v)[N], uint4* lds, int lane) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) lds[64 * j + (lane ^ ((lane >> 4) & 3))] = v[j];
+  wave_sync();
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = lds[64 * j + 4 * i + (g ^ ((i >> 2) & 3))];
+  wave_sync();
+}
+
 template <int RT>
 __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
   const LoraArgs& p = s.p;
+  constexpr int kSumLd = 16 * RT + 4;
+  __shared__ union {
+    uint4 stage[kStreams][512];
+    float sums[kStreams][16][kSumLd];
+  } lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 16;
+  // units: slice (or running sum) major, tiles of 16 rows minor
+  const int64_t tiles = (p.m + 15) / 16, unit = xcd_unit();
+  if (unit >= tiles * s.parts) return;
+  const int32_t part = static_cast<int32_t>(unit / tiles);
+  const int64_t tile = unit - part * tiles, row0 = tile * 16;
   const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
   const int32_t id = row0 + i < p.m ? adapter_of(p, row) : -1;
-  if (blockIdx.y == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
+  if (part == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
       row0 + i < p.m && p.ids[row] != -1)
     atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
-  const int32_t first = s.parts == 1 ? wave : static_cast<int32_t>(blockIdx.y);
-  const int32_t step = s.parts <= kStreams ? kStreams : s.slices;
+  const bool whole = s.frag != nullptr;
+  const int32_t first = whole ? wave : part;
+  const int32_t step = whole || s.parts < s.slices ? kStreams : s.slices;
   int32_t idq[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64);
   floatx4 mine[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) mine[r] = floatx4{0, 0, 0, 0};
+  // as loaded: row lane / 4, columns 8 (lane % 4) on
+  const int64_t lrow = row0 + (lane >> 2) < p.m ? row0 + (lane >> 2) : p.m - 1;
+  const uint16_t* xl = s.x + lrow * s.ldx + 8 * (lane & 3);
   const uint16_t* xr = s.x + row * s.ldx + 8 * g;
+  uint4* stage = lds.stage[wave];
   uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
   uint32_t got = wave == 0 ? 0xFFFFu & ~todo : 0u;   // rows whose sums this wave holds
-  for (int32_t turn = 0; todo != 0; ++turn) {
+  for (int32_t nth = 0; todo != 0; ++nth) {
     const int32_t a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
     const uint32_t match = static_cast<uint32_t>(__ballot(id == a)) & 0xFFFFu;
     todo &= ~match;
-    if (s.parts > 1 && turn % static_cast<int32_t>(blockDim.x >> 6) != wave) continue;
+    if (!whole && nth % static_cast<int32_t>(blockDim.x >> 6) != wave) continue;
     got |= match;
-    const uint16_t* ar[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int32_t rr = 16 * r + i < p.rank ? 16 * r + i : p.rank - 1;
-      ar[r] = p.a + (static_cast<int64_t>(a) * p.rank + rr) * p.k + 8 * g;
-    }
+    const uint16_t* aa = p.a + static_cast<int64_t>(a) * p.rank * p.k;
+    const auto rank_row = [&](int r) { return r < p.rank ? r : p.rank - 1; };
     floatx4 sum[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) sum[r] = floatx4{0, 0, 0, 0};
@@ -144,18 +195,28 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = floatx4{0, 0, 0, 0};
       if (p.k - col >= kSlice) {
-        uint4 xf[8];
+        uint4 xf[8], af[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xf[j] = *reinterpret_cast<const uint4*>(xr + col + 32 * j);
+        for (int j = 0; j < 8; ++j) xf[j] = *reinterpret_cast<const uint4*>(xl + col + 32 * j);
+        const auto load_a = [&](int r) {
+          const uint16_t* al = aa + rank_row(16 * r + (lane >> 2)) * p.k + 8 * (lane & 3) + col;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) af[j] = *reinterpret_cast<const uint4*>(al + 32 * j);
+        };
+        load_a(0);
+        turn(xf, stage, lane);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          uint4 af[8];
+          uint4 bf[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) af[j] = *reinterpret_cast<const uint4*>(ar[r] + col + 32 * j);
+          for (int j = 0; j < 8; ++j) bf[j] = af[j];
+          if (RT < 8 && r + 1 < RT) load_a(r + 1);   // 8 tiles' sums leave no registers for it
+          turn(bf, stage, lane);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf[j]), as_bf16x8(af[j]),
+            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf[j]), as_bf16x8(bf[j]),
                                                              acc[r], 0, 0, 0);
+          if (RT == 8 && r + 1 < RT) load_a(r + 1);
         }
       } else {
         for (int64_t cc = col; cc < p.k; cc += 32) {
@@ -163,8 +224,10 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
 #pragma unroll
           for (int r = 0; r < RT; ++r)
             acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(xf), as_bf16x8(*reinterpret_cast<const uint4*>(ar[r] + cc)), acc[r], 0, 0,
-                0);
+                as_bf16x8(xf),
+                as_bf16x8(*reinterpret_cast<const uint4*>(aa + rank_row(16 * r + i) * p.k + 8 * g +
+                                                          cc)),
+                acc[r], 0, 0, 0);
         }
       }
 #pragma unroll
@@ -176,8 +239,8 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
       for (int q = 0; q < 4; ++q)
         if (idq[q] == a) mine[r][q] = sum[r][q];
   }
-  if (s.parts > 1) {
-    float* out = s.out + static_cast<int64_t>(blockIdx.y) * p.m * p.rank;
+  if (!whole) {
+    float* out = s.out + part * p.m * p.rank;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -188,31 +251,49 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
       }
     return;
   }
-  __shared__ float sums[kStreams][16][16 * RT];
+  __syncthreads();
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sums[wave][4 * g + q][16 * r + i] = mine[r][q];
+    for (int q = 0; q < 4; ++q) lds.sums[wave][4 * g + q][16 * r + i] = mine[r][q];
   __syncthreads();
-  const int32_t live = s.slices < kStreams ? s.slices : kStreams;
-  for (int32_t e = threadIdx.x; e < 16 * p.rank; e += 512) {
-    const int32_t t = e / p.rank, r = e - t * p.rank;
-    float v = 0.0f;
-    for (int32_t w = 0; w < live; ++w) v += sums[w][t][r];
-    if (row0 + t < p.m) s.out[(row0 + t) * p.rank + r] = v;
+  // thread = (K step, lane) of the second product's operand: 8 ranks of a row
+  const int32_t ks = (p.rank + 31) / 32;
+  if (wave >= ks) return;
+  const int32_t r0 = 32 * wave + 8 * g;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if (r0 < p.rank && row0 + i < p.m) {
+    const int32_t live = s.slices < kStreams ? s.slices : kStreams;
+    for (int32_t w = 0; w < live; ++w)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += lds.sums[w][i][r0 + j];
+    if (s.h != nullptr) __builtin_memcpy(s.h + (row0 + i) * p.rank + r0, v, 32);
   }
+  uint16_t d[3][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    s.frag[((tile * 3 + t) * ks + wave) * 64 + lane] = __builtin_bit_cast(uint4, d[t]);
 }
 
-// y[t] = base[t] + s[i] B[i] h[t]: 16 MT rows by 64 CT columns a block of
-// four waves, each wave 16 CT columns. h is split into three bf16 terms in
-// LDS; B's rows go straight into MFMA operands and stay in registers for the
-// block's row tiles of one adapter. Column c of a wave's MFMA tiles is spread
-// so that lane i ends with the CT adjacent columns CT i .. CT i + CT - 1. A
-// tile of 16 rows runs once for each adapter among them; base is loaded one
-// tile ahead of its use.
+// y[t] = base[t] + s[i] B[i] h[t]. Column c of a wave's MFMA tiles is spread so
+// that lane i ends with the CT adjacent columns CT i .. CT i + CT - 1. A tile of
+// 16 rows runs once for each adapter among them and every row keeps its own;
+// base + scale * product is one fma (rows without an adapter: -0 * 0 + base).
+// Two shapes:
+//  - few rows: a block of four waves has 16 rows by 128 columns, joins the
+//    partial sums of h in LDS and splits them into three bf16 terms there;
+//  - many rows: a wave has 64 columns of eight row tiles; h arrives split as
+//    operands, B's rows stay in the wave's LDS while the adapter does not
+//    change (in registers they cost the occupancy that hides a tile's loads),
+//    a tile's base is loaded while the one before it runs.
 struct ExpandArgs {
   LoraArgs p;
-  const float* part;
+  const float* part;       // few rows: partial sums of h
+  const uint4* frag;       // many rows: h as operands
   const void* base;
   void* y;
   float* h;
@@ -224,10 +305,9 @@ struct ExpandArgs {
 
 // The sum of a value's partial sums in the order of the first product, four
 // ranks at a time: at is the first of parts partials, next apart.
-template <int kAhead>
 __device__ __forceinline__ floatx4 join_parts(const float* at, int64_t next, int32_t parts) {
   floatx4 v{0, 0, 0, 0};
-  if (parts == 1) return *reinterpret_cast<const floatx4*>(at);
+  constexpr int kAhead = 4;
   floatx4 sum[kStreams];
 #pragma unroll
   for (int w = 0; w < kStreams; ++w) sum[w] = floatx4{0, 0, 0, 0};
@@ -259,183 +339,358 @@ struct BaseTile {
   uint32_t d[4][BK == kNone ? 1 : BK == kBf16 ? CT / 2 : CT];   // four rows' values, as loaded
 };
 
-template <int KS, int MT, int CT, int BK, int YK>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs s) {
-  const LoraArgs& p = s.p;
-  constexpr int kRows = 16 * MT, kLd = 32 * KS + 8;
-  __shared__ __align__(16) uint16_t hs[3][kRows][kLd];
-  __shared__ __align__(16) int32_t ids[kRows];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kRows;
-  const int32_t rows = static_cast<int32_t>(p.m - row0 < kRows ? p.m - row0 : kRows);
-  const int64_t col = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (16 * CT) + CT * i;
-  const bool full = col + CT <= p.n;
+// Where a lane's values of a tile lie: a uniform address per row q and one
+// 32-bit byte offset for all of them (rows 4 g + q, columns col on).
+template <int K>
+__device__ __forceinline__ uint32_t lane_offset(int64_t ld, int g, int32_t col_in_wave) {
+  return static_cast<uint32_t>(4 * g * ld + col_in_wave) * (K == kBf16 ? 2u : 4u);
+}
 
-  BaseTile<CT, BK> ahead;
-  auto load_base = [&](int m) {
-    if (BK == kNone || !full) return;
+template <int CT, int BK>
+__device__ __forceinline__ void load_base(const ExpandArgs& s, int64_t row0, int32_t rows, int g,
+                                          int64_t wave_col, int32_t col_in_wave, bool full,
+                                          BaseTile<CT, BK>& to) {
+  if (BK == kNone || !full) return;
+  constexpr int kSize = BK == kBf16 ? 2 : 4;
+  const char* at = static_cast<const char*>(s.base) + (row0 * s.ld_base + wave_col) * kSize;
+  const uint32_t off = lane_offset<BK>(s.ld_base, g, col_in_wave);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (rows == 16 || 4 * g + q < rows)
+      __builtin_memcpy(to.d[q], at + q * s.ld_base * kSize + off, CT * kSize);
+}
+
+// Four rows' results from column col on: base + scale * product, stored.
+template <int CT, int BK, int YK>
+__device__ __forceinline__ void finish_rows(const ExpandArgs& s, int64_t row0, int32_t rows, int g,
+                                            int64_t wave_col, int32_t col_in_wave, bool full,
+                                            const BaseTile<CT, BK>& base,
+                                            const floatx4 (&acc)[CT], const float (&scale)[4]) {
+  constexpr int kSize = YK == kBf16 ? 2 : 4;
+  if (full) {
+    char* at = static_cast<char*>(s.y) + (row0 * s.ldy + wave_col) * kSize;
+    const uint32_t off = lane_offset<YK>(s.ldy, g, col_in_wave);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int t = 16 * m + 4 * g + q;
-      const int64_t at = (row0 + (t < rows ? t : rows - 1)) * s.ld_base + col;
-      if (BK == kBf16)
-        __builtin_memcpy(ahead.d[q], static_cast<const uint16_t*>(s.base) + at, 2 * CT);
-      else
-        __builtin_memcpy(ahead.d[q], static_cast<const float*>(s.base) + at, 4 * CT);
+      float f[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float b = 0.0f;
+        if (BK == kBf16)
+          b = c & 1 ? bf16_hi(base.d[q][c / 2]) : bf16_lo(base.d[q][c / 2]);
+        else if (BK == kF32)
+          b = __uint_as_float(base.d[q][c]);
+        f[c] = __builtin_fmaf(scale[q], acc[c][q], b);
+      }
+      if (rows < 16 && 4 * g + q >= rows) continue;
+      if (YK == kBf16) {
+        uint32_t d[CT / 2];
+#pragma unroll
+        for (int c = 0; c < CT / 2; ++c) d[c] = pack_bf16(f[2 * c], f[2 * c + 1]);
+        __builtin_memcpy(at + q * s.ldy * kSize + off, d, 2 * CT);
+      } else {
+        __builtin_memcpy(at + q * s.ldy * kSize + off, f, 4 * CT);
+      }
     }
-  };
-  if (threadIdx.x < kRows)
-    ids[threadIdx.x] =
-        static_cast<int32_t>(threadIdx.x) < rows ? adapter_of(p, row0 + threadIdx.x) : -2;
-  load_base(0);
-  for (int32_t e = threadIdx.x; e < kRows * 8 * KS; e += 256) {
+  } else if (wave_col + col_in_wave < s.p.n) {   // the row's last columns, one by one
+    const int64_t col = wave_col + col_in_wave;
+#pragma unroll
+    for (int c = 0; c < CT - 1; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (4 * g + q >= rows || col + c >= s.p.n) continue;
+        const int64_t t = row0 + 4 * g + q;
+        const float b =
+            BK == kNone ? 0.0f : load_any(s.base, t * s.ld_base + col + c, BK == kBf16);
+        store_any(s.y, t * s.ldy + col + c, YK == kBf16, __builtin_fmaf(scale[q], acc[c][q], b));
+      }
+  }
+}
+
+// B's operands of adapter a for a wave's columns, as loaded; turn() follows.
+// Zeros for ranks beyond the last (h has zeros there too).
+template <int KS, int CT>
+__device__ __forceinline__ void load_b(const LoraArgs& p, int32_t a, int64_t wave_col, int lane,
+                                       uint4 (&bf)[KS][CT]) {
+  const uint16_t* b = p.b + static_cast<int64_t>(a) * p.n * p.rank;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int64_t n = wave_col + CT * (lane >> 2) + c;
+    const uint16_t* row = b + (n < p.n ? n : p.n - 1) * p.rank;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int32_t o = 32 * k + 8 * (lane & 3);
+      bf[k][c] = *reinterpret_cast<const uint4*>(row + (o < p.rank ? o : 0));
+    }
+  }
+  if (32 * KS > p.rank) {
+    const bool live = 32 * (KS - 1) + 8 * (lane & 3) < p.rank;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      uint4& v = bf[KS - 1][c];
+      v.x = live ? v.x : 0u;
+      v.y = live ? v.y : 0u;
+      v.z = live ? v.z : 0u;
+      v.w = live ? v.w : 0u;
+    }
+  }
+}
+
+template <int KS, int BK, int YK>
+__global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs s) {
+  const LoraArgs& p = s.p;
+  constexpr int CT = 2, kLd = 32 * KS + 8;
+  __shared__ __align__(16) uint16_t hs[3][16][kLd];
+  __shared__ uint4 stage[4][64 * CT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  // units: row tiles major, columns minor
+  const int64_t col_blocks = (p.n + 64 * CT - 1) / (64 * CT), unit = xcd_unit();
+  const int64_t row0 = unit / col_blocks * 16, col_block = unit % col_blocks;
+  if (row0 >= p.m) return;
+  const int32_t rows = static_cast<int32_t>(p.m - row0 < 16 ? p.m - row0 : 16);
+  const int64_t wave_col = (col_block * 4 + uniform(wave)) * (16 * CT);
+  const bool full = wave_col + CT * i + CT <= p.n;
+  const int32_t id = i < rows ? adapter_of(p, row0 + i) : -1;
+  BaseTile<CT, BK> base;
+  load_base<CT, BK>(s, row0, rows, g, wave_col, CT * i, full, base);
+  for (int32_t e = threadIdx.x; e < 16 * 8 * KS; e += 256) {
     const int32_t t = e / (8 * KS), r = 4 * (e % (8 * KS));
     floatx4 v{0, 0, 0, 0};
     if (r < p.rank && t < rows) {
       const int64_t at = (row0 + t) * p.rank + r;
-      v = join_parts<MT == 1 ? 4 : 1>(s.part + at, p.m * p.rank, s.parts);
-      if (s.h != nullptr && blockIdx.x == 0) *reinterpret_cast<floatx4*>(s.h + at) = v;
+      v = join_parts(s.part + at, p.m * p.rank, s.parts);
+      if (s.h != nullptr && col_block == 0) *reinterpret_cast<floatx4*>(s.h + at) = v;
     }
     uint16_t d[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);
 #pragma unroll
-    for (int part = 0; part < 3; ++part) __builtin_memcpy(&hs[part][t][r], d[part], 8);
+    for (int t3 = 0; t3 < 3; ++t3) __builtin_memcpy(&hs[t3][t][r], d[t3], 8);
   }
   __syncthreads();
-
-  uint4 bf[CT][KS];
-  int32_t loaded = -1;
-  float scale = 1.0f;
-#pragma unroll 1
-  for (int m = 0; 16 * m < rows; ++m) {
-    const BaseTile<CT, BK> base = ahead;
-    if (16 * (m + 1) < rows) load_base(m + 1);
-    int32_t idq[4];
-    __builtin_memcpy(idq, &ids[16 * m + 4 * g], 16);
-    const int32_t id = ids[16 * m + i];
-    floatx4 mine[CT];
+  int32_t idq[4];
+  float scale[4];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) mine[c] = floatx4{0, 0, 0, 0};
-    uint64_t todo = __ballot(id >= 0) & 0xFFFFu;
-    while (todo != 0) {
-      const int32_t a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-      todo &= ~__ballot(id == a);
-      if (a != loaded) {
-        loaded = a;
-        scale = p.scale != nullptr ? p.scale[a] : 1.0f;
+  for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64), scale[q] = -0.0f;
+  floatx4 mine[CT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int64_t n = col + c < p.n ? col + c : p.n - 1;
-          const uint16_t* b = p.b + (static_cast<int64_t>(a) * p.n + n) * p.rank;
+  for (int c = 0; c < CT; ++c) mine[c] = floatx4{0, 0, 0, 0};
+  // up to kBatch adapters' operands at once: a mixed tile waits for memory once
+  // per batch
+  constexpr int kBatch = KS <= 2 ? 4 : 2;
+  uint64_t todo = __ballot(id >= 0) & 0xFFFFu;
+  while (todo != 0) {
+    int32_t a[kBatch];
+    uint4 bf[kBatch][KS][CT];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const int32_t o = 32 * k + 8 * g;
-            bf[c][k] = *reinterpret_cast<const uint4*>(b + (o < p.rank ? o : 0));
-          }
-        }
-        // ranks beyond the last: zeros (h has zeros there too)
+    for (int z = 0; z < kBatch; ++z) {
+      a[z] = todo != 0 ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : a[0];
+      todo &= ~__ballot(id == a[z]);
+    }
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          if (32 * k + 32 > p.rank) {
-            const bool live = 32 * k + 8 * g < p.rank;
+    for (int z = 0; z < kBatch; ++z) load_b<KS, CT>(p, a[z], wave_col, lane, bf[z]);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              bf[c][k].x = live ? bf[c][k].x : 0u;
-              bf[c][k].y = live ? bf[c][k].y : 0u;
-              bf[c][k].z = live ? bf[c][k].z : 0u;
-              bf[c][k].w = live ? bf[c][k].w : 0u;
-            }
-          }
-      }
+    for (int z = 0; z < kBatch; ++z) {
+      if (z > 0 && a[z] == a[0]) break;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) turn(bf[z][k], stage[wave], lane);
+      const float sc = p.scale != nullptr ? p.scale[a[z]] : 1.0f;
       floatx4 acc[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[c] = floatx4{0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const bf16x8 hf = as_bf16x8(
-              *reinterpret_cast<const uint4*>(&hs[part][16 * m + i][32 * k + 8 * g]));
+        for (int t3 = 0; t3 < 3; ++t3) {
+          const bf16x8 hf =
+              as_bf16x8(*reinterpret_cast<const uint4*>(&hs[t3][i][32 * k + 8 * g]));
 #pragma unroll
           for (int c = 0; c < CT; ++c)
-            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, as_bf16x8(bf[c][k]), acc[c], 0, 0,
-                                                             0);
+            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, as_bf16x8(bf[z][k][c]), acc[c], 0,
+                                                             0, 0);
         }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const bool hit = idq[q] == a;
+        const bool hit = idq[q] == a[z];
+        scale[q] = hit ? sc : scale[q];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) mine[c][q] = hit ? scale * acc[c][q] : mine[c][q];
+        for (int c = 0; c < CT; ++c) mine[c][q] = hit ? acc[c][q] : mine[c][q];
       }
     }
-    if (full) {
+  }
+  finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base, mine, scale);
+}
+
+constexpr int kManyTiles = 8;    // row tiles of a block
+constexpr int kManyCols = 4;     // columns of a lane
+
+// A wave's 64 rows of B (its columns' ranks) in LDS: 16-byte piece o of column
+// CT i + c at 16 c + i rows of rank/8 pieces, o swizzled by i where a row is a
+// power of two of them, so that 8 lanes' reads meet no bank twice.
+template <int KS, int CT>
+struct BTile {
+  uint4 piece[16 * CT * 4 * KS];
+};
+
+// kAll: every piece requested at once (the start of a wave), or one after the
+// other, which takes no registers from a tile under way (a later adapter).
+template <bool kAll, int KS, int CT>
+__device__ __forceinline__ void stage_b(const LoraArgs& p, int32_t a, int64_t wave_col, int lane,
+                                        BTile<KS, CT>& t, int32_t mask, int32_t shift) {
+  const int32_t per = p.rank / 8, count = 16 * CT * per;
+  const int64_t left = (p.n - wave_col) * per - 1;   // the last piece that exists
+  const uint4* b = reinterpret_cast<const uint4*>(
+      p.b + (static_cast<int64_t>(a) * p.n + wave_col) * p.rank);
+  wave_sync();
+  const auto put = [&](int32_t e, uint4 v) {
+    const int32_t col = e / per, o = e - col * per, i = col / CT, c = col % CT;
+    t.piece[(16 * c + i) * per + (o ^ ((i >> shift) & mask))] = v;
+  };
+  if (kAll) {
+    uint4 v[CT * KS];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int t = 16 * m + 4 * g + q;
-        float f[CT];
+    for (int j = 0; j < CT * KS; ++j)
+      if (64 * j < count) v[j] = b[64 * j + lane < left ? 64 * j + lane : left];
+#pragma unroll
+    for (int j = 0; j < CT * KS; ++j)
+      if (64 * j < count) put(64 * j + lane, v[j]);
+  } else {
+#pragma unroll 1
+    for (int32_t e = lane; e < count; e += 64) put(e, b[e < left ? e : left]);
+  }
+  wave_sync();
+}
+
+template <int KS, int BK, int YK>
+__global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) void expand_many_kernel(ExpandArgs s) {
+  const LoraArgs& p = s.p;
+  constexpr int CT = kManyCols, MT = kManyTiles;
+  __shared__ BTile<KS, CT> tiles_b[4];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const uint32_t col_blocks = static_cast<uint32_t>((p.n + 64 * CT - 1) / (64 * CT));
+  // row tiles major, columns minor, dealt to the XCDs as they come: a run of
+  // neighbours on one XCD reads its adapters from one L2 but streams base and
+  // y slower (108 against 101 us with the first product at 4096 rows, rank
+  // 64, 16 adapters, 3840 -> 15360)
+  const uint32_t unit = blockIdx.x;
+  const uint32_t block_row = unit / col_blocks;
+  const int64_t tile0 = static_cast<int64_t>(block_row) * MT;
+  const int64_t wave_col =
+      (static_cast<int64_t>(unit - block_row * col_blocks) * 4 + wave) * (16 * CT);
+  if (tile0 * 16 >= p.m || wave_col >= p.n) return;
+  const bool full = wave_col + CT * i + CT <= p.n;
+  const int32_t live = static_cast<int32_t>(p.m - tile0 * 16 < 16 * MT ? p.m - tile0 * 16 : 16 * MT);
+  const int32_t per = p.rank / 8;
+  const int32_t mask = (per & (per - 1)) == 0 ? (per < 8 ? per : 8) - 1 : 0;
+  const int32_t shift = per >= 8 ? 0 : per == 4 ? 2 : 0;
+  BTile<KS, CT>& bt = tiles_b[wave];
+  int32_t loaded = -1;
+  float sc = 1.0f;
+  BaseTile<CT, BK> base;
+  int32_t id;
+  const auto load_tile = [&](int m) {
+    const int32_t rows = live - 16 * m < 16 ? live - 16 * m : 16;
+    id = i < rows ? adapter_of(p, (tile0 + m) * 16 + i) : -1;
+    load_base<CT, BK>(s, (tile0 + m) * 16, rows, g, wave_col, CT * i, full, base);
+  };
+  load_tile(0);
+  const uint64_t any = __ballot(id >= 0);
+  if (any != 0) {
+    loaded = __builtin_amdgcn_readlane(id, __builtin_ctzll(any));
+    sc = p.scale != nullptr ? p.scale[loaded] : 1.0f;
+    stage_b<true, KS, CT>(p, loaded, wave_col, lane, bt, mask, shift);
+  }
+#pragma unroll 1
+  for (int m = 0; 16 * m < live; ++m) {
+    const int64_t row0 = (tile0 + m) * 16;
+    const int32_t rows = live - 16 * m < 16 ? live - 16 * m : 16, id_now = id;
+    const BaseTile<CT, BK> base_now = base;
+    uint4 hf[3][KS];
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) hf[t][k] = s.frag[(((tile0 + m) * 3 + t) * KS + k) * 64 + lane];
+    if (16 * (m + 1) < live) load_tile(m + 1);
+    float scale[4];
+    floatx4 mine[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) mine[c] = floatx4{0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) scale[q] = -0.0f;
+    uint32_t todo = static_cast<uint32_t>(__ballot(id_now >= 0)) & 0xFFFFu;
+#pragma unroll 1
+    while (todo != 0) {
+      const int32_t a = __builtin_amdgcn_readlane(id_now, __builtin_ctz(todo));
+      const uint32_t match = static_cast<uint32_t>(__ballot(id_now == a)) & 0xFFFFu;
+      todo &= ~match;
+      if (a != loaded) {
+        loaded = a;
+        sc = p.scale != nullptr ? p.scale[a] : 1.0f;
+        stage_b<false, KS, CT>(p, a, wave_col, lane, bt, mask, shift);
+      }
+      floatx4 acc[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = floatx4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint4 bf[CT];
+        const int32_t o = 4 * k + g;
+        const bool ok = o < per;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          float b = 0.0f;
-          if (BK == kBf16)
-            b = c & 1 ? bf16_hi(base.d[q][c / 2]) : bf16_lo(base.d[q][c / 2]);
-          else if (BK == kF32)
-            b = __uint_as_float(base.d[q][c]);
-          f[c] = idq[q] < 0 ? b : b + mine[c][q];
+          bf[c] = bt.piece[(16 * c + i) * per + ((ok ? o : 0) ^ ((i >> shift) & mask))];
+          if (32 * k + 32 > p.rank) {
+            bf[c].x = ok ? bf[c].x : 0u;
+            bf[c].y = ok ? bf[c].y : 0u;
+            bf[c].z = ok ? bf[c].z : 0u;
+            bf[c].w = ok ? bf[c].w : 0u;
+          }
         }
-        if (t >= rows) continue;
-        const int64_t at = (row0 + t) * s.ldy + col;
-        if (YK == kBf16) {
-          uint32_t d[CT / 2];
 #pragma unroll
-          for (int c = 0; c < CT / 2; ++c) d[c] = pack_bf16(f[2 * c], f[2 * c + 1]);
-          __builtin_memcpy(static_cast<uint16_t*>(s.y) + at, d, 2 * CT);
-        } else {
-          __builtin_memcpy(static_cast<float*>(s.y) + at, f, 4 * CT);
-        }
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hf[t][k]), as_bf16x8(bf[c]),
+                                                             acc[c], 0, 0, 0);
       }
-    } else if (col < p.n) {   // the row's last columns, one by one
 #pragma unroll
-      for (int c = 0; c < CT - 1; ++c)
+      for (int q = 0; q < 4; ++q) {
+        const bool hit = (match >> (4 * g + q)) & 1u;
+        scale[q] = hit ? sc : scale[q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int t = 16 * m + 4 * g + q;
-          if (t >= rows || col + c >= p.n) continue;
-          const float b = BK == kNone ? 0.0f
-                                      : load_any(s.base, (row0 + t) * s.ld_base + col + c,
-                                                 BK == kBf16);
-          store_any(s.y, (row0 + t) * s.ldy + col + c, YK == kBf16,
-                    idq[q] < 0 ? b : b + mine[c][q]);
-        }
+        for (int c = 0; c < CT; ++c) mine[c][q] = hit ? acc[c][q] : mine[c][q];
+      }
     }
+    finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base_now, mine, scale);
   }
 }
 
 int32_t slices_of(int64_t k) { return static_cast<int32_t>((k + kSlice - 1) / kSlice); }
 
-// Whether the second product's blocks of 64 rows by 512 columns fill the
-// chip; blocks of 16 by 128 otherwise.
-bool wide_expand(int64_t m, int64_t n) {
-  return ((m + 63) / 64) * ((n + 511) / 512) >= 256;
+// Whether blocks of 64 rows by 256 columns fill the chip.
+bool many_rows(int64_t m, int64_t n) {
+  return m >= 512 && ((m + 63) / 64) * ((n + 255) / 256) >= 256;
 }
 
-// Grain of the first product: partial sums it leaves per value.
+// Grain of the first product: partial sums it leaves per value (1: h whole,
+// as the operands of the many-rows product).
 int32_t shrink_parts(int64_t m, int64_t n, int64_t k) {
+  if (many_rows(m, n)) return 1;
   const int64_t tiles = (m + 15) / 16;
   const int32_t slices = slices_of(k);
-  if (tiles >= 128 || slices == 1) return 1;
-  if ((tiles * kStreams >= 256 || wide_expand(m, n)) && slices > kStreams) return kStreams;
-  return slices;
+  return tiles * kStreams >= 256 && slices > kStreams ? kStreams : slices;
 }
 
-void launch_shrink(const LoraArgs& p, const uint16_t* x, int64_t ldx, int32_t parts, float* out,
-                   hipStream_t st) {
-  const ShrinkArgs s{p, x, out, ldx, slices_of(p.k), parts};
-  const dim3 grid(static_cast<uint32_t>((p.m + 15) / 16), parts == 1 ? 1u : static_cast<uint32_t>(parts));
-  const int64_t mixed = p.ids == nullptr || p.m < p.n_adapters ? p.m : p.n_adapters;
-  const dim3 block(parts == 1 ? 64 * kStreams
-                   : p.ids == nullptr || mixed < 2 ? 64
-                   : mixed < 8 ? 256 : 512);
+int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
+  if (many_rows(m, n)) return (m + 15) / 16 * 3 * ((rank + 31) / 32) * 1024;
+  return shrink_parts(m, n, k) * m * rank * 4;
+}
+
+void launch_shrink(const ShrinkArgs& s, hipStream_t st) {
+  const LoraArgs& p = s.p;
+  const dim3 grid = xcd_grid((p.m + 15) / 16 * s.parts);
+  const int64_t mixed = p.ids == nullptr ? 1 : p.m < p.n_adapters ? p.m : p.n_adapters;
+  const dim3 block(s.frag != nullptr ? 64 * kStreams : mixed < 2 ? 64 : mixed < 8 ? 256 : 512);
   if (p.rank <= 16) hipLaunchKernelGGL(shrink_kernel<1>, grid, block, 0, st, s);
   else if (p.rank <= 32) hipLaunchKernelGGL(shrink_kernel<2>, grid, block, 0, st, s);
   else if (p.rank <= 64) hipLaunchKernelGGL(shrink_kernel<4>, grid, block, 0, st, s);
@@ -445,14 +700,14 @@ void launch_shrink(const LoraArgs& p, const uint16_t* x, int64_t ldx, int32_t pa
 template <int KS, int BK, int YK>
 void launch_expand_shape(const ExpandArgs& s, hipStream_t st) {
   const int64_t m = s.p.m, n = s.p.n;
-  const auto grid = [&](int64_t rows, int64_t cols) {
-    return dim3(static_cast<uint32_t>((n + cols - 1) / cols),
-                static_cast<uint32_t>((m + rows - 1) / rows));
-  };
-  if (wide_expand(m, n))
-    hipLaunchKernelGGL((expand_kernel<KS, 4, 8, BK, YK>), grid(64, 512), dim3(256), 0, st, s);
+  if (s.frag != nullptr)
+    hipLaunchKernelGGL((expand_many_kernel<KS, BK, YK>),
+                       dim3(static_cast<uint32_t>((n + 64 * kManyCols - 1) / (64 * kManyCols) *
+                                                  ((m + 16 * kManyTiles - 1) / (16 * kManyTiles)))),
+                       dim3(256), 0, st, s);
   else
-    hipLaunchKernelGGL((expand_kernel<KS, 1, 2, BK, YK>), grid(16, 128), dim3(256), 0, st, s);
+    hipLaunchKernelGGL((expand_few_kernel<KS, BK, YK>),
+                       xcd_grid((n + 127) / 128 * ((m + 15) / 16)), dim3(256), 0, st, s);
 }
 
 template <int KS>
@@ -470,6 +725,7 @@ void launch_expand_ranks(const ExpandArgs& s, hipStream_t st) {
 void launch_expand(const ExpandArgs& s, hipStream_t st) {
   if (s.p.rank <= 32) launch_expand_ranks<1>(s, st);
   else if (s.p.rank <= 64) launch_expand_ranks<2>(s, st);
+  else if (s.p.rank <= 96) launch_expand_ranks<3>(s, st);
   else launch_expand_ranks<4>(s, st);
 }
 
@@ -552,9 +808,12 @@ uint32_t blocks_for(int64_t n) {
   return static_cast<uint32_t>(b < 65536 ? b : 65536);
 }
 
+// Row strides: 12 rows of fp32 stay below 2^31 bytes (32-bit lane offsets).
+constexpr int64_t kMaxStride = 1 << 24;
+
 bool sizes_ok(int64_t m, int64_t n, int64_t k, int32_t rank) {
-  return m >= 0 && n >= 1 && k >= 1 && k % 32 == 0 && k <= (1 << 30) && n <= (1 << 30) &&
-         m <= (1 << 30) && rank >= 8 && rank <= 128 && rank % 8 == 0;
+  return m >= 0 && n >= 1 && k >= 1 && k % 32 == 0 && k <= (1 << 24) && n <= (1 << 24) &&
+         m <= (1 << 24) && rank >= 8 && rank <= 128 && rank % 8 == 0;
 }
 
 int32_t check_common(const binade_lora* l, const uint16_t* x, int64_t m, int64_t ldx,
@@ -580,7 +839,7 @@ LoraArgs args_of(const binade_lora* l, int64_t m, const int32_t* ids, uint32_t* 
 using namespace binade;
 
 extern "C" int64_t binade_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t rank) {
-  return sizes_ok(m, n, k, rank) ? shrink_parts(m, n, k) * m * rank * 4 : 0;
+  return sizes_ok(m, n, k, rank) ? add_workspace(m, n, k, rank) : 0;
 }
 
 extern "C" int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t rank,
@@ -599,16 +858,20 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
       (y_dtype != BINADE_F32 && y_dtype != BINADE_BF16))
     return BINADE_EINVAL;
   if (m == 0) return BINADE_OK;
+  if (!aligned16(h)) return BINADE_EUNSUPPORTED;
   if (y == nullptr || ldy < l->n || (base != nullptr && ld_base < l->n)) return BINADE_EINVAL;
+  if (ldy > kMaxStride || (base != nullptr && ld_base > kMaxStride)) return BINADE_EUNSUPPORTED;
   if (workspace_bytes < binade_lora_workspace_bytes(m, l->n, l->k, l->rank) ||
       workspace == nullptr)
     return BINADE_ENOSPACE;
   const LoraArgs p = args_of(l, m, ids, dev_status);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int32_t parts = shrink_parts(m, p.n, p.k);
-  float* part = parts == 1 && h != nullptr ? h : static_cast<float*>(workspace);
-  launch_shrink(p, x, ldx, parts, part, st);
-  launch_expand(ExpandArgs{p, part, base, y, h, ld_base, ldy, parts,
+  const bool many = many_rows(m, p.n);
+  float* part = many ? nullptr : static_cast<float*>(workspace);
+  uint4* frag = many ? static_cast<uint4*>(workspace) : nullptr;
+  launch_shrink(ShrinkArgs{p, x, part, h, frag, ldx, slices_of(p.k), many ? 1 : parts}, st);
+  launch_expand(ExpandArgs{p, part, frag, base, y, h, ld_base, ldy, parts,
                            base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
                            y_dtype == BINADE_BF16},
                 st);

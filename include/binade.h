@@ -617,8 +617,9 @@ int32_t binade_moe_route_grad(const void *logits, int32_t dtype, int64_t ld,
  *   a      bf16 [n_adapters, rank, k]
  *   b      bf16 [n_adapters, n, rank]
  *   scale  fp32 [n_adapters], or NULL for ones
- * k % 32 == 0, rank a multiple of 8 in 8..128, n_adapters in 1..65535; a and
- * b 16-byte aligned, else BINADE_EUNSUPPORTED. */
+ * k % 32 == 0, rank a multiple of 8 in 8..128, n_adapters in 1..65535, n, k
+ * and rows and row strides of a call at most 2^24; a and b 16-byte aligned,
+ * else BINADE_EUNSUPPORTED. */
 typedef struct binade_lora {
   int64_t n, k;
   int32_t rank, n_adapters;
@@ -636,8 +637,8 @@ typedef struct binade_lora {
  * x: device bf16, row t at x + t*ldx (ldx >= k, a multiple of 8; 16-byte
  * aligned). base: device fp32 or bf16 per base_dtype, row stride ld_base >=
  * n, or NULL for zeros; y: fp32 or bf16 per y_dtype, row stride ldy >= n; y
- * may be base itself if type and stride agree. h: device fp32 [m, rank] or
- * NULL; gets A[i] x[t] (zeros without adapter), which binade_lora_grad
+ * may be base itself if type and stride agree. h: device fp32 [m, rank],
+ * 16-byte aligned, or NULL; gets A[i] x[t] (zeros without adapter), which binade_lora_grad
  * takes.
  * Arithmetic: A x on bf16 MFMA in fp32, in a fixed order that depends on k
  * alone; h stays fp32 through the second product (three bf16 terms whose
