@@ -61,6 +61,15 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
   return v;
 }
 
+// The same of which only left elements exist; zeros for the others.
+__device__ __forceinline__ uint4 load8_part(const uint16_t* p, int64_t left) {
+  if (left >= 8) return load8(p);
+  uint16_t v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : static_cast<uint16_t>(0);
+  return __builtin_bit_cast(uint4, v);
+}
+
 // Two fp32 values rounded to bf16, nearest-even, packed (gfx950 converts).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float float2v __attribute__((ext_vector_type(2)));
@@ -113,12 +122,12 @@ dim3 xcd_grid(int64_t units) {
 // bound the first version). So every operand is loaded with four lanes on 64
 // contiguous bytes of a row and turned round through 1 KB of LDS.
 struct ShrinkArgs {
-  LoraArgs p;
+  LoraArgs p;              // a: [rank][k] per adapter, zeros from cols to k
   const uint16_t* x;
   float* out;              // streams, slices: partial sums [parts][m][rank]
   float* h;                // whole: fp32 [m][rank] or NULL
   uint4* frag;             // whole: [tiles][3][KS][64] operands (NULL otherwise)
-  int64_t ldx;
+  int64_t ldx, cols;       // columns of x
   int32_t slices, parts;   // parts: 1 (whole), 8 (streams) or slices
 };
 
@@ -143,7 +152,9 @@ __device__ __forceinline__ void turn(uint4 (&v)[N], uint4* lds, int lane) {
   wave_sync();
 }
 
-template <int RT>
+// kAny: rows of x at any 2-byte alignment and of any length (gradients of an
+// odd number of outputs); otherwise 16-byte aligned, a multiple of 32.
+template <int RT, bool kAny>
 __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
   const LoraArgs& p = s.p;
   constexpr int kSumLd = 16 * RT + 4;
@@ -194,10 +205,12 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
       floatx4 acc[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r] = floatx4{0, 0, 0, 0};
-      if (p.k - col >= kSlice) {
+      if (s.cols - col >= kSlice) {
         uint4 xf[8], af[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xf[j] = *reinterpret_cast<const uint4*>(xl + col + 32 * j);
+        for (int j = 0; j < 8; ++j)
+          xf[j] = kAny ? load8(xl + col + 32 * j)
+                       : *reinterpret_cast<const uint4*>(xl + col + 32 * j);
         const auto load_a = [&](int r) {
           const uint16_t* al = aa + rank_row(16 * r + (lane >> 2)) * p.k + 8 * (lane & 3) + col;
 #pragma unroll
@@ -219,8 +232,9 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
           if (RT == 8 && r + 1 < RT) load_a(r + 1);
         }
       } else {
-        for (int64_t cc = col; cc < p.k; cc += 32) {
-          const uint4 xf = *reinterpret_cast<const uint4*>(xr + cc);
+        for (int64_t cc = col; cc < s.cols; cc += 32) {
+          const uint4 xf = kAny ? load8_part(xr + cc, s.cols - cc - 8 * g)
+                                : *reinterpret_cast<const uint4*>(xr + cc);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
             acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -681,20 +695,26 @@ int32_t shrink_parts(int64_t m, int64_t n, int64_t k) {
   return tiles * kStreams >= 256 && slices > kStreams ? kStreams : slices;
 }
 
+// Bytes of h as operands of the many-rows product.
+int64_t frag_bytes(int64_t m, int32_t rank) {
+  return (m + 15) / 16 * 3 * ((rank + 31) / 32) * 1024;
+}
+
 int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
-  if (many_rows(m, n)) return (m + 15) / 16 * 3 * ((rank + 31) / 32) * 1024;
+  if (many_rows(m, n)) return frag_bytes(m, rank);
   return shrink_parts(m, n, k) * m * rank * 4;
 }
 
+template <bool kAny>
 void launch_shrink(const ShrinkArgs& s, hipStream_t st) {
   const LoraArgs& p = s.p;
   const dim3 grid = xcd_grid((p.m + 15) / 16 * s.parts);
   const int64_t mixed = p.ids == nullptr ? 1 : p.m < p.n_adapters ? p.m : p.n_adapters;
   const dim3 block(s.frag != nullptr ? 64 * kStreams : mixed < 2 ? 64 : mixed < 8 ? 256 : 512);
-  if (p.rank <= 16) hipLaunchKernelGGL(shrink_kernel<1>, grid, block, 0, st, s);
-  else if (p.rank <= 32) hipLaunchKernelGGL(shrink_kernel<2>, grid, block, 0, st, s);
-  else if (p.rank <= 64) hipLaunchKernelGGL(shrink_kernel<4>, grid, block, 0, st, s);
-  else hipLaunchKernelGGL(shrink_kernel<8>, grid, block, 0, st, s);
+  if (p.rank <= 16) hipLaunchKernelGGL((shrink_kernel<1, kAny>), grid, block, 0, st, s);
+  else if (p.rank <= 32) hipLaunchKernelGGL((shrink_kernel<2, kAny>), grid, block, 0, st, s);
+  else if (p.rank <= 64) hipLaunchKernelGGL((shrink_kernel<4, kAny>), grid, block, 0, st, s);
+  else hipLaunchKernelGGL((shrink_kernel<8, kAny>), grid, block, 0, st, s);
 }
 
 template <int KS, int BK, int YK>
@@ -730,83 +750,382 @@ void launch_expand(const ExpandArgs& s, hipStream_t st) {
 }
 
 // --------------------------------------------------------------- backward
-// out[t, r] = scale * sum over c of v[t, c] * w[c, r], w strided (A by rows
-// of r, B by rows of c); one block per row, one wave per rank in turn.
-__global__ __launch_bounds__(256) void rows_kernel(LoraArgs p, const uint16_t* v, int64_t ldv,
-                                                   const uint16_t* w, int64_t cols,
-                                                   int64_t stride_r, int64_t stride_c, bool scaled,
-                                                   float* out) {
-  const int64_t t = blockIdx.x;
-  const int32_t i = adapter_of(p, t);
-  if (threadIdx.x == 0 && i < 0 && p.status != nullptr && p.ids[t] != -1)
-    atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
-  const int lane = threadIdx.x & 63;
-  const uint16_t* wi = w + static_cast<int64_t>(i < 0 ? 0 : i) * p.rank * cols;
-  for (int32_t r = threadIdx.x >> 6; r < p.rank; r += 4) {
-    float acc = 0.0f;
-    if (i >= 0)
-      for (int64_t c = lane; c < cols; c += 64)
-        acc = __builtin_fmaf(bf16_f32(v[t * ldv + c]), bf16_f32(wi[r * stride_r + c * stride_c]),
-                             acc);
-    acc = slot_tree(acc);
-    if (lane == 0) {
-      if (scaled && i >= 0 && p.scale != nullptr) acc *= p.scale[i];
-      out[t * p.rank + r] = acc;
+// With Bt and At, B and A turned round (a small copy), the two products of
+// the forward give g = Bt dy and dx = dx_base + s At g. What is new is the
+// sum over rows, dA = s g^T x and dB = s h^T dy:
+//  - order_kernel sorts the rows by adapter, each adapter's from a multiple of
+//    32 rows on (ids NULL: rows as they are);
+//  - turn_rows_kernel splits g and h of a tile of 32 sorted rows into three
+//    bf16 terms, as MFMA operands whose K is the rows;
+//  - outer_kernel: a wave has 128 columns of x or dy, up to 32 ranks and a
+//    range of tiles. A lane loads 8 columns of 8 rows and turns the 8 x 8
+//    block with v_perm, which makes the operand whose K is the rows; sums stay
+//    in registers until the adapter changes. An adapter inside one range is
+//    written at once, one over several leaves a partial sum in each;
+//  - reduce_kernel adds those in range order and writes zeros for adapters
+//    without rows.
+// Rows of another adapter never meet in one MFMA chain.
+constexpr int kRowTile = 32;           // sorted rows of a tile
+constexpr int kMaxSorted = 4096;    // adapters order_kernel counts in LDS
+
+struct TurnArgs {
+  const uint16_t* from;
+  uint16_t* to;
+  int64_t rows, cols, rows_pad;     // from [rows][cols] -> to [cols][rows_pad] per adapter
+  int32_t n_adapters;
+};
+
+// 8 rows of 8 bf16 -> 8 columns of 8.
+__device__ __forceinline__ void turn_block(const uint4 (&v)[8], uint4 (&t)[8]) {
+  uint32_t d[8][4];
+  __builtin_memcpy(d, v, 128);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = vperm(d[2 * j + 1][c], d[2 * j][c], 0x05040100u);
+      hi[j] = vperm(d[2 * j + 1][c], d[2 * j][c], 0x07060302u);
+    }
+    t[2 * c] = uint4{lo[0], lo[1], lo[2], lo[3]};
+    t[2 * c + 1] = uint4{hi[0], hi[1], hi[2], hi[3]};
+  }
+}
+
+__global__ __launch_bounds__(256) void turn_kernel(TurnArgs b, TurnArgs a) {
+  // B's blocks in order of rows (stores coalesced), A's in order of columns
+  const int64_t nb = b.n_adapters * (b.rows_pad / 8) * (b.cols / 8);
+  const int64_t na = a.n_adapters * (a.rows_pad / 8) * (a.cols / 8);
+  int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= nb + na) return;
+  const bool first = e < nb;
+  const TurnArgs& p = first ? b : a;
+  if (!first) e -= nb;
+  const int64_t rb = p.rows_pad / 8, cb = p.cols / 8;
+  const int64_t i = e / (rb * cb), at = e - i * rb * cb;
+  const int64_t r = 8 * (first ? at % rb : at / cb), c = 8 * (first ? at / rb : at % cb);
+  uint4 v[8], t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = r + j < p.rows
+               ? *reinterpret_cast<const uint4*>(p.from + (i * p.rows + r + j) * p.cols + c)
+               : uint4{0, 0, 0, 0};
+  turn_block(v, t);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(p.to + (i * p.cols + c + j) * p.rows_pad + r) = t[j];
+}
+
+// Where sorted rows lie.
+struct Order {
+  const int32_t* perm;     // [tiles * 32] row or -1; NULL: rows as they are, all adapter 0
+  const int32_t* adapter;  // [tiles]
+  const int32_t* tile0;    // [n_adapters + 1] first tile of each adapter
+  int32_t tiles;           // perm NULL: their number
+};
+
+__device__ __forceinline__ int32_t first_tile(const Order& o, int32_t a) {
+  return o.perm != nullptr ? o.tile0[a] : a == 0 ? 0 : o.tiles;
+}
+
+// Block a collects the rows of adapter a in rising order, behind the tiles of
+// the adapters before it.
+__global__ __launch_bounds__(512) void order_kernel(LoraArgs p, int32_t* perm, int32_t* adapter,
+                                                    int32_t* tile0) {
+  __shared__ int32_t counts[kMaxSorted];
+  __shared__ int32_t sums[8];
+  const int32_t a = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int32_t e = threadIdx.x; e <= a && e < p.n_adapters; e += 512) counts[e] = 0;
+  __syncthreads();
+  for (int64_t t = threadIdx.x; t < p.m; t += 512) {
+    const int32_t id = adapter_of(p, t);
+    const int32_t one = __builtin_amdgcn_readfirstlane(id);
+    const uint64_t all = __ballot(true);
+    if (__ballot(id == one) == all) {   // a run of one adapter: one count
+      if (lane == __builtin_ctzll(all) && one >= 0 && one <= a)
+        atomicAdd(&counts[one], __builtin_popcountll(all));
+    } else if (id >= 0 && id <= a) {
+      atomicAdd(&counts[id], 1);
+    }
+  }
+  __syncthreads();
+  int32_t before = 0;
+  for (int32_t e = threadIdx.x; e < a; e += 512) before += (counts[e] + kRowTile - 1) / kRowTile;
+  for (int q = 32; q >= 1; q >>= 1) before += __shfl_xor(before, q, 64);
+  if (lane == 0) sums[wave] = before;
+  __syncthreads();
+  before = 0;
+  for (int w = 0; w < 8; ++w) before += sums[w];
+  const int32_t mine = counts[a], tiles = (mine + kRowTile - 1) / kRowTile;
+  if (threadIdx.x == 0) {
+    tile0[a] = before;
+    if (a == p.n_adapters - 1) tile0[a + 1] = before + tiles;
+  }
+  for (int32_t e = threadIdx.x; e < tiles; e += 512) adapter[before + e] = a;
+  perm += static_cast<int64_t>(before) * kRowTile;
+  for (int32_t e = mine + threadIdx.x; e < tiles * kRowTile; e += 512) perm[e] = -1;
+  int32_t at = 0;
+  for (int64_t t0 = 0; t0 < p.m && at < mine; t0 += 512) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool hit = t < p.m && adapter_of(p, t) == a;
+    const uint64_t hits = __ballot(hit);
+    __syncthreads();
+    if (lane == 0) sums[wave] = __builtin_popcountll(hits);
+    __syncthreads();
+    int32_t off = at;
+    for (int w = 0; w < 8; ++w) {
+      if (w < wave) off += sums[w];
+      at += sums[w];
+    }
+    if (hit) perm[off + __builtin_popcountll(hits & ((1ull << lane) - 1))] = static_cast<int32_t>(t);
+  }
+}
+
+// g and h of each tile as operands [tile][rank tile][3][64]: lane (rank i,
+// rows 8 g ..). One wave per (vector, tile, rank tile).
+__global__ __launch_bounds__(64) void turn_rows_kernel(Order o, const float* g, const float* h,
+                                                       uint4* gt, uint4* ht, int64_t m,
+                                                       int32_t rank, int32_t n_adapters) {
+  const int32_t rts = (rank + 15) / 16;
+  const int64_t tile = blockIdx.x / (2 * rts);
+  const int32_t which = blockIdx.x / rts % 2, rt = blockIdx.x % rts;
+  if (tile >= first_tile(o, n_adapters)) return;
+  const int lane = threadIdx.x, i = lane & 15, q = lane >> 4;
+  const float* v = which ? h : g;
+  const int32_t r = 16 * rt + i;
+  uint16_t d[3][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    int64_t t = tile * kRowTile + 8 * q + j;
+    if (o.perm != nullptr) t = o.perm[t];
+    const float f = t >= 0 && t < m && r < rank ? v[t * rank + r] : 0.0f;
+    split3(f, d[0][j], d[1][j], d[2][j]);
+  }
+  uint4* to = (which ? ht : gt) + (tile * rts + rt) * 3 * 64 + lane;
+#pragma unroll
+  for (int t3 = 0; t3 < 3; ++t3) to[64 * t3] = __builtin_bit_cast(uint4, d[t3]);
+}
+
+struct OuterSide {
+  const uint16_t* s;       // rows [m][cols]
+  const uint4* vt;         // turned g or h
+  void* grad;
+  float* part;             // [2 * splits][rank * cols]
+  int64_t ld, cols;
+  int32_t blocks;          // of four waves, a split
+};
+
+struct OuterArgs {
+  OuterSide side[2];       // 0: x and g -> dA [rank][cols]; 1: dy and h -> dB [cols][rank]
+  Order o;
+  const float* scale;
+  int64_t m;
+  int32_t rank, n_adapters, per_split;
+  bool grad_bf16;
+};
+
+template <int RT>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int32_t per = p.side[0].blocks + p.side[1].blocks;
+  const int32_t split = blockIdx.x / per, at = blockIdx.x - split * per;
+  const bool second = at >= p.side[0].blocks;
+  const OuterSide& s = p.side[second ? 1 : 0];
+  // a block's waves: rank chunks of the same columns side by side
+  const int32_t chunks = (p.rank + 16 * RT - 1) / (16 * RT);
+  const int32_t job = (second ? at - p.side[0].blocks : at) * 4 + wave;
+  const int32_t chunk = job % chunks;
+  const int64_t col0 = static_cast<int64_t>(job / chunks) * 128;
+  if (col0 >= s.cols) return;
+  const int32_t rts = (p.rank + 15) / 16, rt0 = chunk * RT;
+  const int64_t col = col0 + 8 * i, left = s.cols - col;
+  const bool whole = col0 + 128 <= s.cols;
+  const int32_t begin = split * p.per_split, n_tiles = first_tile(p.o, p.n_adapters);
+  const int32_t end = begin + p.per_split < n_tiles ? begin + p.per_split : n_tiles;
+  if (begin >= end) return;
+
+  floatx4 acc[8][RT];
+  const auto clear = [&]() {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
+  };
+  const auto flush = [&](int32_t a) {
+    const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
+    const bool direct = s0 >= begin && s1 <= begin + p.per_split;
+    const int64_t size = p.rank * s.cols;
+    const float f = !direct || p.scale == nullptr ? 1.0f : p.scale[a];
+    void* to = direct ? s.grad : static_cast<void*>(s.part);
+    const int64_t base = direct ? a * size : (2 * split + (s0 < begin ? 0 : 1)) * size;
+    const bool bf16 = direct && p.grad_bf16;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int32_t rank = 16 * (rt0 + r) + i;
+      if (rank >= p.rank) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t cc = col0 + 8 * (4 * g + q);
+        if (!second) {
+          if (cc >= s.cols) continue;
+          const int64_t e = base + rank * s.cols + cc;
+          if (bf16) {
+            uint32_t d[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              d[c] = pack_bf16(f * acc[2 * c][r][q], f * acc[2 * c + 1][r][q]);
+            __builtin_memcpy(static_cast<uint16_t*>(to) + e, d, 16);
+          } else {
+            float d[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = f * acc[c][r][q];
+            __builtin_memcpy(static_cast<float*>(to) + e, d, 32);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (cc + c < s.cols)
+              store_any(to, base + (cc + c) * p.rank + rank, bf16, f * acc[c][r][q]);
+        }
+      }
+    }
+  };
+
+  uint4 next[8];
+  const auto load = [&](int32_t tile) {
+    int32_t t[8];
+    if (p.o.perm != nullptr) {
+      __builtin_memcpy(t, p.o.perm + static_cast<int64_t>(tile) * kRowTile + 8 * g, 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t row = static_cast<int64_t>(tile) * kRowTile + 8 * g + j;
+        t[j] = row < p.m ? static_cast<int32_t>(row) : -1;
+      }
+    }
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        next[j] = load8(s.s + (t[j] < 0 ? 0 : t[j]) * s.ld + col);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        next[j] = load8_part(s.s + (t[j] < 0 ? 0 : t[j]) * s.ld + col, left);
+    }
+    bool gap = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gap |= t[j] < 0;
+    if (__ballot(gap) != 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (t[j] < 0) next[j] = uint4{0, 0, 0, 0};
+    }
+  };
+  clear();
+  int32_t a = p.o.perm != nullptr ? uniform(p.o.adapter[begin]) : 0;
+  load(begin);
+#pragma unroll 1
+  for (int32_t tile = begin; tile < end; ++tile) {
+    uint4 now[8], st[8], vt[RT][3];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) now[j] = next[j];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        const int32_t rt = rt0 + r < rts ? rt0 + r : rts - 1;
+        vt[r][t] = s.vt[((static_cast<int64_t>(tile) * rts + rt) * 3 + t) * 64 + lane];
+      }
+    int32_t a_next = a;
+    if (tile + 1 < end) {
+      load(tile + 1);
+      if (p.o.perm != nullptr) a_next = uniform(p.o.adapter[tile + 1]);
+    }
+    turn_block(now, st);
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(vt[r][t]),
+                                                              acc[c][r], 0, 0, 0);
+    if (a_next != a || tile + 1 == end) {
+      flush(a);
+      clear();
+      a = a_next;
     }
   }
 }
 
-// out[t, c] = base[t, c] + scale * sum over r of v[t, r] * w[c, r].
-__global__ __launch_bounds__(256) void add_kernel(LoraArgs p, const float* v, const uint16_t* w,
-                                                     int64_t cols, int64_t stride_r,
-                                                     int64_t stride_c, bool scaled,
-                                                     const void* base, int64_t ld_base,
-                                                     bool base_bf16, void* out, int64_t ld_out,
-                                                     bool out_bf16) {
-  const int64_t total = p.m * cols;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
-       e += step) {
-    const int64_t t = e / cols, c = e - t * cols;
-    const int32_t i = adapter_of(p, t);
-    float y = base != nullptr ? load_any(base, t * ld_base + c, base_bf16) : 0.0f;
-    if (i >= 0) {
-      const uint16_t* wi = w + static_cast<int64_t>(i) * p.rank * cols;
-      float acc = 0.0f;
-      for (int32_t r = 0; r < p.rank; ++r)
-        acc = __builtin_fmaf(v[t * p.rank + r], bf16_f32(wi[r * stride_r + c * stride_c]), acc);
-      if (scaled && p.scale != nullptr) acc *= p.scale[i];
-      y = y + acc;
-    }
-    store_any(out, t * ld_out + c, out_bf16, y);
+// Four values of a gradient a thread; blockIdx.y: adapter.
+__global__ __launch_bounds__(256) void reduce_kernel(OuterArgs p) {
+  const int32_t a = blockIdx.y;
+  const int64_t size[2] = {p.rank * p.side[0].cols, p.rank * p.side[1].cols};
+  int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (e >= size[0] + size[1]) return;
+  const int side = e >= size[0] ? 1 : 0;
+  if (side) e -= size[0];
+  const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
+  const int32_t q0 = s0 / p.per_split, q1 = s1 > s0 ? (s1 - 1) / p.per_split : q0;
+  if (s1 > s0 && q0 == q1) return;   // outer_kernel wrote it
+  floatx4 v{0, 0, 0, 0};
+  if (s1 > s0) {
+    const float* part = p.side[side].part + e;
+    for (int32_t q = q0; q <= q1; ++q)
+      v += *reinterpret_cast<const floatx4*>(part + (2 * q + (q == q0 ? 1 : 0)) * size[side]);
+    const float f = p.scale != nullptr ? p.scale[a] : 1.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= f;
+  }
+  const int64_t at = a * size[side] + e;
+  if (p.grad_bf16) {
+    const uint32_t d[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    __builtin_memcpy(static_cast<uint16_t*>(p.side[side].grad) + at, d, 8);
+  } else {
+    __builtin_memcpy(static_cast<float*>(p.side[side].grad) + at, &v, 16);
   }
 }
 
-// grad[i, r, c] = scale * sum over rows t of adapter i of v[t, r] * s[t, c].
-__global__ __launch_bounds__(256) void outer_kernel(LoraArgs p, const float* v, const uint16_t* s,
-                                                    int64_t lds, int64_t cols, int64_t stride_r,
-                                                    int64_t stride_c, bool scaled, void* grad,
-                                                    bool grad_bf16) {
-  const int64_t per = static_cast<int64_t>(p.rank) * cols;
-  const int64_t total = per * p.n_adapters;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total;
-       e += step) {
-    const int32_t i = static_cast<int32_t>(e / per);
-    const int64_t at = e - i * per, r = at / cols, c = at - r * cols;
-    double acc = 0.0;
-    for (int64_t t = 0; t < p.m; ++t)
-      if (adapter_of(p, t) == i)
-        acc += static_cast<double>(v[t * p.rank + r]) * static_cast<double>(bf16_f32(s[t * lds + c]));
-    if (scaled && p.scale != nullptr) acc *= p.scale[i];
-    store_any(grad, i * per + r * stride_r + c * stride_c, grad_bf16, static_cast<float>(acc));
+// Sizes and places of a backward call's workspace.
+struct GradPlan {
+  int64_t tiles, n_pad;
+  int32_t splits, per_split, chunk_tiles;
+  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, gt, ht, outer, bytes;
+  GradPlan(int64_t m, int64_t n, int64_t k, int32_t rank, int32_t n_adapters) {
+    tiles = (m + kRowTile - 1) / kRowTile + n_adapters;   // at most
+    n_pad = (n + 31) / 32 * 32;
+    chunk_tiles = rank <= 16 ? 1 : 2;
+    const int64_t chunks = (rank + 16 * chunk_tiles - 1) / (16 * chunk_tiles);
+    const int64_t jobs = ((n + 127) / 128 + (k + 127) / 128) * chunks;
+    // enough waves to fill the chip, at least two tiles each
+    int64_t want = (kOuterWaves + jobs - 1) / jobs;
+    if (want > (tiles + 1) / 2) want = (tiles + 1) / 2;
+    per_split = static_cast<int32_t>((tiles + want - 1) / want);
+    splits = static_cast<int32_t>((tiles + per_split - 1) / per_split);
+    bytes = 0;
+    const auto place = [&](int64_t size) {
+      const int64_t start = bytes;
+      bytes += (size + 255) / 256 * 256;
+      return start;
+    };
+    perm = place(tiles * kRowTile * 4);
+    adapter = place(tiles * 4);
+    tile0 = place((n_adapters + 1) * 4ll);
+    bt = place(n_adapters * n_pad * rank * 2);
+    at = place(n_adapters * k * rank * 2);
+    frag = place(frag_bytes(m, rank));
+    part = place(many_rows(m, k) ? 0 : shrink_parts(m, k, n) * m * rank * 4);
+    g = place(m * rank * 4);
+    h = place(m * rank * 4);
+    const int64_t rts = (rank + 15) / 16;
+    gt = place(tiles * rts * 3 * 1024);
+    ht = place(tiles * rts * 3 * 1024);
+    outer = place(2ll * splits * rank * (n + k) * 4);
   }
-}
-
-uint32_t blocks_for(int64_t n) {
-  const int64_t b = (n + 255) / 256;
-  return static_cast<uint32_t>(b < 65536 ? b : 65536);
-}
+  static constexpr int64_t kOuterWaves = 2048;
+};
 
 // Row strides: 12 rows of fp32 stay below 2^31 bytes (32-bit lane offsets).
 constexpr int64_t kMaxStride = 1 << 24;
@@ -844,7 +1163,8 @@ extern "C" int64_t binade_lora_workspace_bytes(int64_t m, int64_t n, int64_t k, 
 
 extern "C" int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t rank,
                                                     int32_t n_adapters) {
-  return sizes_ok(m, n, k, rank) && n_adapters >= 1 && n_adapters <= 65535 ? 2 * m * rank * 4 : 0;
+  if (!sizes_ok(m, n, k, rank) || n_adapters < 1 || n_adapters > kMaxSorted) return 0;
+  return GradPlan(m, n, k, rank, n_adapters).bytes;
 }
 
 extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int64_t m, int64_t ldx,
@@ -870,7 +1190,8 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
   const bool many = many_rows(m, p.n);
   float* part = many ? nullptr : static_cast<float*>(workspace);
   uint4* frag = many ? static_cast<uint4*>(workspace) : nullptr;
-  launch_shrink(ShrinkArgs{p, x, part, h, frag, ldx, slices_of(p.k), many ? 1 : parts}, st);
+  launch_shrink<false>(ShrinkArgs{p, x, part, h, frag, ldx, p.k, slices_of(p.k), many ? 1 : parts},
+                       st);
   launch_expand(ExpandArgs{p, part, frag, base, y, h, ld_base, ldy, parts,
                            base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
                            y_dtype == BINADE_BF16},
@@ -887,10 +1208,14 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   const int32_t s = check_common(l, x, m, ldx, workspace);
   if (s != BINADE_OK) return s;
   if (grad_dtype != BINADE_F32 && grad_dtype != BINADE_BF16) return BINADE_EINVAL;
+  if (l->n_adapters > kMaxSorted) return BINADE_EUNSUPPORTED;
   if (da == nullptr || db == nullptr) return BINADE_EINVAL;
   if (m > 0 && (dy == nullptr || ld_dy < l->n)) return BINADE_EINVAL;
+  if (!aligned16(da) || !aligned16(db) || !aligned16(h)) return BINADE_EUNSUPPORTED;
   if (dx != nullptr) {
     if (ld_dx < l->k || (dx_base != nullptr && ld_dx_base < l->k)) return BINADE_EINVAL;
+    if (ld_dx > kMaxStride || (dx_base != nullptr && ld_dx_base > kMaxStride))
+      return BINADE_EUNSUPPORTED;
     if (!aligned16(dx) || ld_dx % 8 != 0 ||
         (dx_base != nullptr && (!aligned16(dx_base) || ld_dx_base % 8 != 0)))
       return BINADE_EUNSUPPORTED;
@@ -901,26 +1226,91 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     return BINADE_ENOSPACE;
   const LoraArgs p = args_of(l, m, ids, dev_status);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool gb = grad_dtype == BINADE_BF16;
-  float* g = static_cast<float*>(workspace);
-  float* hw = g + m * p.rank;
+  const GradPlan plan(m, p.n, p.k, p.rank, p.n_adapters);
+  char* ws = static_cast<char*>(workspace);
+  const auto floats = [&](int64_t at) { return reinterpret_cast<float*>(ws + at); };
+  const auto ints = [&](int64_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+  const auto pieces = [&](int64_t at) { return reinterpret_cast<uint4*>(ws + at); };
+  Order o{};
+  o.tiles = static_cast<int32_t>((m + kRowTile - 1) / kRowTile);
+  OuterArgs outer{};
+  outer.scale = p.scale;
+  outer.m = m;
+  outer.rank = p.rank;
+  outer.n_adapters = p.n_adapters;
+  outer.per_split = plan.per_split;
+  outer.grad_bf16 = grad_dtype == BINADE_BF16;
+  const int64_t chunks = (p.rank + 16 * plan.chunk_tiles - 1) / (16 * plan.chunk_tiles);
+  const auto side_blocks = [&](int64_t cols) {
+    return static_cast<int32_t>(((cols + 127) / 128 * chunks + 3) / 4);
+  };
+  outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, side_blocks(p.k)};
+  outer.side[1] = OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, side_blocks(p.n)};
   if (m > 0) {
-    hipLaunchKernelGGL(rows_kernel, dim3(static_cast<uint32_t>(m)), dim3(256), 0, st, p, dy, ld_dy,
-                       p.b, p.n, static_cast<int64_t>(1), static_cast<int64_t>(p.rank), true, g);
-    if (h == nullptr) {
-      hipLaunchKernelGGL(rows_kernel, dim3(static_cast<uint32_t>(m)), dim3(256), 0, st, p, x, ldx,
-                         p.a, p.k, p.k, static_cast<int64_t>(1), false, hw);
-      h = hw;
+    if (ids != nullptr) {
+      hipLaunchKernelGGL(order_kernel, dim3(p.n_adapters), dim3(512), 0, st, p, ints(plan.perm),
+                         ints(plan.adapter), ints(plan.tile0));
+      o.perm = ints(plan.perm);
+      o.adapter = ints(plan.adapter);
+      o.tile0 = ints(plan.tile0);
     }
-    if (dx != nullptr)
-      hipLaunchKernelGGL(add_kernel, dim3(blocks_for(m * p.k)), dim3(256), 0, st, p, g, p.a, p.k,
-                         p.k, static_cast<int64_t>(1), false, static_cast<const void*>(dx_base),
-                         ld_dx_base, true, static_cast<void*>(dx), ld_dx, true);
+    // without ids only adapter 0 is read
+    const int32_t used = ids != nullptr ? p.n_adapters : 1;
+    uint16_t* bt = reinterpret_cast<uint16_t*>(ws + plan.bt);
+    uint16_t* at = reinterpret_cast<uint16_t*>(ws + plan.at);
+    const TurnArgs tb{p.b, bt, p.n, p.rank, plan.n_pad, used};
+    const TurnArgs ta{p.a, at, p.rank, p.k, p.rank, dx != nullptr ? used : 0};
+    const int64_t turns = (tb.n_adapters * plan.n_pad + ta.n_adapters * p.k) / 8 * (p.rank / 8);
+    hipLaunchKernelGGL(turn_kernel, dim3(static_cast<uint32_t>((turns + 255) / 256)), dim3(256), 0,
+                       st, tb, ta);
+    if (h == nullptr) {
+      launch_shrink<false>(ShrinkArgs{p, x, nullptr, floats(plan.h), pieces(plan.frag), ldx, p.k,
+                                      slices_of(p.k), 1},
+                           st);
+      h = floats(plan.h);
+    }
+    // g, and dx from it
+    LoraArgs pg = p;
+    pg.a = bt;
+    pg.k = plan.n_pad;
+    const bool whole = many_rows(m, p.k) || dx == nullptr;
+    const int32_t parts = whole ? 1 : shrink_parts(m, p.k, p.n);
+    launch_shrink<true>(ShrinkArgs{pg, dy, whole ? nullptr : floats(plan.part),
+                                   whole ? floats(plan.g) : nullptr,
+                                   whole ? pieces(plan.frag) : nullptr, ld_dy, p.n,
+                                   slices_of(p.n), parts},
+                        st);
+    if (dx != nullptr) {
+      LoraArgs px = p;
+      px.b = at;
+      px.n = p.k;
+      launch_expand(ExpandArgs{px, whole ? nullptr : floats(plan.part),
+                               whole ? pieces(plan.frag) : nullptr, dx_base, dx,
+                               whole ? nullptr : floats(plan.g), ld_dx_base, ld_dx, parts,
+                               dx_base == nullptr ? 0 : 2, true},
+                    st);
+    }
+    const int64_t rts = (p.rank + 15) / 16;
+    const int64_t tiles = ids != nullptr ? plan.tiles : o.tiles;
+    hipLaunchKernelGGL(turn_rows_kernel, dim3(static_cast<uint32_t>(tiles * 2 * rts)), dim3(64), 0,
+                       st, o, floats(plan.g), h, pieces(plan.gt), pieces(plan.ht), m, p.rank,
+                       p.n_adapters);
+    outer.side[0].vt = pieces(plan.gt);
+    outer.side[1].vt = pieces(plan.ht);
+    outer.side[0].part = floats(plan.outer);
+    outer.side[1].part = floats(plan.outer) + 2ll * plan.splits * p.rank * p.k;
+    outer.o = o;
+    const uint32_t blocks =
+        static_cast<uint32_t>(plan.splits * (outer.side[0].blocks + outer.side[1].blocks));
+    if (plan.chunk_tiles == 1)
+      hipLaunchKernelGGL(outer_kernel<1>, dim3(blocks), dim3(256), 0, st, outer);
+    else
+      hipLaunchKernelGGL(outer_kernel<2>, dim3(blocks), dim3(256), 0, st, outer);
   }
-  hipLaunchKernelGGL(outer_kernel, dim3(blocks_for(p.n_adapters * p.rank * p.k)), dim3(256), 0, st,
-                     p, g, x, ldx, p.k, p.k, static_cast<int64_t>(1), false, da, gb);
-  hipLaunchKernelGGL(outer_kernel, dim3(blocks_for(p.n_adapters * p.rank * p.n)), dim3(256), 0, st,
-                     p, h, dy, ld_dy, p.n, static_cast<int64_t>(1), static_cast<int64_t>(p.rank),
-                     true, db, gb);
+  outer.o = o;
+  hipLaunchKernelGGL(reduce_kernel,
+                     dim3(static_cast<uint32_t>((p.rank * (p.n + p.k) / 4 + 255) / 256),
+                          static_cast<uint32_t>(p.n_adapters)),
+                     dim3(256), 0, st, outer);
   return launch_status();
 }

@@ -670,8 +670,8 @@ int64_t binade_lora_workspace_bytes(int64_t m, int64_t n, int64_t k,
  * (the projection's own input gradient), or NULL for zeros; dx may be
  * dx_base itself if the strides agree. h: device fp32 [m, rank] as
  * binade_lora_add leaves it, or NULL (computed again). Other arguments as
- * in binade_lora_add; dy rows need no alignment, x, dx and dx_base rows are
- * 16-byte aligned. Sums are fp32 in a fixed order for given sizes and ids:
+ * in binade_lora_add; dy rows need no alignment, x, dx and dx_base rows, h,
+ * da and db are 16-byte aligned. n_adapters at most 4096. Sums are fp32 in a fixed order for given sizes and ids:
  * the same call gives the same bits. */
 int32_t binade_lora_grad(const binade_lora *l, const uint16_t *x, int64_t m,
                          int64_t ldx, const int32_t *ids, const uint16_t *dy,
