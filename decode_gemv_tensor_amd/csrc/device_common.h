@@ -142,6 +142,12 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// Orders a wave's LDS writes before its lanes' reads of each other's values
+// (the hardware keeps a wave's LDS operations in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // 32 x values of lane tile t as fp32 (four 16-byte loads).
 __device__ __forceinline__ void load_x_tile(const uint16_t* x, int t,

@@ -131,13 +131,6 @@ struct ShrinkArgs {
   int32_t slices, parts;   // parts: 1 (whole), 8 (streams) or slices
 };
 
-// Orders a wave's LDS writes before its lanes' reads of each other's values
-// (the hardware keeps a wave's LDS operations in order).
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // N operands as loaded (lane 4 row + octet) -> as MFMA takes them (lane row +
 // 16 octet), through N KB of the wave's own; the swizzle spreads the reads of
 // 8 lanes over all banks.

@@ -57,32 +57,113 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* y, const floa
   }
 }
 
+// Four values of a row from column j on (those below n) as fp32.
+template <bool kBf16>
+__device__ __forceinline__ void load4(const void* p, int64_t at, int64_t left, float (&f)[4]) {
+  if (left >= 4) {
+    if (kBf16) {
+      uint32_t d[2];
+      __builtin_memcpy(d, static_cast<const uint16_t*>(p) + at, 8);
+      f[0] = bf16_lo(d[0]), f[1] = bf16_hi(d[0]), f[2] = bf16_lo(d[1]), f[3] = bf16_hi(d[1]);
+    } else {
+      __builtin_memcpy(f, static_cast<const float*>(p) + at, 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    f[j] = j >= left ? 0.0f
+           : kBf16   ? __uint_as_float(
+                         static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + j]) << 16)
+                     : static_cast<const float*>(p)[at + j];
+}
+
 // dy[t, s, :] = w[t, s] * dout[t, :] and dw[t, s] = <dout[t, :], y[t, s, :]>:
-// one block per (token, slot).
+// one block per token and S slots, which share the loads of dout; a thread
+// has columns 4 threadIdx.x .. + 3 of every 1024. S does not change the order
+// of a slot's sum.
+template <int S, bool kDoutBf16, bool kDyBf16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const float* weights,
-                                                           const void* dout, int32_t dout_bf16,
-                                                           int32_t top_k, int64_t n, void* dy,
-                                                           int32_t dy_bf16, float* dweights) {
-  __shared__ float red[4];
-  const int64_t pair = blockIdx.x, t = pair / top_k;
-  const float w = weights[pair];
-  float acc = 0.0f;
-  for (int64_t j = threadIdx.x; j < n; j += 256) {
-    const float d = dout_bf16 ? __uint_as_float(static_cast<uint32_t>(
-                                    static_cast<const uint16_t*>(dout)[t * n + j]) << 16)
-                              : static_cast<const float*>(dout)[t * n + j];
-    acc = __builtin_fmaf(d, y[pair * n + j], acc);
-    if (dy != nullptr) {
-      if (dy_bf16)
-        static_cast<uint16_t*>(dy)[pair * n + j] = to_bf16_rne(w * d);
-      else
-        static_cast<float*>(dy)[pair * n + j] = w * d;
+                                                           const void* dout, int32_t top_k,
+                                                           int64_t n, void* dy, float* dweights) {
+  __shared__ float red[4][S];
+  const int32_t chunks = (top_k + S - 1) / S;
+  const int64_t t = blockIdx.x / chunks;
+  const int32_t s0 = static_cast<int32_t>(blockIdx.x - t * chunks) * S;
+  const int32_t slots = top_k - s0 < S ? top_k - s0 : S;
+  const int64_t pair = t * top_k + s0;
+  float w[S], acc[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    w[s] = weights[pair + (s < slots ? s : 0)];
+    acc[s] = 0.0f;
+  }
+  for (int64_t j = 4 * threadIdx.x; j < n; j += 1024) {
+    float d[4], v[S][4];
+    load4<kDoutBf16>(dout, t * n + j, n - j, d);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s < slots) load4<false>(y, (pair + s) * n + j, n - j, v[s]);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (s >= slots) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[s] = __builtin_fmaf(d[q], v[s][q], acc[s]);
+      if (dy == nullptr) continue;
+      const int64_t at = (pair + s) * n + j;
+      if (n - j >= 4) {
+        if (kDyBf16) {
+          uint32_t o[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            o[q] = to_bf16_rne(w[s] * d[2 * q]) |
+                   (static_cast<uint32_t>(to_bf16_rne(w[s] * d[2 * q + 1])) << 16);
+          __builtin_memcpy(static_cast<uint16_t*>(dy) + at, o, 8);
+        } else {
+          const float o[4] = {w[s] * d[0], w[s] * d[1], w[s] * d[2], w[s] * d[3]};
+          __builtin_memcpy(static_cast<float*>(dy) + at, o, 16);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (j + q < n) {
+            if (kDyBf16)
+              static_cast<uint16_t*>(dy)[at + q] = to_bf16_rne(w[s] * d[q]);
+            else
+              static_cast<float*>(dy)[at + q] = w[s] * d[q];
+          }
+      }
     }
   }
-  acc = slot_tree(acc);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const float v = slot_tree(acc[s]);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][s] = v;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) dweights[pair] = ((red[0] + red[1]) + red[2]) + red[3];
+  if (static_cast<int32_t>(threadIdx.x) < slots) {
+    const int s = threadIdx.x;
+    dweights[pair + s] = ((red[0][s] + red[1][s]) + red[2][s]) + red[3][s];
+  }
+}
+
+template <int S>
+void launch_combine_grad(const float* y, const float* weights, const void* dout, bool dout_bf16,
+                         int64_t n_tokens, int32_t top_k, int64_t n, void* dy, bool dy_bf16,
+                         float* dweights, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(n_tokens * ((top_k + S - 1) / S))), block(256);
+  if (dout_bf16 && dy_bf16)
+    hipLaunchKernelGGL((combine_grad_kernel<S, true, true>), grid, block, 0, st, y, weights, dout,
+                       top_k, n, dy, dweights);
+  else if (dout_bf16)
+    hipLaunchKernelGGL((combine_grad_kernel<S, true, false>), grid, block, 0, st, y, weights, dout,
+                       top_k, n, dy, dweights);
+  else if (dy_bf16)
+    hipLaunchKernelGGL((combine_grad_kernel<S, false, true>), grid, block, 0, st, y, weights, dout,
+                       top_k, n, dy, dweights);
+  else
+    hipLaunchKernelGGL((combine_grad_kernel<S, false, false>), grid, block, 0, st, y, weights, dout,
+                       top_k, n, dy, dweights);
 }
 
 uint32_t elementwise_blocks(int64_t n) {
@@ -131,9 +212,14 @@ extern "C" int32_t binade_moe_combine_grad(const float* y, const float* weights,
   if (n_tokens == 0) return BINADE_OK;
   if (dweights == nullptr || weights == nullptr) return BINADE_EINVAL;
   if (n > 0 && (y == nullptr || dout == nullptr)) return BINADE_EINVAL;
-  hipLaunchKernelGGL(combine_grad_kernel, dim3(static_cast<uint32_t>(n_tokens * top_k)), dim3(256),
-                     0, static_cast<hipStream_t>(stream), y, weights, dout,
-                     static_cast<int32_t>(dout_dtype == BINADE_BF16), top_k, n, dy,
-                     static_cast<int32_t>(dy_dtype == BINADE_BF16), dweights);
+  const bool db = dout_dtype == BINADE_BF16, yb = dy_dtype == BINADE_BF16;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  // a block per slot until the tokens alone fill the chip
+  if (n_tokens < 512)
+    launch_combine_grad<1>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
+  else if (top_k <= 4)
+    launch_combine_grad<4>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
+  else
+    launch_combine_grad<8>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
   return launch_status();
 }

@@ -1,9 +1,23 @@
 // The router of a MoE layer and its backward: softmax, top-k, per-expert
 // counts, balance loss (the arithmetic is stated in binade.h).
 //
-// One wave per row; a lane holds the row's experts lane, lane + 64, ...
-// (at most 16 of 1024).
+// A row belongs to a group of G lanes with V adjacent experts each (64, 128,
+// 256, 512 or 1024 in all), so a wave has 64 / G rows at once: what a row
+// costs is instructions, not bytes, and a lane's own sort is cheaper than
+// steps across lanes. 16 experts a lane for bf16; 8 for fp32, whose keys take
+// two registers each (with 16 they spill). Nothing of a row leaves its group; sums over rows stay
+// in the lanes' registers (a lane's experts never change) until the block
+// ends.
+//
+// Choice. A logit and its expert make one whole-number key (bf16: 16 + 16
+// bits, fp32: 32 + 32), larger for the larger logit and, among equal ones,
+// for the smaller expert, so that max and min alone sort. For top_k <= 8 each
+// lane sorts its keys by a network, and log2 G steps merge a lane's best
+// eight with its partner's (max(a[j], b[7 - j]) keeps the best eight of two
+// sorted lists). For more slots the best key is taken out top_k times.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "binade.h"
 #include "device_common.h"
@@ -14,174 +28,455 @@ namespace {
 using namespace dev;
 
 constexpr int kMaxExperts = 1024;
-constexpr int kPerLane = kMaxExperts / 64;
 constexpr int kMaxTopK = 64;
-constexpr int32_t kPartBlocks = 256;   // blocks that keep a row of partial sums each
+constexpr int kSorted = 8;        // slots the sorting choice fills
+constexpr int32_t kBlocks = 256;  // at most: each leaves one row of partial sums
 
+// ------------------------------------------------------ steps across lanes
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xF, 0xF,
+                                                           true));
+}
+
+// The value of the lane's partner in step kStep of a butterfly over lanes
+// (1, 2, 4, 8, 16, 32 apart; mirrors stand for 4 and 8: all lanes of a half
+// hold the same by then). Both lanes of a pair get the pair as (a, b) in one
+// order, so that what they make of it is the same bits.
+template <int kStep>
+__device__ __forceinline__ void pair_of(uint32_t v, uint32_t& a, uint32_t& b) {
+  if (kStep == 16 || kStep == 32) {
+    const auto r = kStep == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                               : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+    return;
+  }
+  a = v;
+  b = kStep == 1 ? dpp<0xB1>(v)      // quad_perm 1 0 3 2
+      : kStep == 2 ? dpp<0x4E>(v)    // quad_perm 2 3 0 1
+      : kStep == 4 ? dpp<0x141>(v)   // row_half_mirror
+                   : dpp<0x140>(v);  // row_mirror
+}
+
+template <int kStep>
+__device__ __forceinline__ void pair_of(uint64_t v, uint64_t& a, uint64_t& b) {
+  uint32_t a0, a1, b0, b1;
+  pair_of<kStep>(static_cast<uint32_t>(v), a0, b0);
+  pair_of<kStep>(static_cast<uint32_t>(v >> 32), a1, b1);
+  a = (static_cast<uint64_t>(a1) << 32) | a0;
+  b = (static_cast<uint64_t>(b1) << 32) | b0;
+}
+
+template <int G, int kStep = 1, typename F>
+__device__ __forceinline__ void butterfly(F f) {
+  if constexpr (kStep < G) {
+    f(std::integral_constant<int, kStep>());
+    butterfly<G, 2 * kStep>(f);
+  }
+}
+
+// a + b = b + a: every lane of a group ends with the same bits.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  butterfly<G>([&](auto step) {
+    uint32_t a, b;
+    pair_of<decltype(step)::value>(__float_as_uint(v), a, b);
+    v = __uint_as_float(a) + __uint_as_float(b);
+  });
+  return v;
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  butterfly<G>([&](auto step) {
+    uint32_t a, b;
+    pair_of<decltype(step)::value>(__float_as_uint(v), a, b);
+    v = fmaxf(__uint_as_float(a), __uint_as_float(b));
+  });
+  return v;
+}
+
+template <int G, typename Key>
+__device__ __forceinline__ Key group_max_key(Key v) {
+  butterfly<G>([&](auto step) {
+    Key a, b;
+    pair_of<decltype(step)::value>(v, a, b);
+    v = a > b ? a : b;
+  });
+  return v;
+}
+
+// -------------------------------------------------------------------- keys
+// Ordered form of a logit's bits: rising with the value, -0 as +0; -inf and
+// NaN of either sign lie outside (kLow, kHigh].
+struct KeyBf16 {
+  typedef uint32_t Key;
+  static constexpr uint32_t kLow = 0x0080u, kHigh = 0xFF80u;   // of -inf, of +inf
+  static __device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v) >> 16;
+    return u & 0x8000u ? 0x10000u - u : u + 0x8000u;
+  }
+  static __device__ __forceinline__ Key make(uint32_t o, uint32_t e) {
+    return (o << 16) | (0xFFFFu - e);
+  }
+  static __device__ __forceinline__ uint32_t order_of(Key k) { return k >> 16; }
+  static __device__ __forceinline__ int32_t expert(Key k) {
+    return static_cast<int32_t>(0xFFFFu - (k & 0xFFFFu));
+  }
+  static __device__ __forceinline__ float value(Key k) {
+    const uint32_t o = k >> 16;
+    return __uint_as_float((o & 0x8000u ? o - 0x8000u : 0x10000u - o) << 16);
+  }
+};
+
+struct KeyF32 {
+  typedef uint64_t Key;
+  static constexpr uint32_t kLow = 0x00800000u, kHigh = 0xFF800000u;
+  static __device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u & 0x80000000u ? 0u - u : u + 0x80000000u;
+  }
+  static __device__ __forceinline__ Key make(uint32_t o, uint32_t e) {
+    return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - e);
+  }
+  static __device__ __forceinline__ uint32_t order_of(Key k) {
+    return static_cast<uint32_t>(k >> 32);
+  }
+  static __device__ __forceinline__ int32_t expert(Key k) {
+    return static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+  }
+  static __device__ __forceinline__ float value(Key k) {
+    const uint32_t o = order_of(k);
+    return __uint_as_float(o & 0x80000000u ? o - 0x80000000u : 0u - o);
+  }
+};
+
+template <typename Key>
+__device__ __forceinline__ void exchange(Key& a, Key& b) {   // the larger first
+  const Key hi = a > b ? a : b, lo = a > b ? b : a;
+  a = hi;
+  b = lo;
+}
+
+template <typename Key>
+__device__ __forceinline__ void sort8(Key* k) {   // 19 exchanges, falling
+  constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6},
+                              {5, 7}, {1, 2}, {5, 6}, {0, 4}, {3, 7}, {1, 5}, {2, 6},
+                              {1, 4}, {3, 6}, {2, 4}, {3, 5}, {3, 4}};
+#pragma unroll
+  for (int j = 0; j < 19; ++j) exchange(k[net[j][0]], k[net[j][1]]);
+}
+
+template <typename Key>
+__device__ __forceinline__ void sort_bitonic8(Key* k) {
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((j & d) == 0) exchange(k[j], k[j + d]);
+}
+
+// The group's best eight keys, falling, in every lane.
+template <int G, int V, typename Key>
+__device__ __forceinline__ void best8(const Key (&key)[V], Key (&best)[8]) {
+#pragma unroll
+  for (int b = 0; b < V / 8; ++b) {
+    Key k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = key[8 * b + j];
+    sort8(k);
+    if (b == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) best[j] = k[j];
+    } else {
+      Key m[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[j] = best[j] > k[7 - j] ? best[j] : k[7 - j];
+      sort_bitonic8(m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) best[j] = m[j];
+    }
+  }
+  butterfly<G>([&](auto step) {
+    Key a[8], b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pair_of<decltype(step)::value>(best[j], a[j], b[j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) best[j] = a[j] > b[7 - j] ? a[j] : b[7 - j];
+    sort_bitonic8(best);
+  });
+}
+
+// ------------------------------------------------------------------ values
+// exp(d) for d <= 0, or NaN: 2^(d log2 e) with what the product d log2 e
+// loses put back, two steps off at most; 0 below -150.
+__device__ __forceinline__ float exp_of(float d) {
+  constexpr float kL = 1.44269502e+0f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;
+  d = d < -150.0f ? -150.0f : d;
+  const float t = d * kL;
+  const float r = __builtin_fmaf(d, kLlo, __builtin_fmaf(d, kL, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * kLn2, e);
+}
+
+// V logits from expert e0 on as fp32; -inf behind the last expert. vec: rows
+// and their length are whole 16-byte pieces.
+template <int V, bool kBf16>
+__device__ __forceinline__ void load_logits(const void* p, int64_t row, int32_t e0, int32_t n,
+                                            bool vec, float (&v)[V]) {
+  if (vec) {
+#pragma unroll
+    for (int b = 0; b < V / 8; ++b) {
+      const bool in = e0 + 8 * b < n;
+      const int64_t at = row + (in ? e0 + 8 * b : 0);
+      if (kBf16) {
+        const uint4 d = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[8 * b + 2 * j] = bf16_lo(w[j]), v[8 * b + 2 * j + 1] = bf16_hi(w[j]);
+      } else {
+        __builtin_memcpy(&v[8 * b], __builtin_assume_aligned(static_cast<const float*>(p) + at, 16), 32);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * b + j] = in ? v[8 * b + j] : -__builtin_inff();
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int64_t at = row + (e0 + j < n ? e0 + j : 0);
+      const float f = kBf16 ? __uint_as_float(static_cast<uint32_t>(
+                                  static_cast<const uint16_t*>(p)[at]) << 16)
+                            : static_cast<const float*>(p)[at];
+      v[j] = e0 + j < n ? f : -__builtin_inff();
+    }
+  }
+}
+
+// ----------------------------------------------------------------- forward
 struct RouteArgs {
   const void* logits;
   const uint8_t* valid;
   int32_t* idx;
   float* weights;
-  int32_t* part_counts;   // [blocks, n_experts + 1] or NULL
+  int32_t* counts;        // [n_experts + 1], or NULL: no sums over rows
+  float* prob_sum;
+  float* loss;
+  int32_t* part_counts;   // [blocks, n_experts + 1]
   float* part_prob;       // [blocks, n_experts]
   int64_t ld, n_tokens;
   int32_t n_experts, top_k;
-  bool bf16, renorm;
+  bool renorm, vec;
 };
 
-__device__ __forceinline__ float load_logit(const void* p, int64_t i, bool bf16) {
-  return bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16)
-              : static_cast<const float*>(p)[i];
-}
-
-// Ordered key of (logit, expert): larger logit first, then the smaller
-// expert; 0 for an expert that cannot be taken (-inf or NaN).
-__device__ __forceinline__ uint64_t key_of(float v, int32_t e) {
-  if (!(v > -__builtin_inff())) return 0;
-  v = v + 0.0f;   // -0 -> +0: equal logits tie
-  const uint32_t u = __float_as_uint(v);
-  const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
-}
-
-__device__ __forceinline__ uint64_t wave_max(uint64_t k) {
-  for (int s = 32; s >= 1; s >>= 1) {
-    const uint64_t o = __shfl_xor(static_cast<unsigned long long>(k), s, 64);
-    k = o > k ? o : k;
-  }
-  return k;
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int s = 32; s >= 1; s >>= 1) v = v + __shfl_xor(v, s, 64);
-  return v;
-}
-
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  __shared__ int32_t counts[kMaxExperts + 1];
-  __shared__ float prob[4][kMaxExperts];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int32_t e = threadIdx.x; e <= p.n_experts; e += 256) counts[e] = 0;
+// loss = E / (k R R) * sum over e of counts[e] * prob_sum[e]: each thread its
+// term, added by a fixed tree. All threads of a block of whole waves.
+__device__ __forceinline__ void store_loss(float term, int32_t rows, int32_t n_experts,
+                                           int32_t top_k, float* red, float* loss) {
+  const float r = static_cast<float>(rows > 0 ? rows : 1);
+  const float part = group_sum<64>(term / (static_cast<float>(top_k) * r) / r);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = part;
   __syncthreads();
-  float sums[kPerLane];
-#pragma unroll
-  for (int j = 0; j < kPerLane; ++j) sums[j] = 0.0f;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.n_tokens;
-       t += static_cast<int64_t>(gridDim.x) * 4) {
-    const bool valid = p.valid == nullptr || p.valid[t] != 0;
-    float v[kPerLane];
-    uint64_t key[kPerLane];
-    bool nan = false;
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int32_t e = lane + 64 * j;
-      v[j] = e < p.n_experts ? load_logit(p.logits, t * p.ld + e, p.bf16) : -__builtin_inff();
-      nan |= v[j] != v[j];
-      key[j] = key_of(v[j], e);
-    }
-    uint64_t best = 0;
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) best = key[j] > best ? key[j] : best;
-    best = wave_max(best);
-    const bool counted = valid && best != 0;
-    int32_t* idx = p.idx + t * p.top_k;
-    float* w = p.weights + t * p.top_k;
-    if (!counted) {
-      if (lane < p.top_k) idx[lane] = -1, w[lane] = 0.0f;
-      continue;
-    }
-    const uint32_t o = static_cast<uint32_t>(best >> 32);
-    const float top = __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
-    float total = 0.0f, pr[kPerLane];
-#pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      pr[j] = expf(v[j] - top);
-      total += pr[j];
-    }
-    total = wave_sum(total);
-    float mine = 0.0f, taken = 0.0f;   // lane s: the weight of slot s
-    int32_t my_idx = -1;
-    for (int32_t s = 0; s < p.top_k; ++s) {
-      if (s > 0) {
-        best = 0;
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) best = key[j] > best ? key[j] : best;
-        best = wave_max(best);
-      }
-      if (best == 0) break;
-      const int32_t e = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-      float pe = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (key[j] == best) key[j] = 0, pe = pr[j];
-      pe = __shfl(pe, e & 63, 64) / total;
-      taken += pe;
-      if (lane == s) mine = pe, my_idx = e;
-    }
-    if (lane < p.top_k) {
-      idx[lane] = my_idx;
-      w[lane] = my_idx < 0 ? 0.0f : p.renorm ? mine / taken : mine;
-    }
-    if (p.part_counts != nullptr) {
-      if (my_idx >= 0) atomicAdd(&counts[my_idx], 1);
-      if (lane == 0) atomicAdd(&counts[p.n_experts], 1);
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) sums[j] += pr[j] / total;
-    }
-  }
-  if (p.part_counts == nullptr) return;
-#pragma unroll
-  for (int j = 0; j < kPerLane; ++j) prob[wave][lane + 64 * j] = sums[j];
-  __syncthreads();
-  for (int32_t e = threadIdx.x; e <= p.n_experts; e += 256) {
-    p.part_counts[static_cast<int64_t>(blockIdx.x) * (p.n_experts + 1) + e] = counts[e];
-    if (e < p.n_experts)
-      p.part_prob[static_cast<int64_t>(blockIdx.x) * p.n_experts + e] =
-          ((prob[0][e] + prob[1][e]) + prob[2][e]) + prob[3][e];
-  }
-}
-
-// Adds the blocks' partial counts and sums in block order; the loss is a
-// fixed tree over the experts. One block.
-__global__ __launch_bounds__(1024) void route_stats_kernel(const int32_t* part_counts,
-                                                           const float* part_prob, int32_t blocks,
-                                                           int32_t n_experts, int32_t top_k,
-                                                           int32_t* counts, float* prob_sum,
-                                                           float* loss) {
-  __shared__ float red[16];
-  __shared__ int32_t rows_s;
-  const int32_t e = threadIdx.x;
-  if (e == 0) {
-    int32_t rows = 0;
-    for (int32_t b = 0; b < blocks; ++b)
-      rows += part_counts[static_cast<int64_t>(b) * (n_experts + 1) + n_experts];
-    rows_s = rows;
-    counts[n_experts] = rows;
-  }
-  int32_t c = 0;
-  float s = 0.0f;
-  if (e < n_experts) {
-    for (int32_t b = 0; b < blocks; ++b) {
-      c += part_counts[static_cast<int64_t>(b) * (n_experts + 1) + e];
-      s += part_prob[static_cast<int64_t>(b) * n_experts + e];
-    }
-    counts[e] = c;
-    prob_sum[e] = s;
-  }
-  __syncthreads();
-  const float rows = static_cast<float>(rows_s > 0 ? rows_s : 1);
-  const float part = wave_sum(static_cast<float>(c) / (static_cast<float>(top_k) * rows) *
-                              (s / rows));
-  if ((e & 63) == 0) red[e >> 6] = part;
-  __syncthreads();
-  if (e == 0) {
+  if (threadIdx.x == 0) {
     float l = 0.0f;
-    for (int w = 0; w < 16; ++w) l += red[w];
+    for (uint32_t w = 0; w < blockDim.x / 64; ++w) l += red[w];
     loss[0] = static_cast<float>(n_experts) * l;
   }
 }
 
+template <int G, int V, typename K, bool kSort>
+__global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
+  typedef typename K::Key Key;
+  constexpr bool kBf16 = sizeof(Key) == 4;
+  constexpr int kRows = 64 / G;           // of a wave
+  constexpr int kExperts = G * V;
+  __shared__ int32_t counts[kExperts + 1];
+  __shared__ float prob[16][kExperts];
+  __shared__ float red[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int l = lane & (G - 1);
+  const int32_t e0 = l * V;
+  const bool stats = p.counts != nullptr;
+  if (stats) {
+    for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) counts[e] = 0;
+    __syncthreads();
+  }
+  float sums[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sums[j] = 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * waves * kRows;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * waves + wave) * kRows; t0 < p.n_tokens;
+       t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const bool in = t < p.n_tokens;
+    const bool valid = in && (p.valid == nullptr || p.valid[t] != 0);
+    float v[V];
+    load_logits<V, kBf16>(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec, v);
+    Key key[V], best[8];
+    // NaN above +inf is rare: looked for once the best key is known
+    bool nan_rows = false;
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        uint32_t o = K::ordered(v[j]);
+        if (nan_rows && o > K::kHigh) o = 0;
+        key[j] = K::make(o, e0 + j);
+      }
+      if (kSort) {
+        best8<G, V>(key, best);
+      } else {
+        best[0] = key[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) best[0] = key[j] > best[0] ? key[j] : best[0];
+        best[0] = group_max_key<G>(best[0]);
+      }
+      nan_rows = __ballot(K::order_of(best[0]) > K::kHigh) != 0;
+      if (!nan_rows) break;
+    }
+    const bool counted = valid && K::order_of(best[0]) > K::kLow;
+    const float top = K::value(best[0]);
+    float total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = exp_of(v[j] - top);
+      total += v[j];
+    }
+    total = group_sum<G>(total);
+    const float inv = 1.0f / total;
+    if (stats) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sums[j] += counted ? v[j] * inv : 0.0f;
+      if (counted && l == 0) atomicAdd(&counts[p.n_experts], 1);
+    }
+    // lane l of the group: slots l, l + G, ... of the row
+    constexpr int kHeld = kSort ? 1 : kMaxTopK / G > 0 ? kMaxTopK / G : 1;
+    Key slot[kHeld];
+    if (kSort) {
+      slot[0] = best[0];
+#pragma unroll
+      for (int j = 1; j < kSorted; ++j) slot[0] = l == j ? best[j] : slot[0];
+    } else {
+      int32_t s = 0;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        slot[h] = 0;
+        for (int j = 0; j < G && s < p.top_k; ++j, ++s) {
+          if (s > 0) {
+            best[0] = key[0];
+#pragma unroll
+            for (int q = 1; q < V; ++q) best[0] = key[q] > best[0] ? key[q] : best[0];
+            best[0] = group_max_key<G>(best[0]);
+          }
+#pragma unroll
+          for (int q = 0; q < V; ++q) key[q] = key[q] == best[0] ? 0 : key[q];
+          slot[h] = l == j ? best[0] : slot[h];
+        }
+      }
+    }
+    float e[kHeld], taken = 0.0f;
+    // a group of more lanes than sorted slots holds each slot once
+    const bool holds = !kSort || l < kSorted;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const bool some = holds && l + h * G < p.top_k && K::order_of(slot[h]) > K::kLow;
+      e[h] = some ? exp_of(K::value(slot[h]) - top) : 0.0f;
+      taken += e[h];
+    }
+    if (p.renorm) taken = group_sum<G>(taken);
+    // a NaN among the logits is one of every weight
+    const float f = p.renorm ? (total == total ? 1.0f / taken : total) : inv;
+    if (in) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        const int32_t s = l + h * G;
+        if (!holds || s >= p.top_k) continue;
+        const bool some = counted && K::order_of(slot[h]) > K::kLow;
+        const int32_t ex = some ? K::expert(slot[h]) : -1;
+        p.idx[t * p.top_k + s] = ex;
+        p.weights[t * p.top_k + s] = some ? e[h] * f : 0.0f;
+        if (stats && some) atomicAdd(&counts[ex], 1);
+      }
+    }
+  }
+  if (!stats) return;
+  // the wave's groups, then the block's waves, in a fixed order
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float s = sums[j];
+    uint32_t a, b;
+    if (G <= 8) {
+      s += __shfl_xor(s, 8, 64);
+    }
+    if (G <= 16) {
+      pair_of<16>(__float_as_uint(s), a, b);
+      s = __uint_as_float(a) + __uint_as_float(b);
+    }
+    if (G <= 32) {
+      pair_of<32>(__float_as_uint(s), a, b);
+      s = __uint_as_float(a) + __uint_as_float(b);
+    }
+    if (lane < G) prob[wave][e0 + j] = s;
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  float term = 0.0f;
+  for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) {
+    (alone ? p.counts : p.part_counts + static_cast<int64_t>(blockIdx.x) * (p.n_experts + 1))[e] =
+        counts[e];
+    if (e == p.n_experts) continue;
+    float s = 0.0f;
+    for (int w = 0; w < waves; ++w) s += prob[w][e];
+    (alone ? p.prob_sum : p.part_prob + static_cast<int64_t>(blockIdx.x) * p.n_experts)[e] = s;
+    term += static_cast<float>(counts[e]) * s;
+  }
+  if (alone) store_loss(term, counts[p.n_experts], p.n_experts, p.top_k, red, p.loss);
+}
+
+// Adds the blocks' partial counts and sums. One block of 1024: n_experts
+// padded to a power of two of threads side by side, the rest over the blocks;
+// both in a fixed order.
+__global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t blocks,
+                                                           int32_t width_log2) {
+  __shared__ int32_t count_s[1024];
+  __shared__ float sum_s[1024];
+  __shared__ float red[16];
+  __shared__ int32_t rows_s;
+  const int32_t width = 1 << width_log2, e = threadIdx.x & (width - 1);
+  const int32_t lane = threadIdx.x >> width_log2, lanes = 1024 >> width_log2;
+  int32_t rows = 0;
+  if (threadIdx.x < 64) {
+    for (int32_t b = threadIdx.x; b < blocks; b += 64)
+      rows += p.part_counts[static_cast<int64_t>(b) * (p.n_experts + 1) + p.n_experts];
+    for (int s = 32; s >= 1; s >>= 1) rows += __shfl_xor(rows, s, 64);
+    if (threadIdx.x == 0) rows_s = rows;
+  }
+  int32_t c = 0;
+  float s = 0.0f;
+  if (e < p.n_experts) {
+#pragma unroll 8
+    for (int32_t b = lane; b < blocks; b += lanes) {
+      c += p.part_counts[static_cast<int64_t>(b) * (p.n_experts + 1) + e];
+      s += p.part_prob[static_cast<int64_t>(b) * p.n_experts + e];
+    }
+  }
+  count_s[threadIdx.x] = c;
+  sum_s[threadIdx.x] = s;
+  __syncthreads();
+  float term = 0.0f;
+  if (lane == 0 && e < p.n_experts) {
+    for (int32_t q = 1; q < lanes; ++q) {
+      c += count_s[q * width + e];
+      s += sum_s[q * width + e];
+    }
+    p.counts[e] = c;
+    p.prob_sum[e] = s;
+    term = static_cast<float>(c) * s;
+  }
+  if (threadIdx.x == 0) p.counts[p.n_experts] = rows_s;
+  store_loss(term, rows_s, p.n_experts, p.top_k, red, p.loss);
+}
+
+// ---------------------------------------------------------------- backward
 struct RouteGradArgs {
   const void* logits;
   const int32_t* idx;
@@ -192,109 +487,194 @@ struct RouteGradArgs {
   uint32_t* status;
   int64_t ld, ld_d, n_tokens;
   int32_t n_experts, top_k;
-  bool bf16, d_bf16, renorm;
+  bool renorm, vec, vec_d;
 };
 
+// The slots' gradients reach their experts' lanes through a row of LDS a
+// group: the sum of dweights of an expert's slots, and their number (a slot
+// gets its gradient less the row's mean). The row is zero between tokens.
+template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float load[kPerLane];
+  constexpr int kRows = 64 / G, kExperts = G * V;
+  __shared__ __align__(16) float grad_s[4 * kRows][kExperts];
+  __shared__ __align__(16) float hits_s[4 * kRows][kExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (G - 1);
+  const int32_t e0 = l * V;
+  float* grad_row = grad_s[wave * kRows + lane / G];
+  float* hits_row = hits_s[wave * kRows + lane / G];
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) load[j] = 0.0f;
+  for (int j = 0; j < V; ++j) grad_row[e0 + j] = hits_row[e0 + j] = 0.0f;
+  wave_sync();
+  float load[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) load[j] = 0.0f;
   if (p.counts != nullptr) {
     const int32_t r = p.counts[p.n_experts];
     const float rows = static_cast<float>(r > 0 ? r : 1);
     const float f = p.dloss[0] * static_cast<float>(p.n_experts) /
-                    (static_cast<float>(p.top_k) * rows * rows);
+                    (static_cast<float>(p.top_k) * rows) / rows;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int32_t e = lane + 64 * j;
-      if (e < p.n_experts) load[j] = f * static_cast<float>(p.counts[e]);
-    }
+    for (int j = 0; j < V; ++j)
+      if (e0 + j < p.n_experts) load[j] = f * static_cast<float>(p.counts[e0 + j]);
   }
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.n_tokens;
-       t += static_cast<int64_t>(gridDim.x) * 4) {
-    int32_t e_s = -1;
-    float dw = 0.0f;
-    if (lane < p.top_k) {
-      e_s = p.idx[t * p.top_k + lane];
-      if (e_s >= p.n_experts || e_s < 0) {
-        if (e_s != -1 && p.status != nullptr)
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * kRows;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows; t0 < p.n_tokens;
+       t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const bool in = t < p.n_tokens;
+    float v[V];
+    load_logits<V, kBf16>(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec, v);
+    bool counted = false;
+    const auto slots = [&](auto use) {
+      for (int32_t s = l; s < p.top_k; s += G) {
+        if (!in) break;
+        const int32_t e = p.idx[t * p.top_k + s];
+        if (e >= 0 && e < p.n_experts) use(s, e);
+        else if (e != -1 && p.status != nullptr)
           atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
-        e_s = -1;
       }
-      if (p.dweights != nullptr) dw = p.dweights[t * p.top_k + lane];
-    }
-    const bool counted = __shfl(e_s, 0, 64) >= 0;
-    float v[kPerLane];
-    float top = -__builtin_inff();
+    };
+    slots([&](int32_t s, int32_t e) {
+      counted |= s == 0;
+      atomicAdd(&hits_row[e], 1.0f);
+      if (p.dweights != nullptr) atomicAdd(&grad_row[e], p.dweights[t * p.top_k + s]);
+    });
+    wave_sync();
+    counted = (__ballot(counted) >> (lane & ~(G - 1)) & 1u) != 0;
+    float top = v[0];
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int32_t e = lane + 64 * j;
-      v[j] = e < p.n_experts ? load_logit(p.logits, t * p.ld + e, p.bf16) : -__builtin_inff();
-      top = fmaxf(top, v[j]);
-    }
-    for (int s = 32; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
+    for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
+    top = group_max<G>(top);
     float total = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      v[j] = expf(v[j] - top);
+    for (int j = 0; j < V; ++j) {
+      v[j] = exp_of(v[j] - top);
       total += v[j];
     }
-    total = wave_sum(total);
-    float u[kPerLane];
+    const float inv = 1.0f / group_sum<G>(total);
+    float u[V], hits[V], chosen = 0.0f, mean = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      v[j] = v[j] / total;
-      u[j] = load[j];
+    for (int j = 0; j < V; ++j) {
+      v[j] *= inv;
+      u[j] = grad_row[e0 + j];
+      hits[j] = hits_row[e0 + j];
+      chosen = __builtin_fmaf(hits[j], v[j], chosen);
+      mean = __builtin_fmaf(u[j], v[j], mean);
     }
-    float chosen = 0.0f;   // lane s: p of slot s
     if (p.renorm) {
-      for (int32_t s = 0; s < p.top_k; ++s) {
-        const int32_t e = __shfl(e_s, s, 64);
-        if (e < 0) continue;
-        float pe = 0.0f;
+      const float f = 1.0f / group_sum<G>(chosen);
+      mean = group_sum<G>(mean) * f;
 #pragma unroll
-        for (int j = 0; j < kPerLane; ++j)
-          if (e == lane + 64 * j) pe = v[j];
-        pe = __shfl(pe, e & 63, 64);
-        if (lane == s) chosen = pe;
-      }
-      const float sum = wave_sum(chosen);
-      const float mean = wave_sum(e_s >= 0 ? dw * chosen / sum : 0.0f);
-      dw = (dw - mean) / sum;
-    }
-    for (int32_t s = 0; s < p.top_k; ++s) {
-      const int32_t e = __shfl(e_s, s, 64);
-      const float d = __shfl(dw, s, 64);
-      if (e < 0) continue;
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (e == lane + 64 * j) u[j] += d;
+      for (int j = 0; j < V; ++j) u[j] = hits[j] != 0.0f ? (u[j] - hits[j] * mean) * f : 0.0f;
     }
     float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) dot = __builtin_fmaf(v[j], u[j], dot);
-    dot = wave_sum(dot);
+    for (int j = 0; j < V; ++j) {
+      u[j] += load[j];
+      dot = __builtin_fmaf(v[j], u[j], dot);
+    }
+    dot = group_sum<G>(dot);
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      const int32_t e = lane + 64 * j;
-      if (e >= p.n_experts) continue;
-      const float d = counted ? v[j] * (u[j] - dot) : 0.0f;
-      if (p.d_bf16)
-        static_cast<uint16_t*>(p.dlogits)[t * p.ld_d + e] = to_bf16_rne(d);
-      else
-        static_cast<float*>(p.dlogits)[t * p.ld_d + e] = d;
+    for (int j = 0; j < V; ++j) v[j] = counted ? v[j] * (u[j] - dot) : 0.0f;
+    wave_sync();
+    slots([&](int32_t, int32_t e) { grad_row[e] = hits_row[e] = 0.0f; });
+    wave_sync();
+    if (!in) continue;
+    const int64_t row = t * p.ld_d;
+#pragma unroll
+    for (int b = 0; b < V / 8; ++b) {
+      const int32_t e = e0 + 8 * b;
+      if (p.vec_d) {
+        if (e >= p.n_experts) continue;
+        if (kOutBf16) {
+          uint32_t d[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            d[j] = to_bf16_rne(v[8 * b + 2 * j]) |
+                   (static_cast<uint32_t>(to_bf16_rne(v[8 * b + 2 * j + 1])) << 16);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dlogits) + row + e) =
+              uint4{d[0], d[1], d[2], d[3]};
+        } else {
+          __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(p.dlogits) + row + e, 16),
+                           &v[8 * b], 32);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (e + j >= p.n_experts) continue;
+          if (kOutBf16)
+            static_cast<uint16_t*>(p.dlogits)[row + e + j] = to_bf16_rne(v[8 * b + j]);
+          else
+            static_cast<float*>(p.dlogits)[row + e + j] = v[8 * b + j];
+        }
+      }
     }
   }
 }
 
-uint32_t route_blocks(int64_t n_tokens) {
-  const int64_t b = (n_tokens + 3) / 4;
-  return static_cast<uint32_t>(b < 1 ? 1 : b < kPartBlocks ? b : kPartBlocks);
+// ------------------------------------------------------------------- hosts
+// Lanes a row of the choice.
+int32_t lanes_of(int32_t n_experts, bool bf16) {
+  if (n_experts <= 64) return 8;
+  const int32_t lanes = n_experts <= 128 ? 8 : n_experts <= 256 ? 16 : n_experts <= 512 ? 32 : 64;
+  return bf16 || lanes == 64 ? lanes : 2 * lanes;
+}
+
+struct RouteShape {
+  uint32_t blocks, threads;
+};
+
+RouteShape route_shape(int64_t n_tokens, int32_t n_experts, bool bf16) {
+  const int64_t rows = 64 / lanes_of(n_experts, bf16), waves = (n_tokens + rows - 1) / rows;
+  // up to four waves a block while that leaves a block for every CU
+  const int64_t per = waves <= 1 ? 1 : waves <= 4 * kBlocks ? 4 : 16;
+  int64_t blocks = (waves + per - 1) / per;
+  if (blocks > kBlocks) blocks = kBlocks;
+  return {static_cast<uint32_t>(blocks < 1 ? 1 : blocks), static_cast<uint32_t>(64 * per)};
+}
+
+template <int G, int V, typename K>
+void launch_route(const RouteArgs& p, RouteShape s, hipStream_t st) {
+  if (p.top_k <= kSorted)
+    hipLaunchKernelGGL((route_kernel<G, V, K, true>), dim3(s.blocks), dim3(s.threads), 0, st, p);
+  else
+    hipLaunchKernelGGL((route_kernel<G, V, K, false>), dim3(s.blocks), dim3(s.threads), 0, st, p);
+}
+
+void launch_route_experts(const RouteArgs& p, RouteShape s, bool bf16, hipStream_t st) {
+  const int32_t lanes = lanes_of(p.n_experts, bf16);
+  if (bf16) {
+    if (p.n_experts <= 64) launch_route<8, 8, KeyBf16>(p, s, st);
+    else if (lanes == 8) launch_route<8, 16, KeyBf16>(p, s, st);
+    else if (lanes == 16) launch_route<16, 16, KeyBf16>(p, s, st);
+    else if (lanes == 32) launch_route<32, 16, KeyBf16>(p, s, st);
+    else launch_route<64, 16, KeyBf16>(p, s, st);
+  } else {
+    if (p.n_experts <= 64) launch_route<8, 8, KeyF32>(p, s, st);
+    else if (lanes == 16) launch_route<16, 8, KeyF32>(p, s, st);
+    else if (lanes == 32) launch_route<32, 8, KeyF32>(p, s, st);
+    else if (p.n_experts <= 512) launch_route<64, 8, KeyF32>(p, s, st);
+    else launch_route<64, 16, KeyF32>(p, s, st);
+  }
+}
+
+template <int G, int V>
+void launch_grad(const RouteGradArgs& p, bool bf16, bool out_bf16, hipStream_t st) {
+  const int64_t rows = 4 * (64 / G), b = (p.n_tokens + rows - 1) / rows;
+  const dim3 grid(static_cast<uint32_t>(b < 1024 ? b : 1024)), block(256);
+  if (bf16 && out_bf16) hipLaunchKernelGGL((route_grad_kernel<G, V, true, true>), grid, block, 0, st, p);
+  else if (bf16) hipLaunchKernelGGL((route_grad_kernel<G, V, true, false>), grid, block, 0, st, p);
+  else if (out_bf16) hipLaunchKernelGGL((route_grad_kernel<G, V, false, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((route_grad_kernel<G, V, false, false>), grid, block, 0, st, p);
 }
 
 bool route_sizes_ok(int64_t n_tokens, int32_t n_experts) {
   return n_tokens >= 0 && n_tokens <= (1ll << 30) && n_experts >= 1 && n_experts <= kMaxExperts;
+}
+
+// Whether rows of n at stride ld from p are whole 16-byte pieces of 8 values.
+bool whole_pieces(const void* p, int32_t n, int64_t ld, bool bf16) {
+  return aligned16(p) && n % 8 == 0 && ld % (bf16 ? 8 : 4) == 0;
 }
 
 }  // namespace
@@ -304,7 +684,9 @@ using namespace binade;
 
 extern "C" int64_t binade_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts) {
   if (!route_sizes_ok(n_tokens, n_experts)) return 0;
-  return static_cast<int64_t>(route_blocks(n_tokens)) * (2 * n_experts + 1) * 4;
+  // fp32 rows take at least as many lanes as bf16 ones
+  return static_cast<int64_t>(route_shape(n_tokens, n_experts, false).blocks) *
+         (2 * n_experts + 1) * 4;
 }
 
 extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t ld, int64_t n_tokens,
@@ -327,28 +709,32 @@ extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t l
       return BINADE_ENOSPACE;
     if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   }
-  const uint32_t blocks = route_blocks(n_tokens);
+  const RouteShape shape = route_shape(n_tokens, n_experts, dtype == BINADE_BF16);
   RouteArgs p{};
   p.logits = logits;
   p.valid = valid;
   p.idx = idx;
   p.weights = weights;
-  if (stats) {
-    p.part_counts = static_cast<int32_t*>(workspace);
-    p.part_prob =
-        reinterpret_cast<float*>(p.part_counts + static_cast<int64_t>(blocks) * (n_experts + 1));
-  }
+  p.counts = counts;
+  p.prob_sum = prob_sum;
+  p.loss = loss;
+  p.part_counts = static_cast<int32_t*>(workspace);
+  p.part_prob = reinterpret_cast<float*>(p.part_counts + static_cast<int64_t>(shape.blocks) *
+                                                             (n_experts + 1));
   p.ld = ld;
   p.n_tokens = n_tokens;
   p.n_experts = n_experts;
   p.top_k = top_k;
-  p.bf16 = dtype == BINADE_BF16;
   p.renorm = renormalize != 0;
+  p.vec = whole_pieces(logits, n_experts, ld, dtype == BINADE_BF16);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(route_kernel, dim3(blocks), dim3(256), 0, st, p);
-  if (stats)
-    hipLaunchKernelGGL(route_stats_kernel, dim3(1), dim3(1024), 0, st, p.part_counts, p.part_prob,
-                       static_cast<int32_t>(blocks), n_experts, top_k, counts, prob_sum, loss);
+  launch_route_experts(p, shape, dtype == BINADE_BF16, st);
+  if (stats && shape.blocks > 1) {
+    int32_t width_log2 = 0;
+    while ((1 << width_log2) < n_experts) ++width_log2;
+    hipLaunchKernelGGL(route_stats_kernel, dim3(1), dim3(1024), 0, st, p,
+                       static_cast<int32_t>(shape.blocks), width_log2);
+  }
   return launch_status();
 }
 
@@ -367,6 +753,7 @@ extern "C" int32_t binade_moe_route_grad(const void* logits, int32_t dtype, int6
   if ((counts != nullptr) != (dloss != nullptr)) return BINADE_EINVAL;
   if (n_tokens == 0) return BINADE_OK;
   if (logits == nullptr || idx == nullptr || dlogits == nullptr) return BINADE_EINVAL;
+  const bool bf16 = dtype == BINADE_BF16, out_bf16 = dlogits_dtype == BINADE_BF16;
   RouteGradArgs p{};
   p.logits = logits;
   p.idx = idx;
@@ -380,11 +767,14 @@ extern "C" int32_t binade_moe_route_grad(const void* logits, int32_t dtype, int6
   p.n_tokens = n_tokens;
   p.n_experts = n_experts;
   p.top_k = top_k;
-  p.bf16 = dtype == BINADE_BF16;
-  p.d_bf16 = dlogits_dtype == BINADE_BF16;
   p.renorm = renormalize != 0;
-  const int64_t b = (n_tokens + 3) / 4;
-  hipLaunchKernelGGL(route_grad_kernel, dim3(static_cast<uint32_t>(b < 2048 ? b : 2048)), dim3(256),
-                     0, static_cast<hipStream_t>(stream), p);
+  p.vec = whole_pieces(logits, n_experts, ld, bf16);
+  p.vec_d = whole_pieces(dlogits, n_experts, ld_d, out_bf16);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n_experts <= 64) launch_grad<8, 8>(p, bf16, out_bf16, st);
+  else if (n_experts <= 128) launch_grad<8, 16>(p, bf16, out_bf16, st);
+  else if (n_experts <= 256) launch_grad<16, 16>(p, bf16, out_bf16, st);
+  else if (n_experts <= 512) launch_grad<32, 16>(p, bf16, out_bf16, st);
+  else launch_grad<64, 16>(p, bf16, out_bf16, st);
   return launch_status();
 }
