@@ -939,21 +939,44 @@ def bf16_moe_gemv(experts: torch.Tensor, n_experts: int, x: torch.Tensor,
 
 
 # ------------------------------------------------------------------ router
+_bound: dict = {}
+
+
+def _entry(name: str):
+    """A library function, looked up once."""
+    fn = _bound.get(name)
+    if fn is None:
+        fn = _bound[name] = getattr(lib(), name)
+    return fn
+
+
+def _run(name: str, *args):
+    rc = _entry(name)(*args)
+    if rc != OK:
+        raise BinadeError(name, rc, lib().binade_last_hip_error() if rc == EHIP else 0)
+
+
 def _on_device(fn):
-    """Run a device binding on the device of its first argument: its tensors
-    are checked to be there, and kernels, temporaries and a default stream are
-    that device's even when another one is current."""
+    """Run a device binding on the device of its first argument, with `stream`
+    as a raw handle: temporaries and a default stream are that device's even
+    when another one is current, and a given stream is torch's current one
+    meanwhile (as in _on_stream)."""
     @functools.wraps(fn)
     def wrapper(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        index = first.get_device() if isinstance(first, torch.Tensor) else -1
+        if index < 0:
             raise ValueError(f"{fn.__name__} takes device tensors")
-        index = first.device.index
-        if isinstance(stream, torch.cuda.Stream) and stream.device_index != index:
-            raise ValueError("stream of another device")
-        if index == torch.cuda.current_device():
-            return fn(first, *args, stream=stream, **kw)
+        if stream is None and index == torch._C._cuda_getDevice():
+            return fn(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
         with torch.cuda.device(index):
-            return fn(first, *args, stream=stream, **kw)
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            elif not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream))
+            elif stream.device_index != index:
+                raise ValueError("stream of another device")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, stream=stream.cuda_stream, **kw)
     return wrapper
 
 
@@ -961,7 +984,7 @@ def _arg(name: str, t: torch.Tensor, dtypes, shape, device) -> torch.Tensor:
     """t checked: one of dtypes, the shape, the device, and contiguous."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
@@ -977,30 +1000,39 @@ def _out_arg(name: str, t: torch.Tensor | None, dtype, shape, device) -> torch.T
     return _arg(name, t, (dtype,), shape, device)
 
 
-def _status_arg(status: torch.Tensor | None, device) -> torch.Tensor | None:
-    if status is not None and (status.device != device or status.element_size() != 4
-                               or status.numel() < 1):
+def _status_arg(status: torch.Tensor | None, device):
+    """The address of a status word, or None."""
+    if status is None:
+        return None
+    if status.device != device or status.element_size() != 4 or status.numel() < 1:
         raise ValueError("status: one 32-bit word on the device")
-    return status
+    return status.data_ptr()
 
 
 def _scratch(nbytes: int, workspace: torch.Tensor | None, device):
-    """(tensor, bytes) of a workspace: the caller's, or torch's allocator's."""
+    """(tensor, address, bytes) of a workspace: the caller's, or from torch's
+    allocator."""
     if workspace is None:
         if nbytes == 0:
-            return None, 0
+            return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on the device")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 _TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
 
 def _logits_arg(t: torch.Tensor) -> torch.Tensor:
-    if t.dtype not in _FLOATS:
+    if t.dtype not in _CODE:
         raise TypeError(f"logits: {t.dtype}, expected bf16 or fp32")
     if t.dim() != 2:
         raise ValueError("logits: [n_tokens, n_experts]")
@@ -1020,7 +1052,6 @@ class MoeRoute:
 
 
 @_on_device
-@_on_stream
 def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
               valid: torch.Tensor | None = None, stats: bool = True,
               workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
@@ -1032,22 +1063,24 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     T, E = logits.shape
     if valid is not None:
         valid = _arg("valid", valid, (torch.bool, torch.uint8), (T,), dev)
-    out = MoeRoute(torch.empty(T, top_k, dtype=torch.int32, device=dev),
-                   torch.empty(T, top_k, dtype=torch.float32, device=dev))
-    ws, nb = None, 0
+    if top_k < 1:
+        raise BinadeError("binade_moe_route", EINVAL)
+    out = MoeRoute(torch.empty((T, top_k), dtype=torch.int32, device=dev),
+                   torch.empty((T, top_k), dtype=torch.float32, device=dev))
+    ws, at, nb = None, None, 0
     if stats:
         out.counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
         out.prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
         out.loss = torch.empty(1, dtype=torch.float32, device=dev)
-        ws, nb = _scratch(int(lib().binade_moe_route_workspace_bytes(T, E)), workspace, dev)
-    _call("binade_moe_route", _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E,
-          top_k, int(bool(renormalize)), _ptr(valid), _ptr(out.idx), _ptr(out.weights),
-          _ptr(out.counts), _ptr(out.prob_sum), _ptr(out.loss), _ptr(ws), nb, _stream(stream))
+        ws, at, nb = _scratch(_entry("binade_moe_route_workspace_bytes")(T, E), workspace, dev)
+    _run("binade_moe_route", logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), T, E,
+         top_k, 1 if renormalize else 0, _addr(valid), out.idx.data_ptr(),
+         out.weights.data_ptr(), _addr(out.counts), _addr(out.prob_sum), _addr(out.loss), at, nb,
+         stream)
     return out
 
 
 @_on_device
-@_on_stream
 def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
                    dweights: torch.Tensor | None = None, counts: torch.Tensor | None = None,
                    dloss: torch.Tensor | None = None, renormalize: bool = True, out_dtype=None,
@@ -1058,7 +1091,7 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
     logits = _logits_arg(logits)
     dev = logits.device
     T, E = logits.shape
-    code = _dtype_code(logits.dtype if out_dtype is None else out_dtype)
+    code = _CODE[logits.dtype] if out_dtype is None else _dtype_code(out_dtype)
     if idx.dim() != 2:
         raise ValueError("idx: [n_tokens, top_k]")
     top_k = idx.shape[1]
@@ -1071,14 +1104,13 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
         counts = _arg("counts", counts, (torch.int32,), (E + 1,), dev)
         dloss = _arg("dloss", dloss.reshape(-1), (torch.float32,), (1,), dev)
     dlogits = _out_arg("dlogits", dlogits, _TORCH_DTYPE[code], (T, E), dev)
-    _call("binade_moe_route_grad", _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E,
-          top_k, int(bool(renormalize)), _ptr(idx), _ptr(dweights), _ptr(counts), _ptr(dloss),
-          _ptr(dlogits), code, E, _ptr(_status_arg(status, dev)), _stream(stream))
+    _run("binade_moe_route_grad", logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), T, E,
+         top_k, 1 if renormalize else 0, idx.data_ptr(), _addr(dweights), _addr(counts),
+         _addr(dloss), dlogits.data_ptr(), code, E, _status_arg(status, dev), stream)
     return dlogits
 
 
 @_on_device
-@_on_stream
 def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor, top_k: int,
                      out_dtype=torch.float32, need_dy: bool = True, stream=None):
     """binade_moe_combine_grad: (dy [T*top_k, N] or None, dweights fp32
@@ -1093,10 +1125,10 @@ def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor,
     if weights.numel() != T * top_k:
         raise ValueError("weights: n_tokens * top_k")
     w = _arg("weights", weights, (torch.float32,), weights.shape, dev)
-    dy = torch.empty(T * top_k, N, dtype=_TORCH_DTYPE[code], device=dev) if need_dy else None
+    dy = torch.empty((T * top_k, N), dtype=_TORCH_DTYPE[code], device=dev) if need_dy else None
     dw = torch.empty(weights.shape, dtype=torch.float32, device=dev)
-    _call("binade_moe_combine_grad", _ptr(y), _ptr(w), _ptr(dout), _dtype_code(dout.dtype), T,
-          top_k, N, _ptr(dy), code, _ptr(dw), _stream(stream))
+    _run("binade_moe_combine_grad", y.data_ptr(), w.data_ptr(), dout.data_ptr(),
+         _CODE[dout.dtype], T, top_k, N, _addr(dy), code, dw.data_ptr(), stream)
     return dy, dw
 
 
@@ -1111,30 +1143,26 @@ def _rows16(name: str, t: torch.Tensor, cols: int, device, m: int | None = None)
         raise ValueError(f"{name} is on {t.device}, not {device}")
     if t.stride(1) != 1 or t.stride(0) < cols or t.stride(0) % 8 or t.data_ptr() % 16:
         t = t.contiguous()
+        if t.data_ptr() % 16:           # a contiguous view that starts off 16 bytes
+            t = t.clone()
     return t
 
 
 def _lora_desc(a, b, scale, device):
+    """(descriptor, the tensors it points at)."""
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
         raise ValueError("a: [n_adapters, rank, K], b: [n_adapters, N, rank]")
     a = _arg("a", a, (torch.bfloat16,), a.shape, device)
     b = _arg("b", b, (torch.bfloat16,), b.shape, device)
-    d = LoraDesc()
-    d.n_adapters, d.rank, d.k = a.shape
-    d.n = b.shape[1]
-    d.a, d.b = a.data_ptr(), b.data_ptr()
+    n_adapters, rank, k = a.shape
+    at = None
     if scale is not None:
-        scale = _arg("scale", scale, (torch.float32,), (a.shape[0],), device)
-        d.scale = scale.data_ptr()
-    return d, (a, b, scale)
-
-
-def _lora_ids(ids, m, device):
-    return None if ids is None else _arg("ids", ids, (torch.int32,), (m,), device)
+        scale = _arg("scale", scale, (torch.float32,), (n_adapters,), device)
+        at = scale.data_ptr()
+    return LoraDesc(b.shape[1], k, rank, n_adapters, a.data_ptr(), b.data_ptr(), at), (a, b, scale)
 
 
 @_on_device
-@_on_stream
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor | None = None,
              base: torch.Tensor | None = None, scale: torch.Tensor | None = None,
              out_dtype=torch.float32, y: torch.Tensor | None = None, keep_h: bool = False,
@@ -1147,22 +1175,23 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
     code = _dtype_code(out_dtype)
     dev = x.device
     d, keep = _lora_desc(a, b, scale, dev)
-    x = _rows16("x", x, d.k, dev)
+    n, k, rank = d.n, d.k, d.rank
+    x = _rows16("x", x, k, dev)
     m = x.shape[0]
-    ids = _lora_ids(ids, m, dev)
+    if ids is not None:
+        ids = _arg("ids", ids, (torch.int32,), (m,), dev)
     if base is not None:
-        base = _arg("base", base, _FLOATS, (m, d.n), dev)
-    y = _out_arg("y", y, _TORCH_DTYPE[code], (m, d.n), dev)
-    h = torch.empty(m, d.rank, dtype=torch.float32, device=dev) if keep_h else None
-    ws, nb = _scratch(int(lib().binade_lora_workspace_bytes(m, d.n, d.k, d.rank)), workspace, dev)
-    _call("binade_lora_add", ctypes.byref(d), _ptr(x), m, x.stride(0), _ptr(ids), _ptr(base), d.n,
-          F32 if base is None else _dtype_code(base.dtype), _ptr(y), d.n, code, _ptr(h), _ptr(ws),
-          nb, _ptr(_status_arg(status, dev)), _stream(stream))
+        base = _arg("base", base, _FLOATS, (m, n), dev)
+    y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
+    h = torch.empty((m, rank), dtype=torch.float32, device=dev) if keep_h else None
+    ws, at, nb = _scratch(_entry("binade_lora_workspace_bytes")(m, n, k, rank), workspace, dev)
+    _run("binade_lora_add", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
+         _addr(base), n, F32 if base is None else _CODE[base.dtype], y.data_ptr(), n, code,
+         _addr(h), at, nb, _status_arg(status, dev), stream)
     return (y, h) if keep_h else y
 
 
 @_on_device
-@_on_stream
 def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor | None,
               dy: torch.Tensor, h: torch.Tensor | None = None, scale: torch.Tensor | None = None,
               dx_base: torch.Tensor | None = None, grad_dtype=torch.float32,
@@ -1175,21 +1204,23 @@ def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tens
     code = _dtype_code(grad_dtype)
     dev = x.device
     d, keep = _lora_desc(a, b, scale, dev)
-    x = _rows16("x", x, d.k, dev)
+    n, k, rank, n_adapters = d.n, d.k, d.rank, d.n_adapters
+    x = _rows16("x", x, k, dev)
     m = x.shape[0]
-    ids = _lora_ids(ids, m, dev)
-    dy = _arg("dy", dy, (torch.bfloat16,), (m, d.n), dev)
+    if ids is not None:
+        ids = _arg("ids", ids, (torch.int32,), (m,), dev)
+    dy = _arg("dy", dy, (torch.bfloat16,), (m, n), dev)
     if h is not None:
-        h = _arg("h", h, (torch.float32,), (m, d.rank), dev)
+        h = _arg("h", h, (torch.float32,), (m, rank), dev)
     if dx_base is not None:
-        dx_base = _rows16("dx_base", dx_base, d.k, dev, m)
-    dx = _out_arg("dx", dx, torch.bfloat16, (m, d.k), dev) if need_dx or dx is not None else None
-    da = torch.empty(d.n_adapters, d.rank, d.k, dtype=_TORCH_DTYPE[code], device=dev)
-    db = torch.empty(d.n_adapters, d.n, d.rank, dtype=_TORCH_DTYPE[code], device=dev)
-    ws, nb = _scratch(int(lib().binade_lora_grad_workspace_bytes(m, d.n, d.k, d.rank,
-                                                                 d.n_adapters)), workspace, dev)
-    _call("binade_lora_grad", ctypes.byref(d), _ptr(x), m, x.stride(0), _ptr(ids), _ptr(dy), d.n,
-          _ptr(h), _ptr(dx_base), 0 if dx_base is None else dx_base.stride(0), _ptr(dx), d.k,
-          _ptr(da), _ptr(db), code, _ptr(ws), nb, _ptr(_status_arg(status, dev)),
-          _stream(stream))
+        dx_base = _rows16("dx_base", dx_base, k, dev, m)
+    dx = _out_arg("dx", dx, torch.bfloat16, (m, k), dev) if need_dx or dx is not None else None
+    da = torch.empty((n_adapters, rank, k), dtype=_TORCH_DTYPE[code], device=dev)
+    db = torch.empty((n_adapters, n, rank), dtype=_TORCH_DTYPE[code], device=dev)
+    ws, at, nb = _scratch(_entry("binade_lora_grad_workspace_bytes")(m, n, k, rank, n_adapters),
+                          workspace, dev)
+    _run("binade_lora_grad", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
+         dy.data_ptr(), n, _addr(h), _addr(dx_base), 0 if dx_base is None else dx_base.stride(0),
+         _addr(dx), k, da.data_ptr(), db.data_ptr(), code, at, nb, _status_arg(status, dev),
+         stream)
     return dx, da, db
