@@ -750,8 +750,8 @@ void launch_expand(const ExpandArgs& s, hipStream_t st) {
 //    32 rows on (ids NULL: rows as they are);
 //  - turn_rows_kernel splits g and h of a tile of 32 sorted rows into three
 //    bf16 terms, as MFMA operands whose K is the rows;
-//  - outer_kernel: a wave has 128 columns of x or dy, up to 32 ranks and a
-//    range of tiles. A lane loads 8 columns of 8 rows and turns the 8 x 8
+//  - outer_kernel: a wave has 128 columns of x or dy, 16 ranks and a range of
+//    tiles. A lane loads 8 columns of 8 rows and turns the 8 x 8
 //    block with v_perm, which makes the operand whose K is the rows; sums stay
 //    in registers until the adapter changes. An adapter inside one range is
 //    written at once, one over several leaves a partial sum in each;
@@ -901,11 +901,11 @@ __global__ __launch_bounds__(64) void turn_rows_kernel(Order o, const float* g, 
 }
 
 struct OuterSide {
-  const uint16_t* s;       // rows [m][cols]
+  const uint16_t* s;       // rows [m][wide]
   const uint4* vt;         // turned g or h
   void* grad;
   float* part;             // [2 * splits][rank * cols]
-  int64_t ld, cols;
+  int64_t ld, cols, wide;  // wide: cols, or 8 where fewer (zeros behind them)
   int32_t blocks;          // of four waves, a split
 };
 
@@ -918,34 +918,55 @@ struct OuterArgs {
   bool grad_bf16;
 };
 
-template <int RT>
+// v moved down by n of its 8 elements (1..8), zeros behind.
+__device__ __forceinline__ uint4 shift8(uint4 v, int n) {
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+  uint32_t w[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    w[j] = 0;
+#pragma unroll
+    for (int q = 0; q + j < 4; ++q) w[j] = (n >> 1) == q ? d[q + j] : w[j];
+  }
+  if (n & 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (w[j] >> 16) | (w[j + 1] << 16);
+  }
+  return uint4{w[0], w[1], w[2], w[3]};
+}
+
+// A wave: 128 columns, 16 ranks, a split's tiles. A block's waves take the
+// rank chunks of the same columns side by side, so that these meet in the L1.
 __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
   const int32_t per = p.side[0].blocks + p.side[1].blocks;
   const int32_t split = blockIdx.x / per, at = blockIdx.x - split * per;
   const bool second = at >= p.side[0].blocks;
   const OuterSide& s = p.side[second ? 1 : 0];
-  // a block's waves: rank chunks of the same columns side by side
-  const int32_t chunks = (p.rank + 16 * RT - 1) / (16 * RT);
-  const int32_t job = (second ? at - p.side[0].blocks : at) * 4 + wave;
-  const int32_t chunk = job % chunks;
+  const int32_t chunks = (p.rank + 15) / 16;
+  const int32_t job = (second ? at - p.side[0].blocks : at) * 4 + wave, chunk = job % chunks;
   const int64_t col0 = static_cast<int64_t>(job / chunks) * 128;
   if (col0 >= s.cols) return;
-  const int32_t rts = (p.rank + 15) / 16, rt0 = chunk * RT;
-  const int64_t col = col0 + 8 * i, left = s.cols - col;
-  const bool whole = col0 + 128 <= s.cols;
+  const bool whole = col0 + 128 <= s.wide;
+  // a row's last piece is loaded as its last 8 columns and moved down
+  const int64_t col = col0 + 8 * i, over = col + 8 - s.wide;
+  const int shift = over <= 0 ? 0 : over < 8 ? static_cast<int>(over) : 8;
+  const uint16_t* from = s.s + (over <= 0 ? col : s.wide - 8);
   const int32_t begin = split * p.per_split, n_tiles = first_tile(p.o, p.n_adapters);
   const int32_t end = begin + p.per_split < n_tiles ? begin + p.per_split : n_tiles;
   if (begin >= end) return;
 
-  floatx4 acc[8][RT];
+  floatx4 acc[8];
   const auto clear = [&]() {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[c][r] = floatx4{0, 0, 0, 0};
+    for (int c = 0; c < 8; ++c) acc[c] = floatx4{0, 0, 0, 0};
   };
   const auto flush = [&](int32_t a) {
+    // the compiler would compute every address here ahead of the loop and hold
+    // them through it, at the cost of the occupancy
+    int32_t own = lane;
+    asm volatile("" : "+v"(own));
+    const int i = own & 15, g = own >> 4;
     const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
     const bool direct = s0 >= begin && s1 <= begin + p.per_split;
     const int64_t size = p.rank * s.cols;
@@ -953,39 +974,35 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
     void* to = direct ? s.grad : static_cast<void*>(s.part);
     const int64_t base = direct ? a * size : (2 * split + (s0 < begin ? 0 : 1)) * size;
     const bool bf16 = direct && p.grad_bf16;
+    const int32_t rank = 16 * chunk + i;
+    if (rank >= p.rank) return;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int32_t rank = 16 * (rt0 + r) + i;
-      if (rank >= p.rank) continue;
+    for (int q = 0; q < 4; ++q) {
+      const int64_t cc = col0 + 8 * (4 * g + q);
+      if (!second) {
+        if (cc >= s.cols) continue;
+        const int64_t e = base + rank * s.cols + cc;
+        if (bf16) {
+          uint32_t d[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t cc = col0 + 8 * (4 * g + q);
-        if (!second) {
-          if (cc >= s.cols) continue;
-          const int64_t e = base + rank * s.cols + cc;
-          if (bf16) {
-            uint32_t d[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              d[c] = pack_bf16(f * acc[2 * c][r][q], f * acc[2 * c + 1][r][q]);
-            __builtin_memcpy(static_cast<uint16_t*>(to) + e, d, 16);
-          } else {
-            float d[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) d[c] = f * acc[c][r][q];
-            __builtin_memcpy(static_cast<float*>(to) + e, d, 32);
-          }
+          for (int c = 0; c < 4; ++c) d[c] = pack_bf16(f * acc[2 * c][q], f * acc[2 * c + 1][q]);
+          __builtin_memcpy(static_cast<uint16_t*>(to) + e, d, 16);
         } else {
+          float d[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (cc + c < s.cols)
-              store_any(to, base + (cc + c) * p.rank + rank, bf16, f * acc[c][r][q]);
+          for (int c = 0; c < 8; ++c) d[c] = f * acc[c][q];
+          __builtin_memcpy(static_cast<float*>(to) + e, d, 32);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (cc + c < s.cols) store_any(to, base + (cc + c) * p.rank + rank, bf16, f * acc[c][q]);
       }
     }
   };
 
-  uint4 next[8];
+  uint4 next[8], vt[3];
+  bool gap = false;
   const auto load = [&](int32_t tile) {
     int32_t t[8];
     if (p.o.perm != nullptr) {
@@ -997,59 +1014,60 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
         t[j] = row < p.m ? static_cast<int32_t>(row) : -1;
       }
     }
-    if (whole) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        next[j] = load8(s.s + (t[j] < 0 ? 0 : t[j]) * s.ld + col);
-    } else {
+    for (int j = 0; j < 8; ++j) next[j] = load8(from + (t[j] < 0 ? 0 : t[j]) * s.ld);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        next[j] = load8_part(s.s + (t[j] < 0 ? 0 : t[j]) * s.ld + col, left);
-    }
-    bool gap = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) gap |= t[j] < 0;
-    if (__ballot(gap) != 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (t[j] < 0) next[j] = uint4{0, 0, 0, 0};
-    }
+    for (int k = 0; k < 3; ++k)
+      vt[k] = s.vt[((static_cast<int64_t>(tile) * chunks + chunk) * 3 + k) * 64 + lane];
+    // a tile's rows fill it from the front: only its last ones can be missing
+    gap = __ballot(t[7] < 0) != 0;
   };
   clear();
   int32_t a = p.o.perm != nullptr ? uniform(p.o.adapter[begin]) : 0;
   load(begin);
 #pragma unroll 1
   for (int32_t tile = begin; tile < end; ++tile) {
-    uint4 now[8], st[8], vt[RT][3];
+    if (!whole && shift != 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) now[j] = next[j];
+      for (int j = 0; j < 8; ++j) next[j] = shift8(next[j], shift);
+    }
+    if (gap) {
+      const int64_t at0 = static_cast<int64_t>(tile) * kRowTile + 8 * g;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        const int32_t rt = rt0 + r < rts ? rt0 + r : rts - 1;
-        vt[r][t] = s.vt[((static_cast<int64_t>(tile) * rts + rt) * 3 + t) * 64 + lane];
+      for (int j = 0; j < 8; ++j) {
+        const bool in = p.o.perm != nullptr ? p.o.perm[at0 + j] >= 0 : at0 + j < p.m;
+        if (!in) next[j] = uint4{0, 0, 0, 0};
       }
+    }
+    uint4 st[8], v[3];
+    turn_block(next, st);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = vt[k];
     int32_t a_next = a;
     if (tile + 1 < end) {
       load(tile + 1);
       if (p.o.perm != nullptr) a_next = uniform(p.o.adapter[tile + 1]);
     }
-    turn_block(now, st);
 #pragma unroll
     for (int t = 0; t < 3; ++t)
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(vt[r][t]),
-                                                              acc[c][r], 0, 0, 0);
+      for (int c = 0; c < 8; ++c)
+        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(v[t]), acc[c],
+                                                         0, 0, 0);
     if (a_next != a || tile + 1 == end) {
       flush(a);
       clear();
       a = a_next;
     }
   }
+}
+
+// dy with fewer than 8 columns, zeros behind them.
+__global__ __launch_bounds__(256) void widen_kernel(const uint16_t* from, int64_t ld, int64_t cols,
+                                                    int64_t m, uint16_t* to) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= 8 * m) return;
+  to[e] = e % 8 < cols ? from[e / 8 * ld + e % 8] : static_cast<uint16_t>(0);
 }
 
 // Four values of a gradient a thread; blockIdx.y: adapter.
@@ -1084,13 +1102,12 @@ __global__ __launch_bounds__(256) void reduce_kernel(OuterArgs p) {
 // Sizes and places of a backward call's workspace.
 struct GradPlan {
   int64_t tiles, n_pad;
-  int32_t splits, per_split, chunk_tiles;
-  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, gt, ht, outer, bytes;
+  int32_t splits, per_split;
+  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, gt, ht, wide, outer, bytes;
   GradPlan(int64_t m, int64_t n, int64_t k, int32_t rank, int32_t n_adapters) {
     tiles = (m + kRowTile - 1) / kRowTile + n_adapters;   // at most
     n_pad = (n + 31) / 32 * 32;
-    chunk_tiles = rank <= 16 ? 1 : 2;
-    const int64_t chunks = (rank + 16 * chunk_tiles - 1) / (16 * chunk_tiles);
+    const int64_t chunks = (rank + 15) / 16;
     const int64_t jobs = ((n + 127) / 128 + (k + 127) / 128) * chunks;
     // enough waves to fill the chip, at least two tiles each
     int64_t want = (kOuterWaves + jobs - 1) / jobs;
@@ -1112,12 +1129,15 @@ struct GradPlan {
     part = place(many_rows(m, k) ? 0 : shrink_parts(m, k, n) * m * rank * 4);
     g = place(m * rank * 4);
     h = place(m * rank * 4);
-    const int64_t rts = (rank + 15) / 16;
-    gt = place(tiles * rts * 3 * 1024);
-    ht = place(tiles * rts * 3 * 1024);
+    gt = place(tiles * chunks * 3 * 1024);
+    ht = place(tiles * chunks * 3 * 1024);
+    wide = place(n < 8 ? m * 16 : 0);
     outer = place(2ll * splits * rank * (n + k) * 4);
   }
-  static constexpr int64_t kOuterWaves = 2048;
+  #ifndef OUTER_WAVES
+#define OUTER_WAVES 2048
+#endif
+  static constexpr int64_t kOuterWaves = OUTER_WAVES;
 };
 
 // Row strides: 12 rows of fp32 stay below 2^31 bytes (32-bit lane offsets).
@@ -1233,12 +1253,20 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   outer.n_adapters = p.n_adapters;
   outer.per_split = plan.per_split;
   outer.grad_bf16 = grad_dtype == BINADE_BF16;
-  const int64_t chunks = (p.rank + 16 * plan.chunk_tiles - 1) / (16 * plan.chunk_tiles);
+  const int64_t chunks = (p.rank + 15) / 16;
   const auto side_blocks = [&](int64_t cols) {
     return static_cast<int32_t>(((cols + 127) / 128 * chunks + 3) / 4);
   };
-  outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, side_blocks(p.k)};
-  outer.side[1] = OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, side_blocks(p.n)};
+  if (m > 0 && p.n < 8) {
+    uint16_t* wide = reinterpret_cast<uint16_t*>(ws + plan.wide);
+    hipLaunchKernelGGL(widen_kernel, dim3(static_cast<uint32_t>((8 * m + 255) / 256)), dim3(256), 0,
+                       st, dy, ld_dy, p.n, m, wide);
+    dy = wide;
+    ld_dy = 8;
+  }
+  outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, p.k, side_blocks(p.k)};
+  outer.side[1] =
+      OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, p.n < 8 ? 8 : p.n, side_blocks(p.n)};
   if (m > 0) {
     if (ids != nullptr) {
       hipLaunchKernelGGL(order_kernel, dim3(p.n_adapters), dim3(512), 0, st, p, ints(plan.perm),
@@ -1283,9 +1311,8 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
                                dx_base == nullptr ? 0 : 2, true},
                     st);
     }
-    const int64_t rts = (p.rank + 15) / 16;
     const int64_t tiles = ids != nullptr ? plan.tiles : o.tiles;
-    hipLaunchKernelGGL(turn_rows_kernel, dim3(static_cast<uint32_t>(tiles * 2 * rts)), dim3(64), 0,
+    hipLaunchKernelGGL(turn_rows_kernel, dim3(static_cast<uint32_t>(tiles * 2 * chunks)), dim3(64), 0,
                        st, o, floats(plan.g), h, pieces(plan.gt), pieces(plan.ht), m, p.rank,
                        p.n_adapters);
     outer.side[0].vt = pieces(plan.gt);
@@ -1295,10 +1322,7 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     outer.o = o;
     const uint32_t blocks =
         static_cast<uint32_t>(plan.splits * (outer.side[0].blocks + outer.side[1].blocks));
-    if (plan.chunk_tiles == 1)
-      hipLaunchKernelGGL(outer_kernel<1>, dim3(blocks), dim3(256), 0, st, outer);
-    else
-      hipLaunchKernelGGL(outer_kernel<2>, dim3(blocks), dim3(256), 0, st, outer);
+    hipLaunchKernelGGL(outer_kernel, dim3(blocks), dim3(256), 0, st, outer);
   }
   outer.o = o;
   hipLaunchKernelGGL(reduce_kernel,
