@@ -308,6 +308,7 @@ struct ExpandArgs {
   int32_t parts;           // of the first product: 1, 8 or its slices
   int32_t base_kind;       // 0 none, 1 fp32, 2 bf16
   bool y_bf16;
+  int32_t tiles;           // many rows: row tiles of a block
 };
 
 // The sum of a value's partial sums in the order of the first product, four
@@ -528,7 +529,6 @@ __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs s) {
   finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base, mine, scale);
 }
 
-constexpr int kManyTiles = 8;    // row tiles of a block
 constexpr int kManyCols = 4;     // columns of a lane
 
 // A wave's 64 rows of B (its columns' ranks) in LDS: 16-byte piece o of column
@@ -571,7 +571,7 @@ __device__ __forceinline__ void stage_b(const LoraArgs& p, int32_t a, int64_t wa
 template <int KS, int BK, int YK>
 __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) void expand_many_kernel(ExpandArgs s) {
   const LoraArgs& p = s.p;
-  constexpr int CT = kManyCols, MT = kManyTiles;
+  constexpr int CT = kManyCols;
   __shared__ BTile<KS, CT> tiles_b[4];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
   const uint32_t col_blocks = static_cast<uint32_t>((p.n + 64 * CT - 1) / (64 * CT));
@@ -581,12 +581,13 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) v
   // 64, 16 adapters, 3840 -> 15360)
   const uint32_t unit = blockIdx.x;
   const uint32_t block_row = unit / col_blocks;
-  const int64_t tile0 = static_cast<int64_t>(block_row) * MT;
+  const int64_t tile0 = static_cast<int64_t>(block_row) * s.tiles;
   const int64_t wave_col =
       (static_cast<int64_t>(unit - block_row * col_blocks) * 4 + wave) * (16 * CT);
   if (tile0 * 16 >= p.m || wave_col >= p.n) return;
   const bool full = wave_col + CT * i + CT <= p.n;
-  const int32_t live = static_cast<int32_t>(p.m - tile0 * 16 < 16 * MT ? p.m - tile0 * 16 : 16 * MT);
+  const int32_t live =
+      static_cast<int32_t>(p.m - tile0 * 16 < 16 * s.tiles ? p.m - tile0 * 16 : 16 * s.tiles);
   const int32_t per = p.rank / 8;
   const int32_t mask = (per & (per - 1)) == 0 ? (per < 8 ? per : 8) - 1 : 0;
   const int32_t shift = per >= 8 ? 0 : per == 4 ? 2 : 0;
@@ -711,16 +712,21 @@ void launch_shrink(const ShrinkArgs& s, hipStream_t st) {
 }
 
 template <int KS, int BK, int YK>
-void launch_expand_shape(const ExpandArgs& s, hipStream_t st) {
+void launch_expand_shape(ExpandArgs s, hipStream_t st) {
   const int64_t m = s.p.m, n = s.p.n;
-  if (s.frag != nullptr)
+  if (s.frag != nullptr) {
+    // up to eight tiles a block while the blocks fill the chip: 2048 rows, 4096
+    // columns, rank 16: 26 us with eight, 19 with two
+    const int64_t tiles = (m + 15) / 16, cols = (n + 64 * kManyCols - 1) / (64 * kManyCols);
+    s.tiles = 8;
+    while (s.tiles > 1 && (tiles + s.tiles - 1) / s.tiles * cols < 768) s.tiles /= 2;
     hipLaunchKernelGGL((expand_many_kernel<KS, BK, YK>),
-                       dim3(static_cast<uint32_t>((n + 64 * kManyCols - 1) / (64 * kManyCols) *
-                                                  ((m + 16 * kManyTiles - 1) / (16 * kManyTiles)))),
+                       dim3(static_cast<uint32_t>(cols * ((tiles + s.tiles - 1) / s.tiles))),
                        dim3(256), 0, st, s);
-  else
+  } else {
     hipLaunchKernelGGL((expand_few_kernel<KS, BK, YK>),
                        xcd_grid((n + 127) / 128 * ((m + 15) / 16)), dim3(256), 0, st, s);
+  }
 }
 
 template <int KS>
@@ -746,20 +752,20 @@ void launch_expand(const ExpandArgs& s, hipStream_t st) {
 // With Bt and At, B and A turned round (a small copy), the two products of
 // the forward give g = Bt dy and dx = dx_base + s At g. What is new is the
 // sum over rows, dA = s g^T x and dB = s h^T dy:
-//  - order_kernel sorts the rows by adapter, each adapter's from a multiple of
-//    32 rows on (ids NULL: rows as they are);
-//  - turn_rows_kernel splits g and h of a tile of 32 sorted rows into three
-//    bf16 terms, as MFMA operands whose K is the rows;
+//  - prepare_kernel makes Bt and At and sorts the rows by adapter, each
+//    adapter's from a multiple of 32 rows on (ids NULL: rows as they are);
 //  - outer_kernel: a wave has 128 columns of x or dy, 16 ranks and a range of
 //    tiles. A lane loads 8 columns of 8 rows and turns the 8 x 8
-//    block with v_perm, which makes the operand whose K is the rows; sums stay
-//    in registers until the adapter changes. An adapter inside one range is
+//    block with v_perm, which makes the operand whose K is the rows; the other
+//    operand is g or h of these rows in three bf16 terms; sums stay in
+//    registers until the adapter changes. An adapter inside one range is
 //    written at once, one over several leaves a partial sum in each;
 //  - reduce_kernel adds those in range order and writes zeros for adapters
-//    without rows.
+//    without rows. Few rows (a matter of launches) do without it: there a wave
+//    has all tiles of one adapter.
 // Rows of another adapter never meet in one MFMA chain.
 constexpr int kRowTile = 32;           // sorted rows of a tile
-constexpr int kMaxSorted = 4096;    // adapters order_kernel counts in LDS
+constexpr int kMaxSorted = 4096;    // adapters prepare_kernel counts in LDS
 
 struct TurnArgs {
   const uint16_t* from;
@@ -785,12 +791,15 @@ __device__ __forceinline__ void turn_block(const uint4 (&v)[8], uint4 (&t)[8]) {
   }
 }
 
-__global__ __launch_bounds__(256) void turn_kernel(TurnArgs b, TurnArgs a) {
-  // B's blocks in order of rows (stores coalesced), A's in order of columns
-  const int64_t nb = b.n_adapters * (b.rows_pad / 8) * (b.cols / 8);
-  const int64_t na = a.n_adapters * (a.rows_pad / 8) * (a.cols / 8);
-  int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= nb + na) return;
+// Blocks of 8 x 8, one a thread: B's in order of rows (stores coalesced), A's
+// in order of columns.
+__device__ __forceinline__ int64_t turn_count(const TurnArgs& p) {
+  return p.n_adapters * (p.rows_pad / 8) * (p.cols / 8);
+}
+
+__device__ __forceinline__ void turn_matrices(const TurnArgs& b, const TurnArgs& a, int64_t e) {
+  const int64_t nb = turn_count(b);
+  if (e >= nb + turn_count(a)) return;
   const bool first = e < nb;
   const TurnArgs& p = first ? b : a;
   if (!first) e -= nb;
@@ -821,13 +830,12 @@ __device__ __forceinline__ int32_t first_tile(const Order& o, int32_t a) {
   return o.perm != nullptr ? o.tile0[a] : a == 0 ? 0 : o.tiles;
 }
 
-// Block a collects the rows of adapter a in rising order, behind the tiles of
-// the adapters before it.
-__global__ __launch_bounds__(512) void order_kernel(LoraArgs p, int32_t* perm, int32_t* adapter,
-                                                    int32_t* tile0) {
+// A block of 512 collects the rows of adapter a in rising order, behind the
+// tiles of the adapters before it.
+__device__ void order_rows(const LoraArgs& p, int32_t a, int32_t* perm, int32_t* adapter,
+                           int32_t* tile0) {
   __shared__ int32_t counts[kMaxSorted];
   __shared__ int32_t sums[8];
-  const int32_t a = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int32_t e = threadIdx.x; e <= a && e < p.n_adapters; e += 512) counts[e] = 0;
   __syncthreads();
@@ -875,34 +883,9 @@ __global__ __launch_bounds__(512) void order_kernel(LoraArgs p, int32_t* perm, i
   }
 }
 
-// g and h of each tile as operands [tile][rank tile][3][64]: lane (rank i,
-// rows 8 g ..). One wave per (vector, tile, rank tile).
-__global__ __launch_bounds__(64) void turn_rows_kernel(Order o, const float* g, const float* h,
-                                                       uint4* gt, uint4* ht, int64_t m,
-                                                       int32_t rank, int32_t n_adapters) {
-  const int32_t rts = (rank + 15) / 16;
-  const int64_t tile = blockIdx.x / (2 * rts);
-  const int32_t which = blockIdx.x / rts % 2, rt = blockIdx.x % rts;
-  if (tile >= first_tile(o, n_adapters)) return;
-  const int lane = threadIdx.x, i = lane & 15, q = lane >> 4;
-  const float* v = which ? h : g;
-  const int32_t r = 16 * rt + i;
-  uint16_t d[3][8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    int64_t t = tile * kRowTile + 8 * q + j;
-    if (o.perm != nullptr) t = o.perm[t];
-    const float f = t >= 0 && t < m && r < rank ? v[t * rank + r] : 0.0f;
-    split3(f, d[0][j], d[1][j], d[2][j]);
-  }
-  uint4* to = (which ? ht : gt) + (tile * rts + rt) * 3 * 64 + lane;
-#pragma unroll
-  for (int t3 = 0; t3 < 3; ++t3) to[64 * t3] = __builtin_bit_cast(uint4, d[t3]);
-}
-
 struct OuterSide {
   const uint16_t* s;       // rows [m][wide]
-  const uint4* vt;         // turned g or h
+  const float* v;          // g or h, [m][rank]
   void* grad;
   float* part;             // [2 * splits][rank * cols]
   int64_t ld, cols, wide;  // wide: cols, or 8 where fewer (zeros behind them)
@@ -940,38 +923,46 @@ __device__ __forceinline__ uint4 shift8(uint4 v, int n) {
 __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
   const int32_t per = p.side[0].blocks + p.side[1].blocks;
+  // a range of tiles, or an adapter
   const int32_t split = blockIdx.x / per, at = blockIdx.x - split * per;
   const bool second = at >= p.side[0].blocks;
-  const OuterSide& s = p.side[second ? 1 : 0];
+  // picked one by one: through an indexed struct the compiler would lose that
+  // the pointers are global ones, and wait for every load (flat) at once
+  const uint16_t* const rows_in = second ? p.side[1].s : p.side[0].s;
+  const float* const vectors = second ? p.side[1].v : p.side[0].v;
+  const int64_t ld = second ? p.side[1].ld : p.side[0].ld;
+  const int64_t cols = second ? p.side[1].cols : p.side[0].cols;
+  const int64_t wide = second ? p.side[1].wide : p.side[0].wide;
   const int32_t chunks = (p.rank + 15) / 16;
   const int32_t job = (second ? at - p.side[0].blocks : at) * 4 + wave, chunk = job % chunks;
   const int64_t col0 = static_cast<int64_t>(job / chunks) * 128;
-  if (col0 >= s.cols) return;
-  const bool whole = col0 + 128 <= s.wide;
+  if (col0 >= cols) return;
+  const bool whole = col0 + 128 <= wide;
   // a row's last piece is loaded as its last 8 columns and moved down
-  const int64_t col = col0 + 8 * i, over = col + 8 - s.wide;
+  const int64_t col = col0 + 8 * i, over = col + 8 - wide;
   const int shift = over <= 0 ? 0 : over < 8 ? static_cast<int>(over) : 8;
-  const uint16_t* from = s.s + (over <= 0 ? col : s.wide - 8);
-  const int32_t begin = split * p.per_split, n_tiles = first_tile(p.o, p.n_adapters);
-  const int32_t end = begin + p.per_split < n_tiles ? begin + p.per_split : n_tiles;
-  if (begin >= end) return;
+  const uint16_t* from = rows_in + (over <= 0 ? col : wide - 8);
+  const bool by_adapter = p.per_split == 0;
+  const int32_t n_tiles = first_tile(p.o, p.n_adapters);
+  const int32_t begin = by_adapter ? first_tile(p.o, split) : split * p.per_split;
+  const int32_t end = by_adapter                        ? first_tile(p.o, split + 1)
+                      : begin + p.per_split < n_tiles ? begin + p.per_split
+                                                        : n_tiles;
+  if (begin >= end && !by_adapter) return;
 
   floatx4 acc[8];
-  const auto clear = [&]() {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = floatx4{0, 0, 0, 0};
-  };
-  const auto flush = [&](int32_t a) {
-    // the compiler would compute every address here ahead of the loop and hold
-    // them through it, at the cost of the occupancy
+  const auto flush = [&](int32_t a) __attribute__((always_inline)) {
+    // kept from being computed ahead of the loop and held through it
     int32_t own = lane;
     asm volatile("" : "+v"(own));
     const int i = own & 15, g = own >> 4;
     const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
-    const bool direct = s0 >= begin && s1 <= begin + p.per_split;
-    const int64_t size = p.rank * s.cols;
+    const bool direct = by_adapter || (s0 >= begin && s1 <= begin + p.per_split);
+    const int64_t size = p.rank * cols;
     const float f = !direct || p.scale == nullptr ? 1.0f : p.scale[a];
-    void* to = direct ? s.grad : static_cast<void*>(s.part);
+    void* const grad = second ? p.side[1].grad : p.side[0].grad;
+    float* const part = second ? p.side[1].part : p.side[0].part;
+    void* to = direct ? grad : static_cast<void*>(part);
     const int64_t base = direct ? a * size : (2 * split + (s0 < begin ? 0 : 1)) * size;
     const bool bf16 = direct && p.grad_bf16;
     const int32_t rank = 16 * chunk + i;
@@ -980,8 +971,8 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
     for (int q = 0; q < 4; ++q) {
       const int64_t cc = col0 + 8 * (4 * g + q);
       if (!second) {
-        if (cc >= s.cols) continue;
-        const int64_t e = base + rank * s.cols + cc;
+        if (cc >= cols) continue;
+        const int64_t e = base + rank * cols + cc;
         if (bf16) {
           uint32_t d[4];
 #pragma unroll
@@ -996,70 +987,115 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (cc + c < s.cols) store_any(to, base + (cc + c) * p.rank + rank, bf16, f * acc[c][q]);
+          if (cc + c < cols) store_any(to, base + (cc + c) * p.rank + rank, bf16, f * acc[c][q]);
       }
     }
   };
 
-  uint4 next[8], vt[3];
-  bool gap = false;
-  const auto load = [&](int32_t tile) {
-    int32_t t[8];
-    if (p.o.perm != nullptr) {
-      __builtin_memcpy(t, p.o.perm + static_cast<int64_t>(tile) * kRowTile + 8 * g, 32);
-    } else {
+  // One adapter's tiles at a time. Two tiles are on their way while one is
+  // multiplied, and the rows of the one to be requested next are known (their
+  // numbers are a load of their own, sent before the tile's: loads return in
+  // order). Every request is made, the last tile's again behind the end: a
+  // conditional one would leave the compiler to wait for all loads instead of
+  // the oldest ones.
+  const int32_t my_rank = 16 * chunk + i < p.rank ? 16 * chunk + i : p.rank - 1;
+  int32_t tile = begin;
+  do {
+    const int32_t a = by_adapter ? split : p.o.perm != nullptr ? uniform(p.o.adapter[tile]) : 0;
+    const int32_t a_end = by_adapter ? end : first_tile(p.o, a + 1), stop = a_end < end ? a_end : end;
+    uint4 in0[8], in1[8];
+    float v0[8], v1[8];
+    int32_t rows[8], miss0, miss1;
+    const auto find = [&](int32_t t) __attribute__((always_inline)) {
+      t = t < stop ? t : stop - 1;
+      if (p.o.perm != nullptr) {
+        const int4* at = reinterpret_cast<const int4*>(p.o.perm + static_cast<int64_t>(t) * kRowTile +
+                                                       8 * g);
+        const int4 lo = at[0], hi = at[1];
+        rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
+        rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t row = static_cast<int64_t>(t) * kRowTile + 8 * g + j;
+          rows[j] = row < p.m ? static_cast<int32_t>(row) : -1;
+        }
+      }
+    };
+    // the rows found last, then the search for those of tile after
+    const auto request = [&](int32_t after, uint4 (&to)[8], float (&v)[8],
+                             int32_t& mask) __attribute__((always_inline)) {
+      int32_t now[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) now[j] = rows[j];
+      find(after);
+      mask = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t row = static_cast<int64_t>(tile) * kRowTile + 8 * g + j;
-        t[j] = row < p.m ? static_cast<int32_t>(row) : -1;
+        const int64_t row = now[j] < 0 ? 0 : now[j];
+        mask |= now[j] < 0 ? 1 << j : 0;
+        to[j] = load8(from + row * ld);
+        v[j] = vectors[row * p.rank + my_rank];
       }
-    }
+    };
+    const auto multiply = [&](int32_t t, uint4 (&in)[8], float (&vi)[8],
+                              int32_t& mask) __attribute__((always_inline)) {
+      if (!whole && shift != 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) next[j] = load8(from + (t[j] < 0 ? 0 : t[j]) * s.ld);
+        for (int j = 0; j < 8; ++j) in[j] = shift8(in[j], shift);
+      }
+      if (__ballot(mask != 0) != 0) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      vt[k] = s.vt[((static_cast<int64_t>(tile) * chunks + chunk) * 3 + k) * 64 + lane];
-    // a tile's rows fill it from the front: only its last ones can be missing
-    gap = __ballot(t[7] < 0) != 0;
-  };
-  clear();
-  int32_t a = p.o.perm != nullptr ? uniform(p.o.adapter[begin]) : 0;
-  load(begin);
+        for (int j = 0; j < 8; ++j)
+          if (mask >> j & 1) in[j] = uint4{0, 0, 0, 0}, vi[j] = 0.0f;
+      }
+      uint4 st[8], v[3];
+      turn_block(in, st);
+      uint16_t d[3][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split3(vi[j], d[0][j], d[1][j], d[2][j]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[k] = __builtin_bit_cast(uint4, d[k]);
+      request(t + 3, in, vi, mask);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(v[q]),
+                                                           acc[c], 0, 0, 0);
+    };
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = floatx4{0, 0, 0, 0};
+    if (tile < stop) {
+      find(tile);
+      request(tile + 1, in0, v0, miss0);
+      request(tile + 2, in1, v1, miss1);
 #pragma unroll 1
-  for (int32_t tile = begin; tile < end; ++tile) {
-    if (!whole && shift != 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) next[j] = shift8(next[j], shift);
-    }
-    if (gap) {
-      const int64_t at0 = static_cast<int64_t>(tile) * kRowTile + 8 * g;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = p.o.perm != nullptr ? p.o.perm[at0 + j] >= 0 : at0 + j < p.m;
-        if (!in) next[j] = uint4{0, 0, 0, 0};
+      for (; tile < stop; tile += 2) {
+        multiply(tile, in0, v0, miss0);
+        if (tile + 1 < stop) multiply(tile + 1, in1, v1, miss1);
       }
+      tile = stop;
     }
-    uint4 st[8], v[3];
-    turn_block(next, st);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = vt[k];
-    int32_t a_next = a;
-    if (tile + 1 < end) {
-      load(tile + 1);
-      if (p.o.perm != nullptr) a_next = uniform(p.o.adapter[tile + 1]);
-    }
-#pragma unroll
-    for (int t = 0; t < 3; ++t)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(v[t]), acc[c],
-                                                         0, 0, 0);
-    if (a_next != a || tile + 1 == end) {
-      flush(a);
-      clear();
-      a = a_next;
-    }
-  }
+    flush(a);   // an adapter without rows: zeros
+  } while (tile < end);
+}
+
+// The first sort_blocks blocks: sorted rows of an adapter each; the others:
+// Bt and At.
+struct PrepareArgs {
+  LoraArgs p;
+  TurnArgs tb, ta;
+  int32_t *perm, *adapter, *tile0;
+  int32_t sort_blocks;
+};
+
+__global__ __launch_bounds__(512) void prepare_kernel(PrepareArgs s) {
+  const int32_t at = blockIdx.x;
+  if (at < s.sort_blocks)
+    order_rows(s.p, at, s.perm, s.adapter, s.tile0);
+  else
+    turn_matrices(s.tb, s.ta, static_cast<int64_t>(at - s.sort_blocks) * 512 + threadIdx.x);
 }
 
 // dy with fewer than 8 columns, zeros behind them.
@@ -1103,17 +1139,25 @@ __global__ __launch_bounds__(256) void reduce_kernel(OuterArgs p) {
 struct GradPlan {
   int64_t tiles, n_pad;
   int32_t splits, per_split;
-  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, gt, ht, wide, outer, bytes;
+  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, wide, outer, bytes;
   GradPlan(int64_t m, int64_t n, int64_t k, int32_t rank, int32_t n_adapters) {
-    tiles = (m + kRowTile - 1) / kRowTile + n_adapters;   // at most
+    tiles = (m + kRowTile - 1) / kRowTile + (m < n_adapters ? m : n_adapters);   // at most
+    if (tiles < 1) tiles = 1;
     n_pad = (n + 31) / 32 * 32;
     const int64_t chunks = (rank + 15) / 16;
     const int64_t jobs = ((n + 127) / 128 + (k + 127) / 128) * chunks;
-    // enough waves to fill the chip, at least two tiles each
+    // enough waves to fill the chip, at least four tiles each
     int64_t want = (kOuterWaves + jobs - 1) / jobs;
-    if (want > (tiles + 1) / 2) want = (tiles + 1) / 2;
+    if (want > tiles / 4) want = tiles / 4;
+    if (want < 1) want = 1;
     per_split = static_cast<int32_t>((tiles + want - 1) / want);
     splits = static_cast<int32_t>((tiles + per_split - 1) / per_split);
+    // by adapter (per_split 0) while an adapter's tiles are few: 977 rows of 25
+    // adapters 62 us by range, 54 by adapter
+    if (m <= (n_adapters >= 4 ? 1024 : 512)) {
+      per_split = 0;
+      splits = n_adapters;
+    }
     bytes = 0;
     const auto place = [&](int64_t size) {
       const int64_t start = bytes;
@@ -1129,15 +1173,10 @@ struct GradPlan {
     part = place(many_rows(m, k) ? 0 : shrink_parts(m, k, n) * m * rank * 4);
     g = place(m * rank * 4);
     h = place(m * rank * 4);
-    gt = place(tiles * chunks * 3 * 1024);
-    ht = place(tiles * chunks * 3 * 1024);
     wide = place(n < 8 ? m * 16 : 0);
-    outer = place(2ll * splits * rank * (n + k) * 4);
+    outer = place(per_split > 0 ? 2ll * splits * rank * (n + k) * 4 : 0);
   }
-  #ifndef OUTER_WAVES
-#define OUTER_WAVES 2048
-#endif
-  static constexpr int64_t kOuterWaves = OUTER_WAVES;
+    static constexpr int64_t kOuterWaves = 2048;
 };
 
 // Row strides: 12 rows of fp32 stay below 2^31 bytes (32-bit lane offsets).
@@ -1207,7 +1246,7 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
                        st);
   launch_expand(ExpandArgs{p, part, frag, base, y, h, ld_base, ldy, parts,
                            base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
-                           y_dtype == BINADE_BF16},
+                           y_dtype == BINADE_BF16, 0},
                 st);
   return launch_status();
 }
@@ -1267,23 +1306,29 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, p.k, side_blocks(p.k)};
   outer.side[1] =
       OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, p.n < 8 ? 8 : p.n, side_blocks(p.n)};
+  // without ids only adapter 0 is read
+  const int32_t used = m == 0 ? 0 : ids != nullptr ? p.n_adapters : 1;
+  uint16_t* bt = reinterpret_cast<uint16_t*>(ws + plan.bt);
+  uint16_t* at = reinterpret_cast<uint16_t*>(ws + plan.at);
+  PrepareArgs pre{};
+  pre.p = p;
+  pre.tb = TurnArgs{p.b, bt, p.n, p.rank, plan.n_pad, used};
+  pre.ta = TurnArgs{p.a, at, p.rank, p.k, p.rank, dx != nullptr ? used : 0};
+  if (m > 0 && ids != nullptr) {
+    pre.perm = ints(plan.perm);
+    pre.adapter = ints(plan.adapter);
+    pre.tile0 = ints(plan.tile0);
+    pre.sort_blocks = p.n_adapters;
+    o.perm = pre.perm;
+    o.adapter = pre.adapter;
+    o.tile0 = pre.tile0;
+  }
+  const int64_t turns =
+      (pre.tb.n_adapters * plan.n_pad + pre.ta.n_adapters * p.k) / 8 * (p.rank / 8);
+  const uint32_t prepare_blocks = pre.sort_blocks + static_cast<uint32_t>((turns + 511) / 512);
+  if (m > 0)
+    hipLaunchKernelGGL(prepare_kernel, dim3(prepare_blocks), dim3(512), 0, st, pre);
   if (m > 0) {
-    if (ids != nullptr) {
-      hipLaunchKernelGGL(order_kernel, dim3(p.n_adapters), dim3(512), 0, st, p, ints(plan.perm),
-                         ints(plan.adapter), ints(plan.tile0));
-      o.perm = ints(plan.perm);
-      o.adapter = ints(plan.adapter);
-      o.tile0 = ints(plan.tile0);
-    }
-    // without ids only adapter 0 is read
-    const int32_t used = ids != nullptr ? p.n_adapters : 1;
-    uint16_t* bt = reinterpret_cast<uint16_t*>(ws + plan.bt);
-    uint16_t* at = reinterpret_cast<uint16_t*>(ws + plan.at);
-    const TurnArgs tb{p.b, bt, p.n, p.rank, plan.n_pad, used};
-    const TurnArgs ta{p.a, at, p.rank, p.k, p.rank, dx != nullptr ? used : 0};
-    const int64_t turns = (tb.n_adapters * plan.n_pad + ta.n_adapters * p.k) / 8 * (p.rank / 8);
-    hipLaunchKernelGGL(turn_kernel, dim3(static_cast<uint32_t>((turns + 255) / 256)), dim3(256), 0,
-                       st, tb, ta);
     if (h == nullptr) {
       launch_shrink<false>(ShrinkArgs{p, x, nullptr, floats(plan.h), pieces(plan.frag), ldx, p.k,
                                       slices_of(p.k), 1},
@@ -1308,26 +1353,22 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
       launch_expand(ExpandArgs{px, whole ? nullptr : floats(plan.part),
                                whole ? pieces(plan.frag) : nullptr, dx_base, dx,
                                whole ? nullptr : floats(plan.g), ld_dx_base, ld_dx, parts,
-                               dx_base == nullptr ? 0 : 2, true},
+                               dx_base == nullptr ? 0 : 2, true, 0},
                     st);
     }
-    const int64_t tiles = ids != nullptr ? plan.tiles : o.tiles;
-    hipLaunchKernelGGL(turn_rows_kernel, dim3(static_cast<uint32_t>(tiles * 2 * chunks)), dim3(64), 0,
-                       st, o, floats(plan.g), h, pieces(plan.gt), pieces(plan.ht), m, p.rank,
-                       p.n_adapters);
-    outer.side[0].vt = pieces(plan.gt);
-    outer.side[1].vt = pieces(plan.ht);
+    outer.side[0].v = floats(plan.g);
+    outer.side[1].v = h;
     outer.side[0].part = floats(plan.outer);
     outer.side[1].part = floats(plan.outer) + 2ll * plan.splits * p.rank * p.k;
-    outer.o = o;
-    const uint32_t blocks =
-        static_cast<uint32_t>(plan.splits * (outer.side[0].blocks + outer.side[1].blocks));
-    hipLaunchKernelGGL(outer_kernel, dim3(blocks), dim3(256), 0, st, outer);
   }
   outer.o = o;
-  hipLaunchKernelGGL(reduce_kernel,
-                     dim3(static_cast<uint32_t>((p.rank * (p.n + p.k) / 4 + 255) / 256),
-                          static_cast<uint32_t>(p.n_adapters)),
-                     dim3(256), 0, st, outer);
+  const uint32_t blocks =
+      static_cast<uint32_t>(plan.splits * (outer.side[0].blocks + outer.side[1].blocks));
+  hipLaunchKernelGGL(outer_kernel, dim3(blocks), dim3(256), 0, st, outer);
+  if (plan.per_split > 0)
+    hipLaunchKernelGGL(reduce_kernel,
+                       dim3(static_cast<uint32_t>((p.rank * (p.n + p.k) / 4 + 255) / 256),
+                            static_cast<uint32_t>(p.n_adapters)),
+                       dim3(256), 0, st, outer);
   return launch_status();
 }
