@@ -110,6 +110,13 @@ __device__ __forceinline__ uint16_t to_bf16_rne(float f) {
   return static_cast<uint16_t>((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
+// Two fp32 values rounded to bf16, nearest-even, packed (gfx950 converts).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float float2v __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{a, b}), bf16x2));
+}
+
 // Escape patch: replace exponent byte `idx & 3` of dword `idx >> 2` of E[8].
 // idx is wave-uniform; a switch keeps every E[q] in its own register (an
 // indexed form would put E in scratch memory).

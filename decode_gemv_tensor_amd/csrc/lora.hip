@@ -70,13 +70,6 @@ __device__ __forceinline__ uint4 load8_part(const uint16_t* p, int64_t left) {
   return __builtin_bit_cast(uint4, v);
 }
 
-// Two fp32 values rounded to bf16, nearest-even, packed (gfx950 converts).
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  typedef float float2v __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{a, b}), bf16x2));
-}
-
 // v = hi + mid + lo exactly, each a bf16 (8 significant bits by truncation):
 // fp32 values enter a bf16 MFMA as three terms and lose nothing. Infinity
 // and NaN stay in hi alone.
@@ -1146,8 +1139,8 @@ struct GradPlan {
     n_pad = (n + 31) / 32 * 32;
     const int64_t chunks = (rank + 15) / 16;
     const int64_t jobs = ((n + 127) / 128 + (k + 127) / 128) * chunks;
-    // enough waves to fill the chip, at least four tiles each
-    int64_t want = (kOuterWaves + jobs - 1) / jobs;
+    // as many waves as the chip holds at once, at least four tiles each
+    int64_t want = kOuterWaves / jobs;
     if (want > tiles / 4) want = tiles / 4;
     if (want < 1) want = 1;
     per_split = static_cast<int32_t>((tiles + want - 1) / want);

@@ -116,8 +116,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const
           uint32_t o[2];
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            o[q] = to_bf16_rne(w[s] * d[2 * q]) |
-                   (static_cast<uint32_t>(to_bf16_rne(w[s] * d[2 * q + 1])) << 16);
+            o[q] = pack_bf16(w[s] * d[2 * q], w[s] * d[2 * q + 1]);
           __builtin_memcpy(static_cast<uint16_t*>(dy) + at, o, 8);
         } else {
           const float o[4] = {w[s] * d[0], w[s] * d[1], w[s] * d[2], w[s] * d[3]};

@@ -107,18 +107,74 @@ __device__ __forceinline__ Key group_max_key(Key v) {
   return v;
 }
 
+// ------------------------------------------------------------------ logits
+// V logits of a row from expert e0 on, as they are; -inf behind the last
+// expert. vec: rows and their length are whole 16-byte pieces.
+template <int V, bool kBf16>
+struct Logits {
+  uint32_t d[kBf16 ? V / 2 : V];
+
+  __device__ __forceinline__ void load(const void* p, int64_t row, int32_t e0, int32_t n, bool vec) {
+    constexpr int kPiece = kBf16 ? 4 : 8;   // dwords of 8 logits
+    constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+    if (vec) {
+#pragma unroll
+      for (int b = 0; b < V / 8; ++b) {
+        const int64_t at = row + (e0 + 8 * b < n ? e0 + 8 * b : 0);
+        const void* from = kBf16 ? static_cast<const void*>(static_cast<const uint16_t*>(p) + at)
+                                 : static_cast<const void*>(static_cast<const float*>(p) + at);
+        __builtin_memcpy(&d[kPiece * b], __builtin_assume_aligned(from, 16), 4 * kPiece);
+      }
+#pragma unroll
+      for (int b = 0; b < V / 8; ++b)
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j)
+          d[kPiece * b + j] = e0 + 8 * b < n ? d[kPiece * b + j] : kNone;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int64_t at = row + (e0 + j < n ? e0 + j : 0);
+        if (kBf16) {
+          const uint32_t u = e0 + j < n ? static_cast<const uint16_t*>(p)[at] : kNone & 0xFFFFu;
+          d[j / 2] = j & 1 ? d[j / 2] | (u << 16) : u;
+        } else {
+          d[j] = e0 + j < n ? static_cast<const uint32_t*>(p)[at] : kNone;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ float value(int j) const {
+    return kBf16 ? (j & 1 ? bf16_hi(d[j / 2]) : bf16_lo(d[j / 2])) : __uint_as_float(d[j]);
+  }
+};
+
 // -------------------------------------------------------------------- keys
-// Ordered form of a logit's bits: rising with the value, -0 as +0; -inf and
-// NaN of either sign lie outside (kLow, kHigh].
+// Ordered form of a logit's bits: rising with the value, -0 as +0 (for a
+// negative one the two's complement of its bits); -inf and NaN of either sign
+// lie outside (kLow, kHigh].
 struct KeyBf16 {
   typedef uint32_t Key;
   static constexpr uint32_t kLow = 0x0080u, kHigh = 0xFF80u;   // of -inf, of +inf
-  static __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t u = __float_as_uint(v) >> 16;
-    return u & 0x8000u ? 0x10000u - u : u + 0x8000u;
-  }
-  static __device__ __forceinline__ Key make(uint32_t o, uint32_t e) {
-    return (o << 16) | (0xFFFFu - e);
+  template <int V, bool kClean>
+  static __device__ __forceinline__ void make(const Logits<V, true>& x, int32_t e0, Key (&key)[V]) {
+    typedef short short2v __attribute__((ext_vector_type(2)));
+    typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+    const uint32_t last = 0xFFFFu - static_cast<uint32_t>(e0);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {   // two at a time
+      const uint32_t neg = __builtin_bit_cast(uint32_t, __builtin_bit_cast(short2v, x.d[j]) >> 15);
+      const uint32_t add = (neg & 0x00010001u) | (~neg & 0x80008000u);
+      const uint32_t o = __builtin_bit_cast(
+          uint32_t, __builtin_bit_cast(ushort2v, x.d[j] ^ neg) + __builtin_bit_cast(ushort2v, add));
+      uint32_t lo = o << 16, hi = o & 0xFFFF0000u;
+      if (kClean) {
+        lo = lo > (kHigh << 16) ? 0u : lo;
+        hi = hi > (kHigh << 16) ? 0u : hi;
+      }
+      key[2 * j] = lo | (last - 2 * j);
+      key[2 * j + 1] = hi | (last - 2 * j - 1);
+    }
   }
   static __device__ __forceinline__ uint32_t order_of(Key k) { return k >> 16; }
   static __device__ __forceinline__ int32_t expert(Key k) {
@@ -133,12 +189,16 @@ struct KeyBf16 {
 struct KeyF32 {
   typedef uint64_t Key;
   static constexpr uint32_t kLow = 0x00800000u, kHigh = 0xFF800000u;
-  static __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t u = __float_as_uint(v);
-    return u & 0x80000000u ? 0u - u : u + 0x80000000u;
-  }
-  static __device__ __forceinline__ Key make(uint32_t o, uint32_t e) {
-    return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - e);
+  template <int V, bool kClean>
+  static __device__ __forceinline__ void make(const Logits<V, false>& x, int32_t e0,
+                                              Key (&key)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t neg = static_cast<uint32_t>(static_cast<int32_t>(x.d[j]) >> 31);
+      uint32_t o = (x.d[j] ^ neg) + ((neg & 1u) | (~neg & 0x80000000u));
+      if (kClean) o = o > kHigh ? 0u : o;
+      key[j] = (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e0 + j));
+    }
   }
   static __device__ __forceinline__ uint32_t order_of(Key k) {
     return static_cast<uint32_t>(k >> 32);
@@ -209,48 +269,10 @@ __device__ __forceinline__ void best8(const Key (&key)[V], Key (&best)[8]) {
 }
 
 // ------------------------------------------------------------------ values
-// exp(d) for d <= 0, or NaN: 2^(d log2 e) with what the product d log2 e
-// loses put back, two steps off at most; 0 below -150.
+// exp(d) for d <= 0 (-inf: 0), or NaN. The product's rounding costs |d| 2^-24
+// of the value, as much as that of the difference d itself.
 __device__ __forceinline__ float exp_of(float d) {
-  constexpr float kL = 1.44269502e+0f, kLlo = 1.92596303e-8f, kLn2 = 0.693147182f;
-  d = d < -150.0f ? -150.0f : d;
-  const float t = d * kL;
-  const float r = __builtin_fmaf(d, kLlo, __builtin_fmaf(d, kL, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r * kLn2, e);
-}
-
-// V logits from expert e0 on as fp32; -inf behind the last expert. vec: rows
-// and their length are whole 16-byte pieces.
-template <int V, bool kBf16>
-__device__ __forceinline__ void load_logits(const void* p, int64_t row, int32_t e0, int32_t n,
-                                            bool vec, float (&v)[V]) {
-  if (vec) {
-#pragma unroll
-    for (int b = 0; b < V / 8; ++b) {
-      const bool in = e0 + 8 * b < n;
-      const int64_t at = row + (in ? e0 + 8 * b : 0);
-      if (kBf16) {
-        const uint4 d = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[8 * b + 2 * j] = bf16_lo(w[j]), v[8 * b + 2 * j + 1] = bf16_hi(w[j]);
-      } else {
-        __builtin_memcpy(&v[8 * b], __builtin_assume_aligned(static_cast<const float*>(p) + at, 16), 32);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * b + j] = in ? v[8 * b + j] : -__builtin_inff();
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int64_t at = row + (e0 + j < n ? e0 + j : 0);
-      const float f = kBf16 ? __uint_as_float(static_cast<uint32_t>(
-                                  static_cast<const uint16_t*>(p)[at]) << 16)
-                            : static_cast<const float*>(p)[at];
-      v[j] = e0 + j < n ? f : -__builtin_inff();
-    }
-  }
+  return __builtin_amdgcn_exp2f(d * 1.44269502e+0f);
 }
 
 // ----------------------------------------------------------------- forward
@@ -310,18 +332,10 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
     const int64_t t = t0 + lane / G;
     const bool in = t < p.n_tokens;
     const bool valid = in && (p.valid == nullptr || p.valid[t] != 0);
-    float v[V];
-    load_logits<V, kBf16>(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec, v);
+    Logits<V, kBf16> x;
+    x.load(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec);
     Key key[V], best[8];
-    // NaN above +inf is rare: looked for once the best key is known
-    bool nan_rows = false;
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        uint32_t o = K::ordered(v[j]);
-        if (nan_rows && o > K::kHigh) o = 0;
-        key[j] = K::make(o, e0 + j);
-      }
+    const auto choose = [&]() __attribute__((always_inline)) {
       if (kSort) {
         best8<G, V>(key, best);
       } else {
@@ -330,22 +344,32 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
         for (int j = 1; j < V; ++j) best[0] = key[j] > best[0] ? key[j] : best[0];
         best[0] = group_max_key<G>(best[0]);
       }
-      nan_rows = __ballot(K::order_of(best[0]) > K::kHigh) != 0;
-      if (!nan_rows) break;
+    };
+    K::template make<V, false>(x, e0, key);
+    choose();
+    // NaN above +inf is rare: seen by the best key, and left out then
+    if (__ballot(K::order_of(best[0]) > K::kHigh) != 0) {
+      K::template make<V, true>(x, e0, key);
+      choose();
     }
     const bool counted = valid && K::order_of(best[0]) > K::kLow;
     const float top = K::value(best[0]);
-    float total = 0.0f;
+    float v[V], total = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = exp_of(v[j] - top);
+      v[j] = exp_of(x.value(j) - top);
       total += v[j];
     }
     total = group_sum<G>(total);
     const float inv = 1.0f / total;
     if (stats) {
+      if (__ballot(!counted) == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) sums[j] += counted ? v[j] * inv : 0.0f;
+        for (int j = 0; j < V; ++j) sums[j] = __builtin_fmaf(v[j], inv, sums[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sums[j] = counted ? __builtin_fmaf(v[j], inv, sums[j]) : sums[j];
+      }
       if (counted && l == 0) atomicAdd(&counts[p.n_experts], 1);
     }
     // lane l of the group: slots l, l + G, ... of the row
@@ -453,10 +477,27 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
   int32_t c = 0;
   float s = 0.0f;
   if (e < p.n_experts) {
-#pragma unroll 8
-    for (int32_t b = lane; b < blocks; b += lanes) {
-      c += p.part_counts[static_cast<int64_t>(b) * (p.n_experts + 1) + e];
-      s += p.part_prob[static_cast<int64_t>(b) * p.n_experts + e];
+    constexpr int kAhead = 16;   // rows of partial sums on their way at once
+    const int32_t* pc = p.part_counts + e;
+    const float* pp = p.part_prob + e;
+    int32_t b = lane;
+    for (; b + (kAhead - 1) * lanes < blocks; b += kAhead * lanes) {
+      int32_t cs[kAhead];
+      float ss[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        cs[j] = pc[static_cast<int64_t>(b + j * lanes) * (p.n_experts + 1)];
+        ss[j] = pp[static_cast<int64_t>(b + j * lanes) * p.n_experts];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        c += cs[j];
+        s += ss[j];
+      }
+    }
+    for (; b < blocks; b += lanes) {
+      c += pc[static_cast<int64_t>(b) * (p.n_experts + 1)];
+      s += pp[static_cast<int64_t>(b) * p.n_experts];
     }
   }
   count_s[threadIdx.x] = c;
@@ -522,8 +563,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
        t0 += step) {
     const int64_t t = t0 + lane / G;
     const bool in = t < p.n_tokens;
-    float v[V];
-    load_logits<V, kBf16>(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec, v);
+    Logits<V, kBf16> x;
+    x.load(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec);
     bool counted = false;
     const auto slots = [&](auto use) {
       for (int32_t s = l; s < p.top_k; s += G) {
@@ -541,14 +582,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
     });
     wave_sync();
     counted = (__ballot(counted) >> (lane & ~(G - 1)) & 1u) != 0;
-    float top = v[0];
+    float v[V], top = x.value(0);
 #pragma unroll
-    for (int j = 1; j < V; ++j) top = fmaxf(top, v[j]);
+    for (int j = 1; j < V; ++j) top = fmaxf(top, x.value(j));
     top = group_max<G>(top);
     float total = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = exp_of(v[j] - top);
+      v[j] = exp_of(x.value(j) - top);
       total += v[j];
     }
     const float inv = 1.0f / group_sum<G>(total);
@@ -590,8 +631,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
           uint32_t d[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            d[j] = to_bf16_rne(v[8 * b + 2 * j]) |
-                   (static_cast<uint32_t>(to_bf16_rne(v[8 * b + 2 * j + 1])) << 16);
+            d[j] = pack_bf16(v[8 * b + 2 * j], v[8 * b + 2 * j + 1]);
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dlogits) + row + e) =
               uint4{d[0], d[1], d[2], d[3]};
         } else {

@@ -4,9 +4,10 @@ against their formulas in 64 bits.
 
 Choices, counts and flags have to be equal. u = 2^-24. A weight is a
 quotient of an exponential and a sum: exp of a difference d of fp32 logits is
-off by |d| u (the difference's rounding, |d| below 104 where exp is not 0) and
-two steps for the function, the sum adds a tree of at most 16 + 6 levels, the
-quotients one step each: 32 u + |d| u relative. Gradients subtract a mean:
+off by 2 |d| u (the rounding of the difference and that of its product with
+log2 e) and two steps for the function, the sum adds a tree of at most 16 + 6
+levels, the quotients one step each: for |d| up to 26, which logits of the
+scale drawn here (2) stay under, within 32 u + |d| u relative. Gradients subtract a mean:
 they are held to their row's largest term, 64 u + |d| u of it."""
 import ctypes
 import math
