@@ -286,24 +286,28 @@ struct RouteArgs {
   float* loss;
   int32_t* part_counts;   // [blocks, n_experts + 1]
   float* part_prob;       // [blocks, n_experts]
+  float* part_loss;       // [16] of route_stats_kernel's blocks
+  uint32_t* ticket;       // of the same: which block is the last
   int64_t ld, n_tokens;
   int32_t n_experts, top_k;
   bool renorm, vec;
 };
 
-// loss = E / (k R R) * sum over e of counts[e] * prob_sum[e]: each thread its
-// term, added by a fixed tree. All threads of a block of whole waves.
-__device__ __forceinline__ void store_loss(float term, int32_t rows, int32_t n_experts,
-                                           int32_t top_k, float* red, float* loss) {
-  const float r = static_cast<float>(rows > 0 ? rows : 1);
-  const float part = group_sum<64>(term / (static_cast<float>(top_k) * r) / r);
+// The sum of a block's values by a fixed tree, in thread 0. Whole waves.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  const float part = group_sum<64>(v);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = part;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float l = 0.0f;
-    for (uint32_t w = 0; w < blockDim.x / 64; ++w) l += red[w];
-    loss[0] = static_cast<float>(n_experts) * l;
-  }
+  float sum = 0.0f;
+  if (threadIdx.x == 0)
+    for (uint32_t w = 0; w < blockDim.x / 64; ++w) sum += red[w];
+  return sum;
+}
+
+// An expert's share of the loss but for the factor E.
+__device__ __forceinline__ float loss_term(int32_t count, float prob, int32_t rows, int32_t top_k) {
+  const float r = static_cast<float>(rows > 0 ? rows : 1);
+  return static_cast<float>(count) / (static_cast<float>(top_k) * r) * (prob / r);
 }
 
 template <int G, int V, typename K, bool kSort>
@@ -451,28 +455,32 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
     float s = 0.0f;
     for (int w = 0; w < waves; ++w) s += prob[w][e];
     (alone ? p.prob_sum : p.part_prob + static_cast<int64_t>(blockIdx.x) * p.n_experts)[e] = s;
-    term += static_cast<float>(counts[e]) * s;
+    term += loss_term(counts[e], s, counts[p.n_experts], p.top_k);
   }
-  if (alone) store_loss(term, counts[p.n_experts], p.n_experts, p.top_k, red, p.loss);
+  if (alone) {
+    term = block_sum(term, red);
+    if (threadIdx.x == 0) p.loss[0] = static_cast<float>(p.n_experts) * term;
+  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.ticket = 0;
+  }
 }
 
-// Adds the blocks' partial counts and sums. One block of 1024: n_experts
-// padded to a power of two of threads side by side, the rest over the blocks;
-// both in a fixed order.
-__global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t blocks,
-                                                           int32_t width_log2) {
-  __shared__ int32_t count_s[1024];
-  __shared__ float sum_s[1024];
+// Adds the blocks' partial counts and sums: a block has 64 experts side by
+// side and 16 rows of partial sums at a time, in a fixed order. The last block
+// to end adds the blocks' shares of the loss, in block order.
+__global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t blocks) {
+  __shared__ int32_t count_s[16][64];
+  __shared__ float sum_s[16][64];
   __shared__ float red[16];
   __shared__ int32_t rows_s;
-  const int32_t width = 1 << width_log2, e = threadIdx.x & (width - 1);
-  const int32_t lane = threadIdx.x >> width_log2, lanes = 1024 >> width_log2;
-  int32_t rows = 0;
-  if (threadIdx.x < 64) {
-    for (int32_t b = threadIdx.x; b < blocks; b += 64)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t e = blockIdx.x * 64 + lane;
+  if (wave == 0) {
+    int32_t rows = 0;
+    for (int32_t b = lane; b < blocks; b += 64)
       rows += p.part_counts[static_cast<int64_t>(b) * (p.n_experts + 1) + p.n_experts];
     for (int s = 32; s >= 1; s >>= 1) rows += __shfl_xor(rows, s, 64);
-    if (threadIdx.x == 0) rows_s = rows;
+    if (lane == 0) rows_s = rows;
   }
   int32_t c = 0;
   float s = 0.0f;
@@ -480,14 +488,14 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
     constexpr int kAhead = 16;   // rows of partial sums on their way at once
     const int32_t* pc = p.part_counts + e;
     const float* pp = p.part_prob + e;
-    int32_t b = lane;
-    for (; b + (kAhead - 1) * lanes < blocks; b += kAhead * lanes) {
+    int32_t b = wave;
+    for (; b + (kAhead - 1) * 16 < blocks; b += kAhead * 16) {
       int32_t cs[kAhead];
       float ss[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        cs[j] = pc[static_cast<int64_t>(b + j * lanes) * (p.n_experts + 1)];
-        ss[j] = pp[static_cast<int64_t>(b + j * lanes) * p.n_experts];
+        cs[j] = pc[static_cast<int64_t>(b + j * 16) * (p.n_experts + 1)];
+        ss[j] = pp[static_cast<int64_t>(b + j * 16) * p.n_experts];
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -495,26 +503,38 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
         s += ss[j];
       }
     }
-    for (; b < blocks; b += lanes) {
+#pragma unroll 4
+    for (; b < blocks; b += 16) {
       c += pc[static_cast<int64_t>(b) * (p.n_experts + 1)];
       s += pp[static_cast<int64_t>(b) * p.n_experts];
     }
   }
-  count_s[threadIdx.x] = c;
-  sum_s[threadIdx.x] = s;
+  count_s[wave][lane] = c;
+  sum_s[wave][lane] = s;
   __syncthreads();
   float term = 0.0f;
-  if (lane == 0 && e < p.n_experts) {
-    for (int32_t q = 1; q < lanes; ++q) {
-      c += count_s[q * width + e];
-      s += sum_s[q * width + e];
+  if (wave == 0 && e < p.n_experts) {
+    for (int q = 1; q < 16; ++q) {
+      c += count_s[q][lane];
+      s += sum_s[q][lane];
     }
     p.counts[e] = c;
     p.prob_sum[e] = s;
-    term = static_cast<float>(c) * s;
+    term = loss_term(c, s, rows_s, p.top_k);
   }
-  if (threadIdx.x == 0) p.counts[p.n_experts] = rows_s;
-  store_loss(term, rows_s, p.n_experts, p.top_k, red, p.loss);
+  term = block_sum(term, red);
+  if (threadIdx.x != 0) return;
+  if (blockIdx.x == 0) p.counts[p.n_experts] = rows_s;
+  if (gridDim.x > 1) {
+    p.part_loss[blockIdx.x] = term;
+    __threadfence();
+    if (atomicAdd(p.ticket, 1u) != gridDim.x - 1) return;
+    __threadfence();
+    term = 0.0f;
+    for (uint32_t b = 0; b < gridDim.x; ++b)
+      term += __hip_atomic_load(p.part_loss + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  p.loss[0] = static_cast<float>(p.n_experts) * term;
 }
 
 // ---------------------------------------------------------------- backward
@@ -725,8 +745,8 @@ using namespace binade;
 extern "C" int64_t binade_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts) {
   if (!route_sizes_ok(n_tokens, n_experts)) return 0;
   // fp32 rows take at least as many lanes as bf16 ones
-  return static_cast<int64_t>(route_shape(n_tokens, n_experts, false).blocks) *
-         (2 * n_experts + 1) * 4;
+  return 128 + static_cast<int64_t>(route_shape(n_tokens, n_experts, false).blocks) *
+                   (2 * n_experts + 1) * 4;
 }
 
 extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t ld, int64_t n_tokens,
@@ -758,7 +778,9 @@ extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t l
   p.counts = counts;
   p.prob_sum = prob_sum;
   p.loss = loss;
-  p.part_counts = static_cast<int32_t*>(workspace);
+  p.ticket = static_cast<uint32_t*>(workspace);
+  p.part_loss = static_cast<float*>(workspace) + 16;
+  p.part_counts = static_cast<int32_t*>(workspace) + 32;
   p.part_prob = reinterpret_cast<float*>(p.part_counts + static_cast<int64_t>(shape.blocks) *
                                                              (n_experts + 1));
   p.ld = ld;
@@ -770,10 +792,8 @@ extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t l
   const hipStream_t st = static_cast<hipStream_t>(stream);
   launch_route_experts(p, shape, dtype == BINADE_BF16, st);
   if (stats && shape.blocks > 1) {
-    int32_t width_log2 = 0;
-    while ((1 << width_log2) < n_experts) ++width_log2;
-    hipLaunchKernelGGL(route_stats_kernel, dim3(1), dim3(1024), 0, st, p,
-                       static_cast<int32_t>(shape.blocks), width_log2);
+    hipLaunchKernelGGL(route_stats_kernel, dim3(static_cast<uint32_t>((n_experts + 63) / 64)),
+                       dim3(1024), 0, st, p, static_cast<int32_t>(shape.blocks));
   }
   return launch_status();
 }
