@@ -138,48 +138,37 @@ __device__ __forceinline__ void turn(uint4 (&v)[N], uint4* lds, int lane) {
   wave_sync();
 }
 
-// kAny: rows of x at any 2-byte alignment and of any length (gradients of an
-// odd number of outputs); otherwise 16-byte aligned, a multiple of 32.
+// The sums of a tile of 16 rows over slices first, first + step, ...: lane
+// (i, g) gets rank 16 r + i of rows 4 g + q in mine[r][q] (zeros without
+// adapter). With deal > 0 the tile's adapters are dealt to that many waves;
+// the result's bits say which rows this wave holds. id: of row row0 + i, -1
+// behind the last. kAny: rows of x at any 2-byte alignment and of any length
+// (gradients of an odd number of outputs); otherwise 16-byte aligned, a
+// multiple of 32.
 template <int RT, bool kAny>
-__global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
+__device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t row0, int32_t id,
+                                                int32_t first, int32_t step, int32_t deal,
+                                                int wave, int lane, uint4* stage,
+                                                floatx4 (&mine)[RT]) {
   const LoraArgs& p = s.p;
-  constexpr int kSumLd = 16 * RT + 4;
-  __shared__ union {
-    uint4 stage[kStreams][512];
-    float sums[kStreams][16][kSumLd];
-  } lds;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  // units: slice (or running sum) major, tiles of 16 rows minor
-  const int64_t tiles = (p.m + 15) / 16, unit = xcd_unit();
-  if (unit >= tiles * s.parts) return;
-  const int32_t part = static_cast<int32_t>(unit / tiles);
-  const int64_t tile = unit - part * tiles, row0 = tile * 16;
-  const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
-  const int32_t id = row0 + i < p.m ? adapter_of(p, row) : -1;
-  if (part == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
-      row0 + i < p.m && p.ids[row] != -1)
-    atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
-  const bool whole = s.frag != nullptr;
-  const int32_t first = whole ? wave : part;
-  const int32_t step = whole || s.parts < s.slices ? kStreams : s.slices;
+  const int i = lane & 15, g = lane >> 4;
   int32_t idq[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64);
-  floatx4 mine[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) mine[r] = floatx4{0, 0, 0, 0};
+  const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
   // as loaded: row lane / 4, columns 8 (lane % 4) on
   const int64_t lrow = row0 + (lane >> 2) < p.m ? row0 + (lane >> 2) : p.m - 1;
   const uint16_t* xl = s.x + lrow * s.ldx + 8 * (lane & 3);
   const uint16_t* xr = s.x + row * s.ldx + 8 * g;
-  uint4* stage = lds.stage[wave];
   uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
-  uint32_t got = wave == 0 ? 0xFFFFu & ~todo : 0u;   // rows whose sums this wave holds
+  uint32_t got = wave == 0 ? 0xFFFFu & ~todo : 0u;
   for (int32_t nth = 0; todo != 0; ++nth) {
     const int32_t a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
     const uint32_t match = static_cast<uint32_t>(__ballot(id == a)) & 0xFFFFu;
     todo &= ~match;
-    if (!whole && nth % static_cast<int32_t>(blockDim.x >> 6) != wave) continue;
+    if (deal > 0 && nth % deal != wave) continue;
     got |= match;
     const uint16_t* aa = p.a + static_cast<int64_t>(a) * p.rank * p.k;
     const auto rank_row = [&](int r) { return r < p.rank ? r : p.rank - 1; };
@@ -239,6 +228,35 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
       for (int q = 0; q < 4; ++q)
         if (idq[q] == a) mine[r][q] = sum[r][q];
   }
+  return got;
+}
+
+template <int RT, bool kAny>
+__global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
+  const LoraArgs& p = s.p;
+  constexpr int kSumLd = 16 * RT + 4;
+  __shared__ union {
+    uint4 stage[kStreams][512];
+    float sums[kStreams][16][kSumLd];
+  } lds;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  // units: slice (or running sum) major, tiles of 16 rows minor
+  const int64_t tiles = (p.m + 15) / 16, unit = xcd_unit();
+  if (unit >= tiles * s.parts) return;
+  const int32_t part = static_cast<int32_t>(unit / tiles);
+  const int64_t tile = unit - part * tiles, row0 = tile * 16;
+  const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
+  const int32_t id = row0 + i < p.m ? adapter_of(p, row) : -1;
+  if (part == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
+      row0 + i < p.m && p.ids[row] != -1)
+    atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+  const bool whole = s.frag != nullptr;
+  const int32_t first = whole ? wave : part;
+  const int32_t step = whole || s.parts < s.slices ? kStreams : s.slices;
+  floatx4 mine[RT];
+  const uint32_t got =
+      shrink_rows<RT, kAny>(s, row0, id, first, step, whole ? 0 : blockDim.x >> 6, wave, lane,
+                            lds.stage[wave], mine);
   if (!whole) {
     float* out = s.out + part * p.m * p.rank;
 #pragma unroll
@@ -305,19 +323,21 @@ struct ExpandArgs {
 };
 
 // The sum of a value's partial sums in the order of the first product, four
-// ranks at a time: at is the first of parts partials, next apart.
-__device__ __forceinline__ floatx4 join_parts(const float* at, int64_t next, int32_t parts) {
-  floatx4 v{0, 0, 0, 0};
-  constexpr int kAhead = 4;
-  floatx4 sum[kStreams];
+// ranks at a time, by two neighbouring lanes: the even one adds the running
+// sums 0 to 3, the odd one goes on with 4 to 7 and has the result. at: the
+// first of parts partials, next apart.
+__device__ __forceinline__ floatx4 join_parts(const float* at, int64_t next, int32_t parts,
+                                              int half) {
+  constexpr int kAhead = 4, kHalf = kStreams / 2;
+  floatx4 sum[kHalf];
 #pragma unroll
-  for (int w = 0; w < kStreams; ++w) sum[w] = floatx4{0, 0, 0, 0};
-  for (int32_t c = 0; c < parts; c += kAhead * kStreams) {
-    floatx4 d[kAhead][kStreams];
+  for (int w = 0; w < kHalf; ++w) sum[w] = floatx4{0, 0, 0, 0};
+  for (int32_t c = kHalf * half; c < parts; c += kAhead * kStreams) {
+    floatx4 d[kAhead][kHalf];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-      for (int w = 0; w < kStreams; ++w) {
+      for (int w = 0; w < kHalf; ++w) {
         const int32_t q = c + j * kStreams + w;
         d[j][w] = floatx4{0, 0, 0, 0};
         if (q < parts) d[j][w] = *reinterpret_cast<const floatx4*>(at + q * next);
@@ -325,10 +345,18 @@ __device__ __forceinline__ floatx4 join_parts(const float* at, int64_t next, int
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-      for (int w = 0; w < kStreams; ++w) sum[w] += d[j][w];
+      for (int w = 0; w < kHalf; ++w) sum[w] += d[j][w];
   }
+  floatx4 v{0, 0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < kStreams; ++w) v += sum[w];
+  for (int w = 0; w < kHalf; ++w) v += sum[w];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    float o = __shfl_xor(v[r], 1, 64);
+#pragma unroll
+    for (int w = 0; w < kHalf; ++w) o += sum[w][r];
+    v[r] = o;
+  }
   return v;
 }
 
@@ -437,6 +465,79 @@ __device__ __forceinline__ void load_b(const LoraArgs& p, int32_t a, int64_t wav
   }
 }
 
+// A few-rows wave's products: 16 rows, h split in LDS, up to kBatch adapters'
+// operands at once, so that a mixed tile waits for memory once per batch. The
+// first batch is requested by begin(), ahead of h.
+template <int KS, int CT>
+struct FewRows {
+  static constexpr int kBatch = KS <= 2 ? 4 : 2;
+  int32_t a[kBatch];
+  uint4 bf[kBatch][KS][CT];
+  uint64_t todo;
+
+  __device__ __forceinline__ void request(const LoraArgs& p, int32_t id, int64_t wave_col,
+                                          int lane) {
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      a[z] = todo != 0 ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : a[0];
+      todo &= ~__ballot(id == a[z]);
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z)
+      if (z == 0 || a[z] != a[0]) load_b<KS, CT>(p, a[z], wave_col, lane, bf[z]);
+  }
+
+  __device__ __forceinline__ void begin(const LoraArgs& p, int32_t id, int64_t wave_col, int lane) {
+    todo = __ballot(id >= 0) & 0xFFFFu;
+    a[0] = -1;
+    if (todo != 0) request(p, id, wave_col, lane);
+  }
+
+  __device__ __forceinline__ void multiply(const LoraArgs& p, int32_t id, int64_t wave_col,
+                                           int lane, uint4* stage,
+                                           const uint16_t (&hs)[3][16][32 * KS + 8],
+                                           floatx4 (&mine)[CT], float (&scale)[4]) {
+    const int i = lane & 15, g = lane >> 4;
+    int32_t idq[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64), scale[q] = -0.0f;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) mine[c] = floatx4{0, 0, 0, 0};
+    while (a[0] >= 0) {
+#pragma unroll
+      for (int z = 0; z < kBatch; ++z) {
+        if (z > 0 && a[z] == a[0]) break;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) turn(bf[z][k], stage, lane);
+        const float sc = p.scale != nullptr ? p.scale[a[z]] : 1.0f;
+        floatx4 acc[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] = floatx4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t3 = 0; t3 < 3; ++t3) {
+            const bf16x8 hf =
+                as_bf16x8(*reinterpret_cast<const uint4*>(&hs[t3][i][32 * k + 8 * g]));
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+              acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, as_bf16x8(bf[z][k][c]), acc[c],
+                                                               0, 0, 0);
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool hit = idq[q] == a[z];
+          scale[q] = hit ? sc : scale[q];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) mine[c][q] = hit ? acc[c][q] : mine[c][q];
+        }
+      }
+      if (todo == 0) break;
+      request(p, id, wave_col, lane);
+    }
+  }
+};
+
 template <int KS, int BK, int YK>
 __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs s) {
   const LoraArgs& p = s.p;
@@ -454,14 +555,17 @@ __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs s) {
   const int32_t id = i < rows ? adapter_of(p, row0 + i) : -1;
   BaseTile<CT, BK> base;
   load_base<CT, BK>(s, row0, rows, g, wave_col, CT * i, full, base);
-  for (int32_t e = threadIdx.x; e < 16 * 8 * KS; e += 256) {
-    const int32_t t = e / (8 * KS), r = 4 * (e % (8 * KS));
+  FewRows<KS, CT> tile;
+  tile.begin(p, id, wave_col, lane);
+  for (int32_t e = threadIdx.x; e < 2 * 16 * 8 * KS; e += 256) {
+    const int32_t half = e & 1, t = e / (16 * KS), r = 4 * (e / 2 % (8 * KS));
     floatx4 v{0, 0, 0, 0};
     if (r < p.rank && t < rows) {
       const int64_t at = (row0 + t) * p.rank + r;
-      v = join_parts(s.part + at, p.m * p.rank, s.parts);
-      if (s.h != nullptr && col_block == 0) *reinterpret_cast<floatx4*>(s.h + at) = v;
+      v = join_parts(s.part + at, p.m * p.rank, s.parts, half);
+      if (half && s.h != nullptr && col_block == 0) *reinterpret_cast<floatx4*>(s.h + at) = v;
     }
+    if (!half) continue;
     uint16_t d[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);
@@ -469,57 +573,61 @@ __global__ __launch_bounds__(256) void expand_few_kernel(ExpandArgs s) {
     for (int t3 = 0; t3 < 3; ++t3) __builtin_memcpy(&hs[t3][t][r], d[t3], 8);
   }
   __syncthreads();
-  int32_t idq[4];
-  float scale[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64), scale[q] = -0.0f;
   floatx4 mine[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) mine[c] = floatx4{0, 0, 0, 0};
-  // up to kBatch adapters' operands at once: a mixed tile waits for memory once
-  // per batch
-  constexpr int kBatch = KS <= 2 ? 4 : 2;
-  uint64_t todo = __ballot(id >= 0) & 0xFFFFu;
-  while (todo != 0) {
-    int32_t a[kBatch];
-    uint4 bf[kBatch][KS][CT];
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      a[z] = todo != 0 ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : a[0];
-      todo &= ~__ballot(id == a[z]);
-    }
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) load_b<KS, CT>(p, a[z], wave_col, lane, bf[z]);
-#pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      if (z > 0 && a[z] == a[0]) break;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) turn(bf[z][k], stage[wave], lane);
-      const float sc = p.scale != nullptr ? p.scale[a[z]] : 1.0f;
-      floatx4 acc[CT];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[c] = floatx4{0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int t3 = 0; t3 < 3; ++t3) {
-          const bf16x8 hf =
-              as_bf16x8(*reinterpret_cast<const uint4*>(&hs[t3][i][32 * k + 8 * g]));
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hf, as_bf16x8(bf[z][k][c]), acc[c], 0,
-                                                             0, 0);
-        }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bool hit = idq[q] == a[z];
-        scale[q] = hit ? sc : scale[q];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) mine[c][q] = hit ? acc[c][q] : mine[c][q];
-      }
-    }
-  }
+  float scale[4];
+  tile.multiply(p, id, wave_col, lane, stage[wave], hs, mine, scale);
   finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base, mine, scale);
+}
+
+// The fewest rows in one launch: a block of eight waves (16 rows by 256
+// columns) forms h of its rows anew, in the whole grain's order, while B and
+// base are on their way. Reading A once a block costs less than a second
+// launch while A's rows for the tile stay small.
+template <int RT, int BK, int YK>
+__global__ __launch_bounds__(512) void one_pass_kernel(ShrinkArgs sh, ExpandArgs s) {
+  constexpr int CT = 2, KS = (RT + 1) / 2, kLd = 32 * KS + 8, kSumLd = 16 * RT + 4;
+  const LoraArgs& p = s.p;
+  __shared__ union {
+    uint4 stage[kStreams][512];
+    float sums[kStreams][16][kSumLd];
+  } lds;
+  __shared__ __align__(16) uint16_t hs[3][16][kLd];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
+  const int32_t rows = static_cast<int32_t>(p.m);
+  const int64_t wave_col = (static_cast<int64_t>(blockIdx.x) * 8 + wave) * (16 * CT);
+  const bool full = wave_col + CT * i + CT <= p.n;
+  const int32_t id = i < rows ? adapter_of(p, i) : -1;
+  if (blockIdx.x == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
+      i < rows && p.ids[i] != -1)
+    atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+  BaseTile<CT, BK> base;
+  load_base<CT, BK>(s, 0, rows, g, wave_col, CT * i, full, base);
+  FewRows<KS, CT> tile;
+  tile.begin(p, id, wave_col, lane);
+  floatx4 part[RT];
+  shrink_rows<RT, false>(sh, 0, id, wave, kStreams, 0, wave, lane, lds.stage[wave], part);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) lds.sums[wave][4 * g + q][16 * r + i] = part[r][q];
+  __syncthreads();
+  const int32_t live = sh.slices < kStreams ? sh.slices : kStreams;
+  for (int32_t e = threadIdx.x; e < 16 * 32 * KS; e += 512) {
+    const int32_t t = e / (32 * KS), r = e % (32 * KS);
+    float v = 0.0f;
+    if (r < p.rank && t < rows) {
+      for (int32_t w = 0; w < live; ++w) v += lds.sums[w][t][r];
+      if (s.h != nullptr && blockIdx.x == 0) s.h[t * p.rank + r] = v;
+    }
+    split3(v, hs[0][t][r], hs[1][t][r], hs[2][t][r]);
+  }
+  __syncthreads();
+  if (wave_col >= p.n) return;
+  floatx4 mine[CT];
+  float scale[4];
+  tile.multiply(p, id, wave_col, lane, lds.stage[wave], hs, mine, scale);
+  finish_rows<CT, BK, YK>(s, 0, rows, g, wave_col, CT * i, full, base, mine, scale);
 }
 
 constexpr int kManyCols = 4;     // columns of a lane
@@ -685,6 +793,34 @@ int32_t shrink_parts(int64_t m, int64_t n, int64_t k) {
 // Bytes of h as operands of the many-rows product.
 int64_t frag_bytes(int64_t m, int32_t rank) {
   return (m + 15) / 16 * 3 * ((rank + 31) / 32) * 1024;
+}
+
+// Whether one launch does (see one_pass_kernel): at most two adapters whose A
+// is small. In a captured graph one row of rank 16, 3840 -> 15360, takes 6.4 us
+// (two launches: 8.1), 15360 -> 3840 9.3 (9.9), 16 rows of two adapters of rank
+// 32, 512 -> 8192, 7.1 (9.5); eight rows of eight adapters of rank 16, 4096 ->
+// 4096, would take 18.8 (10.7).
+bool one_pass(int64_t m, int64_t k, int32_t rank, int32_t n_adapters, bool mixed) {
+  const int64_t adapters = !mixed ? 1 : m < n_adapters ? m : n_adapters;
+  return m <= 16 && rank <= 32 && adapters <= 2 && rank * k * adapters <= 262144;
+}
+
+template <int RT, int BK, int YK>
+void launch_one_shape(const ShrinkArgs& sh, const ExpandArgs& s, hipStream_t st) {
+  hipLaunchKernelGGL((one_pass_kernel<RT, BK, YK>),
+                     dim3(static_cast<uint32_t>((s.p.n + 255) / 256)), dim3(512), 0, st, sh, s);
+}
+
+template <int RT>
+void launch_one_ranks(const ShrinkArgs& sh, const ExpandArgs& s, hipStream_t st) {
+  switch (s.base_kind * 2 + (s.y_bf16 ? 1 : 0)) {
+    case 0: return launch_one_shape<RT, kNone, kF32>(sh, s, st);
+    case 1: return launch_one_shape<RT, kNone, kBf16>(sh, s, st);
+    case 2: return launch_one_shape<RT, kF32, kF32>(sh, s, st);
+    case 3: return launch_one_shape<RT, kF32, kBf16>(sh, s, st);
+    case 4: return launch_one_shape<RT, kBf16, kF32>(sh, s, st);
+    default: return launch_one_shape<RT, kBf16, kBf16>(sh, s, st);
+  }
 }
 
 int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
@@ -1235,12 +1371,17 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
   const bool many = many_rows(m, p.n);
   float* part = many ? nullptr : static_cast<float*>(workspace);
   uint4* frag = many ? static_cast<uint4*>(workspace) : nullptr;
-  launch_shrink<false>(ShrinkArgs{p, x, part, h, frag, ldx, p.k, slices_of(p.k), many ? 1 : parts},
-                       st);
-  launch_expand(ExpandArgs{p, part, frag, base, y, h, ld_base, ldy, parts,
-                           base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
-                           y_dtype == BINADE_BF16, 0},
-                st);
+  const ShrinkArgs sh{p, x, part, h, frag, ldx, p.k, slices_of(p.k), many ? 1 : parts};
+  const ExpandArgs ex{p, part, frag, base, y, h, ld_base, ldy, parts,
+                      base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
+                      y_dtype == BINADE_BF16, 0};
+  if (one_pass(m, p.k, p.rank, p.n_adapters, ids != nullptr)) {
+    if (p.rank <= 16) launch_one_ranks<1>(sh, ex, st);
+    else launch_one_ranks<2>(sh, ex, st);
+    return launch_status();
+  }
+  launch_shrink<false>(sh, st);
+  launch_expand(ex, st);
   return launch_status();
 }
 
