@@ -54,26 +54,26 @@ def ref_route(x, k, renorm, valid=None):
     p = torch.softmax(x, 1)
     counted = torch.zeros(T, dtype=torch.bool)
     order = torch.sort(x, dim=1, descending=True, stable=True).indices
+    fine = (x > -INF).sum(1)
     for t in range(T):
         if valid is not None and not valid[t]:
             continue
-        e = [int(i) for i in order[t] if x[t, i] > -INF][:k]
-        if not e:
+        e = order[t, :min(k, int(fine[t]))]
+        if not e.numel():
             continue
         counted[t] = True
-        idx[t, :len(e)] = torch.tensor(e)
+        idx[t, :len(e)] = e
         w[t, :len(e)] = p[t, e] / (p[t, e].sum() if renorm else 1.0)
-    counts = torch.zeros(E + 1, dtype=torch.int64)
-    for e in range(E):
-        counts[e] = (idx == e).sum()
-    rows = counts[E] = counted.sum()
+    counts = torch.bincount(idx.flatten() + 1, minlength=E + 1)[1:]
+    counts = torch.cat([counts, counted.sum()[None]])
+    rows = counts[E]
     ps = p[counted].sum(0)
     n = max(int(rows), 1)
     loss = E * float((counts[:E].double() / (k * n) * (ps / n)).sum())
     return idx, w, counts, ps, loss
 
 
-CASES = [(1, 128, 8), (1, 1, 1), (3, 2, 2), (5, 60, 4), (16, 64, 6), (17, 65, 10), (33, 128, 8),
+CASES = [(1, 128, 8), (1, 1, 1), (4000, 256, 8), (3000, 513, 9), (3, 2, 2), (5, 60, 4), (16, 64, 6), (17, 65, 10), (33, 128, 8),
          (64, 256, 8), (67, 300, 1), (9, 512, 64), (21, 1024, 16), (1000, 16, 2), (5000, 8, 3),
          (130, 7, 7), (2100, 128, 8)]
 
@@ -174,9 +174,9 @@ def ref_grad(x, idx, dw, counts, dloss, renorm):
         rows = max(int(counts[E]), 1)
         u += float(dloss) * E * counts[:E].double() / (k * rows * rows)
     terms = torch.zeros(T, 1, dtype=torch.float64)
-    for t in range(T):
-        s = [j for j in range(k) if idx[t, j] >= 0]
-        if not s or dw is None:
+    for t in range(T if dw is not None else 0):
+        s = idx[t] >= 0
+        if not bool(s.any()):
             continue
         e, g = idx[t, s].long(), dw[t, s].double()
         if renorm:
@@ -322,6 +322,27 @@ def test_combine_grad(case):
 
 def rel_norm(a, b):
     return float((a.double() - b.double()).norm() / max(float(a.double().norm()), 1e-300))
+
+
+def test_combine_grad_without_columns_or_tokens():
+    e = torch.empty(0, device=DEV)
+    dy, dw = B.moe_combine_grad(e.reshape(6, 0), torch.ones(3, 2, device=DEV), e.reshape(3, 0), 2)
+    assert dy.shape == (6, 0) and not bool(dw.any())
+    dy, dw = B.moe_combine_grad(e.reshape(0, 5), e.reshape(0, 2), e.reshape(0, 5), 2)
+    assert dy.shape == (0, 5) and dw.shape == (0, 2)
+
+
+def test_many_tokens_of_many_slots():
+    """Tokens enough for the kernel that shares dout among slots, slots beyond
+    its eight, odd columns."""
+    for T, k, n in ((600, 3, 37), (520, 11, 130)):
+        g = gen(T)
+        y = torch.randint(-4, 5, (T * k, n), generator=g).float()
+        w = torch.randint(-3, 4, (T, k), generator=g).float()
+        dout = torch.randint(-4, 5, (T, n), generator=g).float()
+        dy, dw = B.moe_combine_grad(y.to(DEV), w.to(DEV), dout.to(DEV), k)
+        assert torch.equal(dw.cpu(), (dout[:, None] * y.reshape(T, k, n)).sum(2))
+        assert torch.equal(dy.cpu(), (w[:, :, None] * dout[:, None]).reshape(T * k, n))
 
 
 def test_combine_grad_is_the_difference_of_the_combine():
