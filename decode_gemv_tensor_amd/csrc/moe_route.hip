@@ -365,7 +365,7 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
       total += v[j];
     }
     total = group_sum<G>(total);
-    const float inv = 1.0f / total;
+    const float inv = __builtin_amdgcn_rcpf(total);   // 1 step off at most
     if (stats) {
       if (__ballot(!counted) == 0) {
 #pragma unroll
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
     }
     if (p.renorm) taken = group_sum<G>(taken);
     // a NaN among the logits is one of every weight
-    const float f = p.renorm ? (total == total ? 1.0f / taken : total) : inv;
+    const float f = p.renorm ? (total == total ? __builtin_amdgcn_rcpf(taken) : total) : inv;
     if (in) {
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
@@ -553,16 +553,23 @@ struct RouteGradArgs {
 
 // The slots' gradients reach their experts' lanes through a row of LDS a
 // group: the sum of dweights of an expert's slots, and their number (a slot
-// gets its gradient less the row's mean). The row is zero between tokens.
+// gets its gradient less the row's mean). The row is zero between tokens; its
+// pieces of four are swizzled so that eight lanes' reads meet no bank twice.
+// The next token's logits and slots are loaded while one is worked out.
 template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
-  constexpr int kRows = 64 / G, kExperts = G * V;
+  constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;
   __shared__ __align__(16) float grad_s[4 * kRows][kExperts];
   __shared__ __align__(16) float hits_s[4 * kRows][kExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (G - 1);
   const int32_t e0 = l * V;
   float* grad_row = grad_s[wave * kRows + lane / G];
   float* hits_row = hits_s[wave * kRows + lane / G];
+  constexpr int kPieces = V / 4;
+  const auto place = [](int32_t e) {   // of expert e in a row
+    const int32_t of = e / V, piece = e / 4 % kPieces;
+    return of * V + 4 * (piece ^ ((of >> 2) & (kPieces - 1))) + e % 4;
+  };
 #pragma unroll
   for (int j = 0; j < V; ++j) grad_row[e0 + j] = hits_row[e0 + j] = 0.0f;
   wave_sync();
@@ -579,27 +586,47 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
       if (e0 + j < p.n_experts) load[j] = f * static_cast<float>(p.counts[e0 + j]);
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * kRows;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows; t0 < p.n_tokens;
-       t0 += step) {
+  Logits<V, kBf16> next;
+  int32_t e_next[kHeld];
+  float w_next[kHeld];
+  const auto request = [&](int64_t t0) __attribute__((always_inline)) {
     const int64_t t = t0 + lane / G;
     const bool in = t < p.n_tokens;
-    Logits<V, kBf16> x;
-    x.load(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec);
+    const int64_t row = in ? t : p.n_tokens - 1;
+    next.load(p.logits, row * p.ld, e0, p.n_experts, p.vec);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      const int32_t s = l + h * G;
+      const int64_t at = row * p.top_k + (s < p.top_k ? s : 0);
+      e_next[h] = p.idx[at];
+      w_next[h] = p.dweights != nullptr ? p.dweights[at] : 0.0f;
+      if (!in || s >= p.top_k) e_next[h] = -1;
+    }
+  };
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows;
+  if (t0 >= p.n_tokens) return;
+  request(t0);
+  for (; t0 < p.n_tokens; t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const Logits<V, kBf16> x = next;
+    int32_t e[kHeld];
     bool counted = false;
-    const auto slots = [&](auto use) {
-      for (int32_t s = l; s < p.top_k; s += G) {
-        if (!in) break;
-        const int32_t e = p.idx[t * p.top_k + s];
-        if (e >= 0 && e < p.n_experts) use(s, e);
-        else if (e != -1 && p.status != nullptr)
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      e[h] = e_next[h];
+      if (e[h] < 0 || e[h] >= p.n_experts) {
+        if (e[h] != -1 && p.status != nullptr)
           atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+        e[h] = -1;
+        continue;
       }
-    };
-    slots([&](int32_t s, int32_t e) {
-      counted |= s == 0;
-      atomicAdd(&hits_row[e], 1.0f);
-      if (p.dweights != nullptr) atomicAdd(&grad_row[e], p.dweights[t * p.top_k + s]);
-    });
+      counted |= h == 0 && l == 0;
+      atomicAdd(&hits_row[place(e[h])], 1.0f);
+      if (p.dweights != nullptr) atomicAdd(&grad_row[place(e[h])], w_next[h]);
+    }
+    if (t0 + step < p.n_tokens) request(t0 + step);
     wave_sync();
     counted = (__ballot(counted) >> (lane & ~(G - 1)) & 1u) != 0;
     float v[V], top = x.value(0);
@@ -612,18 +639,21 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
       v[j] = exp_of(x.value(j) - top);
       total += v[j];
     }
-    const float inv = 1.0f / group_sum<G>(total);
+    const float inv = __builtin_amdgcn_rcpf(group_sum<G>(total));   // 1 step off at most
     float u[V], hits[V], chosen = 0.0f, mean = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      __builtin_memcpy(&u[4 * q], &grad_row[place(e0 + 4 * q)], 16);
+      __builtin_memcpy(&hits[4 * q], &hits_row[place(e0 + 4 * q)], 16);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       v[j] *= inv;
-      u[j] = grad_row[e0 + j];
-      hits[j] = hits_row[e0 + j];
       chosen = __builtin_fmaf(hits[j], v[j], chosen);
       mean = __builtin_fmaf(u[j], v[j], mean);
     }
     if (p.renorm) {
-      const float f = 1.0f / group_sum<G>(chosen);
+      const float f = __builtin_amdgcn_rcpf(group_sum<G>(chosen));
       mean = group_sum<G>(mean) * f;
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] = hits[j] != 0.0f ? (u[j] - hits[j] * mean) * f : 0.0f;
@@ -638,34 +668,37 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = counted ? v[j] * (u[j] - dot) : 0.0f;
     wave_sync();
-    slots([&](int32_t, int32_t e) { grad_row[e] = hits_row[e] = 0.0f; });
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      if (e[h] >= 0) grad_row[place(e[h])] = hits_row[place(e[h])] = 0.0f;
+    }
     wave_sync();
-    if (!in) continue;
+    if (t >= p.n_tokens) continue;
     const int64_t row = t * p.ld_d;
 #pragma unroll
     for (int b = 0; b < V / 8; ++b) {
-      const int32_t e = e0 + 8 * b;
+      const int32_t ex = e0 + 8 * b;
       if (p.vec_d) {
-        if (e >= p.n_experts) continue;
+        if (ex >= p.n_experts) continue;
         if (kOutBf16) {
           uint32_t d[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            d[j] = pack_bf16(v[8 * b + 2 * j], v[8 * b + 2 * j + 1]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dlogits) + row + e) =
+          for (int j = 0; j < 4; ++j) d[j] = pack_bf16(v[8 * b + 2 * j], v[8 * b + 2 * j + 1]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dlogits) + row + ex) =
               uint4{d[0], d[1], d[2], d[3]};
         } else {
-          __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(p.dlogits) + row + e, 16),
+          __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(p.dlogits) + row + ex, 16),
                            &v[8 * b], 32);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (e + j >= p.n_experts) continue;
+          if (ex + j >= p.n_experts) continue;
           if (kOutBf16)
-            static_cast<uint16_t*>(p.dlogits)[row + e + j] = to_bf16_rne(v[8 * b + j]);
+            static_cast<uint16_t*>(p.dlogits)[row + ex + j] = to_bf16_rne(v[8 * b + j]);
           else
-            static_cast<float*>(p.dlogits)[row + e + j] = v[8 * b + j];
+            static_cast<float*>(p.dlogits)[row + ex + j] = v[8 * b + j];
         }
       }
     }
@@ -720,6 +753,8 @@ void launch_route_experts(const RouteArgs& p, RouteShape s, bool bf16, hipStream
 
 template <int G, int V>
 void launch_grad(const RouteGradArgs& p, bool bf16, bool out_bf16, hipStream_t st) {
+  // as many blocks as the chip holds: a wave's start (its experts' loads) is
+  // worth several tokens (65536 x 256: 24 us; with 4096 blocks 42)
   const int64_t rows = 4 * (64 / G), b = (p.n_tokens + rows - 1) / rows;
   const dim3 grid(static_cast<uint32_t>(b < 1024 ? b : 1024)), block(256);
   if (bf16 && out_bf16) hipLaunchKernelGGL((route_grad_kernel<G, V, true, true>), grid, block, 0, st, p);
