@@ -1027,6 +1027,7 @@ def _addr(t: torch.Tensor | None):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_BF16_ONLY, _F32_ONLY, _I32_ONLY = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _CODE = {torch.float32: F32, torch.bfloat16: BF16}
 _TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -1095,13 +1096,13 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
     if idx.dim() != 2:
         raise ValueError("idx: [n_tokens, top_k]")
     top_k = idx.shape[1]
-    idx = _arg("idx", idx, (torch.int32,), (T, top_k), dev)
+    idx = _arg("idx", idx, _I32_ONLY, (T, top_k), dev)
     if dweights is not None:
-        dweights = _arg("dweights", dweights, (torch.float32,), (T, top_k), dev)
+        dweights = _arg("dweights", dweights, _F32_ONLY, (T, top_k), dev)
     if (counts is None) != (dloss is None):
         raise ValueError("counts and dloss go together")
     if counts is not None:
-        counts = _arg("counts", counts, (torch.int32,), (E + 1,), dev)
+        counts = _arg("counts", counts, _I32_ONLY, (E + 1,), dev)
         dloss = _arg("dloss", dloss.reshape(-1), (torch.float32,), (1,), dev)
     dlogits = _out_arg("dlogits", dlogits, _TORCH_DTYPE[code], (T, E), dev)
     _run("binade_moe_route_grad", logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), T, E,
@@ -1120,11 +1121,11 @@ def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor,
     if y.dim() != 2 or dout.dim() != 2:
         raise ValueError("y: [n_tokens * top_k, N], dout: [n_tokens, N]")
     T, N = dout.shape
-    y = _arg("y", y, (torch.float32,), (T * top_k, N), dev)
+    y = _arg("y", y, _F32_ONLY, (T * top_k, N), dev)
     dout = _arg("dout", dout, _FLOATS, (T, N), dev)
     if weights.numel() != T * top_k:
         raise ValueError("weights: n_tokens * top_k")
-    w = _arg("weights", weights, (torch.float32,), weights.shape, dev)
+    w = _arg("weights", weights, _F32_ONLY, weights.shape, dev)
     dy = torch.empty((T * top_k, N), dtype=_TORCH_DTYPE[code], device=dev) if need_dy else None
     dw = torch.empty(weights.shape, dtype=torch.float32, device=dev)
     _run("binade_moe_combine_grad", y.data_ptr(), w.data_ptr(), dout.data_ptr(),
@@ -1149,17 +1150,19 @@ def _rows16(name: str, t: torch.Tensor, cols: int, device, m: int | None = None)
 
 
 def _lora_desc(a, b, scale, device):
-    """(descriptor, the tensors it points at)."""
-    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+    """(descriptor, the tensors it points at, n, k, rank, n_adapters)."""
+    if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a: [n_adapters, rank, K], b: [n_adapters, N, rank]")
-    a = _arg("a", a, (torch.bfloat16,), a.shape, device)
-    b = _arg("b", b, (torch.bfloat16,), b.shape, device)
-    n_adapters, rank, k = a.shape
+    n_adapters, rank, k = shape = a.shape
+    n = b.shape[1]
+    a = _arg("a", a, _BF16_ONLY, shape, device)
+    b = _arg("b", b, _BF16_ONLY, (n_adapters, n, rank), device)
     at = None
     if scale is not None:
-        scale = _arg("scale", scale, (torch.float32,), (n_adapters,), device)
+        scale = _arg("scale", scale, _F32_ONLY, (n_adapters,), device)
         at = scale.data_ptr()
-    return LoraDesc(b.shape[1], k, rank, n_adapters, a.data_ptr(), b.data_ptr(), at), (a, b, scale)
+    d = LoraDesc(n, k, rank, n_adapters, a.data_ptr(), b.data_ptr(), at)
+    return d, (a, b, scale), n, k, rank, n_adapters
 
 
 @_on_device
@@ -1174,12 +1177,11 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
     lora_grad."""
     code = _dtype_code(out_dtype)
     dev = x.device
-    d, keep = _lora_desc(a, b, scale, dev)
-    n, k, rank = d.n, d.k, d.rank
+    d, keep, n, k, rank, _ = _lora_desc(a, b, scale, dev)
     x = _rows16("x", x, k, dev)
     m = x.shape[0]
     if ids is not None:
-        ids = _arg("ids", ids, (torch.int32,), (m,), dev)
+        ids = _arg("ids", ids, _I32_ONLY, (m,), dev)
     if base is not None:
         base = _arg("base", base, _FLOATS, (m, n), dev)
     y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
@@ -1203,15 +1205,14 @@ def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tens
     dx_base: the projection's own input gradient, added; dx may be dx_base."""
     code = _dtype_code(grad_dtype)
     dev = x.device
-    d, keep = _lora_desc(a, b, scale, dev)
-    n, k, rank, n_adapters = d.n, d.k, d.rank, d.n_adapters
+    d, keep, n, k, rank, n_adapters = _lora_desc(a, b, scale, dev)
     x = _rows16("x", x, k, dev)
     m = x.shape[0]
     if ids is not None:
-        ids = _arg("ids", ids, (torch.int32,), (m,), dev)
-    dy = _arg("dy", dy, (torch.bfloat16,), (m, n), dev)
+        ids = _arg("ids", ids, _I32_ONLY, (m,), dev)
+    dy = _arg("dy", dy, _BF16_ONLY, (m, n), dev)
     if h is not None:
-        h = _arg("h", h, (torch.float32,), (m, rank), dev)
+        h = _arg("h", h, _F32_ONLY, (m, rank), dev)
     if dx_base is not None:
         dx_base = _rows16("dx_base", dx_base, k, dev, m)
     dx = _out_arg("dx", dx, torch.bfloat16, (m, k), dev) if need_dx or dx is not None else None

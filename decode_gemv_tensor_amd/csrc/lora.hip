@@ -825,6 +825,7 @@ void launch_one_ranks(const ShrinkArgs& sh, const ExpandArgs& s, hipStream_t st)
 
 int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
   if (many_rows(m, n)) return frag_bytes(m, rank);
+  if (m == 1 && one_pass(m, k, rank, 1, false)) return 0;
   return shrink_parts(m, n, k) * m * rank * 4;
 }
 
@@ -1362,9 +1363,8 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
   if (!aligned16(h)) return BINADE_EUNSUPPORTED;
   if (y == nullptr || ldy < l->n || (base != nullptr && ld_base < l->n)) return BINADE_EINVAL;
   if (ldy > kMaxStride || (base != nullptr && ld_base > kMaxStride)) return BINADE_EUNSUPPORTED;
-  if (workspace_bytes < binade_lora_workspace_bytes(m, l->n, l->k, l->rank) ||
-      workspace == nullptr)
-    return BINADE_ENOSPACE;
+  const int64_t need = binade_lora_workspace_bytes(m, l->n, l->k, l->rank);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BINADE_ENOSPACE;
   const LoraArgs p = args_of(l, m, ids, dev_status);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int32_t parts = shrink_parts(m, p.n, p.k);

@@ -654,8 +654,8 @@ int32_t binade_lora_add(const binade_lora *l, const uint16_t *x, int64_t m,
                         void *workspace, int64_t workspace_bytes,
                         uint32_t *dev_status, void *stream);
 
-/* Workspace bytes of binade_lora_add (0 for sizes it refuses). Pure host
- * function. */
+/* Workspace bytes of binade_lora_add (0 where it needs none, one row of a
+ * small A, and for sizes it refuses). Pure host function. */
 int64_t binade_lora_workspace_bytes(int64_t m, int64_t n, int64_t k,
                                     int32_t rank);
 

@@ -262,7 +262,7 @@ def test_strides_in_place_and_rows_behind_the_last():
     assert B.lora_add(v["x"], v["a"], v["b"], v["ids"], base=base, scale=v["scale"], y=base) is base
     assert torch.equal(base.cpu().double(), y_ref)
     # through the C ABI: output rows at an odd stride, gaps and rows behind m left alone
-    desc, keep = B._lora_desc(v["a"], v["b"], v["scale"], v["x"].device)
+    desc, keep = B._lora_desc(v["a"], v["b"], v["scale"], v["x"].device)[:2]
     ws = torch.empty(B.lib().binade_lora_workspace_bytes(m, n, k, rank), dtype=torch.uint8,
                      device=DEV)
     for dt, code in ((F32, B.F32), (BF, B.BF16)):
@@ -471,6 +471,9 @@ def test_a_workspace_of_the_size_asked_for_holds_it_all():
             assert bool((pool[:256] == 0xA5).all()) and bool((pool[256 + need:] == 0xA5).all())
             assert all(torch.equal(p, q) for p, q in zip(got, want))
             assert torch.isfinite(got[0]).all()
+            if need == 0:          # one row of a small A needs none
+                assert m == 1
+                continue
             with pytest.raises(B.BinadeError) as e:
                 call(pool[256:256 + need - 1])
             assert e.value.code == B.ENOSPACE
