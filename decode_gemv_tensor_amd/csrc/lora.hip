@@ -8,6 +8,8 @@
 // vectors, one thread per output for the rest.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "binade.h"
 #include "device_common.h"
 
@@ -124,6 +126,12 @@ struct ShrinkArgs {
   int32_t slices, parts;   // parts: 1 (whole), 8 (streams) or slices
 };
 
+// A barrier that waits for LDS alone (__syncthreads() would also wait for the
+// loads on their way).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // N operands as loaded (lane 4 row + octet) -> as MFMA takes them (lane row +
 // 16 octet), through N KB of the wave's own; the swizzle spreads the reads of
 // 8 lanes over all banks.
@@ -157,11 +165,9 @@ __device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t row
   for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64);
 #pragma unroll
   for (int r = 0; r < RT; ++r) mine[r] = floatx4{0, 0, 0, 0};
-  const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
   // as loaded: row lane / 4, columns 8 (lane % 4) on
   const int64_t lrow = row0 + (lane >> 2) < p.m ? row0 + (lane >> 2) : p.m - 1;
   const uint16_t* xl = s.x + lrow * s.ldx + 8 * (lane & 3);
-  const uint16_t* xr = s.x + row * s.ldx + 8 * g;
   uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
   uint32_t got = wave == 0 ? 0xFFFFu & ~todo : 0u;
   for (int32_t nth = 0; todo != 0; ++nth) {
@@ -175,53 +181,60 @@ __device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t row
     floatx4 sum[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) sum[r] = floatx4{0, 0, 0, 0};
-    for (int32_t c = first; c < s.slices; c += step) {
+    uint4 xf[8], af[8];
+    const auto load_x = [&](int32_t c, auto part) __attribute__((always_inline)) {
       const int64_t col = static_cast<int64_t>(c) * kSlice;
-      floatx4 acc[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = floatx4{0, 0, 0, 0};
-      if (s.cols - col >= kSlice) {
-        uint4 xf[8], af[8];
+      for (int j = 0; j < 8; ++j) {
+        const uint16_t* from = xl + col + 32 * j;
+        const int64_t left = s.cols - col - 32 * j;
+        if (!part || left >= 32) {
+          xf[j] = kAny ? load8(from) : *reinterpret_cast<const uint4*>(from);
+        } else {
+          xf[j] = uint4{0, 0, 0, 0};
+          if (kAny && left > 0) xf[j] = load8_part(from, left - 8 * (lane & 3));
+        }
+      }
+    };
+    const auto load_a = [&](int32_t c, auto part, int r) __attribute__((always_inline)) {
+      const int64_t col = static_cast<int64_t>(c) * kSlice;
+      const uint16_t* al = aa + rank_row(16 * r + (lane >> 2)) * p.k + 8 * (lane & 3) + col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!part || s.cols - col > 32 * j)
+          af[j] = *reinterpret_cast<const uint4*>(al + 32 * j);
+        else
+          af[j] = uint4{0, 0, 0, 0};
+      }
+    };
+    // part: a last slice of fewer columns, zeros behind them
+    const auto slice = [&](int32_t c, auto part) __attribute__((always_inline)) {
+      floatx4 acc[RT];
+      load_x(c, part);
+      load_a(c, part, 0);
+      turn(xf, stage, lane);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        acc[r] = floatx4{0, 0, 0, 0};
+        uint4 bf[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bf[j] = af[j];
+        if (RT < 8 && r + 1 < RT) load_a(c, part, r + 1);   // 8 tiles' sums leave no registers
+        turn(bf, stage, lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          xf[j] = kAny ? load8(xl + col + 32 * j)
-                       : *reinterpret_cast<const uint4*>(xl + col + 32 * j);
-        const auto load_a = [&](int r) {
-          const uint16_t* al = aa + rank_row(16 * r + (lane >> 2)) * p.k + 8 * (lane & 3) + col;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) af[j] = *reinterpret_cast<const uint4*>(al + 32 * j);
-        };
-        load_a(0);
-        turn(xf, stage, lane);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          uint4 bf[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) bf[j] = af[j];
-          if (RT < 8 && r + 1 < RT) load_a(r + 1);   // 8 tiles' sums leave no registers for it
-          turn(bf, stage, lane);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf[j]), as_bf16x8(bf[j]),
-                                                             acc[r], 0, 0, 0);
-          if (RT == 8 && r + 1 < RT) load_a(r + 1);
-        }
-      } else {
-        for (int64_t cc = col; cc < s.cols; cc += 32) {
-          const uint4 xf = kAny ? load8_part(xr + cc, s.cols - cc - 8 * g)
-                                : *reinterpret_cast<const uint4*>(xr + cc);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf16x8(xf),
-                as_bf16x8(*reinterpret_cast<const uint4*>(aa + rank_row(16 * r + i) * p.k + 8 * g +
-                                                          cc)),
-                acc[r], 0, 0, 0);
-        }
+          acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(xf[j]), as_bf16x8(bf[j]),
+                                                           acc[r], 0, 0, 0);
+        if (RT == 8 && r + 1 < RT) load_a(c, part, r + 1);
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) sum[r] += acc[r];
-    }
+    };
+    const int32_t whole = static_cast<int32_t>(s.cols / kSlice);
+    int32_t c = first;
+#pragma unroll 1
+    for (; c < whole; c += step) slice(c, std::false_type());
+    if (c < s.slices) slice(c, std::true_type());
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -1019,7 +1032,8 @@ struct OuterSide {
   void* grad;
   float* part;             // [2 * splits][rank * cols]
   int64_t ld, cols, wide;  // wide: cols, or 8 where fewer (zeros behind them)
-  int32_t blocks;          // of four waves, a split
+  int32_t blocks;          // of four waves, a split (0: not in this launch)
+  int32_t per_split;       // tiles of a split; 0: a split is an adapter
 };
 
 struct OuterArgs {
@@ -1027,8 +1041,11 @@ struct OuterArgs {
   Order o;
   const float* scale;
   int64_t m;
-  int32_t rank, n_adapters, per_split;
+  int32_t rank, n_adapters;
   bool grad_bf16;
+  const uint16_t* bt;      // kSums: [n_adapters][rank][n_pad]
+  float* sums;             // [blocks][tiles][32][16]
+  int64_t n_pad, tiles;
 };
 
 // v moved down by n of its 8 elements (1..8), zeros behind.
@@ -1050,7 +1067,14 @@ __device__ __forceinline__ uint4 shift8(uint4 v, int n) {
 
 // A wave: 128 columns, 16 ranks, a split's tiles. A block's waves take the
 // rank chunks of the same columns side by side, so that these meet in the L1.
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
+//
+// kSums (one rank chunk, dy alone): the block also leaves what its 512 columns
+// add to g = Bt dy, so that dy is read once. The rows as loaded go through LDS
+// into operands whose K is the columns.
+template <bool kSums, bool kSorted>
+__global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
+  __shared__ uint4 loaded[kSums ? 4 : 1][kSums ? 512 : 1];
+  __shared__ float sums[4][kSums ? 4 : 1][kSums ? 640 : 1];   // row r, rank i at 16 (r + r / 4) + i
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), i = lane & 15, g = lane >> 4;
   const int32_t per = p.side[0].blocks + p.side[1].blocks;
   // a range of tiles, or an adapter
@@ -1058,26 +1082,31 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
   const bool second = at >= p.side[0].blocks;
   // picked one by one: through an indexed struct the compiler would lose that
   // the pointers are global ones, and wait for every load (flat) at once
-  const uint16_t* const rows_in = second ? p.side[1].s : p.side[0].s;
-  const float* const vectors = second ? p.side[1].v : p.side[0].v;
-  const int64_t ld = second ? p.side[1].ld : p.side[0].ld;
+  const char* const rows_in = reinterpret_cast<const char*>(second ? p.side[1].s : p.side[0].s);
+  const char* const vectors = reinterpret_cast<const char*>(second ? p.side[1].v : p.side[0].v);
+  const uint32_t row_bytes = static_cast<uint32_t>(second ? p.side[1].ld : p.side[0].ld) * 2;
+  const uint32_t vector_bytes = p.rank * 4;
   const int64_t cols = second ? p.side[1].cols : p.side[0].cols;
   const int64_t wide = second ? p.side[1].wide : p.side[0].wide;
+  const int64_t group = second ? at - p.side[0].blocks : at;   // kSums
   const int32_t chunks = (p.rank + 15) / 16;
   const int32_t job = (second ? at - p.side[0].blocks : at) * 4 + wave, chunk = job % chunks;
   const int64_t col0 = static_cast<int64_t>(job / chunks) * 128;
-  if (col0 >= cols) return;
+  if (!kSums && col0 >= cols) return;   // with kSums the wave adds zeros: the block meets
   const bool whole = col0 + 128 <= wide;
   // a row's last piece is loaded as its last 8 columns and moved down
   const int64_t col = col0 + 8 * i, over = col + 8 - wide;
   const int shift = over <= 0 ? 0 : over < 8 ? static_cast<int>(over) : 8;
-  const uint16_t* from = rows_in + (over <= 0 ? col : wide - 8);
-  const bool by_adapter = p.per_split == 0;
+  const uint32_t offset0 = static_cast<uint32_t>(over <= 0 ? col : wide - 8) * 2;
+  const uint32_t offset = offset0 + 8 * g * row_bytes;
+  const char* const from = rows_in + offset0;
+  const int32_t per_split = second ? p.side[1].per_split : p.side[0].per_split;
+  const bool by_adapter = per_split == 0;
   const int32_t n_tiles = first_tile(p.o, p.n_adapters);
-  const int32_t begin = by_adapter ? first_tile(p.o, split) : split * p.per_split;
+  const int32_t begin = by_adapter ? first_tile(p.o, split) : split * per_split;
   const int32_t end = by_adapter                        ? first_tile(p.o, split + 1)
-                      : begin + p.per_split < n_tiles ? begin + p.per_split
-                                                        : n_tiles;
+                      : begin + per_split < n_tiles ? begin + per_split
+                                                      : n_tiles;
   if (begin >= end && !by_adapter) return;
 
   floatx4 acc[8];
@@ -1087,7 +1116,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
     asm volatile("" : "+v"(own));
     const int i = own & 15, g = own >> 4;
     const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
-    const bool direct = by_adapter || (s0 >= begin && s1 <= begin + p.per_split);
+    const bool direct = by_adapter || (s0 >= begin && s1 <= begin + per_split);
     const int64_t size = p.rank * cols;
     const float f = !direct || p.scale == nullptr ? 1.0f : p.scale[a];
     void* const grad = second ? p.side[1].grad : p.side[0].grad;
@@ -1128,65 +1157,120 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
   // order). Every request is made, the last tile's again behind the end: a
   // conditional one would leave the compiler to wait for all loads instead of
   // the oldest ones.
+  uint4 bt[4];
+  int32_t buffer = 0;   // of sums: two tiles' at a time
   const int32_t my_rank = 16 * chunk + i < p.rank ? 16 * chunk + i : p.rank - 1;
   int32_t tile = begin;
   do {
-    const int32_t a = by_adapter ? split : p.o.perm != nullptr ? uniform(p.o.adapter[tile]) : 0;
+    const int32_t a = by_adapter ? split : kSorted ? uniform(p.o.adapter[tile]) : 0;
     const int32_t a_end = by_adapter ? end : first_tile(p.o, a + 1), stop = a_end < end ? a_end : end;
     uint4 in0[8], in1[8];
     float v0[8], v1[8];
     int32_t rows[8], miss0, miss1;
     const auto find = [&](int32_t t) __attribute__((always_inline)) {
+      if (!kSorted) return;
       t = t < stop ? t : stop - 1;
-      if (p.o.perm != nullptr) {
-        const int4* at = reinterpret_cast<const int4*>(p.o.perm + static_cast<int64_t>(t) * kRowTile +
-                                                       8 * g);
-        const int4 lo = at[0], hi = at[1];
-        rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
-        rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
-      } else {
+      const int4* at =
+          reinterpret_cast<const int4*>(p.o.perm + static_cast<int64_t>(t) * kRowTile + 8 * g);
+      const int4 lo = at[0], hi = at[1];
+      rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
+      rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
+    };
+    // tile t, whose rows were found last, then the search for the next one's.
+    // Rows as they are lie at 32-bit offsets from the tile's first (strides are
+    // at most 2^24), others at a 64-bit product each.
+    const auto request = [&](int32_t t, uint4 (&to)[8], float (&v)[8],
+                             int32_t& mask) __attribute__((always_inline)) {
+      mask = 0;
+      if (kSorted) {
+        int32_t now[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) now[j] = rows[j];
+        find(t + 1);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int64_t row = static_cast<int64_t>(t) * kRowTile + 8 * g + j;
-          rows[j] = row < p.m ? static_cast<int32_t>(row) : -1;
+          const uint64_t row = now[j] < 0 ? 0 : now[j];
+          mask |= now[j] < 0 ? 1 << j : 0;
+          to[j] = load8(reinterpret_cast<const uint16_t*>(from + row * row_bytes));
+          v[j] = *reinterpret_cast<const float*>(vectors + row * vector_bytes + 4 * my_rank);
         }
-      }
-    };
-    // the rows found last, then the search for those of tile after
-    const auto request = [&](int32_t after, uint4 (&to)[8], float (&v)[8],
-                             int32_t& mask) __attribute__((always_inline)) {
-      int32_t now[8];
+      } else {
+        t = t < stop ? t : stop - 1;
+        const char* const tile_rows = rows_in + static_cast<int64_t>(t) * kRowTile * row_bytes;
+        const char* const tile_vectors = vectors + static_cast<int64_t>(t) * kRowTile * vector_bytes;
+        const int64_t left = p.m - static_cast<int64_t>(t) * kRowTile;
+        uint32_t r[8], d[8], r0 = offset, d0 = 8 * g * vector_bytes + 4 * my_rank;
+        asm volatile("" : "+v"(r0), "+v"(d0));   // the others are no registers through the loop
 #pragma unroll
-      for (int j = 0; j < 8; ++j) now[j] = rows[j];
-      find(after);
-      mask = 0;
+        for (int j = 0; j < 8; ++j) {
+          r[j] = r0 + j * row_bytes;
+          d[j] = d0 + j * vector_bytes;
+        }
+        if (left < kRowTile) {   // its last row again in place of those behind it
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t row = now[j] < 0 ? 0 : now[j];
-        mask |= now[j] < 0 ? 1 << j : 0;
-        to[j] = load8(from + row * ld);
-        v[j] = vectors[row * p.rank + my_rank];
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t row = 8 * g + j < left ? 8 * g + j : static_cast<uint32_t>(left) - 1;
+            mask |= 8 * g + j < left ? 0 : 1 << j;
+            r[j] = offset0 + row * row_bytes;
+            d[j] = row * vector_bytes + 4 * my_rank;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          to[j] = load8(reinterpret_cast<const uint16_t*>(tile_rows + r[j]));
+          v[j] = *reinterpret_cast<const float*>(tile_vectors + d[j]);
+        }
       }
     };
     const auto multiply = [&](int32_t t, uint4 (&in)[8], float (&vi)[8],
                               int32_t& mask) __attribute__((always_inline)) {
+      uint4 rows_in[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) rows_in[j] = in[j], w[j] = vi[j];
       if (!whole && shift != 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) in[j] = shift8(in[j], shift);
+        for (int j = 0; j < 8; ++j) rows_in[j] = shift8(in[j], shift);
       }
       if (__ballot(mask != 0) != 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (mask >> j & 1) in[j] = uint4{0, 0, 0, 0}, vi[j] = 0.0f;
+          if (mask >> j & 1) rows_in[j] = uint4{0, 0, 0, 0}, w[j] = 0.0f;
       }
       uint4 st[8], v[3];
-      turn_block(in, st);
+      if (kSums) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) loaded[wave][16 * (8 * g + j) + (i ^ j)] = rows_in[j];
+      }
+      turn_block(rows_in, st);
       uint16_t d[3][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) split3(vi[j], d[0][j], d[1][j], d[2][j]);
+      for (int j = 0; j < 8; ++j) split3(w[j], d[0][j], d[1][j], d[2][j]);
 #pragma unroll
       for (int k = 0; k < 3; ++k) v[k] = __builtin_bit_cast(uint4, d[k]);
-      request(t + 3, in, vi, mask);
+      // what was loaded is used up by now: a last use behind the request would
+      // have it take other registers, and their copy back wait for the loads
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        asm volatile("" : "+v"(v[k].x), "+v"(v[k].y), "+v"(v[k].z), "+v"(v[k].w));
+      request(t + 2, in, vi, mask);
+      if (kSums) {
+        wave_sync();
+        floatx4 add[2] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            add[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                as_bf16x8(loaded[wave][16 * (16 * h + i) + ((4 * k + g) ^ (i & 7))]),
+                as_bf16x8(bt[k]), add[h], 0, 0, 0);
+        float* mine = sums[buffer][wave];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mine[16 * (20 * h + 5 * g + q) + i] = add[h][q];
+        buffer = (buffer + 1) & 3;
+      }
 #pragma unroll
       for (int q = 0; q < 3; ++q)
 #pragma unroll
@@ -1194,21 +1278,99 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
           acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[c]), as_bf16x8(v[q]),
                                                            acc[c], 0, 0, 0);
     };
+    // the block's sum of tile t
+    const auto join = [&](int32_t t, int32_t from) __attribute__((always_inline)) {
+      const int row = threadIdx.x >> 3, at = 16 * (row + (row >> 2)) + 2 * (threadIdx.x & 7);
+      float2 d = *reinterpret_cast<const float2*>(&sums[from][0][at]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float2 e = *reinterpret_cast<const float2*>(&sums[from][kSums ? w : 0][at]);
+        d.x += e.x, d.y += e.y;
+      }
+      reinterpret_cast<float2*>(p.sums)[(group * p.tiles + t) * 256 + threadIdx.x] = d;
+    };
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = floatx4{0, 0, 0, 0};
+    if (kSums) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t c = col0 + 32 * k + 8 * g;
+        bt[k] = i < p.rank && c < p.n_pad
+                    ? *reinterpret_cast<const uint4*>(p.bt + (static_cast<int64_t>(a) * p.rank + i) *
+                                                                 p.n_pad + c)
+                    : uint4{0, 0, 0, 0};
+      }
+    }
     if (tile < stop) {
       find(tile);
-      request(tile + 1, in0, v0, miss0);
-      request(tile + 2, in1, v1, miss1);
+      request(tile, in0, v0, miss0);
+      __builtin_amdgcn_sched_barrier(0);   // in this order also here
+      request(tile + 1, in1, v1, miss1);
+      __builtin_amdgcn_sched_barrier(0);
+      // (an odd last tile is not a second one under a condition: the compiler
+      // would wait for both tiles' loads)
 #pragma unroll 1
-      for (; tile < stop; tile += 2) {
+      for (; tile + 1 < stop; tile += 2) {
         multiply(tile, in0, v0, miss0);
-        if (tile + 1 < stop) multiply(tile + 1, in1, v1, miss1);
+        multiply(tile + 1, in1, v1, miss1);
+        if (kSums) {
+          // two buffers of two: who writes one again has met all who read it
+          lds_barrier();
+          join(tile, buffer ^ 2);
+          join(tile + 1, (buffer ^ 2) + 1);
+        }
+      }
+      if (tile < stop) {
+        multiply(tile, in0, v0, miss0);
+        if (kSums) {
+          buffer = (buffer + 1) & 3;
+          lds_barrier();
+          join(tile, buffer ^ 2);
+        }
       }
       tile = stop;
     }
     flush(a);   // an adapter without rows: zeros
   } while (tile < end);
+}
+
+// The blocks' sums of g (outer_kernel, kSums) in their order, four ranks of a
+// sorted row a thread: as fp32 and as the operands of dx's product.
+struct JoinArgs {
+  LoraArgs p;
+  Order o;
+  const float* sums;
+  float* g;
+  uint4* frag;             // or NULL
+  int64_t tiles;
+  int32_t blocks;
+};
+
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs s) {
+  const LoraArgs& p = s.p;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, at = e >> 2;
+  const int quad = static_cast<int>(e & 3);
+  if (p.ids != nullptr && p.status != nullptr && e < p.m && p.ids[e] != -1 && adapter_of(p, e) < 0)
+    atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+  if (at >= static_cast<int64_t>(first_tile(s.o, p.n_adapters)) * kRowTile) return;
+  const int64_t row = s.o.perm != nullptr ? s.o.perm[at] : at < p.m ? at : -1;
+  if (row < 0) return;
+  const floatx4* from = reinterpret_cast<const floatx4*>(s.sums) + e;
+  floatx4 v{0, 0, 0, 0};
+#pragma unroll 8
+  for (int32_t b = 0; b < s.blocks; ++b) v += from[b * s.tiles * (kRowTile * 4)];
+  if (4 * quad < p.rank) *reinterpret_cast<floatx4*>(s.g + row * p.rank + 4 * quad) = v;
+  if (s.frag == nullptr) return;
+  uint16_t d[3][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);
+  // ranks 8 (quad / 2) on of the row; zeros 16 ranks further
+  uint4* to = s.frag + row / 16 * 192 + 16 * (quad >> 1) + row % 16;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    reinterpret_cast<uint2*>(to + 64 * t)[quad & 1] = __builtin_bit_cast(uint2, d[t]);
+    reinterpret_cast<uint2*>(to + 64 * t + 32)[quad & 1] = uint2{0, 0};
+  }
 }
 
 // The first sort_blocks blocks: sorted rows of an adapter each; the others:
@@ -1245,13 +1407,16 @@ __global__ __launch_bounds__(256) void reduce_kernel(OuterArgs p) {
   const int side = e >= size[0] ? 1 : 0;
   if (side) e -= size[0];
   const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
-  const int32_t q0 = s0 / p.per_split, q1 = s1 > s0 ? (s1 - 1) / p.per_split : q0;
+  const int32_t per = p.side[side].per_split;
+  const int32_t q0 = s0 / per, q1 = s1 > s0 ? (s1 - 1) / per : q0;
   if (s1 > s0 && q0 == q1) return;   // outer_kernel wrote it
   floatx4 v{0, 0, 0, 0};
   if (s1 > s0) {
     const float* part = p.side[side].part + e;
-    for (int32_t q = q0; q <= q1; ++q)
-      v += *reinterpret_cast<const floatx4*>(part + (2 * q + (q == q0 ? 1 : 0)) * size[side]);
+    v = *reinterpret_cast<const floatx4*>(part + (2 * q0 + 1) * size[side]);
+#pragma unroll 8
+    for (int32_t q = q0 + 1; q <= q1; ++q)
+      v += *reinterpret_cast<const floatx4*>(part + 2 * q * size[side]);
     const float f = p.scale != nullptr ? p.scale[a] : 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] *= f;
@@ -1265,28 +1430,40 @@ __global__ __launch_bounds__(256) void reduce_kernel(OuterArgs p) {
   }
 }
 
+int32_t side_blocks(int64_t cols, int32_t rank) {
+  return static_cast<int32_t>(((cols + 127) / 128 * ((rank + 15) / 16) + 3) / 4);
+}
+
 // Sizes and places of a backward call's workspace.
 struct GradPlan {
   int64_t tiles, n_pad;
-  int32_t splits, per_split;
-  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, wide, outer, bytes;
+  int32_t splits[2], per_split[2];   // x, dy
+  bool one_read;                     // of dy: dB and g together
+  int64_t perm, adapter, tile0, bt, at, frag, part, g, h, wide, sums, outer, bytes;
   GradPlan(int64_t m, int64_t n, int64_t k, int32_t rank, int32_t n_adapters) {
     tiles = (m + kRowTile - 1) / kRowTile + (m < n_adapters ? m : n_adapters);   // at most
     if (tiles < 1) tiles = 1;
     n_pad = (n + 31) / 32 * 32;
     const int64_t chunks = (rank + 15) / 16;
-    const int64_t jobs = ((n + 127) / 128 + (k + 127) / 128) * chunks;
-    // as many waves as the chip holds at once, at least four tiles each
-    int64_t want = kOuterWaves / jobs;
-    if (want > tiles / 4) want = tiles / 4;
-    if (want < 1) want = 1;
-    per_split = static_cast<int32_t>((tiles + want - 1) / want);
-    splits = static_cast<int32_t>((tiles + per_split - 1) / per_split);
+    const int64_t jobs[2] = {(k + 127) / 128 * chunks, (n + 127) / 128 * chunks};
     // by adapter (per_split 0) while an adapter's tiles are few: 977 rows of 25
     // adapters 62 us by range, 54 by adapter
-    if (m <= (n_adapters >= 4 ? 1024 : 512)) {
-      per_split = 0;
-      splits = n_adapters;
+    const bool by_adapter = m <= (n_adapters >= 4 ? 1024 : 512);
+    // one read of a large dy (rank 16, one adapter: 8192 x 15360 136 us, two
+    // reads 171; 2300 x 15360 59 and 63; 33000 x 1024 248 and 250; below 2^25
+    // elements the second launch costs more, 16384 x 1024 149 and 139)
+    one_read = !by_adapter && rank <= 16 && m * n >= (1 << 25);
+    for (int side = 0; side < 2; ++side) {
+      // as many waves as the chip holds at once, of at least four tiles, or
+      // eight in a launch of its own (partial sums are written and read: 8192
+      // rows of 15360 and 3840 columns 143 us with four, 136 with eight)
+      int64_t want = kOuterWaves / (one_read ? jobs[side] : jobs[0] + jobs[1]);
+      const int64_t most = tiles / (one_read ? 8 : 4);
+      if (want > most) want = most;
+      if (want < 1) want = 1;
+      per_split[side] = by_adapter ? 0 : static_cast<int32_t>((tiles + want - 1) / want);
+      splits[side] = by_adapter ? n_adapters
+                                : static_cast<int32_t>((tiles + per_split[side] - 1) / per_split[side]);
     }
     bytes = 0;
     const auto place = [&](int64_t size) {
@@ -1304,10 +1481,18 @@ struct GradPlan {
     g = place(m * rank * 4);
     h = place(m * rank * 4);
     wide = place(n < 8 ? m * 16 : 0);
-    outer = place(per_split > 0 ? 2ll * splits * rank * (n + k) * 4 : 0);
+    sums = place(one_read ? side_blocks(n, rank) * tiles * kRowTile * 16 * 4 : 0);
+    outer = place(by_adapter ? 0 : 2ll * rank * (splits[0] * k + splits[1] * n) * 4);
   }
     static constexpr int64_t kOuterWaves = 2048;
 };
+
+template <bool kSums>
+void launch_outer(const OuterArgs& p, int64_t splits, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>(splits * (p.side[0].blocks + p.side[1].blocks)));
+  if (p.o.perm != nullptr) hipLaunchKernelGGL((outer_kernel<kSums, true>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((outer_kernel<kSums, false>), grid, dim3(256), 0, st, p);
+}
 
 // Row strides: 12 rows of fp32 stay below 2^31 bytes (32-bit lane offsets).
 constexpr int64_t kMaxStride = 1 << 24;
@@ -1321,7 +1506,8 @@ int32_t check_common(const binade_lora* l, const uint16_t* x, int64_t m, int64_t
                      const void* workspace) {
   if (l == nullptr || m < 0 || l->n <= 0 || l->k <= 0 || l->rank <= 0 || l->n_adapters <= 0)
     return BINADE_EINVAL;
-  if (!sizes_ok(m, l->n, l->k, l->rank) || l->n_adapters > 65535) return BINADE_EUNSUPPORTED;
+  if (!sizes_ok(m, l->n, l->k, l->rank) || l->n_adapters > 65535 || ldx > kMaxStride)
+    return BINADE_EUNSUPPORTED;
   if (l->a == nullptr || l->b == nullptr) return BINADE_EINVAL;
   if (m > 0 && (x == nullptr || ldx < l->k)) return BINADE_EINVAL;
   if (!aligned16(l->a) || !aligned16(l->b) || !aligned16(x) || ldx % 8 != 0 ||
@@ -1397,6 +1583,7 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   if (l->n_adapters > kMaxSorted) return BINADE_EUNSUPPORTED;
   if (da == nullptr || db == nullptr) return BINADE_EINVAL;
   if (m > 0 && (dy == nullptr || ld_dy < l->n)) return BINADE_EINVAL;
+  if (ld_dy > kMaxStride) return BINADE_EUNSUPPORTED;
   if (!aligned16(da) || !aligned16(db) || !aligned16(h)) return BINADE_EUNSUPPORTED;
   if (dx != nullptr) {
     if (ld_dx < l->k || (dx_base != nullptr && ld_dx_base < l->k)) return BINADE_EINVAL;
@@ -1424,12 +1611,7 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   outer.m = m;
   outer.rank = p.rank;
   outer.n_adapters = p.n_adapters;
-  outer.per_split = plan.per_split;
   outer.grad_bf16 = grad_dtype == BINADE_BF16;
-  const int64_t chunks = (p.rank + 15) / 16;
-  const auto side_blocks = [&](int64_t cols) {
-    return static_cast<int32_t>(((cols + 127) / 128 * chunks + 3) / 4);
-  };
   if (m > 0 && p.n < 8) {
     uint16_t* wide = reinterpret_cast<uint16_t*>(ws + plan.wide);
     hipLaunchKernelGGL(widen_kernel, dim3(static_cast<uint32_t>((8 * m + 255) / 256)), dim3(256), 0,
@@ -1437,9 +1619,11 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     dy = wide;
     ld_dy = 8;
   }
-  outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, p.k, side_blocks(p.k)};
+  outer.side[0] = OuterSide{x, nullptr, da, nullptr, ldx, p.k, p.k,
+                            side_blocks(p.k, p.rank), plan.per_split[0]};
   outer.side[1] =
-      OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, p.n < 8 ? 8 : p.n, side_blocks(p.n)};
+      OuterSide{dy, nullptr, db, nullptr, ld_dy, p.n, p.n < 8 ? 8 : p.n,
+                side_blocks(p.n, p.rank), plan.per_split[1]};
   // without ids only adapter 0 is read
   const int32_t used = m == 0 ? 0 : ids != nullptr ? p.n_adapters : 1;
   uint16_t* bt = reinterpret_cast<uint16_t*>(ws + plan.bt);
@@ -1474,32 +1658,46 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     pg.a = bt;
     pg.k = plan.n_pad;
     const bool whole = many_rows(m, p.k) || dx == nullptr;
-    const int32_t parts = whole ? 1 : shrink_parts(m, p.k, p.n);
-    launch_shrink<true>(ShrinkArgs{pg, dy, whole ? nullptr : floats(plan.part),
-                                   whole ? floats(plan.g) : nullptr,
-                                   whole ? pieces(plan.frag) : nullptr, ld_dy, p.n,
-                                   slices_of(p.n), parts},
-                        st);
+    const int32_t parts = whole || plan.one_read ? 1 : shrink_parts(m, p.k, p.n);
+    float* const g = floats(plan.g);
+    uint4* const frag = whole ? pieces(plan.frag) : nullptr;
+    float* const part = plan.one_read ? g : floats(plan.part);
+    outer.o = o;
+    outer.side[0].v = g;
+    outer.side[1].v = h;
+    outer.side[0].part = floats(plan.outer);
+    outer.side[1].part = floats(plan.outer) + 2ll * plan.splits[0] * p.rank * p.k;
+    if (plan.one_read) {
+      OuterArgs dy_alone = outer;
+      dy_alone.side[0].blocks = 0;
+      dy_alone.bt = bt;
+      dy_alone.n_pad = plan.n_pad;
+      dy_alone.sums = floats(plan.sums);
+      dy_alone.tiles = plan.tiles;
+      launch_outer<true>(dy_alone, plan.splits[1], st);
+      hipLaunchKernelGGL(join_kernel, dim3(static_cast<uint32_t>((plan.tiles * 128 + 255) / 256)),
+                         dim3(256), 0, st,
+                         JoinArgs{p, o, dy_alone.sums, g, dx != nullptr ? frag : nullptr,
+                                  plan.tiles, outer.side[1].blocks});
+    } else {
+      launch_shrink<true>(ShrinkArgs{pg, dy, whole ? nullptr : part, whole ? g : nullptr, frag,
+                                     ld_dy, p.n, slices_of(p.n), parts},
+                          st);
+    }
     if (dx != nullptr) {
       LoraArgs px = p;
       px.b = at;
       px.n = p.k;
-      launch_expand(ExpandArgs{px, whole ? nullptr : floats(plan.part),
-                               whole ? pieces(plan.frag) : nullptr, dx_base, dx,
-                               whole ? nullptr : floats(plan.g), ld_dx_base, ld_dx, parts,
+      launch_expand(ExpandArgs{px, whole ? nullptr : part, frag, dx_base, dx,
+                               whole || plan.one_read ? nullptr : g, ld_dx_base, ld_dx, parts,
                                dx_base == nullptr ? 0 : 2, true, 0},
                     st);
     }
-    outer.side[0].v = floats(plan.g);
-    outer.side[1].v = h;
-    outer.side[0].part = floats(plan.outer);
-    outer.side[1].part = floats(plan.outer) + 2ll * plan.splits * p.rank * p.k;
   }
-  outer.o = o;
-  const uint32_t blocks =
-      static_cast<uint32_t>(plan.splits * (outer.side[0].blocks + outer.side[1].blocks));
-  hipLaunchKernelGGL(outer_kernel, dim3(blocks), dim3(256), 0, st, outer);
-  if (plan.per_split > 0)
+  OuterArgs rest = outer;
+  if (plan.one_read) rest.side[1].blocks = 0;
+  launch_outer<false>(rest, plan.splits[0], st);
+  if (plan.per_split[0] > 0)
     hipLaunchKernelGGL(reduce_kernel,
                        dim3(static_cast<uint32_t>((p.rank * (p.n + p.k) / 4 + 255) / 256),
                             static_cast<uint32_t>(p.n_adapters)),

@@ -46,6 +46,7 @@ def test_lora_descriptor_and_input_refusals(call):
     assert call(_desc(), x=None) == B.EINVAL
     assert call(_desc(), ldx=56) == B.EINVAL
     assert call(_desc(), ldx=68) == B.EUNSUPPORTED
+    assert call(_desc(), ldx=(1 << 24) + 8) == B.EUNSUPPORTED
     assert call(_desc(), x=P(4104)) == B.EUNSUPPORTED
     assert call(_desc(), nb=0) == B.ENOSPACE
     assert call(_desc(), ws=None) == B.ENOSPACE
@@ -64,6 +65,7 @@ def test_lora_add_refusals():
 def test_lora_grad_refusals():
     assert _grad(_desc(), dy=None) == B.EINVAL
     assert _grad(_desc(), ld_dy=39) == B.EINVAL
+    assert _grad(_desc(), ld_dy=(1 << 24) + 1) == B.EUNSUPPORTED
     assert _grad(_desc(), da=None) == B.EINVAL
     assert _grad(_desc(), db=None) == B.EINVAL
     assert _grad(_desc(), gdt=5) == B.EINVAL

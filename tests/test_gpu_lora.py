@@ -301,7 +301,10 @@ GRAD = [(1, 64, 64, 8, 1, "one"), (1, 33, 96, 16, 2, "mix"), (16, 128, 128, 16, 
         (2100, 136, 64, 16, 1, "one"),
         # running sums apart, many rows of dx, ranges of tiles over adapters
         (520, 2337, 64, 16, 3, "mix"), (577, 130, 6720, 16, 3, "mix"), (1030, 33, 4224, 72, 5, "runs"),
-        (2051, 5, 2080, 24, 3, "runs"), (1500, 520, 96, 64, 1, "one"), (3000, 300, 64, 16, 200, "mix")]
+        (2051, 5, 2080, 24, 3, "runs"), (1500, 520, 96, 64, 1, "one"), (3000, 300, 64, 16, 200, "mix"),
+        # dy read once for dB and g
+        (34000, 1001, 32, 8, 1, "one"), (4100, 8321, 64, 16, 200, "mix"), (2200, 15400, 96, 16, 3, "mix"),
+        (8300, 4100, 4128, 16, 6, "runs")]
 
 
 @pytest.mark.parametrize("case", GRAD, ids=lambda c: "x".join(map(str, c)))
@@ -408,7 +411,8 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(db.double(), hb)
 
 
-@pytest.mark.parametrize("size", [(40, 136, 544, 16), (2, 136, 544, 16), (1100, 4200, 96, 16)],
+@pytest.mark.parametrize("size", [(40, 136, 544, 16), (2, 136, 544, 16), (1100, 4200, 96, 16),
+                                  (2200, 15400, 96, 16)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_streams_and_graphs(size):
     m, n, k, rank = size
@@ -455,7 +459,8 @@ def test_a_workspace_of_the_size_asked_for_holds_it_all():
     """The caller's workspace, exactly as large as asked for, inside a larger
     buffer whose other bytes stay."""
     for m, n, k, rank, na in [(1, 64, 64, 8, 2), (45, 142, 96, 16, 12), (520, 2337, 64, 16, 3),
-                              (600, 6700, 96, 40, 5), (2100, 3, 2080, 128, 7)]:
+                              (600, 6700, 96, 40, 5), (2100, 3, 2080, 128, 7),
+                              (2200, 15400, 96, 16, 5)]:
         d = make(m, n, k, rank, na, seed=m)
         v = to_dev(d)
         _, h_ref = ref_add(d, scale=False)
@@ -464,11 +469,11 @@ def test_a_workspace_of_the_size_asked_for_holds_it_all():
                  lambda w: B.lora_add(v["x"], v["a"], v["b"], v["ids"], keep_h=True, workspace=w)),
                 (B.lib().binade_lora_grad_workspace_bytes(m, n, k, rank, na),
                  lambda w: B.lora_grad(v["x"], v["a"], v["b"], v["ids"], v["dy"], workspace=w))]:
-            pool = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+            pool = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
             assert pool.data_ptr() % 256 == 0
             got = call(pool[256:256 + need])
             want = call(None)
-            assert bool((pool[:256] == 0xA5).all()) and bool((pool[256 + need:] == 0xA5).all())
+            assert bool((pool[:256] == 0xFF).all()) and bool((pool[256 + need:] == 0xFF).all())
             assert all(torch.equal(p, q) for p, q in zip(got, want))
             assert torch.isfinite(got[0]).all()
             if need == 0:          # one row of a small A needs none
