@@ -402,6 +402,30 @@ __device__ __forceinline__ void load_base(const ExpandArgs& s, int64_t row0, int
       __builtin_memcpy(to.d[q], at + q * s.ld_base * kSize + off, CT * kSize);
 }
 
+// The same without a branch (a load under a condition is one that the compiler
+// cannot count, and it waits for all loads instead of the oldest ones): rows
+// behind the last are the last, the columns of a lane that is not full the
+// row's last CT; neither is used. n >= CT.
+template <int CT, int BK>
+__device__ __forceinline__ void load_base_any(const ExpandArgs& s, int64_t row0, int32_t rows, int g,
+                                              int64_t col, BaseTile<CT, BK>& to) {
+  if (BK == kNone) return;
+  constexpr uint32_t kSize = BK == kBf16 ? 2 : 4;
+  const char* at = static_cast<const char*>(s.base) + row0 * s.ld_base * kSize;
+  const uint32_t row_bytes = static_cast<uint32_t>(s.ld_base) * kSize;
+  const uint32_t col_bytes = static_cast<uint32_t>(col) * kSize;
+  uint32_t off[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) off[q] = 4 * g * row_bytes + col_bytes + q * row_bytes;
+  if (rows < 16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      off[q] = static_cast<uint32_t>(4 * g + q < rows ? 4 * g + q : rows - 1) * row_bytes + col_bytes;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) __builtin_memcpy(to.d[q], at + off[q], CT * kSize);
+}
+
 // Four rows' results from column col on: base + scale * product, stored.
 template <int CT, int BK, int YK>
 __device__ __forceinline__ void finish_rows(const ExpandArgs& s, int64_t row0, int32_t rows, int g,
@@ -682,8 +706,10 @@ __device__ __forceinline__ void stage_b(const LoraArgs& p, int32_t a, int64_t wa
   wave_sync();
 }
 
+// Waves a SIMD: as many as leave the registers of two tiles without spills.
 template <int KS, int BK, int YK>
-__global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) void expand_many_kernel(ExpandArgs s) {
+__global__ __launch_bounds__(256, KS > 2 ? 2 : BK == kNone || (KS == 1 && BK == kBf16) ? 4 : 3)
+void expand_many_kernel(ExpandArgs s) {
   const LoraArgs& p = s.p;
   constexpr int CT = kManyCols;
   __shared__ BTile<KS, CT> tiles_b[4];
@@ -708,31 +734,44 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) v
   BTile<KS, CT>& bt = tiles_b[wave];
   int32_t loaded = -1;
   float sc = 1.0f;
-  BaseTile<CT, BK> base;
-  int32_t id;
-  const auto load_tile = [&](int m) {
-    const int32_t rows = live - 16 * m < 16 ? live - 16 * m : 16;
-    id = i < rows ? adapter_of(p, (tile0 + m) * 16 + i) : -1;
-    load_base<CT, BK>(s, (tile0 + m) * 16, rows, g, wave_col, CT * i, full, base);
+  const int32_t count = (live + 15) / 16;
+  const int64_t col = full ? wave_col + CT * i : p.n - CT;
+  const auto rows_of = [&](int m) { return live - 16 * m < 16 ? live - 16 * m : 16; };
+  // as loaded: looked at a tile later
+  const auto load_id = [&](int m, int32_t& id) __attribute__((always_inline)) {
+    if (p.ids != nullptr) id = p.ids[(tile0 + m) * 16 + (i < rows_of(m) ? i : 0)];
   };
-  load_tile(0);
-  const uint64_t any = __ballot(id >= 0);
+  const auto adapter = [&](int32_t id, int32_t rows) __attribute__((always_inline)) {
+    return i < rows && id >= 0 && id < p.n_adapters ? id : -1;
+  };
+  BaseTile<CT, BK> base0, base1;
+  int32_t id0 = 0, id1 = 0;
+  load_id(0, id0);
+  load_base_any<CT, BK>(s, tile0 * 16, rows_of(0), g, col, base0);
+  const int32_t first = adapter(id0, rows_of(0));
+  const uint64_t any = __ballot(first >= 0);
   if (any != 0) {
-    loaded = __builtin_amdgcn_readlane(id, __builtin_ctzll(any));
+    loaded = __builtin_amdgcn_readlane(first, __builtin_ctzll(any));
     sc = p.scale != nullptr ? p.scale[loaded] : 1.0f;
     stage_b<true, KS, CT>(p, loaded, wave_col, lane, bt, mask, shift);
   }
-#pragma unroll 1
-  for (int m = 0; 16 * m < live; ++m) {
+  // Tile m, whose base is on its way; the next one's (the last again behind the
+  // end) is requested behind this one's operands, since loads return in order.
+  // Two tiles' registers in turn: a copy would wait for the load.
+  const auto step = [&](int m, const int32_t& raw, const BaseTile<CT, BK>& base_now,
+                        int32_t& id_next, BaseTile<CT, BK>& base_next)
+                        __attribute__((always_inline)) {
     const int64_t row0 = (tile0 + m) * 16;
-    const int32_t rows = live - 16 * m < 16 ? live - 16 * m : 16, id_now = id;
-    const BaseTile<CT, BK> base_now = base;
+    const int32_t rows = rows_of(m), next = m + 1 < count ? m + 1 : m;
+    const int32_t id_now = adapter(raw, rows);
+    load_id(next, id_next);
     uint4 hf[3][KS];
 #pragma unroll
     for (int t = 0; t < 3; ++t)
 #pragma unroll
       for (int k = 0; k < KS; ++k) hf[t][k] = s.frag[(((tile0 + m) * 3 + t) * KS + k) * 64 + lane];
-    if (16 * (m + 1) < live) load_tile(m + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_base_any<CT, BK>(s, (tile0 + next) * 16, rows_of(next), g, col, base_next);
     float scale[4];
     floatx4 mine[CT];
 #pragma unroll
@@ -749,6 +788,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) v
         loaded = a;
         sc = p.scale != nullptr ? p.scale[a] : 1.0f;
         stage_b<false, KS, CT>(p, a, wave_col, lane, bt, mask, shift);
+        asm volatile("" : "+v"(sc));   // waited for here, not by every tile
       }
       floatx4 acc[CT];
 #pragma unroll
@@ -784,14 +824,21 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 && BK != kF32 ? 4 : 2) v
       }
     }
     finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base_now, mine, scale);
+  };
+  int32_t m = 0;
+#pragma unroll 1
+  for (; m + 1 < count; m += 2) {
+    step(m, id0, base0, id1, base1);
+    step(m + 1, id1, base1, id0, base0);
   }
+  if (m < count) step(m, id0, base0, id1, base1);
 }
 
 int32_t slices_of(int64_t k) { return static_cast<int32_t>((k + kSlice - 1) / kSlice); }
 
 // Whether blocks of 64 rows by 256 columns fill the chip.
 bool many_rows(int64_t m, int64_t n) {
-  return m >= 512 && ((m + 63) / 64) * ((n + 255) / 256) >= 256;
+  return m >= 512 && n >= kManyCols && ((m + 63) / 64) * ((n + 255) / 256) >= 256;
 }
 
 // Grain of the first product: partial sums it leaves per value (1: h whole,
