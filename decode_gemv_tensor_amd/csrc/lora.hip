@@ -1421,7 +1421,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs s) {
 }
 
 // The first sort_blocks blocks: sorted rows of an adapter each; the others:
-// Bt and At.
+// Bt and At, by one wave a block (600 rows of 24 adapters of rank 64, 15360 x
+// 3840: the call 158 us, with eight waves 181).
 struct PrepareArgs {
   LoraArgs p;
   TurnArgs tb, ta;
@@ -1433,8 +1434,8 @@ __global__ __launch_bounds__(512) void prepare_kernel(PrepareArgs s) {
   const int32_t at = blockIdx.x;
   if (at < s.sort_blocks)
     order_rows(s.p, at, s.perm, s.adapter, s.tile0);
-  else
-    turn_matrices(s.tb, s.ta, static_cast<int64_t>(at - s.sort_blocks) * 512 + threadIdx.x);
+  else if (threadIdx.x < 64)
+    turn_matrices(s.tb, s.ta, static_cast<int64_t>(at - s.sort_blocks) * 64 + threadIdx.x);
 }
 
 // dy with fewer than 8 columns, zeros behind them.
@@ -1493,9 +1494,10 @@ struct GradPlan {
     n_pad = (n + 31) / 32 * 32;
     const int64_t chunks = (rank + 15) / 16;
     const int64_t jobs[2] = {(k + 127) / 128 * chunks, (n + 127) / 128 * chunks};
-    // by adapter (per_split 0) while an adapter's tiles are few: 977 rows of 25
-    // adapters 62 us by range, 54 by adapter
-    const bool by_adapter = m <= (n_adapters >= 4 ? 1024 : 512);
+    // by adapter (per_split 0) while an adapter's tiles are few (4096 -> 4096,
+    // rank 64: 1100 rows of 6 adapters 56 us, by range 67; of one 55 and 50;
+    // 2051 of 24 adapters 97 and 118; 4096 rows of 6, 1001 columns 88 and 74)
+    const bool by_adapter = m <= 512 * (n_adapters < 5 ? n_adapters : 5);
     // one read of a large dy (rank 16, one adapter: 8192 x 15360 136 us, two
     // reads 171; 2300 x 15360 59 and 63; 33000 x 1024 248 and 250; below 2^25
     // elements the second launch costs more, 16384 x 1024 149 and 139)
@@ -1690,9 +1692,10 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   }
   const int64_t turns =
       (pre.tb.n_adapters * plan.n_pad + pre.ta.n_adapters * p.k) / 8 * (p.rank / 8);
-  const uint32_t prepare_blocks = pre.sort_blocks + static_cast<uint32_t>((turns + 511) / 512);
+  const uint32_t prepare_blocks = pre.sort_blocks + static_cast<uint32_t>((turns + 63) / 64);
   if (m > 0)
-    hipLaunchKernelGGL(prepare_kernel, dim3(prepare_blocks), dim3(512), 0, st, pre);
+    hipLaunchKernelGGL(prepare_kernel, dim3(prepare_blocks), dim3(pre.sort_blocks > 0 ? 512 : 64), 0,
+                       st, pre);
   if (m > 0) {
     if (h == nullptr) {
       launch_shrink<false>(ShrinkArgs{p, x, nullptr, floats(plan.h), pieces(plan.frag), ldx, p.k,

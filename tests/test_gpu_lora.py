@@ -301,6 +301,7 @@ GRAD = [(1, 64, 64, 8, 1, "one"), (1, 33, 96, 16, 2, "mix"), (16, 128, 128, 16, 
         (2100, 136, 64, 16, 1, "one"),
         # running sums apart, many rows of dx, ranges of tiles over adapters
         (520, 2337, 64, 16, 3, "mix"), (577, 130, 6720, 16, 3, "mix"), (1030, 33, 4224, 72, 5, "runs"),
+        (3001, 130, 288, 40, 9, "mix"), (2700, 72, 160, 120, 5, "runs"),
         (2051, 5, 2080, 24, 3, "runs"), (1500, 520, 96, 64, 1, "one"), (3000, 300, 64, 16, 200, "mix"),
         # dy read once for dB and g
         (34000, 1001, 32, 8, 1, "one"), (4100, 8321, 64, 16, 200, "mix"), (2200, 15400, 96, 16, 3, "mix"),
