@@ -4,8 +4,12 @@
 //   g[t] = s[i] B[i]^T dy[t]      dx[t] = dx_base[t] + A[i]^T g[t]
 //   dA[i] = sum_t g[t] x[t]^T     dB[i] = sum_t s[i] dy[t] h[t]^T
 //
-// for i = ids[t]. Plain form of each: one block per row for the rank-wide
-// vectors, one thread per output for the rest.
+// for i = ids[t]. A rank is small beside n and k (4 R flop a value of base, dy
+// or x, some 60 at rank 16 and 250 at 64, against a ridge of 200 and more), so
+// memory bounds all of it, and launches where rows are few. The forward is two
+// kernels (h; y), or one for the fewest rows; the backward sorts the rows, then
+// g, dx and the gradients. Every product runs on bf16 MFMA in fp32, with h and
+// g, which are fp32, as three bf16 terms.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -111,6 +115,11 @@ dim3 xcd_grid(int64_t units) {
 // The two finer ones deal the tile's adapters to the block's waves and leave
 // partial sums [parts][m][rank] that the second product's kernel adds.
 // The whole grain also splits h into the second product's MFMA operands.
+// Measured: 4096 rows of 3840 columns, rank 64, 16 adapters, 23.7 us (x alone
+// 6: A is read once a tile, 126 MB out of the L2, and a wave has its own
+// loads' latency to wait for eight times); 61 rows of 15360, 32 adapters of
+// rank 32, in slices 10.6 (A's 31 MB alone 6). Loading a slice ahead changed
+// nothing, 101.0 and 101.1 us for both products of the 4096 rows.
 //
 // MFMA wants 16 rows in consecutive lanes, and a load whose neighbouring lanes
 // sit in different rows costs the L1 one access a lane (64 of 16 bytes; that
@@ -314,7 +323,10 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
 // that lane i ends with the CT adjacent columns CT i .. CT i + CT - 1. A tile of
 // 16 rows runs once for each adapter among them and every row keeps its own;
 // base + scale * product is one fma (rows without an adapter: -0 * 0 + base).
-// Two shapes:
+// Two shapes, at 4096 rows of bf16 base and y, 15360 columns, rank 64, 73.6 us
+// (252 MB, 3.4 TB/s; reading base and writing y alone 44: a wave's tile of 2 KB
+// waits for its operands, and more waves have no registers) and at 61 rows of
+// 3840 columns, fp32 base, 32 adapters of rank 32, 11.1:
 //  - few rows: a block of four waves has 16 rows by 128 columns, joins the
 //    partial sums of h in LDS and splits them into three bf16 terms there;
 //  - many rows: a wave has 64 columns of eight row tiles; h arrives split as
@@ -836,15 +848,21 @@ void expand_many_kernel(ExpandArgs s) {
 
 int32_t slices_of(int64_t k) { return static_cast<int32_t>((k + kSlice - 1) / kSlice); }
 
-// Whether blocks of 64 rows by 256 columns fill the chip.
-bool many_rows(int64_t m, int64_t n) {
-  return m >= 512 && n >= kManyCols && ((m + 63) / 64) * ((n + 255) / 256) >= 256;
+// Whether the many-rows product does: one adapter, 4096 columns of rank 16, 512
+// rows 10.1 us and 13.4 by few rows (256: 9.4 and 9.0), 128 rows of 15360 10.1
+// and 13.0. Several adapters may be mixed in every tile, which only the few-rows
+// kernels deal to waves: 256 rows of 15360 columns, rank 64, 16 adapters in runs
+// 37 and 34, 512 rows 41 and 51, so these ask for more rows.
+bool many_rows(int64_t m, int64_t n, bool one_adapter) {
+  if (n < kManyCols) return false;
+  return one_adapter ? m >= 128 && m * n >= (1 << 21) : m >= 512 && m * n >= (1 << 22);
 }
 
-// Grain of the first product: partial sums it leaves per value (1: h whole,
-// as the operands of the many-rows product).
-int32_t shrink_parts(int64_t m, int64_t n, int64_t k) {
-  if (many_rows(m, n)) return 1;
+// Grain of the first product before the few-rows one: partial sums it leaves
+// per value. 61 rows of 32 adapters, rank 32, 15360 -> 3840: both products 21 us
+// in slices, 44 in running sums; 700 rows of one, rank 64, 15360 -> 1024: 37 and
+// 24.
+int32_t shrink_parts(int64_t m, int64_t k) {
   const int64_t tiles = (m + 15) / 16;
   const int32_t slices = slices_of(k);
   return tiles * kStreams >= 256 && slices > kStreams ? kStreams : slices;
@@ -884,9 +902,10 @@ void launch_one_ranks(const ShrinkArgs& sh, const ExpandArgs& s, hipStream_t st)
 }
 
 int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
-  if (many_rows(m, n)) return frag_bytes(m, rank);
   if (m == 1 && one_pass(m, k, rank, 1, false)) return 0;
-  return shrink_parts(m, n, k) * m * rank * 4;
+  const int64_t few = shrink_parts(m, k) * m * rank * 4, many = frag_bytes(m, rank);
+  if (many_rows(m, n, false)) return many;
+  return many_rows(m, n, true) && many > few ? many : few;
 }
 
 template <bool kAny>
@@ -954,8 +973,14 @@ void launch_expand(const ExpandArgs& s, hipStream_t st) {
 //    without rows. Few rows (a matter of launches) do without it: there a wave
 //    has all tiles of one adapter.
 // Rows of another adapter never meet in one MFMA chain.
+// A large dy of one rank chunk is read once, g's sums beside dB's (join_kernel
+// adds them), in a launch of its own; else g is the first product on Bt.
+// Measured, 8192 rows, 15360 and 3840 columns, one adapter of rank 16: prepare
+// 4.8 us, dy 68.3 (252 MB, 3.7 TB/s: a CU has some 75 lines under way, which
+// its L1 allows, for 1300 clocks each), join 6.7, dx 28.2 (126 MB), x 16.6,
+// reduce 6.8; with dy read twice 55.6 for g and 70.4 for both sums.
 constexpr int kRowTile = 32;           // sorted rows of a tile
-constexpr int kMaxSorted = 4096;    // adapters prepare_kernel counts in LDS
+constexpr int kMaxSorted = 4096;       // adapters prepare_kernel counts in LDS
 
 struct TurnArgs {
   const uint16_t* from;
@@ -1526,14 +1551,14 @@ struct GradPlan {
     bt = place(n_adapters * n_pad * rank * 2);
     at = place(n_adapters * k * rank * 2);
     frag = place(frag_bytes(m, rank));
-    part = place(many_rows(m, k) ? 0 : shrink_parts(m, k, n) * m * rank * 4);
+    part = place(many_rows(m, k, n_adapters == 1) ? 0 : shrink_parts(m, n) * m * rank * 4);
     g = place(m * rank * 4);
     h = place(m * rank * 4);
     wide = place(n < 8 ? m * 16 : 0);
     sums = place(one_read ? side_blocks(n, rank) * tiles * kRowTile * 16 * 4 : 0);
     outer = place(by_adapter ? 0 : 2ll * rank * (splits[0] * k + splits[1] * n) * 4);
   }
-    static constexpr int64_t kOuterWaves = 2048;
+  static constexpr int64_t kOuterWaves = 2048;
 };
 
 template <bool kSums>
@@ -1602,11 +1627,11 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BINADE_ENOSPACE;
   const LoraArgs p = args_of(l, m, ids, dev_status);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const int32_t parts = shrink_parts(m, p.n, p.k);
-  const bool many = many_rows(m, p.n);
+  const bool many = many_rows(m, p.n, ids == nullptr || p.n_adapters == 1);
+  const int32_t parts = many ? 1 : shrink_parts(m, p.k);
   float* part = many ? nullptr : static_cast<float*>(workspace);
   uint4* frag = many ? static_cast<uint4*>(workspace) : nullptr;
-  const ShrinkArgs sh{p, x, part, h, frag, ldx, p.k, slices_of(p.k), many ? 1 : parts};
+  const ShrinkArgs sh{p, x, part, h, frag, ldx, p.k, slices_of(p.k), parts};
   const ExpandArgs ex{p, part, frag, base, y, h, ld_base, ldy, parts,
                       base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
                       y_dtype == BINADE_BF16, 0};
@@ -1707,8 +1732,9 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     LoraArgs pg = p;
     pg.a = bt;
     pg.k = plan.n_pad;
-    const bool whole = many_rows(m, p.k) || dx == nullptr;
-    const int32_t parts = whole || plan.one_read ? 1 : shrink_parts(m, p.k, p.n);
+    const bool whole =
+        many_rows(m, p.k, ids == nullptr || p.n_adapters == 1) || dx == nullptr;
+    const int32_t parts = whole || plan.one_read ? 1 : shrink_parts(m, p.n);
     float* const g = floats(plan.g);
     uint4* const frag = whole ? pieces(plan.frag) : nullptr;
     float* const part = plan.one_read ? g : floats(plan.part);

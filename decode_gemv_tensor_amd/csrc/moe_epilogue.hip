@@ -81,7 +81,8 @@ __device__ __forceinline__ void load4(const void* p, int64_t at, int64_t left, f
 // dy[t, s, :] = w[t, s] * dout[t, :] and dw[t, s] = <dout[t, :], y[t, s, :]>:
 // one block per token and S slots, which share the loads of dout; a thread
 // has columns 4 threadIdx.x .. + 3 of every 1024. S does not change the order
-// of a slot's sum.
+// of a slot's sum. Bound by y (read) and dy (written): 4096 tokens of 8 slots
+// of 2816 columns, bf16 dout and dy, 105 us (577 MB, 5.5 TB/s).
 template <int S, bool kDoutBf16, bool kDyBf16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const float* weights,
                                                            const void* dout, int32_t top_k,
@@ -213,12 +214,12 @@ extern "C" int32_t binade_moe_combine_grad(const float* y, const float* weights,
   if (n > 0 && (y == nullptr || dout == nullptr)) return BINADE_EINVAL;
   const bool db = dout_dtype == BINADE_BF16, yb = dy_dtype == BINADE_BF16;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  // a block per slot until the tokens alone fill the chip
+  // a block per slot until the tokens alone fill the chip (8 slots of 2816
+  // columns: 8 tokens 4.4 us, with eight a block 10.3; 256 tokens 9.4, with two
+  // 9.4; 4096 tokens 110, with two 105, four 111, eight 121)
   if (n_tokens < 512)
     launch_combine_grad<1>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
-  else if (top_k <= 4)
-    launch_combine_grad<4>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
   else
-    launch_combine_grad<8>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
+    launch_combine_grad<2>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
   return launch_status();
 }

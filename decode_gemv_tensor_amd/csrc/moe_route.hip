@@ -310,6 +310,10 @@ __device__ __forceinline__ float loss_term(int32_t count, float prob, int32_t ro
   return static_cast<float>(count) / (static_cast<float>(top_k) * r) * (prob / r);
 }
 
+// Measured: 65536 tokens of 256 bf16 experts, top 8, counts and sums, 21.4 us
+// (7 us of bytes): some 600 vector instructions a wave's four rows, most of
+// them the keys' sorting and the merge's eight steps; 2048 tokens of 128 fp32
+// experts 6.2, one token 2.5.
 template <int G, int V, typename K, bool kSort>
 __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
   typedef typename K::Key Key;
@@ -556,6 +560,9 @@ struct RouteGradArgs {
 // gets its gradient less the row's mean). The row is zero between tokens; its
 // pieces of four are swizzled so that eight lanes' reads meet no bank twice.
 // The next token's logits and slots are loaded while one is worked out.
+// Measured: 65536 tokens of 256 bf16 experts, top 8, 26 us under the trace (71
+// MB, 13.6 us of bytes): bound by instructions, the exponentials and the two
+// LDS rows of a token; 333 tokens of 60 fp32 experts 5.1.
 template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;

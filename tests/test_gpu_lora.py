@@ -131,7 +131,9 @@ ADD = [(1, 64, 64, 8, 1, "one"), (1, 1001, 96, 16, 3, "mix"), (2, 17, 32, 128, 5
        # running sums apart, many rows
        (520, 48, 2336, 16, 3, "mix"), (577, 6700, 96, 8, 3, "mix"), (600, 6661, 544, 40, 5, "runs"),
        (1030, 4200, 64, 72, 4, "mix"), (530, 7200, 288, 128, 2, "one"), (2051, 2050, 2080, 32, 6, "runs"),
-       (5, 40, 128, 8, 3, "none"), (600, 6661, 64, 8, 3, "none")]
+       (5, 40, 128, 8, 3, "none"), (600, 6661, 64, 8, 3, "none"),
+       # many rows for one adapter alone
+       (130, 16500, 96, 16, 1, "mix"), (257, 8201, 160, 72, 3, "one")]
 
 
 @pytest.mark.parametrize("case", ADD, ids=lambda c: "x".join(map(str, c)))
@@ -154,7 +156,7 @@ def test_add_is_exact_on_whole_numbers(case):
     assert torch.equal(y.cpu().double(), ref_add(d, scale=False, base=False)[0])
 
 
-@pytest.mark.parametrize("case", ADD[:-2], ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("case", [c for c in ADD if c[5] != "none"], ids=lambda c: "x".join(map(str, c)))
 def test_add_rounds_as_fp32_sums_do(case):
     m, n, k, rank, na, ids = case
     d = make(m, n, k, rank, na, seed=7 + sum(case[:5]), whole=False, ids=ids)
@@ -304,7 +306,7 @@ GRAD = [(1, 64, 64, 8, 1, "one"), (1, 33, 96, 16, 2, "mix"), (16, 128, 128, 16, 
         (3001, 130, 288, 40, 9, "mix"), (2700, 72, 160, 120, 5, "runs"),
         (2051, 5, 2080, 24, 3, "runs"), (1500, 520, 96, 64, 1, "one"), (3000, 300, 64, 16, 200, "mix"),
         # dy read once for dB and g
-        (34000, 1001, 32, 8, 1, "one"), (4100, 8321, 64, 16, 200, "mix"), (2200, 15400, 96, 16, 3, "mix"),
+        (34000, 1001, 32, 8, 1, "one"), (200, 64, 16416, 8, 1, "mix"), (4100, 8321, 64, 16, 200, "mix"), (2200, 15400, 96, 16, 3, "mix"),
         (8300, 4100, 4128, 16, 6, "runs")]
 
 
@@ -460,7 +462,7 @@ def test_a_workspace_of_the_size_asked_for_holds_it_all():
     """The caller's workspace, exactly as large as asked for, inside a larger
     buffer whose other bytes stay."""
     for m, n, k, rank, na in [(1, 64, 64, 8, 2), (45, 142, 96, 16, 12), (520, 2337, 64, 16, 3),
-                              (600, 6700, 96, 40, 5), (2100, 3, 2080, 128, 7),
+                              (600, 6700, 96, 40, 5), (300, 8000, 96, 24, 1), (2100, 3, 2080, 128, 7),
                               (2200, 15400, 96, 16, 5)]:
         d = make(m, n, k, rank, na, seed=m)
         v = to_dev(d)
