@@ -81,16 +81,21 @@ __device__ __forceinline__ void load4(const void* p, int64_t at, int64_t left, f
 // dy[t, s, :] = w[t, s] * dout[t, :] and dw[t, s] = <dout[t, :], y[t, s, :]>:
 // one block per token and S slots, which share the loads of dout; a thread
 // has columns 4 threadIdx.x .. + 3 of every 1024. S does not change the order
-// of a slot's sum. Bound by y (read) and dy (written): 4096 tokens of 8 slots
+// of a slot's sum. Blocks go to the 8 XCDs in turn, so a token's are 8 apart
+// and find its dout in one L2 (1024 tokens of 8 slots 25.4 -> 23.2 us, 105 the
+// same at 4096, as large as the caches above). Bound by y (read) and dy (written): 4096 tokens of 8 slots
 // of 2816 columns, bf16 dout and dy, 105 us (577 MB, 5.5 TB/s).
 template <int S, bool kDoutBf16, bool kDyBf16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const float* weights,
-                                                           const void* dout, int32_t top_k,
-                                                           int64_t n, void* dy, float* dweights) {
+                                                           const void* dout, int64_t n_tokens,
+                                                           int32_t top_k, int64_t n, void* dy,
+                                                           float* dweights) {
   __shared__ float red[4][S];
   const int32_t chunks = (top_k + S - 1) / S;
-  const int64_t t = blockIdx.x / chunks;
-  const int32_t s0 = static_cast<int32_t>(blockIdx.x - t * chunks) * S;
+  const uint32_t nth = blockIdx.x / 8;
+  const int64_t t = static_cast<int64_t>(nth / chunks) * 8 + blockIdx.x % 8;
+  if (t >= n_tokens) return;
+  const int32_t s0 = static_cast<int32_t>(nth % chunks) * S;
   const int32_t slots = top_k - s0 < S ? top_k - s0 : S;
   const int64_t pair = t * top_k + s0;
   float w[S], acc[S];
@@ -151,19 +156,19 @@ template <int S>
 void launch_combine_grad(const float* y, const float* weights, const void* dout, bool dout_bf16,
                          int64_t n_tokens, int32_t top_k, int64_t n, void* dy, bool dy_bf16,
                          float* dweights, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>(n_tokens * ((top_k + S - 1) / S))), block(256);
+  const dim3 grid(static_cast<uint32_t>((n_tokens + 7) / 8 * 8 * ((top_k + S - 1) / S))), block(256);
   if (dout_bf16 && dy_bf16)
     hipLaunchKernelGGL((combine_grad_kernel<S, true, true>), grid, block, 0, st, y, weights, dout,
-                       top_k, n, dy, dweights);
+                       n_tokens, top_k, n, dy, dweights);
   else if (dout_bf16)
     hipLaunchKernelGGL((combine_grad_kernel<S, true, false>), grid, block, 0, st, y, weights, dout,
-                       top_k, n, dy, dweights);
+                       n_tokens, top_k, n, dy, dweights);
   else if (dy_bf16)
     hipLaunchKernelGGL((combine_grad_kernel<S, false, true>), grid, block, 0, st, y, weights, dout,
-                       top_k, n, dy, dweights);
+                       n_tokens, top_k, n, dy, dweights);
   else
     hipLaunchKernelGGL((combine_grad_kernel<S, false, false>), grid, block, 0, st, y, weights, dout,
-                       top_k, n, dy, dweights);
+                       n_tokens, top_k, n, dy, dweights);
 }
 
 uint32_t elementwise_blocks(int64_t n) {
@@ -215,8 +220,8 @@ extern "C" int32_t binade_moe_combine_grad(const float* y, const float* weights,
   const bool db = dout_dtype == BINADE_BF16, yb = dy_dtype == BINADE_BF16;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   // a block per slot until the tokens alone fill the chip (8 slots of 2816
-  // columns: 8 tokens 4.4 us, with eight a block 10.3; 256 tokens 9.4, with two
-  // 9.4; 4096 tokens 110, with two 105, four 111, eight 121)
+  // columns: 8 tokens 4.4 us, with eight a block 10.3; 256 tokens 8.2, with two
+  // 8.9; 4096 tokens 109, with two 105, four 111, eight 121)
   if (n_tokens < 512)
     launch_combine_grad<1>(y, weights, dout, db, n_tokens, top_k, n, dy, yb, dweights, st);
   else

@@ -311,9 +311,9 @@ __device__ __forceinline__ float loss_term(int32_t count, float prob, int32_t ro
 }
 
 // Measured: 65536 tokens of 256 bf16 experts, top 8, counts and sums, 21.4 us
-// (7 us of bytes): some 600 vector instructions a wave's four rows, most of
-// them the keys' sorting and the merge's eight steps; 2048 tokens of 128 fp32
-// experts 6.2, one token 2.5.
+// (7 us of bytes): 540 vector instructions a wave's four rows, most of them
+// the keys' sorting and the merge's four steps, 14 us at the issue rate; 2048
+// tokens of 128 fp32 experts 6.2, one token 2.5.
 template <int G, int V, typename K, bool kSort>
 __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
   typedef typename K::Key Key;
@@ -561,8 +561,8 @@ struct RouteGradArgs {
 // pieces of four are swizzled so that eight lanes' reads meet no bank twice.
 // The next token's logits and slots are loaded while one is worked out.
 // Measured: 65536 tokens of 256 bf16 experts, top 8, 26 us under the trace (71
-// MB, 13.6 us of bytes): bound by instructions, the exponentials and the two
-// LDS rows of a token; 333 tokens of 60 fp32 experts 5.1.
+// MB, 13.6 us of bytes; 470 vector instructions a wave's four rows, 13 us at
+// the issue rate); 333 tokens of 60 fp32 experts 5.1.
 template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;
