@@ -83,8 +83,9 @@ __device__ __forceinline__ void load4(const void* p, int64_t at, int64_t left, f
 // has columns 4 threadIdx.x .. + 3 of every 1024. S does not change the order
 // of a slot's sum. Blocks go to the 8 XCDs in turn, so a token's are 8 apart
 // and find its dout in one L2 (1024 tokens of 8 slots 25.4 -> 23.2 us, 105 the
-// same at 4096, as large as the caches above). Bound by y (read) and dy (written): 4096 tokens of 8 slots
-// of 2816 columns, bf16 dout and dy, 105 us (577 MB, 5.5 TB/s).
+// same at 4096, as large as the caches above). Bound by y (read) and dy
+// (written): 4096 tokens of 8 slots of 2816 columns, bf16 dout and dy, 105 us
+// (577 MB, 5.5 TB/s).
 template <int S, bool kDoutBf16, bool kDyBf16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const float* weights,
                                                            const void* dout, int64_t n_tokens,

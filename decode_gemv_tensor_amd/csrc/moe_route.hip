@@ -5,9 +5,9 @@
 // 256, 512 or 1024 in all), so a wave has 64 / G rows at once: what a row
 // costs is instructions, not bytes, and a lane's own sort is cheaper than
 // steps across lanes. 16 experts a lane for bf16; 8 for fp32, whose keys take
-// two registers each (with 16 they spill). Nothing of a row leaves its group; sums over rows stay
-// in the lanes' registers (a lane's experts never change) until the block
-// ends.
+// two registers each (with 16 they spill). Nothing of a row leaves its group;
+// sums over rows stay in the lanes' registers (a lane's experts never change)
+// until the block ends.
 //
 // Choice. A logit and its expert make one whole-number key (bf16: 16 + 16
 // bits, fp32: 32 + 32), larger for the larger logit and, among equal ones,
