@@ -1014,7 +1014,6 @@ __device__ __forceinline__ int64_t turn_count(const TurnArgs& p) {
 
 __device__ __forceinline__ void turn_matrices(const TurnArgs& b, const TurnArgs& a, int64_t e) {
   const int64_t nb = turn_count(b);
-  if (e >= nb + turn_count(a)) return;
   const bool first = e < nb;
   const TurnArgs& p = first ? b : a;
   if (!first) e -= nb;
@@ -1453,6 +1452,7 @@ struct PrepareArgs {
   TurnArgs tb, ta;
   int32_t *perm, *adapter, *tile0;
   int32_t sort_blocks;
+  int64_t turns;
 };
 
 __global__ __launch_bounds__(512) void prepare_kernel(PrepareArgs s) {
@@ -1460,7 +1460,9 @@ __global__ __launch_bounds__(512) void prepare_kernel(PrepareArgs s) {
   if (at < s.sort_blocks)
     order_rows(s.p, at, s.perm, s.adapter, s.tile0);
   else if (threadIdx.x < 64)
-    turn_matrices(s.tb, s.ta, static_cast<int64_t>(at - s.sort_blocks) * 64 + threadIdx.x);
+    for (int64_t e = static_cast<int64_t>(at - s.sort_blocks) * 64 + threadIdx.x; e < s.turns;
+         e += static_cast<int64_t>(gridDim.x - s.sort_blocks) * 64)
+      turn_matrices(s.tb, s.ta, e);
 }
 
 // dy with fewer than 8 columns, zeros behind them.
@@ -1715,9 +1717,10 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
     o.adapter = pre.adapter;
     o.tile0 = pre.tile0;
   }
-  const int64_t turns =
-      (pre.tb.n_adapters * plan.n_pad + pre.ta.n_adapters * p.k) / 8 * (p.rank / 8);
-  const uint32_t prepare_blocks = pre.sort_blocks + static_cast<uint32_t>((turns + 63) / 64);
+  pre.turns = (pre.tb.n_adapters * plan.n_pad + pre.ta.n_adapters * p.k) / 8 * (p.rank / 8);
+  const int64_t turn_blocks = (pre.turns + 63) / 64;
+  const uint32_t prepare_blocks =
+      pre.sort_blocks + static_cast<uint32_t>(turn_blocks < (1 << 20) ? turn_blocks : 1 << 20);
   if (m > 0)
     hipLaunchKernelGGL(prepare_kernel, dim3(prepare_blocks), dim3(pre.sort_blocks > 0 ? 512 : 64), 0,
                        st, pre);

@@ -78,6 +78,9 @@ __device__ __forceinline__ void load4(const void* p, int64_t at, int64_t left, f
                      : static_cast<const float*>(p)[at + j];
 }
 
+// Tokens along the grid's first axis, which ends at 2^32 threads.
+constexpr int64_t kCombineRun = 1 << 17;
+
 // dy[t, s, :] = w[t, s] * dout[t, :] and dw[t, s] = <dout[t, :], y[t, s, :]>:
 // one block per token and S slots, which share the loads of dout; a thread
 // has columns 4 threadIdx.x .. + 3 of every 1024. S does not change the order
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const float* y, const
   __shared__ float red[4][S];
   const int32_t chunks = (top_k + S - 1) / S;
   const uint32_t nth = blockIdx.x / 8;
-  const int64_t t = static_cast<int64_t>(nth / chunks) * 8 + blockIdx.x % 8;
+  const int64_t t = blockIdx.y * kCombineRun + static_cast<int64_t>(nth / chunks) * 8 + blockIdx.x % 8;
   if (t >= n_tokens) return;
   const int32_t s0 = static_cast<int32_t>(nth % chunks) * S;
   const int32_t slots = top_k - s0 < S ? top_k - s0 : S;
@@ -157,7 +160,10 @@ template <int S>
 void launch_combine_grad(const float* y, const float* weights, const void* dout, bool dout_bf16,
                          int64_t n_tokens, int32_t top_k, int64_t n, void* dy, bool dy_bf16,
                          float* dweights, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>((n_tokens + 7) / 8 * 8 * ((top_k + S - 1) / S))), block(256);
+  const int64_t run = n_tokens < kCombineRun ? (n_tokens + 7) / 8 * 8 : kCombineRun;
+  const dim3 grid(static_cast<uint32_t>(run * ((top_k + S - 1) / S)),
+                  static_cast<uint32_t>((n_tokens + kCombineRun - 1) / kCombineRun)),
+      block(256);
   if (dout_bf16 && dy_bf16)
     hipLaunchKernelGGL((combine_grad_kernel<S, true, true>), grid, block, 0, st, y, weights, dout,
                        n_tokens, top_k, n, dy, dweights);

@@ -345,6 +345,18 @@ def test_many_tokens_of_many_slots():
         assert torch.equal(dy.cpu(), (w[:, :, None] * dout[:, None]).reshape(T * k, n))
 
 
+@pytest.mark.parametrize("T,k,n", [((1 << 17) + 9, 3, 5), ((1 << 22) + 5, 8, 4)])
+def test_more_tokens_than_one_axis_of_the_grid(T, k, n):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    y = torch.randint(-4, 5, (T * k, n), generator=g, device=DEV).float()
+    w = torch.randint(-3, 4, (T, k), generator=g, device=DEV).float()
+    dout = torch.randint(-4, 5, (T, n), generator=g, device=DEV).float()
+    dy, dw = B.moe_combine_grad(y, w, dout, k)
+    assert torch.equal(dw, (dout[:, None] * y.reshape(T, k, n)).sum(2))
+    assert torch.equal(dy, (w[:, :, None] * dout[:, None]).reshape(T * k, n))
+
+
 def test_combine_grad_is_the_difference_of_the_combine():
     """moe_combine is linear in the weights and in y: exact on whole numbers."""
     T, k, n = 6, 4, 75
