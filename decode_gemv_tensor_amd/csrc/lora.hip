@@ -55,6 +55,7 @@ __device__ __forceinline__ void store_any(void* v, int64_t i, bool is_bf16, floa
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
+constexpr int kRowTile = 32;   // rows sorted by adapter: of a tile
 constexpr int kSlice = 256;    // columns whose products one MFMA chain adds
 constexpr int kStreams = 8;    // running sums the slices are dealt to
 
@@ -133,6 +134,10 @@ struct ShrinkArgs {
   uint4* frag;             // whole: [tiles][3][KS][64] operands (NULL otherwise)
   int64_t ldx, cols;       // columns of x
   int32_t slices, parts;   // parts: 1 (whole), 8 (streams) or slices
+  // Rows sorted by adapter (Order below; kAny only) or NULL: then no tile is
+  // mixed. tiles: of 16, at most.
+  const int32_t *perm, *adapter, *tile0;
+  int64_t tiles;
 };
 
 // A barrier that waits for LDS alone (__syncthreads() would also wait for the
@@ -158,12 +163,13 @@ __device__ __forceinline__ void turn(uint4 (&v)[N], uint4* lds, int lane) {
 // The sums of a tile of 16 rows over slices first, first + step, ...: lane
 // (i, g) gets rank 16 r + i of rows 4 g + q in mine[r][q] (zeros without
 // adapter). With deal > 0 the tile's adapters are dealt to that many waves;
-// the result's bits say which rows this wave holds. id: of row row0 + i, -1
-// behind the last. kAny: rows of x at any 2-byte alignment and of any length
+// the result's bits say which rows this wave holds. id: of the tile's row i, -1
+// behind the last; lrow: the row a lane loads, the tile's row lane / 4 (any
+// one in place of one that does not exist). kAny: rows of x at any 2-byte alignment and of any length
 // (gradients of an odd number of outputs); otherwise 16-byte aligned, a
 // multiple of 32.
 template <int RT, bool kAny>
-__device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t row0, int32_t id,
+__device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t lrow, int32_t id,
                                                 int32_t first, int32_t step, int32_t deal,
                                                 int wave, int lane, uint4* stage,
                                                 floatx4 (&mine)[RT]) {
@@ -174,8 +180,6 @@ __device__ __forceinline__ uint32_t shrink_rows(const ShrinkArgs& s, int64_t row
   for (int q = 0; q < 4; ++q) idq[q] = __shfl(id, 4 * g + q, 64);
 #pragma unroll
   for (int r = 0; r < RT; ++r) mine[r] = floatx4{0, 0, 0, 0};
-  // as loaded: row lane / 4, columns 8 (lane % 4) on
-  const int64_t lrow = row0 + (lane >> 2) < p.m ? row0 + (lane >> 2) : p.m - 1;
   const uint16_t* xl = s.x + lrow * s.ldx + 8 * (lane & 3);
   uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
   uint32_t got = wave == 0 ? 0xFFFFu & ~todo : 0u;
@@ -263,32 +267,43 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
   } lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   // units: slice (or running sum) major, tiles of 16 rows minor
-  const int64_t tiles = (p.m + 15) / 16, unit = xcd_unit();
+  const int64_t tiles = s.tiles, unit = xcd_unit();
   if (unit >= tiles * s.parts) return;
   const int32_t part = static_cast<int32_t>(unit / tiles);
   const int64_t tile = unit - part * tiles, row0 = tile * 16;
-  const int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
-  const int32_t id = row0 + i < p.m ? adapter_of(p, row) : -1;
+  int64_t row = row0 + i < p.m ? row0 + i : p.m - 1;
+  int32_t id = row0 + i < p.m ? adapter_of(p, row) : -1;
   if (part == 0 && threadIdx.x < 16 && p.status != nullptr && p.ids != nullptr && id < 0 &&
       row0 + i < p.m && p.ids[row] != -1)
     atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+  bool exists = row0 + i < p.m;
+  if (kAny && s.perm != nullptr) {
+    if (row0 >= static_cast<int64_t>(s.tile0[p.n_adapters]) * kRowTile) return;
+    const int32_t at = s.perm[row0 + i];
+    exists = at >= 0;
+    row = exists ? at : 0;
+    id = exists ? s.adapter[row0 / kRowTile] : -1;
+  }
+  // of the row a lane loads
+  const int32_t row32 = static_cast<int32_t>(row);
+  const int64_t lrow = __shfl(row32, lane >> 2, 64);
   const bool whole = s.frag != nullptr;
   const int32_t first = whole ? wave : part;
   const int32_t step = whole || s.parts < s.slices ? kStreams : s.slices;
   floatx4 mine[RT];
   const uint32_t got =
-      shrink_rows<RT, kAny>(s, row0, id, first, step, whole ? 0 : blockDim.x >> 6, wave, lane,
+      shrink_rows<RT, kAny>(s, lrow, id, first, step, whole ? 0 : blockDim.x >> 6, wave, lane,
                             lds.stage[wave], mine);
   if (!whole) {
     float* out = s.out + part * p.m * p.rank;
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int q = 0; q < 4; ++q) {
+      const int32_t t = __shfl(exists ? row32 : -1, 4 * g + q, 64);
+      if (t < 0 || !((got >> (4 * g + q)) & 1u)) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t t = row0 + 4 * g + q;
-        if (t < p.m && 16 * r + i < p.rank && (got >> (4 * g + q)) & 1u)
-          out[t * p.rank + 16 * r + i] = mine[r][q];
-      }
+      for (int r = 0; r < RT; ++r)
+        if (16 * r + i < p.rank) out[static_cast<int64_t>(t) * p.rank + 16 * r + i] = mine[r][q];
+    }
     return;
   }
   __syncthreads();
@@ -304,19 +319,22 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-  if (r0 < p.rank && row0 + i < p.m) {
+  if (kAny && s.perm != nullptr && !exists) return;
+  const int64_t place = kAny && s.perm != nullptr ? row : row0 + i;
+  if (r0 < p.rank && exists) {
     const int32_t live = s.slices < kStreams ? s.slices : kStreams;
     for (int32_t w = 0; w < live; ++w)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += lds.sums[w][i][r0 + j];
-    if (s.h != nullptr) __builtin_memcpy(s.h + (row0 + i) * p.rank + r0, v, 32);
+    if (s.h != nullptr) __builtin_memcpy(s.h + row * p.rank + r0, v, 32);
   }
   uint16_t d[3][8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);
 #pragma unroll
   for (int t = 0; t < 3; ++t)
-    s.frag[((tile * 3 + t) * ks + wave) * 64 + lane] = __builtin_bit_cast(uint4, d[t]);
+    s.frag[((place / 16 * 3 + t) * ks + wave) * 64 + 16 * g + place % 16] =
+        __builtin_bit_cast(uint4, d[t]);
 }
 
 // y[t] = base[t] + s[i] B[i] h[t]. Column c of a wave's MFMA tiles is spread so
@@ -654,7 +672,8 @@ __global__ __launch_bounds__(512) void one_pass_kernel(ShrinkArgs sh, ExpandArgs
   FewRows<KS, CT> tile;
   tile.begin(p, id, wave_col, lane);
   floatx4 part[RT];
-  shrink_rows<RT, false>(sh, 0, id, wave, kStreams, 0, wave, lane, lds.stage[wave], part);
+  shrink_rows<RT, false>(sh, (lane >> 2) < rows ? lane >> 2 : rows - 1, id, wave, kStreams, 0, wave,
+                         lane, lds.stage[wave], part);
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -911,8 +930,10 @@ int64_t add_workspace(int64_t m, int64_t n, int64_t k, int32_t rank) {
 template <bool kAny>
 void launch_shrink(const ShrinkArgs& s, hipStream_t st) {
   const LoraArgs& p = s.p;
-  const dim3 grid = xcd_grid((p.m + 15) / 16 * s.parts);
-  const int64_t mixed = p.ids == nullptr ? 1 : p.m < p.n_adapters ? p.m : p.n_adapters;
+  const dim3 grid = xcd_grid(s.tiles * s.parts);
+  const int64_t mixed = p.ids == nullptr || s.perm != nullptr ? 1
+                        : p.m < p.n_adapters                  ? p.m
+                                                              : p.n_adapters;
   const dim3 block(s.frag != nullptr ? 64 * kStreams : mixed < 2 ? 64 : mixed < 8 ? 256 : 512);
   if (p.rank <= 16) hipLaunchKernelGGL((shrink_kernel<1, kAny>), grid, block, 0, st, s);
   else if (p.rank <= 32) hipLaunchKernelGGL((shrink_kernel<2, kAny>), grid, block, 0, st, s);
@@ -973,13 +994,14 @@ void launch_expand(const ExpandArgs& s, hipStream_t st) {
 //    without rows. Few rows (a matter of launches) do without it: there a wave
 //    has all tiles of one adapter.
 // Rows of another adapter never meet in one MFMA chain.
+// g runs over the sorted rows too, so that none of its tiles is mixed (2048
+// rows of 8 adapters at random, rank 32, 4096 -> 4096: the call 86 -> 62 us).
 // A large dy of one rank chunk is read once, g's sums beside dB's (join_kernel
 // adds them), in a launch of its own; else g is the first product on Bt.
 // Measured, 8192 rows, 15360 and 3840 columns, one adapter of rank 16: prepare
 // 4.8 us, dy 68.3 (252 MB, 3.7 TB/s: a CU has some 75 lines under way, which
 // its L1 allows, for 1300 clocks each), join 6.7, dx 28.2 (126 MB), x 16.6,
 // reduce 6.8; with dy read twice 55.6 for g and 70.4 for both sums.
-constexpr int kRowTile = 32;           // sorted rows of a tile
 constexpr int kMaxSorted = 4096;       // adapters prepare_kernel counts in LDS
 
 struct TurnArgs {
@@ -1633,7 +1655,8 @@ extern "C" int32_t binade_lora_add(const binade_lora* l, const uint16_t* x, int6
   const int32_t parts = many ? 1 : shrink_parts(m, p.k);
   float* part = many ? nullptr : static_cast<float*>(workspace);
   uint4* frag = many ? static_cast<uint4*>(workspace) : nullptr;
-  const ShrinkArgs sh{p, x, part, h, frag, ldx, p.k, slices_of(p.k), parts};
+  const ShrinkArgs sh{p, x, part, h, frag, ldx, p.k, slices_of(p.k), parts,
+                      nullptr, nullptr, nullptr, (m + 15) / 16};
   const ExpandArgs ex{p, part, frag, base, y, h, ld_base, ldy, parts,
                       base == nullptr ? 0 : base_dtype == BINADE_BF16 ? 2 : 1,
                       y_dtype == BINADE_BF16, 0};
@@ -1727,7 +1750,7 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
   if (m > 0) {
     if (h == nullptr) {
       launch_shrink<false>(ShrinkArgs{p, x, nullptr, floats(plan.h), pieces(plan.frag), ldx, p.k,
-                                      slices_of(p.k), 1},
+                                      slices_of(p.k), 1, nullptr, nullptr, nullptr, (m + 15) / 16},
                            st);
       h = floats(plan.h);
     }
@@ -1760,7 +1783,8 @@ extern "C" int32_t binade_lora_grad(const binade_lora* l, const uint16_t* x, int
                                   plan.tiles, outer.side[1].blocks});
     } else {
       launch_shrink<true>(ShrinkArgs{pg, dy, whole ? nullptr : part, whole ? g : nullptr, frag,
-                                     ld_dy, p.n, slices_of(p.n), parts},
+                                     ld_dy, p.n, slices_of(p.n), parts, o.perm, o.adapter, o.tile0,
+                                     o.perm != nullptr ? 2 * plan.tiles : (m + 15) / 16},
                           st);
     }
     if (dx != nullptr) {
