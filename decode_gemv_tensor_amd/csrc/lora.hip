@@ -1066,6 +1066,18 @@ __device__ __forceinline__ int32_t first_tile(const Order& o, int32_t a) {
   return o.perm != nullptr ? o.tile0[a] : a == 0 ? 0 : o.tiles;
 }
 
+constexpr int kSortStep = 8;   // rows a thread looks at together
+
+// The ids of rows t to t + 7 as they are; -1 behind the last.
+__device__ __forceinline__ void load_ids(const LoraArgs& p, int64_t t, int32_t (&ids)[kSortStep]) {
+  if (t + kSortStep <= p.m) {
+    __builtin_memcpy(ids, p.ids + t, sizeof(ids));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kSortStep; ++j) ids[j] = t + j < p.m ? p.ids[t + j] : -1;
+}
+
 // A block of 512 collects the rows of adapter a in rising order, behind the
 // tiles of the adapters before it.
 __device__ void order_rows(const LoraArgs& p, int32_t a, int32_t* perm, int32_t* adapter,
@@ -1075,15 +1087,21 @@ __device__ void order_rows(const LoraArgs& p, int32_t a, int32_t* perm, int32_t*
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int32_t e = threadIdx.x; e <= a && e < p.n_adapters; e += 512) counts[e] = 0;
   __syncthreads();
-  for (int64_t t = threadIdx.x; t < p.m; t += 512) {
-    const int32_t id = adapter_of(p, t);
-    const int32_t one = __builtin_amdgcn_readfirstlane(id);
-    const uint64_t all = __ballot(true);
-    if (__ballot(id == one) == all) {   // a run of one adapter: one count
-      if (lane == __builtin_ctzll(all) && one >= 0 && one <= a)
-        atomicAdd(&counts[one], __builtin_popcountll(all));
-    } else if (id >= 0 && id <= a) {
-      atomicAdd(&counts[id], 1);
+  int32_t ids[kSortStep], next[kSortStep];
+  const int64_t mine0 = kSortStep * threadIdx.x;
+  load_ids(p, mine0, next);
+  for (int64_t t0 = 0; t0 < p.m; t0 += 512 * kSortStep) {
+#pragma unroll
+    for (int j = 0; j < kSortStep; ++j) ids[j] = next[j];
+    load_ids(p, t0 + 512 * kSortStep + mine0, next);
+#pragma unroll
+    for (int j = 0; j < kSortStep; ++j) {
+      const int32_t id = ids[j], one = __builtin_amdgcn_readfirstlane(id);
+      if (__ballot(id == one) == ~0ull) {   // a run of one adapter: one count
+        if (lane == 0 && one >= 0 && one <= a) atomicAdd(&counts[one], 64);
+      } else if (id >= 0 && id <= a) {
+        atomicAdd(&counts[id], 1);
+      }
     }
   }
   __syncthreads();
@@ -1102,20 +1120,32 @@ __device__ void order_rows(const LoraArgs& p, int32_t a, int32_t* perm, int32_t*
   for (int32_t e = threadIdx.x; e < tiles; e += 512) adapter[before + e] = a;
   perm += static_cast<int64_t>(before) * kRowTile;
   for (int32_t e = mine + threadIdx.x; e < tiles * kRowTile; e += 512) perm[e] = -1;
+  // kSortStep neighbouring rows a thread
   int32_t at = 0;
-  for (int64_t t0 = 0; t0 < p.m && at < mine; t0 += 512) {
-    const int64_t t = t0 + threadIdx.x;
-    const bool hit = t < p.m && adapter_of(p, t) == a;
-    const uint64_t hits = __ballot(hit);
+  load_ids(p, mine0, next);
+  for (int64_t t0 = 0; t0 < p.m && at < mine; t0 += 512 * kSortStep) {
+    const int64_t t = t0 + mine0;
+    int32_t ahead = 0, all = 0;
+#pragma unroll
+    for (int j = 0; j < kSortStep; ++j) ids[j] = next[j];
+    load_ids(p, t + 512 * kSortStep, next);
+#pragma unroll
+    for (int j = 0; j < kSortStep; ++j) {
+      const uint64_t hits = __ballot(ids[j] == a);
+      ahead += __builtin_popcountll(hits & ((1ull << lane) - 1));
+      all += __builtin_popcountll(hits);
+    }
     __syncthreads();
-    if (lane == 0) sums[wave] = __builtin_popcountll(hits);
+    if (lane == 0) sums[wave] = all;
     __syncthreads();
-    int32_t off = at;
+    int32_t off = at + ahead;
     for (int w = 0; w < 8; ++w) {
       if (w < wave) off += sums[w];
       at += sums[w];
     }
-    if (hit) perm[off + __builtin_popcountll(hits & ((1ull << lane) - 1))] = static_cast<int32_t>(t);
+#pragma unroll
+    for (int j = 0; j < kSortStep; ++j)
+      if (ids[j] == a) perm[off++] = static_cast<int32_t>(t + j);
   }
 }
 
