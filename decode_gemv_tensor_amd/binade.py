@@ -1126,8 +1126,8 @@ def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor,
     if weights.numel() != T * top_k:
         raise ValueError("weights: n_tokens * top_k")
     w = _arg("weights", weights, _F32_ONLY, weights.shape, dev)
-    dy = torch.empty((T * top_k, N), dtype=_TORCH_DTYPE[code], device=dev) if need_dy else None
-    dw = torch.empty(weights.shape, dtype=torch.float32, device=dev)
+    dy = torch.empty_like(y, dtype=_TORCH_DTYPE[code]) if need_dy else None
+    dw = torch.empty_like(w)
     _run("binade_moe_combine_grad", y.data_ptr(), w.data_ptr(), dout.data_ptr(),
          _CODE[dout.dtype], T, top_k, N, _addr(dy), code, dw.data_ptr(), stream)
     return dy, dw
@@ -1184,7 +1184,10 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
         ids = _arg("ids", ids, _I32_ONLY, (m,), dev)
     if base is not None:
         base = _arg("base", base, _FLOATS, (m, n), dev)
-    y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
+    if y is None and base is not None:
+        y = torch.empty_like(base, dtype=_TORCH_DTYPE[code])
+    else:
+        y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
     h = torch.empty((m, rank), dtype=torch.float32, device=dev) if keep_h else None
     ws, at, nb = _scratch(_entry("binade_lora_workspace_bytes")(m, n, k, rank), workspace, dev)
     _run("binade_lora_add", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
@@ -1216,8 +1219,7 @@ def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tens
     if dx_base is not None:
         dx_base = _rows16("dx_base", dx_base, k, dev, m)
     dx = _out_arg("dx", dx, torch.bfloat16, (m, k), dev) if need_dx or dx is not None else None
-    da = torch.empty((n_adapters, rank, k), dtype=_TORCH_DTYPE[code], device=dev)
-    db = torch.empty((n_adapters, n, rank), dtype=_TORCH_DTYPE[code], device=dev)
+    da, db = (torch.empty_like(t, dtype=_TORCH_DTYPE[code]) for t in keep[:2])
     ws, at, nb = _scratch(_entry("binade_lora_grad_workspace_bytes")(m, n, k, rank, n_adapters),
                           workspace, dev)
     _run("binade_lora_grad", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
