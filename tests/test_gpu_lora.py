@@ -132,6 +132,7 @@ ADD = [(1, 64, 64, 8, 1, "one"), (1, 1001, 96, 16, 3, "mix"), (2, 17, 32, 128, 5
        (520, 48, 2336, 16, 3, "mix"), (577, 6700, 96, 8, 3, "mix"), (600, 6661, 544, 40, 5, "runs"),
        (1030, 4200, 64, 72, 4, "mix"), (530, 7200, 288, 128, 2, "one"), (2051, 2050, 2080, 32, 6, "runs"),
        (5, 40, 128, 8, 3, "none"), (600, 6661, 64, 8, 3, "none"),
+       (1500, 3001, 96, 16, 40, "mix"),
        # many rows for one adapter alone
        (130, 16500, 96, 16, 1, "mix"), (257, 8201, 160, 72, 3, "one")]
 
@@ -196,7 +197,8 @@ def test_a_row_does_not_depend_on_the_others(size):
         assert torch.equal(y2, y[t])
 
 
-@pytest.mark.parametrize("size", [(70, 136, 544, 16), (640, 6700, 288, 24), (1100, 64, 4224, 40)],
+@pytest.mark.parametrize("size", [(70, 136, 544, 16), (640, 6700, 288, 24), (1100, 64, 4224, 40),
+                                  (2200, 15400, 96, 16)],
                          ids=lambda c: "x".join(map(str, c)))
 def test_nan_and_infinity_stay_in_their_rows_and_adapters(size):
     m, n, k, rank = size
