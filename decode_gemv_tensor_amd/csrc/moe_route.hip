@@ -786,9 +786,12 @@ using namespace binade;
 
 extern "C" int64_t binade_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_experts) {
   if (!route_sizes_ok(n_tokens, n_experts)) return 0;
-  // fp32 rows take at least as many lanes as bf16 ones
-  return 128 + static_cast<int64_t>(route_shape(n_tokens, n_experts, false).blocks) *
-                   (2 * n_experts + 1) * 4;
+  // Either type's call may have more blocks: fp32 rows take more lanes and with
+  // them more waves, but above 1024 waves a block holds sixteen instead of four
+  // (8192 tokens of 128 experts: 256 blocks in bf16, 128 in fp32).
+  const int64_t f32 = route_shape(n_tokens, n_experts, false).blocks,
+                bf16 = route_shape(n_tokens, n_experts, true).blocks;
+  return 128 + (f32 > bf16 ? f32 : bf16) * (2 * n_experts + 1) * 4;
 }
 
 extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t ld, int64_t n_tokens,

@@ -163,3 +163,29 @@ int main(void) {
                                           text=True).stdout.split()]
     assert got == [ctypes.sizeof(B.LoraDesc), B.LoraDesc.rank.offset, B.LoraDesc.a.offset,
                    B.LoraDesc.scale.offset]
+
+
+def _router_blocks(tokens, experts, bf16):
+    """Blocks of the router's kernel, each of which leaves a row of partial
+    counts and sums. lanes: those of a token; a wave has 64 / lanes tokens."""
+    lanes = 8 if experts <= 128 else 16 if experts <= 256 else 32 if experts <= 512 else 64
+    if not bf16 and 64 < experts <= 512:
+        lanes *= 2
+    waves = -(-tokens * lanes // 64)
+    a_block = 1 if waves <= 1 else 4 if waves <= 1024 else 16
+    return max(1, min(256, -(-waves // a_block)))
+
+
+@pytest.mark.parametrize("experts", [1, 64, 65, 128, 129, 256, 257, 512, 513, 1024])
+def test_router_workspace_holds_the_blocks_of_both_types(experts):
+    """More waves may mean fewer blocks (four waves a block up to 1024 waves,
+    sixteen behind), so neither type's size covers the other's everywhere."""
+    f = B.lib().binade_moe_route_workspace_bytes
+    at = {0, 1 << 20, 1 << 30}
+    for lanes in (8, 16, 32, 64):
+        for waves in (1, 1024, 4096):       # the switches, and where the blocks are full
+            at.update(range(max(0, waves * 64 // lanes - 70), waves * 64 // lanes + 70))
+    at.update(range(0, 70000, 97))
+    for tokens in sorted(at):
+        blocks = max(_router_blocks(tokens, experts, bf16) for bf16 in (False, True))
+        assert f(tokens, experts) >= 128 + 4 * blocks * (2 * experts + 1), tokens

@@ -453,3 +453,27 @@ def test_a_routed_layer_and_its_router_gradient():
     assert abs(float(loss.detach()) - float(r.loss)) <= 64 * U * float(loss.detach())
     ((ref * dout.double()).sum() + 0.01 * loss).backward()
     assert rel_norm(q.grad, grad.cpu()) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_a_workspace_of_the_size_asked_for_holds_it_all(dtype):
+    """The caller's workspace, exactly as large as asked for, inside a larger
+    buffer whose other bytes stay: on both sides of the step from four waves a
+    block to sixteen, for every number of lanes a token."""
+    for T, E, k in [(8192, 128, 8), (8193, 128, 8), (4096, 128, 8), (4000, 256, 8), (2049, 256, 8),
+                    (2048, 512, 4), (1025, 512, 4), (1024, 1024, 8), (5, 1024, 64), (9000, 60, 2),
+                    (0, 16, 2)]:
+        say("workspace", T, E, k, dtype)
+        x = make_logits(T, E, T + E, dtype).to(DEV)
+        need = B.lib().binade_moe_route_workspace_bytes(T, E)
+        pool = torch.full((2 * need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+        assert pool.data_ptr() % 256 == 0
+        got = B.moe_route(x, k, workspace=pool[256:256 + need])
+        want = B.moe_route(x, k)
+        assert bool((pool[:256] == 0xFF).all()) and bool((pool[256 + need:] == 0xFF).all())
+        for name in ("idx", "weights", "counts", "prob_sum", "loss"):
+            assert torch.equal(getattr(got, name), getattr(want, name)), name
+        assert int(got.counts[E]) == T and int(got.counts[:E].sum()) == T * k
+        with pytest.raises(B.BinadeError) as e:
+            B.moe_route(x, k, workspace=pool[256:256 + need - 1])
+        assert e.value.code == B.ENOSPACE
