@@ -269,10 +269,20 @@ __device__ __forceinline__ void best8(const Key (&key)[V], Key (&best)[8]) {
 }
 
 // ------------------------------------------------------------------ values
-// exp(d) for d <= 0 (-inf: 0), or NaN. The product's rounding costs |d| 2^-24
-// of the value, as much as that of the difference d itself.
+// exp(d) for d <= 0 (-inf: 0), or NaN. log2 e is taken as the sum of two fp32:
+// the first alone is 1.3e-8 too small, which moves every small probability the
+// same way. What is left is the product's rounding, |d| 2^-24 of the value to
+// either side, as much as that of the difference d itself.
 __device__ __forceinline__ float exp_of(float d) {
-  return __builtin_amdgcn_exp2f(d * 1.44269502e+0f);
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, 1.44269502e+0f, d * 1.92596303e-8f));
+}
+
+// 1 / v within 2^-24 and a little: a Newton step behind the instruction, which
+// is one step off. v is at least 2^-10 here; 0 (a row that does not count)
+// gives NaN, which nothing takes.
+__device__ __forceinline__ float inverse(float v) {
+  const float r = __builtin_amdgcn_rcpf(v);
+  return __builtin_fmaf(__builtin_fmaf(-v, r, 1.0f), r, r);
 }
 
 // ----------------------------------------------------------------- forward
@@ -369,7 +379,7 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
       total += v[j];
     }
     total = group_sum<G>(total);
-    const float inv = __builtin_amdgcn_rcpf(total);   // 1 step off at most
+    const float inv = inverse(total);
     if (stats) {
       if (__ballot(!counted) == 0) {
 #pragma unroll
@@ -416,7 +426,7 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
     }
     if (p.renorm) taken = group_sum<G>(taken);
     // a NaN among the logits is one of every weight
-    const float f = p.renorm ? (total == total ? __builtin_amdgcn_rcpf(taken) : total) : inv;
+    const float f = p.renorm ? (total == total ? inverse(taken) : total) : inv;
     if (in) {
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
@@ -646,7 +656,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
       v[j] = exp_of(x.value(j) - top);
       total += v[j];
     }
-    const float inv = __builtin_amdgcn_rcpf(group_sum<G>(total));   // 1 step off at most
+    const float inv = inverse(group_sum<G>(total));
     float u[V], hits[V], chosen = 0.0f, mean = 0.0f;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
@@ -660,7 +670,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
       mean = __builtin_fmaf(u[j], v[j], mean);
     }
     if (p.renorm) {
-      const float f = __builtin_amdgcn_rcpf(group_sum<G>(chosen));
+      const float f = inverse(group_sum<G>(chosen));
       mean = group_sum<G>(mean) * f;
 #pragma unroll
       for (int j = 0; j < V; ++j) u[j] = hits[j] != 0.0f ? (u[j] - hits[j] * mean) * f : 0.0f;

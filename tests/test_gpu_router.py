@@ -477,3 +477,27 @@ def test_a_workspace_of_the_size_asked_for_holds_it_all(dtype):
         with pytest.raises(B.BinadeError) as e:
             B.moe_route(x, k, workspace=pool[256:256 + need - 1])
         assert e.value.code == B.ENOSPACE
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_small_probabilities_do_not_lean_to_one_side(dtype):
+    """Rows (0, -d) for d in 8..80, weights not renormalised: w1 is
+    e / (1 + e) with e = exp(-d). The difference d is exact; its product with
+    log2 e rounds by |d| u of e to either side, and what may lean to one side
+    is at most the exponential's step (2 u), the sum (u), the reciprocal and
+    the last product (u together, half steps either way): 4 u of w1. So every
+    error is within (|d| + 8) u, and the mean of error / d is within 4 u times
+    the mean of 1 / d, and four standard deviations of |d| u / sqrt(3) each."""
+    g = gen(17)
+    d = (8 + 72 * torch.rand(20000, generator=g)).to(dtype)
+    x = torch.stack([torch.zeros_like(d), -d], 1)
+    r = B.moe_route(x.to(DEV), 2, renormalize=False, stats=False)
+    assert r.idx.cpu().tolist() == [[0, 1]] * d.numel()
+    d = d.double()
+    want = torch.exp(-d) / (1 + torch.exp(-d))
+    off = (r.weights[:, 1].cpu().double() - want) / want
+    say("leaning", float((off / d).mean()), float((off.abs() / ((d + 8) * U)).max()))
+    assert bool((off.abs() <= (d + 8) * U).all())
+    n = d.unique().numel()              # equal values err alike
+    mean = float((off / d).mean())
+    assert abs(mean) <= 4 * U * float((1 / d).mean()) + 4 * U / math.sqrt(3 * n)
