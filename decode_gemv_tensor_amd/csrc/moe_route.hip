@@ -31,6 +31,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kSorted = 8;        // slots the sorting choice fills
 constexpr int32_t kBlocks = 256;  // at most: each leaves one row of partial sums
+constexpr int64_t kHead = 192;    // bytes of a workspace before these: ticket, shares of the loss
 
 // ------------------------------------------------------ steps across lanes
 template <int kCtrl>
@@ -296,28 +297,38 @@ struct RouteArgs {
   float* loss;
   int32_t* part_counts;   // [blocks, n_experts + 1]
   float* part_prob;       // [blocks, n_experts]
-  float* part_loss;       // [16] of route_stats_kernel's blocks
+  double* part_loss;      // [16] of route_stats_kernel's blocks
   uint32_t* ticket;       // of the same: which block is the last
   int64_t ld, n_tokens;
   int32_t n_experts, top_k;
   bool renorm, vec;
 };
 
+// Sums over waves, blocks and experts run in fp64: there are few, and a chain
+// of 16 or 32 fp32 additions of like size would cost the summed probabilities
+// and the loss more than everything before it (2048 tokens of 128 experts:
+// 6.1e-8 off in place of 2.7e-8).
+
 // The sum of a block's values by a fixed tree, in thread 0. Whole waves.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  const float part = group_sum<64>(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = part;
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  butterfly<64>([&](auto step) {
+    uint64_t a, b;
+    pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, v), a, b);
+    v = __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
+  });
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  float sum = 0.0f;
+  double sum = 0.0;
   if (threadIdx.x == 0)
     for (uint32_t w = 0; w < blockDim.x / 64; ++w) sum += red[w];
   return sum;
 }
 
-// An expert's share of the loss but for the factor E.
-__device__ __forceinline__ float loss_term(int32_t count, float prob, int32_t rows, int32_t top_k) {
-  const float r = static_cast<float>(rows > 0 ? rows : 1);
-  return static_cast<float>(count) / (static_cast<float>(top_k) * r) * (prob / r);
+// The loss from sum_e counts[e] * prob_sum[e].
+__device__ __forceinline__ float loss_of(double sum, int32_t n_experts, int32_t top_k,
+                                         int32_t rows) {
+  const double r = rows > 0 ? rows : 1;
+  return static_cast<float>(n_experts * sum / (top_k * r * r));
 }
 
 // Measured: 65536 tokens of 256 bf16 experts, top 8, counts and sums, 21.4 us
@@ -332,7 +343,7 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
   constexpr int kExperts = G * V;
   __shared__ int32_t counts[kExperts + 1];
   __shared__ float prob[16][kExperts];
-  __shared__ float red[16];
+  __shared__ double red[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int l = lane & (G - 1);
   const int32_t e0 = l * V;
@@ -461,19 +472,20 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
   }
   __syncthreads();
   const bool alone = gridDim.x == 1;
-  float term = 0.0f;
+  double term = 0.0;
   for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) {
     (alone ? p.counts : p.part_counts + static_cast<int64_t>(blockIdx.x) * (p.n_experts + 1))[e] =
         counts[e];
     if (e == p.n_experts) continue;
-    float s = 0.0f;
+    double s = 0.0;
     for (int w = 0; w < waves; ++w) s += prob[w][e];
-    (alone ? p.prob_sum : p.part_prob + static_cast<int64_t>(blockIdx.x) * p.n_experts)[e] = s;
-    term += loss_term(counts[e], s, counts[p.n_experts], p.top_k);
+    (alone ? p.prob_sum : p.part_prob + static_cast<int64_t>(blockIdx.x) * p.n_experts)[e] =
+        static_cast<float>(s);
+    term += counts[e] * s;
   }
   if (alone) {
     term = block_sum(term, red);
-    if (threadIdx.x == 0) p.loss[0] = static_cast<float>(p.n_experts) * term;
+    if (threadIdx.x == 0) p.loss[0] = loss_of(term, p.n_experts, p.top_k, counts[p.n_experts]);
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
     *p.ticket = 0;
   }
@@ -484,8 +496,8 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
 // to end adds the blocks' shares of the loss, in block order.
 __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t blocks) {
   __shared__ int32_t count_s[16][64];
-  __shared__ float sum_s[16][64];
-  __shared__ float red[16];
+  __shared__ double sum_s[16][64];
+  __shared__ double red[16];
   __shared__ int32_t rows_s;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t e = blockIdx.x * 64 + lane;
@@ -497,7 +509,7 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
     if (lane == 0) rows_s = rows;
   }
   int32_t c = 0;
-  float s = 0.0f;
+  double s = 0.0;
   if (e < p.n_experts) {
     constexpr int kAhead = 16;   // rows of partial sums on their way at once
     const int32_t* pc = p.part_counts + e;
@@ -526,15 +538,15 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
   count_s[wave][lane] = c;
   sum_s[wave][lane] = s;
   __syncthreads();
-  float term = 0.0f;
+  double term = 0.0;
   if (wave == 0 && e < p.n_experts) {
     for (int q = 1; q < 16; ++q) {
       c += count_s[q][lane];
       s += sum_s[q][lane];
     }
     p.counts[e] = c;
-    p.prob_sum[e] = s;
-    term = loss_term(c, s, rows_s, p.top_k);
+    p.prob_sum[e] = static_cast<float>(s);
+    term = c * s;
   }
   term = block_sum(term, red);
   if (threadIdx.x != 0) return;
@@ -544,11 +556,11 @@ __global__ __launch_bounds__(1024) void route_stats_kernel(RouteArgs p, int32_t 
     __threadfence();
     if (atomicAdd(p.ticket, 1u) != gridDim.x - 1) return;
     __threadfence();
-    term = 0.0f;
+    term = 0.0;
     for (uint32_t b = 0; b < gridDim.x; ++b)
       term += __hip_atomic_load(p.part_loss + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  p.loss[0] = static_cast<float>(p.n_experts) * term;
+  p.loss[0] = loss_of(term, p.n_experts, p.top_k, rows_s);
 }
 
 // ---------------------------------------------------------------- backward
@@ -801,7 +813,7 @@ extern "C" int64_t binade_moe_route_workspace_bytes(int64_t n_tokens, int32_t n_
   // (8192 tokens of 128 experts: 256 blocks in bf16, 128 in fp32).
   const int64_t f32 = route_shape(n_tokens, n_experts, false).blocks,
                 bf16 = route_shape(n_tokens, n_experts, true).blocks;
-  return 128 + (f32 > bf16 ? f32 : bf16) * (2 * n_experts + 1) * 4;
+  return kHead + (f32 > bf16 ? f32 : bf16) * (2 * n_experts + 1) * 4;
 }
 
 extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t ld, int64_t n_tokens,
@@ -834,8 +846,8 @@ extern "C" int32_t binade_moe_route(const void* logits, int32_t dtype, int64_t l
   p.prob_sum = prob_sum;
   p.loss = loss;
   p.ticket = static_cast<uint32_t*>(workspace);
-  p.part_loss = static_cast<float*>(workspace) + 16;
-  p.part_counts = static_cast<int32_t*>(workspace) + 32;
+  p.part_loss = static_cast<double*>(workspace) + 8;
+  p.part_counts = static_cast<int32_t*>(workspace) + kHead / 4;
   p.part_prob = reinterpret_cast<float*>(p.part_counts + static_cast<int64_t>(shape.blocks) *
                                                              (n_experts + 1));
   p.ld = ld;

@@ -501,3 +501,19 @@ def test_small_probabilities_do_not_lean_to_one_side(dtype):
     n = d.unique().numel()              # equal values err alike
     mean = float((off / d).mean())
     assert abs(mean) <= 4 * U * float((1 / d).mean()) + 4 * U / math.sqrt(3 * n)
+
+
+def test_the_loss_is_that_of_its_counts_and_sums():
+    """The summed probabilities are rounded once, for the output, and so is the
+    loss, which comes from them unrounded: it is within u + u of the formula
+    with the returned counts and sums."""
+    for T, E, k, dtype in [(2048, 128, 8, F32), (8192, 128, 8, BF), (4000, 256, 8, BF),
+                           (3000, 512, 4, F32), (60, 64, 6, F32), (700, 1000, 2, BF), (1, 8, 2, F32)]:
+        for seed in range(4):
+            x = make_logits(T, E, 100 * seed + E, dtype)
+            r = B.moe_route(x.to(DEV), k)
+            c, ps = r.counts.cpu().double(), r.prob_sum.cpu().double()
+            want = E * float((c[:E] * ps).sum()) / (k * T * T)
+            say("loss", T, E, (float(r.loss) - want) / want / U)
+            assert abs(float(r.loss) - want) <= 2.01 * U * want
+            assert int(c[E]) == T
