@@ -1032,12 +1032,18 @@ _CODE = {torch.float32: F32, torch.bfloat16: BF16}
 _TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
 
-def _logits_arg(t: torch.Tensor) -> torch.Tensor:
+def _logits_arg(t: torch.Tensor):
+    """(logits [n_tokens, n_experts], their row stride); copied if a row's
+    values do not lie side by side or rows overlap. A single row's stride is
+    of no matter (torch calls it contiguous whatever it is)."""
     if t.dtype not in _CODE:
         raise TypeError(f"logits: {t.dtype}, expected bf16 or fp32")
     if t.dim() != 2:
         raise ValueError("logits: [n_tokens, n_experts]")
-    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+    rows, cols = t.shape
+    if t.stride(1) == 1 and rows > 1 and t.stride(0) >= cols:
+        return t, t.stride(0)
+    return t.contiguous(), cols
 
 
 @dataclass
@@ -1059,7 +1065,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
     """binade_moe_route: each token's top_k experts (idx int32 [T, top_k], for
     r4_moe_gemv) and their weights (fp32 [T, top_k], for moe_combine) from
     logits [T, E]; valid: bool or uint8 [T], False for padding."""
-    logits = _logits_arg(logits)
+    logits, ld = _logits_arg(logits)
     dev = logits.device
     T, E = logits.shape
     if valid is not None:
@@ -1074,7 +1080,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
         out.prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
         out.loss = torch.empty(1, dtype=torch.float32, device=dev)
         ws, at, nb = _scratch(_entry("binade_moe_route_workspace_bytes")(T, E), workspace, dev)
-    _run("binade_moe_route", logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), T, E,
+    _run("binade_moe_route", logits.data_ptr(), _CODE[logits.dtype], ld, T, E,
          top_k, 1 if renormalize else 0, _addr(valid), out.idx.data_ptr(),
          out.weights.data_ptr(), _addr(out.counts), _addr(out.prob_sum), _addr(out.loss), at, nb,
          stream)
@@ -1089,7 +1095,7 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
                    stream=None) -> torch.Tensor:
     """binade_moe_route_grad: the gradient of the logits from that of the
     weights and (counts and dloss together) of the balance loss."""
-    logits = _logits_arg(logits)
+    logits, ld = _logits_arg(logits)
     dev = logits.device
     T, E = logits.shape
     code = _CODE[logits.dtype] if out_dtype is None else _dtype_code(out_dtype)
@@ -1105,7 +1111,7 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
         counts = _arg("counts", counts, _I32_ONLY, (E + 1,), dev)
         dloss = _arg("dloss", dloss.reshape(-1), (torch.float32,), (1,), dev)
     dlogits = _out_arg("dlogits", dlogits, _TORCH_DTYPE[code], (T, E), dev)
-    _run("binade_moe_route_grad", logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), T, E,
+    _run("binade_moe_route_grad", logits.data_ptr(), _CODE[logits.dtype], ld, T, E,
          top_k, 1 if renormalize else 0, idx.data_ptr(), _addr(dweights), _addr(counts),
          _addr(dloss), dlogits.data_ptr(), code, E, _status_arg(status, dev), stream)
     return dlogits
@@ -1134,19 +1140,27 @@ def moe_combine_grad(y: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor,
 
 
 # ---------------------------------------------------------------- adapters
-def _rows16(name: str, t: torch.Tensor, cols: int, device, m: int | None = None) -> torch.Tensor:
-    """bf16 [m, cols] rows at a 16-byte aligned stride (copied otherwise)."""
+_MAX_STRIDE = 1 << 24
+
+
+def _rows16(name: str, t: torch.Tensor, cols: int, device, m: int | None = None):
+    """(bf16 [m, cols] rows at a 16-byte aligned stride that the calls take,
+    copied otherwise; that stride). A single row's stride is of no matter
+    (torch calls it contiguous whatever it is)."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: {t.dtype}, expected bf16")
     if t.dim() != 2 or t.shape[1] != cols or (m is not None and t.shape[0] != m):
         raise ValueError(f"{name}: shape {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
-    if t.stride(1) != 1 or t.stride(0) < cols or t.stride(0) % 8 or t.data_ptr() % 16:
-        t = t.contiguous()
-        if t.data_ptr() % 16:           # a contiguous view that starts off 16 bytes
-            t = t.clone()
-    return t
+    ld = t.stride(0)
+    if t.shape[0] > 1 and t.stride(1) == 1 and cols <= ld <= _MAX_STRIDE and ld % 8 == 0 \
+            and t.data_ptr() % 16 == 0:
+        return t, ld
+    t = t.contiguous()
+    if t.data_ptr() % 16:               # a contiguous view that starts off 16 bytes
+        t = t.clone()
+    return t, cols
 
 
 def _lora_desc(a, b, scale, device):
@@ -1178,7 +1192,7 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
     code = _dtype_code(out_dtype)
     dev = x.device
     d, keep, n, k, rank, _ = _lora_desc(a, b, scale, dev)
-    x = _rows16("x", x, k, dev)
+    x, ldx = _rows16("x", x, k, dev)
     m = x.shape[0]
     if ids is not None:
         ids = _arg("ids", ids, _I32_ONLY, (m,), dev)
@@ -1190,7 +1204,7 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tenso
         y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
     h = torch.empty((m, rank), dtype=torch.float32, device=dev) if keep_h else None
     ws, at, nb = _scratch(_entry("binade_lora_workspace_bytes")(m, n, k, rank), workspace, dev)
-    _run("binade_lora_add", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
+    _run("binade_lora_add", ctypes.byref(d), x.data_ptr(), m, ldx, _addr(ids),
          _addr(base), n, F32 if base is None else _CODE[base.dtype], y.data_ptr(), n, code,
          _addr(h), at, nb, _status_arg(status, dev), stream)
     return (y, h) if keep_h else y
@@ -1209,21 +1223,22 @@ def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tens
     code = _dtype_code(grad_dtype)
     dev = x.device
     d, keep, n, k, rank, n_adapters = _lora_desc(a, b, scale, dev)
-    x = _rows16("x", x, k, dev)
+    x, ldx = _rows16("x", x, k, dev)
     m = x.shape[0]
     if ids is not None:
         ids = _arg("ids", ids, _I32_ONLY, (m,), dev)
     dy = _arg("dy", dy, _BF16_ONLY, (m, n), dev)
     if h is not None:
         h = _arg("h", h, _F32_ONLY, (m, rank), dev)
+    ld_dx_base = 0
     if dx_base is not None:
-        dx_base = _rows16("dx_base", dx_base, k, dev, m)
+        dx_base, ld_dx_base = _rows16("dx_base", dx_base, k, dev, m)
     dx = _out_arg("dx", dx, torch.bfloat16, (m, k), dev) if need_dx or dx is not None else None
     da, db = (torch.empty_like(t, dtype=_TORCH_DTYPE[code]) for t in keep[:2])
     ws, at, nb = _scratch(_entry("binade_lora_grad_workspace_bytes")(m, n, k, rank, n_adapters),
                           workspace, dev)
-    _run("binade_lora_grad", ctypes.byref(d), x.data_ptr(), m, x.stride(0), _addr(ids),
-         dy.data_ptr(), n, _addr(h), _addr(dx_base), 0 if dx_base is None else dx_base.stride(0),
+    _run("binade_lora_grad", ctypes.byref(d), x.data_ptr(), m, ldx, _addr(ids),
+         dy.data_ptr(), n, _addr(h), _addr(dx_base), ld_dx_base,
          _addr(dx), k, da.data_ptr(), db.data_ptr(), code, at, nb, _status_arg(status, dev),
          stream)
     return dx, da, db

@@ -189,3 +189,43 @@ def test_router_workspace_holds_the_blocks_of_both_types(experts):
     for tokens in sorted(at):
         blocks = max(_router_blocks(tokens, experts, bf16) for bf16 in (False, True))
         assert f(tokens, experts) >= 128 + 4 * blocks * (2 * experts + 1), tokens
+
+
+def _one_row_views(k, dtype):
+    """Single rows of k values that torch calls contiguous, at row strides
+    that the calls do not take."""
+    column = torch.arange(k, dtype=torch.float32).to(dtype).reshape(k, 1)
+    wide = torch.zeros(3, k + 4, dtype=dtype)
+    wide[:, :k] = column.t()
+    far = torch.zeros((1 << 24) // k + 2, k, dtype=dtype)
+    far[-1] = column[:, 0]
+    return [column.t(), wide[:1, :k], far[None][:, -1], column.t().contiguous().expand(1, k)]
+
+
+def test_a_single_rows_stride_is_of_no_matter():
+    cpu = torch.device("cpu")
+    for t in _one_row_views(64, torch.bfloat16):
+        rows, ld = B._rows16("x", t, 64, cpu)
+        assert ld == 64 and rows.data_ptr() % 16 == 0 and torch.equal(rows, t)
+    for t in _one_row_views(64, torch.float32):
+        rows, ld = B._logits_arg(t)
+        assert ld == 64 and torch.equal(rows, t)
+    off = torch.arange(72, dtype=torch.float32).to(torch.bfloat16)[1:65].as_strided((1, 64), (3, 1))
+    rows, ld = B._rows16("x", off, 64, cpu)
+    assert ld == 64 and rows.data_ptr() % 16 == 0 and torch.equal(rows, off)
+
+
+def test_rows_at_strides_that_the_calls_do_not_take_are_copied():
+    cpu = torch.device("cpu")
+    big = torch.zeros(2 << 24, dtype=torch.bfloat16)
+    for ld, copied in ((64, False), (72, False), (68, True), (0, True), (1 << 24, False),
+                       ((1 << 24) + 8, True)):
+        t = big.as_strided((2, 64), (ld, 1))
+        rows, got = B._rows16("x", t, 64, cpu)
+        assert (rows.data_ptr() != t.data_ptr()) == copied
+        assert got == (64 if copied else ld)
+    x = torch.arange(40, dtype=torch.float32)
+    for t, ld in ((x.reshape(5, 8), 8), (x.reshape(5, 8)[:, :3], 8), (x.reshape(8, 5).t(), 8),
+                  (x.as_strided((5, 8), (0, 1)), 8), (x[:5, None], 1), (x[:0].reshape(0, 8), 8)):
+        rows, got = B._logits_arg(t)
+        assert got == ld and torch.equal(rows, t)

@@ -511,3 +511,26 @@ def test_beside_the_packed_products():
         rx, ra, rb = ref_grad(d, ref_add(d)[1], base=up.cpu())
         assert rel(da, ra) <= chain(n) + chain(3 * m) and rel(db, rb) <= chain(k) + chain(3 * m)
         assert rel(dx, rx) <= 2.0 ** -8
+
+
+def test_one_row_at_any_stride():
+    """A single row's stride is of no matter, whatever torch says it is."""
+    k, n, rank = 64, 72, 8
+    d = make(1, n, k, rank, 2, seed=6, ids="one")
+    v = to_dev(d)
+    want = B.lora_add(v["x"], v["a"], v["b"], None, base=v["base"])
+    grads = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"], dx_base=v["x"])
+    wide = torch.zeros(3, k + 4, dtype=BF, device=DEV)
+    wide[:1, :k] = v["x"]
+    far = torch.zeros(1, (1 << 24) // k + 2, k, dtype=BF, device=DEV)
+    far[:, -1] = v["x"]
+    for x in (v["x"].reshape(k, 1).t(), wide[:1, :k], far[:, -1]):
+        say("one row", x.stride())
+        assert torch.equal(B.lora_add(x, v["a"], v["b"], None, base=v["base"]), want)
+        got = B.lora_grad(x, v["a"], v["b"], None, v["dy"], dx_base=x)
+        assert all(torch.equal(p, q) for p, q in zip(got, grads))
+        # of the other operands
+        got = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"].reshape(n, 1).t(), dx_base=v["x"])
+        assert all(torch.equal(p, q) for p, q in zip(got, grads))
+        assert torch.equal(B.lora_add(v["x"], v["a"], v["b"], None,
+                                      base=v["base"].reshape(n, 1).t()), want)

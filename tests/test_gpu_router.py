@@ -517,3 +517,15 @@ def test_the_loss_is_that_of_its_counts_and_sums():
             say("loss", T, E, (float(r.loss) - want) / want / U)
             assert abs(float(r.loss) - want) <= 2.01 * U * want
             assert int(c[E]) == T
+
+
+def test_one_token_at_any_stride():
+    E, k = 60, 4
+    x = make_logits(1, E, 9, F32).to(DEV)
+    want = B.moe_route(x, k)
+    dw = torch.ones(1, k, device=DEV)
+    grad = B.moe_route_grad(x, want.idx, dweights=dw, renormalize=False)
+    for t in (x.reshape(E, 1).t(), x.as_strided((1, E), (3, 1))):
+        got = B.moe_route(t, k)
+        assert torch.equal(got.idx, want.idx) and torch.equal(got.weights, want.weights)
+        assert torch.equal(B.moe_route_grad(t, want.idx, dweights=dw, renormalize=False), grad)
