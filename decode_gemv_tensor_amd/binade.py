@@ -961,13 +961,16 @@ def _on_device(fn):
     as a raw handle: temporaries and a default stream are that device's even
     when another one is current, and a given stream is torch's current one
     meanwhile (as in _on_stream)."""
+    lead = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def wrapper(first, *args, stream=None, **kw):
+    def wrapper(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(lead)
         index = first.get_device() if isinstance(first, torch.Tensor) else -1
         if index < 0:
             raise ValueError(f"{fn.__name__} takes device tensors")
         if stream is None and index == torch._C._cuda_getDevice():
-            return fn(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
+            return fn(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kw)
         with torch.cuda.device(index):
             if stream is None:
                 stream = torch.cuda.current_stream()
@@ -976,7 +979,7 @@ def _on_device(fn):
             elif stream.device_index != index:
                 raise ValueError("stream of another device")
             with torch.cuda.stream(stream):
-                return fn(first, *args, stream=stream.cuda_stream, **kw)
+                return fn(*args, stream=stream.cuda_stream, **kw)
     return wrapper
 
 

@@ -229,3 +229,16 @@ def test_rows_at_strides_that_the_calls_do_not_take_are_copied():
                   (x.as_strided((5, 8), (0, 1)), 8), (x[:5, None], 1), (x[:0].reshape(0, 8), 8)):
         rows, got = B._logits_arg(t)
         assert got == ld and torch.equal(rows, t)
+
+
+def test_bindings_take_every_argument_by_name():
+    """The first one too: host tensors get as far as the check for them."""
+    x, z = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 16)
+    a, b = torch.zeros(1, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 40, 8, dtype=torch.bfloat16)
+    for call, kw in ((B.lora_add, dict(x=x, a=a, b=b)),
+                     (B.lora_grad, dict(b=b, a=a, x=x, ids=None, dy=x)),
+                     (B.moe_route, dict(top_k=2, logits=z)),
+                     (B.moe_route_grad, dict(logits=z, idx=z)),
+                     (B.moe_combine_grad, dict(y=z, weights=z, dout=z, top_k=1))):
+        with pytest.raises(ValueError, match="takes device tensors"):
+            call(**kw)

@@ -534,3 +534,14 @@ def test_one_row_at_any_stride():
         assert all(torch.equal(p, q) for p, q in zip(got, grads))
         assert torch.equal(B.lora_add(v["x"], v["a"], v["b"], None,
                                       base=v["base"].reshape(n, 1).t()), want)
+
+
+def test_arguments_by_name():
+    v = to_dev(make(5, 40, 64, 8, 2, seed=2))
+    y, h = B.lora_add(v["x"], v["a"], v["b"], v["ids"], keep_h=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {"stream": s}, {"stream": s.cuda_stream}):
+        got = B.lora_add(a=v["a"], b=v["b"], x=v["x"], ids=v["ids"], keep_h=True, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], y) and torch.equal(got[1], h)
