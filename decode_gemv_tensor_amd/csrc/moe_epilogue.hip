@@ -220,7 +220,7 @@ extern "C" int32_t binade_moe_combine_grad(const float* y, const float* weights,
   if ((dout_dtype != BINADE_F32 && dout_dtype != BINADE_BF16) ||
       (dy_dtype != BINADE_F32 && dy_dtype != BINADE_BF16))
     return BINADE_EINVAL;
-  if (n_tokens * top_k > (1ll << 30) || n > (1ll << 30)) return BINADE_EUNSUPPORTED;
+  if (n_tokens > (1ll << 30) / top_k || n > (1ll << 30)) return BINADE_EUNSUPPORTED;
   if (n_tokens == 0) return BINADE_OK;
   if (dweights == nullptr || weights == nullptr) return BINADE_EINVAL;
   if (n > 0 && (y == nullptr || dout == nullptr)) return BINADE_EINVAL;

@@ -546,8 +546,8 @@ int32_t binade_moe_combine(const float *y, const float *weights,
  * binade_moe_combine takes them. dout: device fp32 or bf16 [n_tokens, n] per
  * dout_dtype. dy: device [n_tokens*top_k, n] fp32 or bf16 per dy_dtype, or
  * NULL (the experts are frozen and nothing below them learns). dweights:
- * device fp32 [n_tokens*top_k]. EINVAL: top_k outside 1..64, sizes, null
- * pointers. */
+ * device fp32 [n_tokens*top_k]. EINVAL: top_k outside 1..64, negative
+ * sizes, null pointers. EUNSUPPORTED: n_tokens * top_k or n above 2^30. */
 int32_t binade_moe_combine_grad(const float *y, const float *weights,
                                 const void *dout, int32_t dout_dtype,
                                 int64_t n_tokens, int32_t top_k, int64_t n,
@@ -578,7 +578,8 @@ int32_t binade_moe_combine_grad(const float *y, const float *weights,
  * bits. workspace: device, 16-byte aligned, binade_moe_route_workspace_bytes
  * bytes (0 and NULL without counts); not read before written; calls that
  * overlap need their own. n_experts in 1..1024, top_k in 1..min(64,
- * n_experts), ld >= n_experts, else EINVAL; ENOSPACE: workspace_bytes. */
+ * n_experts), n_tokens in 0..2^30, ld >= n_experts, else EINVAL; ENOSPACE:
+ * workspace_bytes; EUNSUPPORTED: a workspace that is not 16-byte aligned. */
 int32_t binade_moe_route(const void *logits, int32_t dtype, int64_t ld,
                          int64_t n_tokens, int32_t n_experts, int32_t top_k,
                          int32_t renormalize, const uint8_t *valid,

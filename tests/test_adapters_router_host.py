@@ -242,3 +242,13 @@ def test_bindings_take_every_argument_by_name():
                      (B.moe_combine_grad, dict(y=z, weights=z, dout=z, top_k=1))):
         with pytest.raises(ValueError, match="takes device tensors"):
             call(**kw)
+
+
+def test_combine_grad_refuses_more_slots_than_it_counts():
+    """Also where the product of tokens and slots does not fit 64 bits."""
+    L = B.lib()
+    for t, k, n in (((1 << 30) + 1, 1, 8), ((1 << 24) + 1, 64, 8), ((1 << 30) // 3 + 1, 3, 8),
+                    (1 << 58, 64, 8), (1 << 62, 4, 8), ((1 << 63) - 1, 64, 8),
+                    ((1 << 63) // 64 + 1, 64, 8), (2, 2, (1 << 30) + 1)):
+        assert L.binade_moe_combine_grad(GOOD, GOOD, GOOD, B.F32, t, k, n, GOOD, B.F32, GOOD,
+                                         None) == B.EUNSUPPORTED, (t, k, n)
