@@ -934,7 +934,11 @@ void launch_shrink(const ShrinkArgs& s, hipStream_t st) {
   const int64_t mixed = p.ids == nullptr || s.perm != nullptr ? 1
                         : p.m < p.n_adapters                  ? p.m
                                                               : p.n_adapters;
-  const dim3 block(s.frag != nullptr ? 64 * kStreams : mixed < 2 ? 64 : mixed < 8 ? 256 : 512);
+  uint32_t threads = s.frag != nullptr ? 64 * kStreams : mixed < 2 ? 64 : mixed < 8 ? 256 : 512;
+  // a grid ends below 2^32 threads (2^24 rows in 8 running sums have 2^23
+  // blocks); any number of waves can be dealt a tile's adapters
+  if (static_cast<uint64_t>(grid.x) * threads > 0xFFFFFFFFull) threads = 256;
+  const dim3 block(threads);
   if (p.rank <= 16) hipLaunchKernelGGL((shrink_kernel<1, kAny>), grid, block, 0, st, s);
   else if (p.rank <= 32) hipLaunchKernelGGL((shrink_kernel<2, kAny>), grid, block, 0, st, s);
   else if (p.rank <= 64) hipLaunchKernelGGL((shrink_kernel<4, kAny>), grid, block, 0, st, s);

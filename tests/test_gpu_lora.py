@@ -545,3 +545,26 @@ def test_arguments_by_name():
         got = B.lora_add(a=v["a"], b=v["b"], x=v["x"], ids=v["ids"], keep_h=True, **kw)
         torch.cuda.synchronize()
         assert torch.equal(got[0], y) and torch.equal(got[1], h)
+
+
+def test_the_most_rows_of_the_fewest_columns():
+    """2^24 rows beside a projection of one output, several adapters in a
+    tile: as many blocks of the first product as there can be."""
+    m, n, k, rank, na = 1 << 24, 1, 1824, 8, 8
+    g = gen(14)
+    x = torch.zeros(m, k, dtype=BF, device=DEV)            # 61 GB
+    a = torch.randint(-1, 2, (na, rank, k), generator=g).to(BF).to(DEV)
+    b = torch.randint(-1, 2, (na, n, rank), generator=g).to(BF).to(DEV)
+    ids = torch.full((m,), -1, dtype=torch.int32)
+    rows = torch.cat([torch.arange(0, 40), torch.randint(0, m, (500,), generator=g),
+                      torch.arange(m - 40, m)]).unique()
+    ids[rows] = torch.randint(0, na, (rows.numel(),), generator=g).to(torch.int32)
+    some = torch.randint(-1, 2, (rows.numel(), k), generator=g).to(BF)
+    x[rows.to(DEV)] = some.to(DEV)
+    y = B.lora_add(x, a, b, ids.to(DEV))
+    del x
+    torch.cuda.empty_cache()
+    d = {"x": some, "a": a.cpu(), "b": b.cpu(), "ids": ids[rows], "base": torch.zeros(rows.numel(), n)}
+    want = torch.zeros(m, n)
+    want[rows] = ref_add(d, scale=False)[0].float()
+    assert torch.equal(y.cpu(), want)
