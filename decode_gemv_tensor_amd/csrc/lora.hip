@@ -1245,7 +1245,8 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
     const int32_t s0 = first_tile(p.o, a), s1 = first_tile(p.o, a + 1);
     const bool direct = by_adapter || (s0 >= begin && s1 <= begin + per_split);
     const int64_t size = p.rank * cols;
-    const float f = !direct || p.scale == nullptr ? 1.0f : p.scale[a];
+    // an adapter without rows gets zeros, whatever its scale
+    const float f = !direct || p.scale == nullptr || s0 == s1 ? 1.0f : p.scale[a];
     void* const grad = second ? p.side[1].grad : p.side[0].grad;
     float* const part = second ? p.side[1].part : p.side[0].part;
     void* to = direct ? grad : static_cast<void*>(part);

@@ -568,3 +568,23 @@ def test_the_most_rows_of_the_fewest_columns():
     want = torch.zeros(m, n)
     want[rows] = ref_add(d, scale=False)[0].float()
     assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("m", [40, 3000])
+def test_an_adapter_without_rows_gets_zeros_whatever_its_scale(m):
+    """Gradients by adapter (few rows) and by ranges of rows (many)."""
+    d = make(m, 72, 96, 16, 5, seed=m)
+    d["ids"][d["ids"] == 2] = -1
+    d["ids"][d["ids"] == 4] = 0
+    v = to_dev(d)
+    want = B.lora_grad(v["x"], v["a"], v["b"], v["ids"], v["dy"], scale=v["scale"])
+    v["scale"][2], v["scale"][4] = math.inf, math.nan
+    for dt in (F32, BF):
+        _, da, db = B.lora_grad(v["x"], v["a"], v["b"], v["ids"], v["dy"], scale=v["scale"],
+                                grad_dtype=dt)
+        assert not bool(da[[2, 4]].any()) and not bool(db[[2, 4]].any())
+        assert torch.equal(da, want[1].to(dt)) and torch.equal(db, want[2].to(dt))
+    # no ids: adapter 0 alone has rows
+    v["scale"][1] = -math.inf
+    _, da, db = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"], scale=v["scale"])
+    assert not bool(da[1:].any()) and not bool(db[1:].any()) and bool(db[0].any())
