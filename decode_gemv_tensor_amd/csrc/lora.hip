@@ -1489,6 +1489,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs s) {
   for (int32_t b = 0; b < s.blocks; ++b) v += from[b * s.tiles * (kRowTile * 4)];
   if (4 * quad < p.rank) *reinterpret_cast<floatx4*>(s.g + row * p.rank + 4 * quad) = v;
   if (s.frag == nullptr) return;
+  // ranks behind the last meet zeros of At: an infinite dy has made them NaN
+  if (4 * quad >= p.rank) v = floatx4{0, 0, 0, 0};
   uint16_t d[3][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) split3(v[j], d[0][j], d[1][j], d[2][j]);

@@ -588,3 +588,20 @@ def test_an_adapter_without_rows_gets_zeros_whatever_its_scale(m):
     v["scale"][1] = -math.inf
     _, da, db = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"], scale=v["scale"])
     assert not bool(da[1:].any()) and not bool(db[1:].any()) and bool(db[0].any())
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24])
+@pytest.mark.parametrize("m,n,k", [(2200, 15400, 960), (2200, 15400, 64), (2200, 300, 960),
+                                   (20, 72, 64)])
+def test_an_infinite_gradient_gives_an_infinite_input_gradient(m, n, k, rank):
+    """Positive weights: g and dx of the row are +inf; ranks behind the last
+    (8 of 16, 24 of 32) add nothing to it."""
+    d = make(m, n, k, rank, 1, seed=rank, ids="one")
+    d["a"][:], d["b"][:] = 1.0, 1.0
+    v = to_dev(d)
+    want = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"])[0]
+    v["dy"][5, 3] = math.inf
+    dx = B.lora_grad(v["x"], v["a"], v["b"], None, v["dy"])[0]
+    assert bool((dx[5] == math.inf).all())
+    fine = torch.arange(m) != 5
+    assert torch.equal(dx[fine], want[fine])
