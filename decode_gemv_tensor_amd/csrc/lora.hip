@@ -79,7 +79,8 @@ __device__ __forceinline__ uint4 load8_part(const uint16_t* p, int64_t left) {
 
 // v = hi + mid + lo exactly, each a bf16 (8 significant bits by truncation):
 // fp32 values enter a bf16 MFMA as three terms and lose nothing. Infinity
-// and NaN stay in hi alone.
+// and NaN stay in hi alone; an infinite value on the other side meets terms
+// that are 0, see redo_nan.
 __device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
   const uint32_t u = __float_as_uint(v), top = u & 0xFFFF0000u;
   float rest = v - __uint_as_float(top);
@@ -503,6 +504,51 @@ __device__ __forceinline__ void finish_rows(const ExpandArgs& s, int64_t row0, i
   }
 }
 
+__device__ __forceinline__ bool is_nan(float v) { return v != v; }
+
+// An infinite value of B beside an h that fewer than three bf16 terms hold: the
+// terms that are 0 make NaN of what is infinite. (The terms of a value have one
+// sign, so nothing else goes wrong.) A NaN is formed again from h itself, rank
+// by rank in fp32, and stays one if it is. h: (row of the tile, rank) -> h. id:
+// of the tile's row in a lane.
+template <int CT, typename H>
+__device__ __forceinline__ void redo_nan(const LoraArgs& p, int32_t id, int64_t wave_col, int lane,
+                                         floatx4 (&mine)[CT], H h) {
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) any |= is_nan(mine[c][q]);
+  if (__ballot(any) == 0) return;
+  asm volatile("" : "+v"(lane));   // nothing of this is kept through the caller's loop
+  const int g = lane >> 4;
+  const int64_t col = wave_col + CT * (lane & 15);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int32_t a = __shfl(id, 4 * g + q, 64);
+    bool open = false;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) open |= is_nan(mine[c][q]);
+    if (a < 0 || col >= p.n || !open) continue;
+    float sum[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) sum[c] = 0.0f;
+#pragma unroll 1
+    for (int32_t r = 0; r < p.rank && open; ++r) {
+      const float v = h(4 * g + q, r);
+      open = false;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int64_t n = col + c < p.n ? col + c : p.n - 1;
+        sum[c] = __builtin_fmaf(v, bf16_f32(p.b[(a * p.n + n) * p.rank + r]), sum[c]);
+        open |= !is_nan(sum[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) mine[c][q] = is_nan(mine[c][q]) ? sum[c] : mine[c][q];
+  }
+}
+
 // B's operands of adapter a for a wave's columns, as loaded; turn() follows.
 // Zeros for ranks beyond the last (h has zeros there too).
 template <int KS, int CT>
@@ -602,6 +648,9 @@ struct FewRows {
       if (todo == 0) break;
       request(p, id, wave_col, lane);
     }
+    redo_nan(p, id, wave_col, lane, mine, [&](int t, int32_t r) {
+      return (bf16_f32(hs[0][t][r]) + bf16_f32(hs[1][t][r])) + bf16_f32(hs[2][t][r]);
+    });
   }
 };
 
@@ -854,6 +903,11 @@ void expand_many_kernel(ExpandArgs s) {
         for (int c = 0; c < CT; ++c) mine[c][q] = hit ? acc[c][q] : mine[c][q];
       }
     }
+    redo_nan(p, id_now, wave_col, lane, mine, [&](int t, int32_t r) {
+      const uint16_t* term = reinterpret_cast<const uint16_t*>(
+          s.frag + ((tile0 + m) * 3 * KS + r / 32) * 64 + 16 * (r % 32 / 8) + t) + r % 8;
+      return (bf16_f32(term[0]) + bf16_f32(term[KS * 512])) + bf16_f32(term[2 * KS * 512]);
+    });
     finish_rows<CT, BK, YK>(s, row0, rows, g, wave_col, CT * i, full, base_now, mine, scale);
   };
   int32_t m = 0;
@@ -1237,7 +1291,59 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
   if (begin >= end && !by_adapter) return;
 
   floatx4 acc[8];
-  const auto flush = [&](int32_t a) __attribute__((always_inline)) {
+  // The sums' NaN of one adapter's tiles t0 to t1 again from the values, as in
+  // redo_nan: an infinite row value beside a v of fewer than three terms.
+  const auto redo = [&](int32_t t0, int32_t t1) __attribute__((always_inline)) {
+    int32_t own = lane;
+    asm volatile("" : "+v"(own));
+    const int32_t rank = 16 * chunk + (own & 15);
+    constexpr int kAhead = 4;   // rows on their way at once, of a tile
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t cc = col0 + 8 * (4 * (own >> 4) + q);
+      bool open = false;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) open |= cc + c < cols && is_nan(acc[c][q]);
+      if (rank >= p.rank || !open) continue;
+      float sum[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
+#pragma unroll 1
+      for (int64_t e = static_cast<int64_t>(t0) * kRowTile;
+           e < static_cast<int64_t>(t1) * kRowTile && open; e += kAhead) {
+        float v[kAhead];
+        uint32_t d[kAhead][4];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int64_t row = kSorted ? p.o.perm[e + j] : e + j < p.m ? e + j : -1;
+          const int64_t at = row < 0 ? 0 : row;   // behind the adapter's last: zeros
+          const uint4 piece = load8_part(
+              reinterpret_cast<const uint16_t*>(rows_in + at * row_bytes) + cc, cols - cc);
+          v[j] = *reinterpret_cast<const float*>(vectors + at * vector_bytes + 4 * rank);
+          __builtin_memcpy(d[j], &piece, 16);
+          if (row < 0) v[j] = 0.0f, d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0;
+        }
+        open = false;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            sum[c] = __builtin_fmaf(v[j], c & 1 ? bf16_hi(d[j][c / 2]) : bf16_lo(d[j][c / 2]),
+                                    sum[c]);
+          open |= !is_nan(sum[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c][q] = is_nan(acc[c][q]) ? sum[c] : acc[c][q];
+    }
+  };
+  const auto flush = [&](int32_t a, int32_t t0, int32_t t1) __attribute__((always_inline)) {
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) any |= is_nan(acc[c][q]);
+    if (__ballot(any) != 0) redo(t0, t1);
     // kept from being computed ahead of the loop and held through it
     int32_t own = lane;
     asm volatile("" : "+v"(own));
@@ -1292,6 +1398,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
   do {
     const int32_t a = by_adapter ? split : kSorted ? uniform(p.o.adapter[tile]) : 0;
     const int32_t a_end = by_adapter ? end : first_tile(p.o, a + 1), stop = a_end < end ? a_end : end;
+    const int32_t start = tile;
     uint4 in0[8], in1[8];
     float v0[8], v1[8];
     int32_t rows[8], miss0, miss1;
@@ -1458,7 +1565,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
       }
       tile = stop;
     }
-    flush(a);   // an adapter without rows: zeros
+    flush(a, start, stop);   // an adapter without rows: zeros
   } while (tile < end);
 }
 

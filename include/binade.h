@@ -644,7 +644,8 @@ typedef struct binade_lora {
  * Arithmetic: A x on bf16 MFMA in fp32, in a fixed order that depends on k
  * alone; h stays fp32 through the second product (three bf16 terms whose
  * sum is h to 2^-24); y is rounded once. A row's result does not depend on
- * the other rows, on m or on its place.
+ * the other rows, on m or on its place. Infinities and NaN come out as in the
+ * formula, here and in binade_lora_grad.
  * workspace: device, 16-byte aligned, binade_lora_workspace_bytes bytes; not
  * read before written; calls that overlap need their own. ENOSPACE: too
  * small. */

@@ -605,3 +605,75 @@ def test_an_infinite_gradient_gives_an_infinite_input_gradient(m, n, k, rank):
     assert bool((dx[5] == math.inf).all())
     fine = torch.arange(m) != 5
     assert torch.equal(dx[fine], want[fine])
+
+
+def same(got, ref):
+    """Equal, NaN where the reference has it and nowhere else."""
+    got, ref = got.cpu(), ref.to(got.dtype)
+    nan = torch.isnan(ref)
+    return torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], ref[~nan])
+
+
+@pytest.mark.parametrize("case", [(1, 64, 64, 8, 1, "one"), (16, 300, 288, 32, 2, "mix"),
+                                  (33, 515, 544, 24, 7, "mix"), (65, 1000, 4128, 8, 9, "runs"),
+                                  (257, 264, 1024, 120, 33, "mix"), (577, 6700, 96, 8, 3, "mix"),
+                                  (600, 6661, 544, 40, 5, "runs"), (1030, 4200, 64, 72, 4, "mix"),
+                                  (530, 7200, 288, 128, 2, "one"), (300, 8000, 96, 24, 1, "mix")],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_infinite_weights_give_what_the_formula_gives(case):
+    """h holds whole numbers, whose lower bf16 terms are 0: an infinite B
+    beside them gives infinity (NaN only where h is 0), a NaN stays one. The
+    same for A through h."""
+    m, n, k, rank, na, ids = case
+    d = make(m, n, k, rank, na, seed=3 * sum(case[:5]), ids=ids)
+    i = int(d["ids"].max()) if d["ids"] is not None else 0
+    i = max(i, 0)
+    d["b"][i, n // 3, 2] = math.inf
+    d["b"][i, n - 1, rank - 1] = -math.inf
+    d["b"][i, 0, 1] = math.nan
+    v = to_dev(d)
+    y_ref, h_ref = ref_add(d)
+    assert bool(torch.isinf(y_ref).any()) or m == 1
+    for base_dt, dt in ((BF, F32), (F32, BF)):
+        say("infinite b", case, base_dt)
+        y, h = B.lora_add(v["x"], v["a"], v["b"], v["ids"], base=v["base"].to(base_dt),
+                          scale=v["scale"], out_dtype=dt, keep_h=True)
+        assert same(y, y_ref) and same(h, h_ref)
+    d["a"][i, 3, k // 2] = math.inf
+    d["x"][m // 2, 5] = -math.inf
+    v = to_dev(d)
+    y_ref, h_ref = ref_add(d)
+    y, h = B.lora_add(v["x"], v["a"], v["b"], v["ids"], base=v["base"], scale=v["scale"],
+                      keep_h=True)
+    assert same(h, h_ref) and same(y, y_ref)
+
+
+@pytest.mark.parametrize("case", [(1, 64, 64, 8, 1, "one"), (33, 515, 544, 24, 7, "mix"),
+                                  (100, 130, 2080, 8, 5, "runs"), (577, 130, 6720, 16, 3, "mix"),
+                                  (2051, 5, 2080, 24, 3, "runs"), (2100, 136, 64, 16, 1, "one"),
+                                  (3001, 130, 288, 40, 9, "mix"), (1030, 33, 4224, 72, 5, "runs"),
+                                  (34000, 1001, 32, 8, 1, "one"), (2200, 15400, 96, 16, 3, "mix"),
+                                  (8300, 4100, 4128, 16, 6, "runs")],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_infinite_operands_of_the_gradients_give_what_the_formulas_give(case):
+    m, n, k, rank, na, ids = case
+    d = make(m, n, k, rank, na, seed=5 * sum(case[:5]), ids=ids)
+    _, h = ref_add(d)
+    rows = torch.arange(m) if d["ids"] is None else (d["ids"] >= 0).nonzero()[:, 0]
+    at = lambda f: int(rows[min(len(rows) - 1, int(f * len(rows)))])
+    clean = d
+    for name, r, c, val in (("x", at(0.3), k - 1, math.inf), ("x", at(0.99), 0, -math.inf),
+                            ("dy", at(0.6), n - 1, math.inf), ("dy", at(0.1), n // 2, math.nan),
+                            ("a", rank - 1, k // 2, -math.inf), ("x", at(0.5), None, math.inf)):
+        say("infinite", name, case)
+        d = dict(clean, **{name: clean[name].clone()})
+        t = d[name][0] if name == "a" else d[name]
+        t[r, slice(None) if c is None else c] = val
+        v = to_dev(d)
+        ref = ref_grad(d, h, base=d["x"] if name != "x" else None)
+        for dt in (F32, BF):
+            dx, da, db = B.lora_grad(v["x"], v["a"], v["b"], v["ids"], v["dy"],
+                                     h=h.float().to(DEV), scale=v["scale"],
+                                     dx_base=v["x"] if name != "x" else None, grad_dtype=dt)
+            for got, want, what in ((dx, ref[0], "dx"), (da, ref[1], "da"), (db, ref[2], "db")):
+                assert same(got, want), (name, what, dt)
