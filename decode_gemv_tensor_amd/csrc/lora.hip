@@ -506,6 +506,16 @@ __device__ __forceinline__ void finish_rows(const ExpandArgs& s, int64_t row0, i
 
 __device__ __forceinline__ bool is_nan(float v) { return v != v; }
 
+// Whether a lane has a NaN in v: two values a comparison.
+template <int N>
+__device__ __forceinline__ bool any_nan(const floatx4 (&v)[N]) {
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    any |= __builtin_isunordered(v[c][0], v[c][1]) | __builtin_isunordered(v[c][2], v[c][3]);
+  return any;
+}
+
 // An infinite value of B beside an h that fewer than three bf16 terms hold: the
 // terms that are 0 make NaN of what is infinite. (The terms of a value have one
 // sign, so nothing else goes wrong.) A NaN is formed again from h itself, rank
@@ -514,12 +524,7 @@ __device__ __forceinline__ bool is_nan(float v) { return v != v; }
 template <int CT, typename H>
 __device__ __forceinline__ void redo_nan(const LoraArgs& p, int32_t id, int64_t wave_col, int lane,
                                          floatx4 (&mine)[CT], H h) {
-  bool any = false;
-#pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) any |= is_nan(mine[c][q]);
-  if (__ballot(any) == 0) return;
+  if (__ballot(any_nan(mine)) == 0) return;
   asm volatile("" : "+v"(lane));   // nothing of this is kept through the caller's loop
   const int g = lane >> 4;
   const int64_t col = wave_col + CT * (lane & 15);
@@ -1338,12 +1343,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(OuterArgs p) {
     }
   };
   const auto flush = [&](int32_t a, int32_t t0, int32_t t1) __attribute__((always_inline)) {
-    bool any = false;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) any |= is_nan(acc[c][q]);
-    if (__ballot(any) != 0) redo(t0, t1);
+    if (__ballot(any_nan(acc)) != 0) redo(t0, t1);
     // kept from being computed ahead of the loop and held through it
     int32_t own = lane;
     asm volatile("" : "+v"(own));
