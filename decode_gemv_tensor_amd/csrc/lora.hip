@@ -342,8 +342,8 @@ __global__ __launch_bounds__(512) void shrink_kernel(ShrinkArgs s) {
 // that lane i ends with the CT adjacent columns CT i .. CT i + CT - 1. A tile of
 // 16 rows runs once for each adapter among them and every row keeps its own;
 // base + scale * product is one fma (rows without an adapter: -0 * 0 + base).
-// Two shapes, at 4096 rows of bf16 base and y, 15360 columns, rank 64, 73.6 us
-// (252 MB, 3.4 TB/s; reading base and writing y alone 44: a wave's tile of 2 KB
+// Two shapes, at 4096 rows of bf16 base and y, 15360 columns, rank 64, 75.5 us
+// (252 MB, 3.3 TB/s; reading base and writing y alone 44: a wave's tile of 2 KB
 // waits for its operands, and more waves have no registers) and at 61 rows of
 // 3840 columns, fp32 base, 32 adapters of rank 32, 11.1:
 //  - few rows: a block of four waves has 16 rows by 128 columns, joins the

@@ -331,10 +331,11 @@ __device__ __forceinline__ float loss_of(double sum, int32_t n_experts, int32_t 
   return static_cast<float>(n_experts * sum / (top_k * r * r));
 }
 
-// Measured: 65536 tokens of 256 bf16 experts, top 8, counts and sums, 21.4 us
-// (7 us of bytes): 540 vector instructions a wave's four rows, most of them
-// the keys' sorting and the merge's four steps, 14 us at the issue rate; 2048
-// tokens of 128 fp32 experts 6.2, one token 2.5.
+// Measured: 65536 tokens of 256 bf16 experts, top 8, counts and sums, 22.1 us
+// (7 us of bytes): 563 vector instructions a wave's four rows, most of them
+// the keys' sorting and the merge's four steps, 15 us at the issue rate; 2048
+// tokens of 128 fp32 experts 5.8, one token 2.5. Both kernels in a captured
+// graph 27.3 us for 8 slots of the first, 33.9 for 10, 41 for 16, 110 for 64.
 template <int G, int V, typename K, bool kSort>
 __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) {
   typedef typename K::Key Key;
@@ -582,9 +583,9 @@ struct RouteGradArgs {
 // gets its gradient less the row's mean). The row is zero between tokens; its
 // pieces of four are swizzled so that eight lanes' reads meet no bank twice.
 // The next token's logits and slots are loaded while one is worked out.
-// Measured: 65536 tokens of 256 bf16 experts, top 8, 26 us under the trace (71
-// MB, 13.6 us of bytes; 470 vector instructions a wave's four rows, 13 us at
-// the issue rate); 333 tokens of 60 fp32 experts 5.1.
+// Measured: 65536 tokens of 256 bf16 experts, top 8, 27 us under the trace (71
+// MB, 13.6 us of bytes; 494 vector instructions a wave's four rows, 14 us at
+// the issue rate); 333 tokens of 60 fp32 experts 5.3.
 template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p) {
   constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;
