@@ -14,7 +14,7 @@ weights:
 ``own`` is true, with this repository's kernels. Formulas:
 
   blocks     a block of 128 values v has the scale 2^e, e the least whole
-             number >= -127 with max|v| <= 448 2^e (0 for a block of zeros),
+             number >= -126 with max|v| <= 448 2^e (0 for a block of zeros),
              and the values Q(v) = 2^e e4m3(v 2^-e), to the nearest, ties to
              even; the last block of a row may be shorter
   product    y[t, n] = sum_k Q(x)[t, k] S[n / 128, k / 128] W[n, k], x in
@@ -270,9 +270,8 @@ def prepare(case, seed):
 
 # -------------------------------------------------------------- plain forms
 def _power(e):
-    """fp32 2^e of whole e in -127..127, from its bits."""
-    e = e.to(torch.int32)
-    return torch.where(e > -127, (e + 127) << 23, 1 << 22).view(F32)
+    """fp32 2^e of whole e in -126..127, from its bits."""
+    return ((e.to(torch.int32) + 127) << 23).view(F32)
 
 
 def _q(v):
@@ -281,7 +280,7 @@ def _q(v):
     pad = torch.nn.functional.pad(v.float(), (0, _blocks(n) * BLOCK - n))
     tiles = pad.view(*v.shape[:-1], -1, BLOCK)
     mant, ex = torch.frexp(tiles.abs().amax(-1, keepdim=True))
-    e = torch.where(mant > 0, ex - 9 + (mant > 0.875).to(ex.dtype), 0).clamp(min=-127)
+    e = torch.where(mant > 0, ex - 9 + (mant > 0.875).to(ex.dtype), 0).clamp(min=-126)
     back = (tiles * _power(-e)).to(E4M3).float() * _power(e)
     return back.view(pad.shape)[..., :n]
 
@@ -461,7 +460,7 @@ def _exact_q(v):
         top = part.abs().max(1, keepdim=True).values
         e = _log2_floor(top.clamp(min=1e-200)) - 8
         e = torch.where(top > 448.0 * _two_to(e), e + 1, e)
-        e = torch.where(top == 0, torch.zeros_like(e), e.clamp(min=-127))
+        e = torch.where(top == 0, torch.zeros_like(e), e.clamp(min=-126))
         u = part * _two_to(-e)
         step = _two_to(_log2_floor(u.abs().clamp(min=2.0 ** -6)) - 3)
         out[:, b:b + BLOCK] = torch.round(u / step) * step * _two_to(e)
