@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libbinade.so")
 CHUNK = 2048
 
 OK, EINVAL, ECORRUPT, EUNSUPPORTED, EHIP, ENOSPACE = 0, -1, -2, -3, -4, -5
-F32, BF16 = 0, 1
+F32, BF16, E8M0 = 0, 1, 2
 DEV_CORRUPT_STREAM, DEV_BAD_INDEX, DEV_CORRUPT_ESC = 0x1, 0x2, 0x4
 
 EXPORTS = ["binade_status_str", "binade_last_hip_error", "binade_build_table",
@@ -39,7 +39,10 @@ EXPORTS = ["binade_status_str", "binade_last_hip_error", "binade_build_table",
            "binade_rice_to_r4_run", "binade_moe_combine_grad", "binade_moe_route",
            "binade_moe_route_workspace_bytes", "binade_moe_route_grad", "binade_lora_add",
            "binade_lora_workspace_bytes", "binade_lora_grad",
-           "binade_lora_grad_workspace_bytes"]
+           "binade_lora_grad_workspace_bytes", "binade_f8_sizes_of", "binade_f8_pack",
+           "binade_f8_layout", "binade_f8_gemm", "binade_f8_gemm_workspace_bytes",
+           "binade_f8_gemm_grad", "binade_f8_gemm_grad_workspace_bytes", "binade_f8_moe_gemm",
+           "binade_f8_moe_workspace_bytes"]
 
 
 class Table(ctypes.Structure):
@@ -103,6 +106,18 @@ class LoraDesc(ctypes.Structure):
                 ("scale", ctypes.c_void_p)]
 
 
+class F8Desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("count", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("values", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("values_t", ctypes.c_void_p),
+                ("scales_t", ctypes.c_void_p)]
+
+
+class F8Sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in
+                ("values_bytes", "scales_bytes", "values_t_bytes", "scales_t_bytes")]
+
+
 class BinadeError(RuntimeError):
     def __init__(self, fn: str, code: int, hip: int = 0):
         lib = _lib_or_none()
@@ -149,6 +164,12 @@ def lib() -> ctypes.CDLL:
             L.binade_lora_workspace_bytes.restype = I64
             L.binade_lora_grad_workspace_bytes.argtypes = [I64, I64, I64, I32, I32]
             L.binade_lora_grad_workspace_bytes.restype = I64
+            L.binade_f8_gemm_workspace_bytes.argtypes = [I64, I64, I64, I32]
+            L.binade_f8_gemm_workspace_bytes.restype = I64
+            L.binade_f8_gemm_grad_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, I32]
+            L.binade_f8_gemm_grad_workspace_bytes.restype = I64
+            L.binade_f8_moe_workspace_bytes.argtypes = [I64, I32, I32, I32, I64, I64]
+            L.binade_f8_moe_workspace_bytes.restype = I64
             sig = {
                 "binade_build_table": [P, I64, P],
                 "binade_sizes_of": [P, I64, I64, P],
@@ -190,6 +211,12 @@ def lib() -> ctypes.CDLL:
                                     P],
                 "binade_lora_grad": [P, P, I64, I64, P, P, I64, P, P, I64, P, I64, P, P, I32, P,
                                      I64, P, P],
+                "binade_f8_sizes_of": [I64, I64, I32, I32, P],
+                "binade_f8_pack": [P, P, P],
+                "binade_f8_layout": [P, P, P, P],
+                "binade_f8_gemm": [P, P, I64, I64, P, I64, I32, P, I64, P],
+                "binade_f8_gemm_grad": [P, P, I64, I64, P, I64, P, I64, P, I32, P, I64, P],
+                "binade_f8_moe_gemm": [P, P, I64, I32, P, I64, I32, P, I64, I32, P, I64, P, P],
             }
             for name, args in sig.items():
                 if hasattr(L, name):
@@ -1245,3 +1272,173 @@ def lora_grad(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tens
          _addr(dx), k, da.data_ptr(), db.data_ptr(), code, at, nb, _status_arg(status, dev),
          stream)
     return dx, da, db
+
+
+# ------------------------------------------------------------ 8-bit products
+_BYTES_OF_F8 = (torch.float8_e4m3fn, torch.uint8)
+_BYTES_OF_E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+
+
+@dataclass
+class F8Weight:
+    """Weights in 8 bits with a scale for each block of 128 x 128, as f8_pack
+    and f8_weight lay them out: count matrices [rows, cols] (experts), and with
+    train their transposed planes, which f8_gemm_grad's dx reads."""
+    rows: int
+    cols: int
+    count: int
+    scale_dtype: int
+    values: torch.Tensor
+    scales: torch.Tensor
+    values_t: torch.Tensor | None = None
+    scales_t: torch.Tensor | None = None
+
+    def __post_init__(self):
+        self._desc = F8Desc(self.rows, self.cols, self.count, self.scale_dtype,
+                            self.values.data_ptr(), self.scales.data_ptr(), _addr(self.values_t),
+                            _addr(self.scales_t))
+
+    def desc(self) -> F8Desc:
+        return self._desc
+
+
+def _f8_planes(rows, cols, count, scale_dtype, train, device, values=None) -> F8Weight:
+    sizes = F8Sizes()
+    _run("binade_f8_sizes_of", rows, cols, count, scale_dtype, ctypes.byref(sizes))
+    new = lambda n: torch.empty(n, dtype=torch.uint8, device=device)
+    if values is None:
+        values = new(sizes.values_bytes)
+    w = F8Weight(rows, cols, count, scale_dtype, values, new(sizes.scales_bytes),
+                 new(sizes.values_t_bytes) if train else None,
+                 new(sizes.scales_t_bytes) if train else None)
+    return w
+
+
+def _matrices(name: str, t: torch.Tensor):
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name}: [N, K] or [count, N, K]")
+    return (t.shape if t.dim() == 3 else (1, *t.shape))
+
+
+def _whole16(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and 16-byte aligned, copied if it is not."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+@_on_device
+def f8_pack(w: torch.Tensor, train: bool = False, out: F8Weight | None = None,
+            stream=None) -> F8Weight:
+    """binade_f8_pack: bf16 [N, K] or [count, N, K] in 8 bits with a
+    power-of-two scale for each block of 128 x 128 (of a packed weight:
+    f8_pack(unpack(w))). train: the transposed planes too. out: planes of an
+    earlier call for the same sizes, written again (after an update)."""
+    if w.dtype != torch.bfloat16:
+        raise TypeError(f"w: {w.dtype}, expected bf16")
+    count, rows, cols = _matrices("w", w)
+    w = _whole16(w)
+    if out is None:
+        out = _f8_planes(rows, cols, count, E8M0, train, w.device)
+    elif (out.rows, out.cols, out.count, out.scale_dtype) != (rows, cols, count, E8M0) or \
+            out.values.device != w.device or train != (out.values_t is not None):
+        raise ValueError("out: planes of other sizes, another type or device")
+    _run("binade_f8_pack", w.data_ptr(), ctypes.byref(out.desc()), stream)
+    return out
+
+
+@_on_device
+def f8_weight(values: torch.Tensor, scales: torch.Tensor, train: bool = False,
+              stream=None) -> F8Weight:
+    """binade_f8_layout: a checkpoint's e4m3 values [N, K] or [count, N, K]
+    (float8_e4m3fn or their bytes) and their blocks' scales [(count,) ceil(N /
+    128), ceil(K / 128)], fp32 or powers of two (float8_e8m0fnu or their
+    bytes). The values are kept as they are where K % 128 == 0."""
+    if values.dtype not in _BYTES_OF_F8:
+        raise TypeError(f"values: {values.dtype}, expected float8_e4m3fn")
+    count, rows, cols = _matrices("values", values)
+    blocks = (-(-rows // 128), -(-cols // 128))
+    if scales.dtype != torch.float32 and scales.dtype not in _BYTES_OF_E8M0:
+        raise TypeError(f"scales: {scales.dtype}, expected fp32 or float8_e8m0fnu")
+    scales = _arg("scales", scales, (scales.dtype,), (*values.shape[:-2], *blocks), values.device)
+    values = _whole16(values)
+    code = F32 if scales.dtype == torch.float32 else E8M0
+    out = _f8_planes(rows, cols, count, code, train, values.device,
+                     values.view(torch.uint8) if cols % 128 == 0 else None)
+    _run("binade_f8_layout", values.data_ptr(), scales.data_ptr(), ctypes.byref(out.desc()), stream)
+    return out
+
+
+def _f8_arg(w: F8Weight, device):
+    if not isinstance(w, F8Weight):
+        raise TypeError("w: an F8Weight of f8_pack or f8_weight")
+    if w.values.device != device:
+        raise ValueError(f"w is on {w.values.device}, not {device}")
+    return ctypes.byref(w._desc)
+
+
+@_on_device
+def f8_gemm(x: torch.Tensor, w: F8Weight, out_dtype=torch.float32, y: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """binade_f8_gemm: Q(x) W^T of bf16 x [m, K], x quantised in blocks of 128
+    along K. A bf16 result of more than 16 rows takes the 8-bit matrix
+    instruction, an fp32 one exact products at half its rate."""
+    code = _dtype_code(out_dtype)
+    dev = x.device
+    d = _f8_arg(w, dev)
+    x, ldx = _rows16("x", x, w.cols, dev)
+    m, n = x.shape[0], w.rows
+    y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
+    ws, at, nb = _scratch(_entry("binade_f8_gemm_workspace_bytes")(m, n, w.cols, code), workspace,
+                          dev)
+    _run("binade_f8_gemm", d, x.data_ptr(), m, ldx, y.data_ptr(), n, code, at, nb, stream)
+    return y
+
+
+@_on_device
+def f8_gemm_grad(x: torch.Tensor, w: F8Weight, dy: torch.Tensor, grad_dtype=torch.float32,
+                 need_dx: bool = True, need_dw: bool = True, dx: torch.Tensor | None = None,
+                 dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None):
+    """binade_f8_gemm_grad: (dx bf16 [m, K] or None, dw [N, K] of grad_dtype or
+    None) of f8_gemm from dy bf16 [m, N]; dx needs a weight made with train."""
+    code = _dtype_code(grad_dtype)
+    dev = x.device
+    d = _f8_arg(w, dev)
+    n, k = w.rows, w.cols
+    x, ldx = _rows16("x", x, k, dev)
+    m = x.shape[0]
+    dy = _arg("dy", dy, _BF16_ONLY, (m, n), dev)
+    dx = _out_arg("dx", dx, torch.bfloat16, (m, k), dev) if need_dx or dx is not None else None
+    dw = _out_arg("dw", dw, _TORCH_DTYPE[code], (n, k), dev) if need_dw or dw is not None else None
+    need = _entry("binade_f8_gemm_grad_workspace_bytes")(m, n, k, dx is not None, dw is not None,
+                                                         code)
+    ws, at, nb = _scratch(need, workspace, dev)
+    _run("binade_f8_gemm_grad", d, x.data_ptr(), m, ldx, dy.data_ptr(), n, _addr(dx), k, _addr(dw),
+         code, at, nb, stream)
+    return dx, dw
+
+
+@_on_device
+def f8_moe_gemm(x: torch.Tensor, experts: F8Weight, idx: torch.Tensor, x_per_slot: bool = False,
+                out_dtype=torch.float32, y: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """binade_f8_moe_gemm: [n_tokens * top_k, N], row t * top_k + s the product
+    of expert idx[t, s] (moe_route's; -1: zeros) with x[t], or with
+    x[t * top_k + s] where x_per_slot."""
+    code = _dtype_code(out_dtype)
+    dev = x.device
+    d = _f8_arg(experts, dev)
+    if idx.dim() != 2:
+        raise ValueError("idx: [n_tokens, top_k]")
+    tokens, top_k = idx.shape
+    idx = _arg("idx", idx, _I32_ONLY, (tokens, top_k), dev)
+    n, k = experts.rows, experts.cols
+    x, ldx = _rows16("x", x, k, dev, tokens * top_k if x_per_slot else tokens)
+    y = _out_arg("y", y, _TORCH_DTYPE[code], (tokens * top_k, n), dev)
+    per_slot = 1 if x_per_slot else 0
+    need = _entry("binade_f8_moe_workspace_bytes")(tokens, top_k, per_slot, experts.count, n, k)
+    ws, at, nb = _scratch(need, workspace, dev)
+    _run("binade_f8_moe_gemm", d, x.data_ptr(), ldx, per_slot, idx.data_ptr(), tokens, top_k,
+         y.data_ptr(), n, code, at, nb, _status_arg(status, dev), stream)
+    return y

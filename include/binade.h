@@ -75,7 +75,9 @@ typedef enum binade_status {
 /* Output element type of the products. */
 typedef enum binade_dtype {
   BINADE_F32 = 0,     /* fp32 as accumulated */
-  BINADE_BF16 = 1     /* the fp32 result rounded to bf16, nearest-even */
+  BINADE_BF16 = 1,    /* the fp32 result rounded to bf16, nearest-even */
+  BINADE_E8M0 = 2     /* a power of two as its exponent + 127 in a byte
+                         (255: NaN); scales of 8-bit weights only */
 } binade_dtype;
 
 /* Device status word bits (set with atomic OR by the kernels; the caller
@@ -688,6 +690,126 @@ int32_t binade_lora_grad(const binade_lora *l, const uint16_t *x, int64_t m,
  * function. */
 int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
                                          int32_t rank, int32_t n_adapters);
+
+/* Weights in 8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, no
+ * infinity, largest 448) with a scale for each block of 128 x 128 (device
+ * pointers): count matrices [rows = N, cols = K], such as a layer's experts.
+ *   values    u8 [count, rows, P(cols)], zeros behind cols; P(v) is v
+ *             rounded up to a multiple of 128
+ *   scales    u8 or fp32 per scale_dtype (BINADE_E8M0 or BINADE_F32)
+ *             [count, P(rows) / 128, P(cols) / 128 rounded up to a multiple
+ *             of 4]; entries behind the last block are not used
+ *   values_t, scales_t   the same of the transposed matrices [cols, rows],
+ *             for binade_f8_gemm_grad's dx; or NULL
+ * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. cols % 32 == 0, rows
+ * and cols at most 2^22, count at most 65535; planes 16-byte aligned, else
+ * BINADE_EUNSUPPORTED. */
+typedef struct binade_f8 {
+  int64_t rows, cols;
+  int32_t count, scale_dtype;
+  const uint8_t *values;
+  const void *scales;
+  const uint8_t *values_t;
+  const void *scales_t;
+} binade_f8;
+
+/* Bytes a caller allocates for a binade_f8's planes. */
+typedef struct binade_f8_sizes {
+  uint64_t values_bytes, scales_bytes, values_t_bytes, scales_t_bytes;
+} binade_f8_sizes;
+
+/* Plane sizes (host). EINVAL: null out, rows, cols or count < 1, scale_dtype.
+ * EUNSUPPORTED: sizes that binade_f8 does not take. */
+int32_t binade_f8_sizes_of(int64_t rows, int64_t cols, int32_t count,
+                           int32_t scale_dtype, binade_f8_sizes *out);
+
+/* Quantising, here and of x and dy in the products below: a block of values
+ * v gets the scale 2^e, e the least whole number >= -126 with |v| <= 448 2^e
+ * for its finite values (0 for a block of zeros), and each value becomes
+ * e4m3(v 2^-e), to the nearest, ties to even; infinities and NaN become NaN
+ * and have no part in the scale. v 2^-e is exact.
+ *
+ * binade_f8_pack: bf16 w [count, rows, cols] (device, contiguous, 16-byte
+ * aligned) in blocks of 128 x 128 into the planes of out, whose sizes, type
+ * (BINADE_E8M0) and pointers the caller has set (values_t and scales_t both
+ * or none). A training program calls it after each update. */
+int32_t binade_f8_pack(const uint16_t *w, binade_f8 *out, void *stream);
+
+/* A checkpoint's 8-bit weights into the layout above: values u8 [count,
+ * rows, cols] and scales [count, P(rows) / 128, P(cols) / 128] of
+ * out->scale_dtype (device, contiguous, values 16-byte aligned). out as for
+ * binade_f8_pack; out->values may be values itself where cols % 128 == 0
+ * (then only scales and the transposed planes are written). */
+int32_t binade_f8_layout(const uint8_t *values, const void *scales,
+                         binade_f8 *out, void *stream);
+
+/* Y[m, N] = Q(X) W^T with one matrix W (count 1) in 8 bits: Q(X) is X
+ * quantised in blocks of 128 along K. X: device bf16, row t at x + t*ldx
+ * (ldx >= K, a multiple of 8, at most 2^24; 16-byte aligned). Y: fp32 or bf16
+ * per y_dtype, row stride ldy >= N, at most 2^24. m from 0 to 2^22, m * N at
+ * most 2^36.
+ * Arithmetic: an fp32 Y, and up to 16 rows of either type, add exact products
+ * in fp32. A bf16 Y of more rows goes through the 8-bit matrix instruction,
+ * at twice the rate: it adds eight products at a time, cut to about 13 bits
+ * below the largest, in fp32 sums (1.4e-5 of Y's norm for normal data, less
+ * than 1/100 of the output's own rounding). The order depends on m, N and K:
+ * the same call gives the same bits. A NaN in a row of X, or in a row or a
+ * scale of W, gives NaN in that row or column (block) of Y alone.
+ * workspace: device, 16-byte aligned, binade_f8_gemm_workspace_bytes (0 for m
+ * <= 16: may be NULL), not read before written; calls that overlap need their
+ * own. ENOSPACE: too small. */
+int32_t binade_f8_gemm(const binade_f8 *w, const uint16_t *x, int64_t m,
+                       int64_t ldx, void *y, int64_t ldy, int32_t y_dtype,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of binade_f8_gemm (0 for sizes it refuses). Pure host
+ * function. */
+int64_t binade_f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                       int32_t y_dtype);
+
+/* Its gradients from dy (device bf16 [m, N], row stride ld_dy >= N, any
+ * alignment):
+ *   dx[t, k] = sum_n Q(dy)[t, n] W[n, k]         bf16; dy in blocks along N
+ *   dw[n, k] = sum_t Qt(dy)[t, n] Qt(x)[t, k]    fp32 or bf16 per dw_dtype,
+ *              [N, K] contiguous; blocks of 128 rows t of a column
+ * dx (row stride ld_dx >= K) or dw may be NULL: not computed. dx needs w's
+ * transposed planes, dw needs x (as in binade_f8_gemm; otherwise x may be
+ * NULL) and of w the sizes alone. Arithmetic by the output's type as above.
+ * m = 0 leaves dw zeros. workspace: binade_f8_gemm_grad_workspace_bytes with
+ * need_dx, need_dw 0 or 1. */
+int32_t binade_f8_gemm_grad(const binade_f8 *w, const uint16_t *x, int64_t m,
+                            int64_t ldx, const uint16_t *dy, int64_t ld_dy,
+                            uint16_t *dx, int64_t ld_dx, void *dw,
+                            int32_t dw_dtype, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+
+int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                            int32_t need_dx, int32_t need_dw,
+                                            int32_t dw_dtype);
+
+/* The products of the experts that a router chose (binade_moe_route's idx),
+ * with the experts' weights in 8 bits: y[p] = W[idx[p]] Q(x of pair p) for
+ * the pairs p = t * top_k + s. x: device bf16 [n_tokens, K] (x_per_slot = 0)
+ * or [n_tokens * top_k, K] (1), strides as in binade_f8_gemm. idx: device
+ * int32 [n_tokens * top_k]. y: fp32 or bf16 per y_dtype, pair p at y + p*ldy.
+ * A pair of index -1 has no expert (a padded token's slot): its row is zeros.
+ * An index outside [-1, count) sets BINADE_DEV_BAD_INDEX in dev_status (if
+ * not NULL) and counts as -1. Each used expert is read about once (once for
+ * each 128 of its pairs); arithmetic as in binade_f8_gemm, exact products up
+ * to 256 pairs; a pair's result does not depend on the other pairs' order.
+ * top_k in 1..64, count at most 4096, n_tokens * top_k at most 2^24.
+ * workspace: binade_f8_moe_workspace_bytes (0 for few pairs). */
+int32_t binade_f8_moe_gemm(const binade_f8 *experts, const uint16_t *x,
+                           int64_t ldx, int32_t x_per_slot,
+                           const int32_t *idx, int64_t n_tokens,
+                           int32_t top_k, void *y, int64_t ldy,
+                           int32_t y_dtype, void *workspace,
+                           int64_t workspace_bytes, uint32_t *dev_status,
+                           void *stream);
+
+int64_t binade_f8_moe_workspace_bytes(int64_t n_tokens, int32_t top_k,
+                                      int32_t x_per_slot, int32_t n_experts,
+                                      int64_t n, int64_t k);
 
 #ifdef __cplusplus
 }
