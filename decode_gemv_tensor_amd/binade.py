@@ -42,7 +42,8 @@ EXPORTS = ["binade_status_str", "binade_last_hip_error", "binade_build_table",
            "binade_lora_grad_workspace_bytes", "binade_f8_sizes_of", "binade_f8_pack",
            "binade_f8_layout", "binade_f8_gemm", "binade_f8_gemm_workspace_bytes",
            "binade_f8_gemm_grad", "binade_f8_gemm_grad_workspace_bytes", "binade_f8_moe_gemm",
-           "binade_f8_moe_workspace_bytes"]
+           "binade_f8_moe_workspace_bytes", "binade_moe_route_scored",
+           "binade_moe_route_scored_workspace_bytes", "binade_moe_route_scored_grad"]
 
 
 class Table(ctypes.Structure):
@@ -106,6 +107,13 @@ class LoraDesc(ctypes.Structure):
                 ("scale", ctypes.c_void_p)]
 
 
+class RouteRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
 class F8Desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("count", ctypes.c_int32),
                 ("scale_dtype", ctypes.c_int32), ("values", ctypes.c_void_p),
@@ -164,6 +172,8 @@ def lib() -> ctypes.CDLL:
             L.binade_lora_workspace_bytes.restype = I64
             L.binade_lora_grad_workspace_bytes.argtypes = [I64, I64, I64, I32, I32]
             L.binade_lora_grad_workspace_bytes.restype = I64
+            L.binade_moe_route_scored_workspace_bytes.argtypes = [I64, I32]
+            L.binade_moe_route_scored_workspace_bytes.restype = I64
             L.binade_f8_gemm_workspace_bytes.argtypes = [I64, I64, I64, I32]
             L.binade_f8_gemm_workspace_bytes.restype = I64
             L.binade_f8_gemm_grad_workspace_bytes.argtypes = [I64, I64, I64, I32, I32, I32]
@@ -211,6 +221,10 @@ def lib() -> ctypes.CDLL:
                                     P],
                 "binade_lora_grad": [P, P, I64, I64, P, P, I64, P, P, I64, P, I64, P, P, I32, P,
                                      I64, P, P],
+                "binade_moe_route_scored": [P, I32, I64, I64, I32, I32, P, P, P, P, P, P, P, P,
+                                            I64, P],
+                "binade_moe_route_scored_grad": [P, I32, I64, I64, I32, I32, I32, I32,
+                                                 ctypes.c_float, P, P, P, P, P, I32, I64, P, P],
                 "binade_f8_sizes_of": [I64, I64, I32, I32, P],
                 "binade_f8_pack": [P, P, P],
                 "binade_f8_layout": [P, P, P, P],
@@ -1088,13 +1102,28 @@ class MoeRoute:
     loss: torch.Tensor | None = None
 
 
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score_code(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score: {score!r}, expected 'softmax' or 'sigmoid'")
+    return _SCORES[score]
+
+
 @_on_device
 def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
               valid: torch.Tensor | None = None, stats: bool = True,
-              workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
+              workspace: torch.Tensor | None = None, stream=None, *, score: str = "softmax",
+              bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
+              group_best: int = 2, scale: float = 1.0) -> MoeRoute:
     """binade_moe_route: each token's top_k experts (idx int32 [T, top_k], for
-    r4_moe_gemv) and their weights (fp32 [T, top_k], for moe_combine) from
-    logits [T, E]; valid: bool or uint8 [T], False for padding."""
+    r4_moe_gemv and f8_moe_gemm) and their weights (fp32 [T, top_k], for
+    moe_combine) from logits [T, E]; valid: bool or uint8 [T], False for
+    padding. With another score than softmax, a bias (fp32 [E], added for the
+    choice alone), groups or a scale: binade_moe_route_scored, the top_k best
+    experts of the top_groups best of `groups` groups, a group's score the sum
+    of its group_best best."""
     logits, ld = _logits_arg(logits)
     dev = logits.device
     T, E = logits.shape
@@ -1109,6 +1138,20 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True,
         out.counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
         out.prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
         out.loss = torch.empty(1, dtype=torch.float32, device=dev)
+    code = _score_code(score)
+    if code or bias is not None or groups != 1 or top_groups != 1 or scale != 1.0:
+        if bias is not None:
+            bias = _arg("bias", bias, _F32_ONLY, (E,), dev)
+        rule = RouteRule(code, 1 if renormalize else 0, groups, top_groups, group_best, scale,
+                         _addr(bias))
+        if stats:
+            ws, at, nb = _scratch(_entry("binade_moe_route_scored_workspace_bytes")(T, E),
+                                  workspace, dev)
+        _run("binade_moe_route_scored", logits.data_ptr(), _CODE[logits.dtype], ld, T, E, top_k,
+             ctypes.byref(rule), _addr(valid), out.idx.data_ptr(), out.weights.data_ptr(),
+             _addr(out.counts), _addr(out.prob_sum), _addr(out.loss), at, nb, stream)
+        return out
+    if stats:
         ws, at, nb = _scratch(_entry("binade_moe_route_workspace_bytes")(T, E), workspace, dev)
     _run("binade_moe_route", logits.data_ptr(), _CODE[logits.dtype], ld, T, E,
          top_k, 1 if renormalize else 0, _addr(valid), out.idx.data_ptr(),
@@ -1122,9 +1165,13 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
                    dweights: torch.Tensor | None = None, counts: torch.Tensor | None = None,
                    dloss: torch.Tensor | None = None, renormalize: bool = True, out_dtype=None,
                    dlogits: torch.Tensor | None = None, status: torch.Tensor | None = None,
-                   stream=None) -> torch.Tensor:
+                   stream=None, *, score: str = "softmax", bias: torch.Tensor | None = None,
+                   groups: int = 1, scale: float = 1.0) -> torch.Tensor:
     """binade_moe_route_grad: the gradient of the logits from that of the
-    weights and (counts and dloss together) of the balance loss."""
+    weights and (counts and dloss together) of the balance loss. score, bias,
+    groups and scale as moe_route had them (binade_moe_route_scored_grad where
+    one of them is not the default; of bias and groups no value matters, only
+    that the choice went by them)."""
     logits, ld = _logits_arg(logits)
     dev = logits.device
     T, E = logits.shape
@@ -1141,6 +1188,13 @@ def moe_route_grad(logits: torch.Tensor, idx: torch.Tensor,
         counts = _arg("counts", counts, _I32_ONLY, (E + 1,), dev)
         dloss = _arg("dloss", dloss.reshape(-1), (torch.float32,), (1,), dev)
     dlogits = _out_arg("dlogits", dlogits, _TORCH_DTYPE[code], (T, E), dev)
+    kind = _score_code(score)
+    if kind or bias is not None or groups != 1 or scale != 1.0:
+        _run("binade_moe_route_scored_grad", logits.data_ptr(), _CODE[logits.dtype], ld, T, E,
+             top_k, kind, 1 if renormalize else 0, scale, idx.data_ptr(), _addr(dweights),
+             _addr(counts), _addr(dloss), dlogits.data_ptr(), code, E, _status_arg(status, dev),
+             stream)
+        return dlogits
     _run("binade_moe_route_grad", logits.data_ptr(), _CODE[logits.dtype], ld, T, E,
          top_k, 1 if renormalize else 0, idx.data_ptr(), _addr(dweights), _addr(counts),
          _addr(dloss), dlogits.data_ptr(), code, E, _status_arg(status, dev), stream)

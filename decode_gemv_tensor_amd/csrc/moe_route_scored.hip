@@ -1,0 +1,735 @@
+// The router by scores and its backward: sigmoid or softmax scores, a bias for
+// balance, groups of experts, top-k of the best groups, scaled weights (the
+// arithmetic is stated in binade.h). Rows, lanes and sums over rows as in
+// moe_route.hip: a row belongs to G lanes with V adjacent experts each.
+//
+// Choice. What is compared is score + bias in fp64. Nearly every row is
+// settled in fp32: a value and its expert make one whole-number key, the keys
+// are sorted, and the row counts as settled if every gap that decides
+// something (between the slots, to the best expert left out, between the last
+// group taken and the first left out) is larger than the fp32 values can be
+// off. A wave with a row that is not settled works its rows out again in
+// fp64. Without bias the logits themselves are the order, which is exact.
+//
+// Scores relative to the row's largest: sigmoid(x) = exp(min(x, 0)) / (1 +
+// exp(-|x|)), and quotients of scores do not change when exp(min(x, 0)) is
+// taken as exp(min(x, 0) - c) with c = min(0, the largest x); so neither sums
+// of scores nor their quotients underflow, however low a row's logits are.
+#include "moe_route.h"
+
+namespace binade {
+namespace {
+
+constexpr int kWavesABlock = 4;
+constexpr int32_t kScoredBlocks = 1024;   // at most: each leaves one row of partial sums
+constexpr int kMaxGroups = 64;
+
+struct ScoredArgs {
+  RouteArgs r;
+  const float* bias;
+  int32_t groups, group_size, top_groups, group_best;
+  float scale;
+  bool sigmoid;
+};
+
+// 1 / v for v >= 1/2 here; and exp(-|x|).
+__device__ __forceinline__ float low_exp(float x) { return exp_of(-fabsf(x)); }
+
+// KeyF32's key of any value: rising with it, -0 as +0; NaN and -inf as 0
+// (never taken); among equal values larger for the smaller expert.
+__device__ __forceinline__ uint64_t key_of(float v, int32_t expert) {
+  const uint32_t b = __float_as_uint(v);
+  const uint32_t neg = static_cast<uint32_t>(static_cast<int32_t>(b) >> 31);
+  const uint32_t o = (b ^ neg) + ((neg & 1u) | (~neg & 0x80000000u));
+  return v > -__builtin_inff() ? (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(expert))
+                               : 0u;
+}
+
+// How far apart two fp32 values have to be for their order to be the exact
+// one. A sigmoid is within 4 u of its value (u = 2^-24: the exponential's
+// product and result, the sum and its inverse, the product), at most 4 u; a
+// softmax p within (|d| + 9) u p <= 10 u; the bias's addition rounds by u |v|.
+// Twice that for two values is less than 32 u (1 + |v|); sums of two of them
+// twice that again.
+__device__ __forceinline__ float apart(float v) { return 1.9073486e-6f * (1.0f + fabsf(v)); }
+
+// The groups taken, as bits. row: the row's values in LDS; score: 64 places a
+// row. kF32: says in `sure` whether rounding could have changed the answer.
+template <int G, typename T>
+__device__ __forceinline__ uint64_t groups_taken(const ScoredArgs& p, const T* row, T* score, int l,
+                                                 bool exact, bool& sure) {
+  constexpr int kTurns = kMaxGroups / G > 0 ? kMaxGroups / G : 1;
+  const T none = -static_cast<T>(__builtin_inff());
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int32_t g = l + i * G;
+    if (g >= p.groups) break;
+    T a = none, b = none;
+    const T* from = row + g * p.group_size;
+    int32_t z = l % p.group_size;          // lanes start apart: other banks
+    for (int32_t n = 0; n < p.group_size; ++n) {
+      const T t = from[z];
+      b = t > a ? a : t > b ? t : b;
+      a = t > a ? t : a;
+      z = z + 1 == p.group_size ? 0 : z + 1;
+    }
+    score[g] = p.group_best == 2 && b > none ? a + b : a;
+  }
+  wave_sync();
+  uint64_t taken = 0;
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    if (i * G >= p.groups) break;
+    const int32_t g = l + i * G;
+    bool keep = false;
+    if (g < p.groups) {
+      const T mine = score[g];
+      if (mine > none) {
+        const T d = exact ? static_cast<T>(0) : static_cast<T>(2.0f * apart(static_cast<float>(mine)));
+        int32_t before = 0, over = 0, near = 0;
+        for (int32_t h = 0; h < p.groups; ++h) {
+          const T s = score[h];
+          before += s > mine || (s == mine && h < g) ? 1 : 0;
+          over += s > mine + d ? 1 : 0;
+          near += h != g && s >= mine - d ? 1 : 0;
+        }
+        keep = before < p.top_groups;
+        if (!exact && !(near < p.top_groups || over >= p.top_groups)) sure = false;
+      }
+    }
+    const uint64_t bits = __ballot(keep);
+    const int base = (threadIdx.x & 63) & ~(G - 1);
+    const uint64_t mine = G == 64 ? bits : (bits >> base) & ((1ull << (G & 63)) - 1);
+    taken |= mine << (i * G & 63);
+  }
+  return taken;
+}
+
+template <int G, int V, bool kBf16, bool kSort>
+__global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a) {
+  constexpr int kRows = 64 / G, kExperts = G * V;
+  constexpr int kHeld = kSort ? 1 : kMaxTopK / G;
+  __shared__ int32_t counts[kExperts + 1];
+  __shared__ double red[kWavesABlock];
+  __shared__ __align__(16) float x_s[kWavesABlock][kRows][kExperts];
+  __shared__ __align__(16) double v_s[kWavesABlock][kRows][kExperts];
+  __shared__ double g_s[kWavesABlock][kRows][kMaxGroups];
+  const RouteArgs& p = a.r;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l = lane & (G - 1), mine = lane / G;
+  const int32_t e0 = l * V;
+  const bool stats = p.counts != nullptr;
+  if (stats) {
+    for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) counts[e] = 0;
+    __syncthreads();
+  }
+  const bool by_logit = a.bias == nullptr, grouped = a.groups > 1 && a.top_groups < a.groups;
+  float bias[V], sums[V];
+  uint32_t group[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    bias[j] = !by_logit && e0 + j < p.n_experts ? a.bias[e0 + j] : 0.0f;
+    group[j] = grouped ? static_cast<uint32_t>(e0 + j) / static_cast<uint32_t>(a.group_size) & 63u : 0u;
+    sums[j] = 0.0f;
+  }
+  float* x_row = x_s[wave][mine];
+  double* v_row = v_s[wave][mine];
+  float* vf_row = reinterpret_cast<float*>(v_row);
+  double* g_row = g_s[wave][mine];
+  const float none = -__builtin_inff();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesABlock * kRows;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWavesABlock + wave) * kRows; t0 < p.n_tokens;
+       t0 += step) {
+    const int64_t t = t0 + mine;
+    const bool in = t < p.n_tokens;
+    const bool valid = in && (p.valid == nullptr || p.valid[t] != 0);
+    Logits<V, kBf16> x;
+    x.load(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec);
+    float top = x.value(0);
+#pragma unroll
+    for (int j = 1; j < V; ++j) top = fmaxf(top, x.value(j));
+    top = group_max<G>(top);
+    // scores relative to exp(shift), and their sum
+    const float shift = a.sigmoid ? fminf(top, 0.0f) : top;
+    float s[V], total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float xv = x.value(j);
+      if (a.sigmoid) {
+        s[j] = exp_of(fminf(xv, 0.0f) - shift) * inverse(1.0f + low_exp(xv));
+        if (xv != xv) s[j] = xv;
+      } else {
+        s[j] = exp_of(xv - top);
+      }
+      x_row[e0 + j] = xv;
+      total += s[j];
+    }
+    total = group_sum<G>(total);
+    const float inv = inverse(total);
+    // what is compared
+    const bool plain = by_logit || (!a.sigmoid && total != total);
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float xv = x.value(j);
+      const float abs = a.sigmoid ? s[j] * (shift < 0.0f ? exp_of(shift) : 1.0f) : s[j] * inv;
+      v[j] = !(xv > none) ? none : plain ? xv : abs + bias[j];
+      if (grouped) vf_row[e0 + j] = !(xv > none) ? none
+                                    : plain && (a.group_best == 1 || total != total) ? xv : abs + bias[j];
+    }
+    wave_sync();
+    bool sure = true;
+    if (grouped) {
+      const uint64_t taken = groups_taken<G, float>(a, vf_row, reinterpret_cast<float*>(g_row), l,
+                                                    plain && (a.group_best == 1 || total != total), sure);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = (taken >> group[j]) & 1 ? v[j] : none;
+    }
+    uint64_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = key_of(v[j], e0 + j);
+    // lane l of the row: slots l, l + G, ..; -1 where none is left
+    int32_t slot[kHeld];
+    float first = 0.0f;
+    uint64_t last;
+    if (kSort) {
+      uint64_t best[8];
+      best8<G, V>(key, best);
+      slot[0] = -1;
+      last = best[0];
+#pragma unroll
+      for (int j = 0; j < kSorted; ++j) {
+        if (l == j && best[j] != 0) slot[0] = KeyF32::expert(best[j]);
+        if (j >= p.top_k) continue;
+        last = best[j];
+        if (!plain && j > 0 && best[j] != 0) {
+          const float b = KeyF32::value(best[j]);
+          sure &= KeyF32::value(best[j - 1]) - b > apart(b) + apart(first);
+        }
+        if (j == 0) first = KeyF32::value(best[0]);
+      }
+    } else {
+      int32_t n = 0;
+      last = 0;
+      float before = 0.0f;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        slot[h] = -1;
+        for (int j = 0; j < G && n < p.top_k; ++j, ++n) {
+          last = key[0];
+#pragma unroll
+          for (int q = 1; q < V; ++q) last = key[q] > last ? key[q] : last;
+          last = group_max_key<G>(last);
+#pragma unroll
+          for (int q = 0; q < V; ++q) key[q] = key[q] == last ? 0 : key[q];
+          if (l == j && last != 0) slot[h] = KeyF32::expert(last);
+          const float b = KeyF32::value(last);
+          if (n == 0) first = b;
+          if (!plain && n > 0 && last != 0) sure &= before - b > apart(b) + apart(first);
+          before = b;
+        }
+      }
+    }
+    if (!plain && last != 0) {   // the best one left out
+      uint64_t next = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) next = key[j] < last && key[j] > next ? key[j] : next;
+      next = group_max_key<G>(next);
+      if (next != 0) {
+        const float b = KeyF32::value(next);
+        sure &= KeyF32::value(last) - b > apart(b) + apart(first);
+      }
+    }
+    if (__ballot(!sure && valid) != 0) {   // rare: these rows in fp64
+      double w[V], all = 0.0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const double xv = x.value(j);
+        w[j] = a.sigmoid ? (xv < 0.0 ? exp(xv) : 1.0) / (1.0 + exp(-fabs(xv))) : exp(xv - static_cast<double>(top));
+        all += w[j];
+      }
+      butterfly<G>([&](auto step) {
+        uint64_t c, d;
+        pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, all), c, d);
+        all = __builtin_bit_cast(double, c) + __builtin_bit_cast(double, d);
+      });
+      wave_sync();
+      const double nothing = -static_cast<double>(__builtin_inff());
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const double xv = x.value(j), score = (a.sigmoid ? w[j] : w[j] / all) + static_cast<double>(bias[j]);
+        const bool open = x.value(j) > none;
+        v_row[e0 + j] = !open ? nothing : plain && (a.group_best == 1 || total != total) ? xv : score;
+        w[j] = !open ? nothing : plain ? xv : score;
+        if (!(w[j] > nothing)) w[j] = nothing;
+      }
+      wave_sync();
+      if (grouped) {
+        const uint64_t taken = groups_taken<G, double>(a, v_row, g_row, l, true, sure);
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = (taken >> group[j]) & 1 ? w[j] : nothing;
+      }
+      int32_t n = 0;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        slot[h] = -1;
+        for (int q = 0; q < G && n < p.top_k; ++q, ++n) {
+          double best = w[0];
+          uint32_t at = e0;
+#pragma unroll
+          for (int j = 1; j < V; ++j) {
+            at = w[j] > best ? e0 + j : at;
+            best = w[j] > best ? w[j] : best;
+          }
+          butterfly<G>([&](auto step) {
+            uint64_t c, d;
+            uint32_t ac, ad;
+            pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, best), c, d);
+            pair_of<decltype(step)::value>(at, ac, ad);
+            const double bc = __builtin_bit_cast(double, c), bd = __builtin_bit_cast(double, d);
+            const bool second = bd > bc || (bd == bc && ad < ac);
+            best = second ? bd : bc;
+            at = second ? ad : ac;
+          });
+#pragma unroll
+          for (int j = 0; j < V; ++j) w[j] = at == static_cast<uint32_t>(e0 + j) ? nothing : w[j];
+          if (l == q && best > nothing) slot[h] = static_cast<int32_t>(at);
+        }
+      }
+    }
+    // weights of the slots
+    float e[kHeld], xs[kHeld], high = none, taken = 0.0f;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if ((kSort && l >= kSorted) || l + h * G >= p.top_k) slot[h] = -1;
+      xs[h] = slot[h] >= 0 ? x_row[slot[h]] : none;
+      high = fmaxf(high, xs[h]);
+    }
+    high = group_max<G>(high);
+    const bool counted = valid && high > none;
+    const float base = !p.renorm ? (a.sigmoid ? 0.0f : top) : a.sigmoid ? fminf(high, 0.0f) : high;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      e[h] = 0.0f;
+      if (slot[h] >= 0)
+        e[h] = a.sigmoid ? exp_of(fminf(xs[h], 0.0f) - base) * inverse(1.0f + low_exp(xs[h]))
+                         : exp_of(xs[h] - base);
+      taken += e[h];
+    }
+    if (p.renorm) taken = group_sum<G>(taken);
+    // a NaN among the logits is one of every softmax weight
+    const float f = !a.sigmoid && total != total ? total
+                    : p.renorm ? inverse(taken) : a.sigmoid ? 1.0f : inv;
+    if (stats) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sums[j] = counted ? __builtin_fmaf(s[j], inv, sums[j]) : sums[j];
+      if (counted && l == 0) atomicAdd(&counts[p.n_experts], 1);
+    }
+    if (in) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        const int32_t n = l + h * G;
+        if ((kSort && l >= kSorted) || n >= p.top_k) continue;
+        const bool some = counted && slot[h] >= 0;
+        p.idx[t * p.top_k + n] = some ? slot[h] : -1;
+        p.weights[t * p.top_k + n] = some ? e[h] * f * a.scale : 0.0f;
+        if (stats && some) atomicAdd(&counts[slot[h]], 1);
+      }
+    }
+    wave_sync();
+  }
+  if (!stats) return;
+  __syncthreads();
+  // the wave's rows, then the block's waves, in a fixed order
+  float(*prob)[kExperts] = reinterpret_cast<float(*)[kExperts]>(&x_s[0][0][0]);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float s = sums[j];
+    uint32_t b, c;
+    if (G <= 8) s += __shfl_xor(s, 8, 64);
+    if (G <= 16) {
+      pair_of<16>(__float_as_uint(s), b, c);
+      s = __uint_as_float(b) + __uint_as_float(c);
+    }
+    if (G <= 32) {
+      pair_of<32>(__float_as_uint(s), b, c);
+      s = __uint_as_float(b) + __uint_as_float(c);
+    }
+    if (lane < G) prob[wave][e0 + j] = s;
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  double term = 0.0;
+  for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) {
+    (alone ? p.counts : p.part_counts + static_cast<int64_t>(blockIdx.x) * (p.n_experts + 1))[e] =
+        counts[e];
+    if (e == p.n_experts) continue;
+    double s = 0.0;
+    for (int w = 0; w < kWavesABlock; ++w) s += prob[w][e];
+    (alone ? p.prob_sum : p.part_prob + static_cast<int64_t>(blockIdx.x) * p.n_experts)[e] =
+        static_cast<float>(s);
+    term += counts[e] * s;
+  }
+  if (alone) {
+    term = block_sum(term, red);
+    if (threadIdx.x == 0) p.loss[0] = loss_of(term, p.n_experts, p.top_k, counts[p.n_experts]);
+  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.ticket = 0;
+  }
+}
+
+// ---------------------------------------------------------------- backward
+struct ScoredGradArgs {
+  const void* logits;
+  const int32_t* idx;
+  const float* dweights;
+  const int32_t* counts;
+  const float* dloss;
+  void* dlogits;
+  uint32_t* status;
+  int64_t ld, ld_d, n_tokens;
+  int32_t n_experts, top_k;
+  float scale;
+  bool renorm, sigmoid, vec, vec_d;
+};
+
+// With t[e] the slots' scores over their sum (renormalised) and q[e] all
+// scores over theirs, u and h the sums of dweights and the number of an
+// expert's slots and f the loss's share: the weights give t (u - h sum u t) or
+// s u, the loss q (f - sum f q), each times 1 - s for a sigmoid; a softmax that
+// is not renormalised p (u - sum u p). The slots' gradients reach their
+// experts' lanes through rows of LDS, as in moe_route.hip.
+template <int G, int V, bool kBf16, bool kOutBf16>
+__global__ __launch_bounds__(256) void scored_grad_kernel(ScoredGradArgs p) {
+  constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;
+  __shared__ __align__(16) float grad_s[4 * kRows][kExperts];
+  __shared__ __align__(16) float hits_s[4 * kRows][kExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & (G - 1);
+  const int32_t e0 = l * V;
+  float* grad_row = grad_s[wave * kRows + lane / G];
+  float* hits_row = hits_s[wave * kRows + lane / G];
+  constexpr int kPieces = V / 4;
+  const auto place = [](int32_t e) {   // of expert e in a row
+    const int32_t of = e / V, piece = e / 4 % kPieces;
+    return of * V + 4 * (piece ^ ((of >> 2) & (kPieces - 1))) + e % 4;
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) grad_row[e0 + j] = hits_row[e0 + j] = 0.0f;
+  wave_sync();
+  float load[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) load[j] = 0.0f;
+  const bool balance = p.counts != nullptr;
+  if (balance) {
+    const int32_t r = p.counts[p.n_experts];
+    const float rows = static_cast<float>(r > 0 ? r : 1);
+    const float f = p.dloss[0] * static_cast<float>(p.n_experts) /
+                    (static_cast<float>(p.top_k) * rows) / rows;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (e0 + j < p.n_experts) load[j] = f * static_cast<float>(p.counts[e0 + j]);
+  }
+  const float none = -__builtin_inff();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * kRows;
+  Logits<V, kBf16> next;
+  int32_t e_next[kHeld];
+  float w_next[kHeld];
+  const auto request = [&](int64_t t0) __attribute__((always_inline)) {
+    const int64_t t = t0 + lane / G;
+    const bool in = t < p.n_tokens;
+    const int64_t row = in ? t : p.n_tokens - 1;
+    next.load(p.logits, row * p.ld, e0, p.n_experts, p.vec);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      const int32_t s = l + h * G;
+      const int64_t at = row * p.top_k + (s < p.top_k ? s : 0);
+      e_next[h] = p.idx[at];
+      w_next[h] = p.dweights != nullptr ? p.dweights[at] : 0.0f;
+      if (!in || s >= p.top_k) e_next[h] = -1;
+    }
+  };
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kRows;
+  if (t0 >= p.n_tokens) return;
+  request(t0);
+  for (; t0 < p.n_tokens; t0 += step) {
+    const int64_t t = t0 + lane / G;
+    const Logits<V, kBf16> x = next;
+    int32_t e[kHeld];
+    bool counted = false;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      e[h] = e_next[h];
+      if (e[h] < 0 || e[h] >= p.n_experts) {
+        if (e[h] != -1 && p.status != nullptr)
+          atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+        e[h] = -1;
+        continue;
+      }
+      counted |= h == 0 && l == 0;
+      atomicAdd(&hits_row[place(e[h])], 1.0f);
+      if (p.dweights != nullptr) atomicAdd(&grad_row[place(e[h])], w_next[h]);
+    }
+    if (t0 + step < p.n_tokens) request(t0 + step);
+    wave_sync();
+    counted = (__ballot(counted) >> (lane & ~(G - 1)) & 1u) != 0;
+    float u[V], hits[V];
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      __builtin_memcpy(&u[4 * q], &grad_row[place(e0 + 4 * q)], 16);
+      __builtin_memcpy(&hits[4 * q], &hits_row[place(e0 + 4 * q)], 16);
+    }
+    float top = x.value(0), high = none;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      top = fmaxf(top, x.value(j));
+      high = hits[j] != 0.0f ? fmaxf(high, x.value(j)) : high;
+    }
+    top = group_max<G>(top);
+    high = group_max<G>(high);
+    float d[V];
+    // scores over their sum q; for a sigmoid also s itself and 1 - s
+    float q[V], s[V], rest[V], total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float xv = x.value(j);
+      if (p.sigmoid) {
+        const float ex = low_exp(xv), in = inverse(1.0f + ex);
+        s[j] = xv >= 0.0f ? in : ex * in;
+        rest[j] = xv >= 0.0f ? ex * in : in;
+        q[j] = exp_of(fminf(xv, 0.0f) - fminf(top, 0.0f)) * in;
+      } else {
+        q[j] = exp_of(xv - top);
+        rest[j] = 1.0f;
+      }
+      total += q[j];
+    }
+    const float inv = inverse(group_sum<G>(total));
+    float mean = 0.0f, shares = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      q[j] *= inv;
+      shares = __builtin_fmaf(q[j], load[j], shares);
+    }
+    if (p.renorm) {
+      float tv[V], sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xv = x.value(j);
+        tv[j] = 0.0f;
+        if (hits[j] != 0.0f)
+          tv[j] = p.sigmoid ? exp_of(fminf(xv, 0.0f) - fminf(high, 0.0f)) * inverse(1.0f + low_exp(xv))
+                            : exp_of(xv - high);
+        sum = __builtin_fmaf(hits[j], tv[j], sum);
+        mean = __builtin_fmaf(u[j], tv[j], mean);
+      }
+      const float f = inverse(group_sum<G>(sum));
+      mean = group_sum<G>(mean) * f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = p.scale * (tv[j] * f) * (u[j] - hits[j] * mean);
+    } else if (p.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = u[j] != 0.0f ? p.scale * s[j] * u[j] : 0.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) mean = __builtin_fmaf(q[j], u[j], mean);
+      mean = group_sum<G>(mean);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = p.scale * q[j] * (u[j] - mean);
+    }
+    if (balance) {
+      shares = group_sum<G>(shares);
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = __builtin_fmaf(q[j], load[j] - shares, d[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = counted ? d[j] * rest[j] : 0.0f;
+    wave_sync();
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      if (h * G >= p.top_k) break;
+      if (e[h] >= 0) grad_row[place(e[h])] = hits_row[place(e[h])] = 0.0f;
+    }
+    wave_sync();
+    if (t >= p.n_tokens) continue;
+    const int64_t row = t * p.ld_d;
+#pragma unroll
+    for (int b = 0; b < V / 8; ++b) {
+      const int32_t ex = e0 + 8 * b;
+      if (p.vec_d) {
+        if (ex >= p.n_experts) continue;
+        if (kOutBf16) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = pack_bf16(d[8 * b + 2 * j], d[8 * b + 2 * j + 1]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dlogits) + row + ex) =
+              uint4{o[0], o[1], o[2], o[3]};
+        } else {
+          __builtin_memcpy(__builtin_assume_aligned(static_cast<float*>(p.dlogits) + row + ex, 16),
+                           &d[8 * b], 32);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (ex + j >= p.n_experts) continue;
+          if (kOutBf16) static_cast<uint16_t*>(p.dlogits)[row + ex + j] = to_bf16_rne(d[8 * b + j]);
+          else static_cast<float*>(p.dlogits)[row + ex + j] = d[8 * b + j];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- hosts
+int32_t scored_lanes(int32_t n_experts) {
+  return n_experts <= 64 ? 8 : n_experts <= 128 ? 16 : n_experts <= 256 ? 32 : 64;
+}
+
+uint32_t scored_blocks(int64_t n_tokens, int32_t n_experts) {
+  const int64_t rows = kWavesABlock * (64 / scored_lanes(n_experts));
+  const int64_t b = (n_tokens + rows - 1) / rows;
+  return static_cast<uint32_t>(b < 1 ? 1 : b > kScoredBlocks ? kScoredBlocks : b);
+}
+
+template <int G, int V>
+void launch_scored(const ScoredArgs& p, uint32_t blocks, bool bf16, hipStream_t st) {
+  const dim3 grid(blocks), block(64 * kWavesABlock);
+  const bool sort = p.r.top_k <= kSorted;
+  if (bf16 && sort) hipLaunchKernelGGL((scored_kernel<G, V, true, true>), grid, block, 0, st, p);
+  else if (bf16) hipLaunchKernelGGL((scored_kernel<G, V, true, false>), grid, block, 0, st, p);
+  else if (sort) hipLaunchKernelGGL((scored_kernel<G, V, false, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((scored_kernel<G, V, false, false>), grid, block, 0, st, p);
+}
+
+template <int G, int V>
+void launch_scored_grad(const ScoredGradArgs& p, bool bf16, bool out_bf16, hipStream_t st) {
+  const int64_t rows = 4 * (64 / G), b = (p.n_tokens + rows - 1) / rows;
+  const dim3 grid(static_cast<uint32_t>(b < 1024 ? b : 1024)), block(256);
+  if (bf16 && out_bf16) hipLaunchKernelGGL((scored_grad_kernel<G, V, true, true>), grid, block, 0, st, p);
+  else if (bf16) hipLaunchKernelGGL((scored_grad_kernel<G, V, true, false>), grid, block, 0, st, p);
+  else if (out_bf16) hipLaunchKernelGGL((scored_grad_kernel<G, V, false, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((scored_grad_kernel<G, V, false, false>), grid, block, 0, st, p);
+}
+
+bool score_ok(int32_t score) { return score == BINADE_SOFTMAX || score == BINADE_SIGMOID; }
+
+}  // namespace
+}  // namespace binade
+
+using namespace binade;
+
+extern "C" int64_t binade_moe_route_scored_workspace_bytes(int64_t n_tokens, int32_t n_experts) {
+  if (!route_sizes_ok(n_tokens, n_experts)) return 0;
+  return kHead + static_cast<int64_t>(scored_blocks(n_tokens, n_experts)) * (2 * n_experts + 1) * 4;
+}
+
+extern "C" int32_t binade_moe_route_scored(const void* logits, int32_t dtype, int64_t ld,
+                                           int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                                           const binade_route_rule* rule, const uint8_t* valid,
+                                           int32_t* idx, float* weights, int32_t* counts,
+                                           float* prob_sum, float* loss, void* workspace,
+                                           int64_t workspace_bytes, void* stream) {
+  if (!route_sizes_ok(n_tokens, n_experts) || top_k < 1 || top_k > n_experts || top_k > kMaxTopK ||
+      ld < n_experts || rule == nullptr)
+    return BINADE_EINVAL;
+  if (dtype != BINADE_F32 && dtype != BINADE_BF16) return BINADE_EINVAL;
+  if (!score_ok(rule->score) || rule->groups < 1 || rule->groups > kMaxGroups ||
+      n_experts % rule->groups != 0 || rule->top_groups < 1 || rule->top_groups > rule->groups ||
+      (rule->group_best != 1 && rule->group_best != 2) ||
+      top_k > rule->top_groups * (n_experts / rule->groups) || !__builtin_isfinite(rule->scale))
+    return BINADE_EINVAL;
+  const bool stats = counts != nullptr;
+  if (stats != (prob_sum != nullptr) || stats != (loss != nullptr)) return BINADE_EINVAL;
+  if (n_tokens == 0 && !stats) return BINADE_OK;
+  if (n_tokens > 0 && (logits == nullptr || idx == nullptr || weights == nullptr))
+    return BINADE_EINVAL;
+  if (stats) {
+    if (workspace == nullptr ||
+        workspace_bytes < binade_moe_route_scored_workspace_bytes(n_tokens, n_experts))
+      return BINADE_ENOSPACE;
+    if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
+  }
+  const uint32_t blocks = scored_blocks(n_tokens, n_experts);
+  ScoredArgs a{};
+  RouteArgs& p = a.r;
+  p.logits = logits;
+  p.valid = valid;
+  p.idx = idx;
+  p.weights = weights;
+  p.counts = counts;
+  p.prob_sum = prob_sum;
+  p.loss = loss;
+  p.ticket = static_cast<uint32_t*>(workspace);
+  p.part_loss = static_cast<double*>(workspace) + 8;
+  p.part_counts = static_cast<int32_t*>(workspace) + kHead / 4;
+  p.part_prob = reinterpret_cast<float*>(p.part_counts + static_cast<int64_t>(blocks) * (n_experts + 1));
+  p.ld = ld;
+  p.n_tokens = n_tokens;
+  p.n_experts = n_experts;
+  p.top_k = top_k;
+  p.renorm = rule->renormalize != 0;
+  const bool bf16 = dtype == BINADE_BF16;
+  p.vec = whole_pieces(logits, n_experts, ld, bf16);
+  a.bias = rule->bias;
+  a.groups = rule->groups;
+  a.group_size = n_experts / rule->groups;
+  a.top_groups = rule->top_groups;
+  a.group_best = rule->group_best;
+  a.scale = rule->scale;
+  a.sigmoid = rule->score == BINADE_SIGMOID;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n_experts <= 64) launch_scored<8, 8>(a, blocks, bf16, st);
+  else if (n_experts <= 128) launch_scored<16, 8>(a, blocks, bf16, st);
+  else if (n_experts <= 256) launch_scored<32, 8>(a, blocks, bf16, st);
+  else if (n_experts <= 512) launch_scored<64, 8>(a, blocks, bf16, st);
+  else launch_scored<64, 16>(a, blocks, bf16, st);
+  if (stats && blocks > 1)
+    hipLaunchKernelGGL(route_stats_kernel, dim3(static_cast<uint32_t>((n_experts + 63) / 64)),
+                       dim3(1024), 0, st, p, static_cast<int32_t>(blocks));
+  return launch_status();
+}
+
+extern "C" int32_t binade_moe_route_scored_grad(const void* logits, int32_t dtype, int64_t ld,
+                                                int64_t n_tokens, int32_t n_experts, int32_t top_k,
+                                                int32_t score, int32_t renormalize, float scale,
+                                                const int32_t* idx, const float* dweights,
+                                                const int32_t* counts, const float* dloss,
+                                                void* dlogits, int32_t dlogits_dtype, int64_t ld_d,
+                                                uint32_t* dev_status, void* stream) {
+  if (!route_sizes_ok(n_tokens, n_experts) || top_k < 1 || top_k > n_experts || top_k > kMaxTopK ||
+      ld < n_experts || ld_d < n_experts || !score_ok(score) || !__builtin_isfinite(scale))
+    return BINADE_EINVAL;
+  if ((dtype != BINADE_F32 && dtype != BINADE_BF16) ||
+      (dlogits_dtype != BINADE_F32 && dlogits_dtype != BINADE_BF16))
+    return BINADE_EINVAL;
+  if ((counts != nullptr) != (dloss != nullptr)) return BINADE_EINVAL;
+  if (n_tokens == 0) return BINADE_OK;
+  if (logits == nullptr || idx == nullptr || dlogits == nullptr) return BINADE_EINVAL;
+  const bool bf16 = dtype == BINADE_BF16, out_bf16 = dlogits_dtype == BINADE_BF16;
+  ScoredGradArgs p{};
+  p.logits = logits;
+  p.idx = idx;
+  p.dweights = dweights;
+  p.counts = counts;
+  p.dloss = dloss;
+  p.dlogits = dlogits;
+  p.status = dev_status;
+  p.ld = ld;
+  p.ld_d = ld_d;
+  p.n_tokens = n_tokens;
+  p.n_experts = n_experts;
+  p.top_k = top_k;
+  p.scale = scale;
+  p.renorm = renormalize != 0;
+  p.sigmoid = score == BINADE_SIGMOID;
+  p.vec = whole_pieces(logits, n_experts, ld, bf16);
+  p.vec_d = whole_pieces(dlogits, n_experts, ld_d, out_bf16);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n_experts <= 64) launch_scored_grad<8, 8>(p, bf16, out_bf16, st);
+  else if (n_experts <= 128) launch_scored_grad<16, 8>(p, bf16, out_bf16, st);
+  else if (n_experts <= 256) launch_scored_grad<32, 8>(p, bf16, out_bf16, st);
+  else if (n_experts <= 512) launch_scored_grad<64, 8>(p, bf16, out_bf16, st);
+  else launch_scored_grad<64, 16>(p, bf16, out_bf16, st);
+  return launch_status();
+}

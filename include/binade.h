@@ -614,6 +614,70 @@ int32_t binade_moe_route_grad(const void *logits, int32_t dtype, int64_t ld,
                               int64_t ld_d, uint32_t *dev_status,
                               void *stream);
 
+/* The router by scores. Where binade_moe_route compares logits and weighs by
+ * softmax, a rule says here what scores are, what is added to them for the
+ * choice alone, and which groups of experts a token may use:
+ *   s[e] = sigmoid(logits[t, e]), or softmax(logits[t])[e];
+ *   v[e] = s[e] + bias[e] (bias: device fp32 [n_experts]; it moves load
+ *   between experts and has no part in the weights or gradients), in fp64.
+ *   Without bias (NULL) the order of the logits is v's;
+ *   groups: the experts in that many equal runs; a group's score is the sum
+ *   of its group_best (1 or 2) largest v, or its one v where no other of it
+ *   can be taken; only experts of the top_groups groups of largest score,
+ *   equal ones by rising group, can be taken;
+ *   idx: the top_k largest v among these in falling order, equal ones by
+ *   rising expert. Experts of logit or v -inf or NaN are never taken;
+ *   weights = scale * s of the slot's expert, or scale * s over the sum of s
+ *   of the row's taken experts if renormalize != 0.
+ * A NaN or +inf among a softmax row's logits makes its weights NaN, and its
+ * choice the logits'. */
+typedef enum binade_score { BINADE_SOFTMAX = 0, BINADE_SIGMOID = 1 } binade_score;
+
+typedef struct binade_route_rule {
+  int32_t score;          /* binade_score */
+  int32_t renormalize;
+  int32_t groups;         /* 1..64, a divisor of n_experts (1: no groups) */
+  int32_t top_groups;     /* 1..groups; top_k <= top_groups * group size */
+  int32_t group_best;     /* 1 or 2 */
+  float scale;            /* finite */
+  const float *bias;      /* device, or NULL */
+} binade_route_rule;
+
+/* The choice by a rule; everything else (valid, slots with no expert left,
+ * counts, loss, refusals) as in binade_moe_route, with prob_sum[e] the sum of
+ * s[e] / sum_j s[j] over the rows that count. workspace:
+ * binade_moe_route_scored_workspace_bytes. */
+int32_t binade_moe_route_scored(const void *logits, int32_t dtype, int64_t ld,
+                                int64_t n_tokens, int32_t n_experts,
+                                int32_t top_k, const binade_route_rule *rule,
+                                const uint8_t *valid, int32_t *idx,
+                                float *weights, int32_t *counts,
+                                float *prob_sum, float *loss, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+int64_t binade_moe_route_scored_workspace_bytes(int64_t n_tokens,
+                                                int32_t n_experts);
+
+/* Its backward: dlogits of sum(dweights * weights) + dloss * loss for the
+ * choice idx, which is constant. Arguments as in binade_moe_route_grad, with
+ * the rule's score, renormalize and scale. With u[e] and h[e] the sum of
+ * dweights and the number of the slots that took e, f[e] = dloss * n_experts
+ * * counts[e] / (top_k R R), q = s / sum_j s[j], t = s / (sum of s over the
+ * slots): the weights give scale * t (u - h sum_j u t), or scale * s u (softmax:
+ * scale * s (u - sum_j s u)) if not renormalised; the loss q (f - sum_j f q);
+ * both times 1 - s for a sigmoid. It holds for any choice, also where the
+ * experts taken score far below others. */
+int32_t binade_moe_route_scored_grad(const void *logits, int32_t dtype,
+                                     int64_t ld, int64_t n_tokens,
+                                     int32_t n_experts, int32_t top_k,
+                                     int32_t score, int32_t renormalize,
+                                     float scale, const int32_t *idx,
+                                     const float *dweights,
+                                     const int32_t *counts, const float *dloss,
+                                     void *dlogits, int32_t dlogits_dtype,
+                                     int64_t ld_d, uint32_t *dev_status,
+                                     void *stream);
+
 /* Low-rank adapters of a projection with n outputs and k inputs (device
  * pointers): n_adapters adapters stacked at one rank, those of a smaller
  * rank padded with zeros.
