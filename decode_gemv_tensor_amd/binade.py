@@ -1356,16 +1356,13 @@ class F8Weight:
         return self._desc
 
 
-def _f8_planes(rows, cols, count, scale_dtype, train, device, values=None) -> F8Weight:
+def _f8_planes(rows, cols, count, scale_dtype, train, device) -> F8Weight:
     sizes = F8Sizes()
     _run("binade_f8_sizes_of", rows, cols, count, scale_dtype, ctypes.byref(sizes))
     new = lambda n: torch.empty(n, dtype=torch.uint8, device=device)
-    if values is None:
-        values = new(sizes.values_bytes)
-    w = F8Weight(rows, cols, count, scale_dtype, values, new(sizes.scales_bytes),
-                 new(sizes.values_t_bytes) if train else None,
-                 new(sizes.scales_t_bytes) if train else None)
-    return w
+    return F8Weight(rows, cols, count, scale_dtype, new(sizes.values_bytes),
+                    new(sizes.scales_bytes), new(sizes.values_t_bytes) if train else None,
+                    new(sizes.scales_t_bytes) if train else None)
 
 
 def _matrices(name: str, t: torch.Tensor):
@@ -1406,7 +1403,7 @@ def f8_weight(values: torch.Tensor, scales: torch.Tensor, train: bool = False,
     """binade_f8_layout: a checkpoint's e4m3 values [N, K] or [count, N, K]
     (float8_e4m3fn or their bytes) and their blocks' scales [(count,) ceil(N /
     128), ceil(K / 128)], fp32 or powers of two (float8_e8m0fnu or their
-    bytes). The values are kept as they are where K % 128 == 0."""
+    bytes). Both are copied."""
     if values.dtype not in _BYTES_OF_F8:
         raise TypeError(f"values: {values.dtype}, expected float8_e4m3fn")
     count, rows, cols = _matrices("values", values)
@@ -1416,8 +1413,7 @@ def f8_weight(values: torch.Tensor, scales: torch.Tensor, train: bool = False,
     scales = _arg("scales", scales, (scales.dtype,), (*values.shape[:-2], *blocks), values.device)
     values = _whole16(values)
     code = F32 if scales.dtype == torch.float32 else E8M0
-    out = _f8_planes(rows, cols, count, code, train, values.device,
-                     values.view(torch.uint8) if cols % 128 == 0 else None)
+    out = _f8_planes(rows, cols, count, code, train, values.device)
     _run("binade_f8_layout", values.data_ptr(), scales.data_ptr(), ctypes.byref(out.desc()), stream)
     return out
 

@@ -47,6 +47,8 @@ constexpr int kSmallPairs = 256;         // pairs that the few-row kernel sorts 
 inline int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
 inline int64_t padded(int64_t n) { return blocks_of(n) * 128; }
 inline int64_t codes_of(int64_t n) { return (blocks_of(n) + 3) / 4 * 4; }   // bytes of a row's codes
+// Columns of an operand that is quantised here: whole pairs of blocks.
+inline int64_t paired(int64_t n) { return (n + 255) / 256 * 256; }
 inline int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------- scales
@@ -136,13 +138,18 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n,
 }
 
 // ----------------------------------------------------------------- quantise
-// Rows of v [m, n] as e4m3 [m, padded(n)] with a code for 128 columns: 16
-// lanes a block, 8 values a lane.
+// Operands lie block by block of 128 columns, a block's rows one behind the
+// other: a tile's step is one piece of memory, whatever the row's length (rows
+// of 15360 bytes one below the other meet only four of an L2's sixteen
+// channels: 1.5 times the time of a large product).
+//
+// Rows of v [m, n] as e4m3, paired(n) / 128 blocks of m_pad rows, with a code
+// for each block of a row: 16 lanes a block, 8 values a lane.
 __global__ __launch_bounds__(256) void quantise_rows_kernel(const uint16_t* v, int64_t ld,
                                                             int64_t m, int64_t n, bool vec,
-                                                            uint8_t* q, int64_t ldq, uint8_t* codes,
+                                                            uint8_t* q, int64_t m_pad, uint8_t* codes,
                                                             int64_t ldc) {
-  const int64_t nb = (n + 127) / 128, units = m * nb;
+  const int64_t nb = (n + 255) / 256 * 2, units = m * nb;
   const int l = threadIdx.x & 15;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 16;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); u < units;
@@ -154,13 +161,13 @@ __global__ __launch_bounds__(256) void quantise_rows_kernel(const uint16_t* v, i
                                                     max_pair(finite_abs(d[2]), finite_abs(d[3])))));
     const uint32_t code = code_of(top);
     const float s = scale_of_code(code);
-    *reinterpret_cast<uint2*>(q + row * ldq + b * 128 + l * 8) =
+    *reinterpret_cast<uint2*>(q + (b * m_pad + row) * 128 + l * 8) =
         uint2{to_f8(d[0], d[1], s), to_f8(d[2], d[3], s)};
     if (l == 0) codes[row * ldc + b] = static_cast<uint8_t>(code);
   }
 }
 
-// 128 x 128 tiles of v [m, n], turned: qt [n, padded(m)] with codes for 128
+// 128 x 128 tiles of v [m, n], turned: qt of n_pad rows with codes for 128
 // rows of a column, and (kRows) also as quantise_rows_kernel leaves them; or
 // (kOne) with one code for the tile, as weights are kept, q and (qt not NULL)
 // qt. A tile lies in LDS as pairs of columns; rows 32 apart, which four
@@ -169,7 +176,8 @@ struct TileArgs {
   const uint16_t* v;
   int64_t ld, m, n;
   uint8_t *q, *codes, *qt, *codes_t;
-  int64_t ldq, ldc, ldqt, ldct;
+  int64_t m_pad, n_pad;      // rows of a block of q, of qt
+  int64_t ldc, ldct;
   int64_t v_next, q_next, c_next, qt_next, ct_next;   // from one matrix to the next
   bool vec;
 };
@@ -204,7 +212,7 @@ __global__ __launch_bounds__(256) void quantise_tile_kernel(TileArgs p) {
       const uint32_t c = code_of(max16(max_of_pair(a)));
       const float s = scale_of_code(c);
       if (r0 + row < p.m) {
-        *reinterpret_cast<uint2*>(p.q + (r0 + row) * p.ldq + c0 + l * 8) =
+        *reinterpret_cast<uint2*>(p.q + (blockIdx.x * p.m_pad + r0 + row) * 128 + l * 8) =
             uint2{to_f8(d[i][0], d[i][1], s), to_f8(d[i][2], d[i][3], s)};
         if (l == 0) p.codes[(r0 + row) * p.ldc + blockIdx.x] = static_cast<uint8_t>(c);
       }
@@ -228,7 +236,7 @@ __global__ __launch_bounds__(256) void quantise_tile_kernel(TileArgs p) {
     for (int i = 0; i < 8; ++i) {
       const int64_t row = r0 + i * 16 + (t >> 4);
       if (row < p.m)
-        *reinterpret_cast<uint2*>(q + row * p.ldq + c0 + l * 8) =
+        *reinterpret_cast<uint2*>(q + (blockIdx.x * p.m_pad + row) * 128 + l * 8) =
             uint2{to_f8(d[i][0], d[i][1], s), to_f8(d[i][2], d[i][3], s)};
     }
     if (t == 0) {
@@ -268,7 +276,7 @@ __global__ __launch_bounds__(256) void quantise_tile_kernel(TileArgs p) {
       o[i] = to_f8(vperm(c[4 * i + 1], c[4 * i], h ? kHi : kLo),
                    vperm(c[4 * i + 3], c[4 * i + 2], h ? kHi : kLo), s);
     }
-    uint4* out = reinterpret_cast<uint4*>(qt + col * p.ldqt + r0 + quarter * 32);
+    uint4* out = reinterpret_cast<uint4*>(qt + (blockIdx.y * p.n_pad + col) * 128 + quarter * 32);
     out[0] = uint4{o[0], o[1], o[2], o[3]};
     out[1] = uint4{o[4], o[5], o[6], o[7]};
     if (!kOne && quarter == 0)
@@ -277,11 +285,11 @@ __global__ __launch_bounds__(256) void quantise_tile_kernel(TileArgs p) {
 }
 
 // ------------------------------------------------------------------- layout
-// e4m3 bytes [rows, cols] into rows of padded(cols), zeros behind, and turned.
+// e4m3 bytes [rows, cols] into blocks of 128 columns, zeros behind, and turned.
 struct LayoutArgs {
   const uint8_t* v;
   uint8_t *q, *qt;
-  int64_t rows, cols, ldq, ldqt;
+  int64_t rows, cols;
 };
 
 __global__ __launch_bounds__(256) void layout_kernel(LayoutArgs p) {
@@ -297,8 +305,9 @@ __global__ __launch_bounds__(256) void layout_kernel(LayoutArgs p) {
     uint4 d{0, 0, 0, 0};
     if (r0 + row < p.rows && c < p.cols)   // cols is a multiple of 16
       d = *reinterpret_cast<const uint4*>(v + (r0 + row) * p.cols + c);
-    if (p.q != nullptr && r0 + row < p.rows)
-      *reinterpret_cast<uint4*>(p.q + (z * p.rows + r0 + row) * p.ldq + c) = d;
+    if (r0 + row < p.rows)
+      *reinterpret_cast<uint4*>(p.q + ((z * gridDim.x + blockIdx.x) * p.rows + r0 + row) * 128 +
+                                piece * 16) = d;
     tile[row][piece * 4] = d.x;
     tile[row][piece * 4 + 1] = d.y;
     tile[row][piece * 4 + 2] = d.z;
@@ -324,7 +333,7 @@ __global__ __launch_bounds__(256) void layout_kernel(LayoutArgs p) {
   for (int j = 0; j < 4; ++j) {
     const int64_t col = c0 + four * 4 + j;
     if (col < p.cols)
-      *reinterpret_cast<uint4*>(p.qt + (z * p.cols + col) * p.ldqt + r0 + part * 16) =
+      *reinterpret_cast<uint4*>(p.qt + ((z * gridDim.y + blockIdx.y) * p.cols + col) * 128 + part * 16) =
           uint4{o[j][0], o[j][1], o[j][2], o[j][3]};
   }
 }
@@ -345,14 +354,15 @@ __global__ __launch_bounds__(256) void layout_scales_kernel(const T* s, T* out, 
 // ------------------------------------------------------------------ product
 // Scales of the weights' side: a code for 128 x 128 values, a code for 128
 // columns of each row, or an fp32 number for 128 x 128 values.
-enum Scales { kBlockCode, kRowCode, kBlockF32 };
+enum Scales { kBlockCode, kRowCode, kBlockF32, kWide };
 
 struct GemmArgs {
   const uint8_t *x, *x_codes, *w;
   const void* w_scales;
   void* y;
   float* part;             // [splits, m, n], or NULL: one split, straight to y
-  int64_t ldx, ldw, ldy, m, n;
+  int64_t x_block, w_block;   // bytes of a block of 128 columns
+  int64_t ldy, m, n;
   int32_t ld_xc, ld_ws;    // codes or scales of a row
   int32_t kb, per_split, splits, mt, nt;
   bool y_bf16, y_vec;
@@ -385,6 +395,38 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& p, int32_t& mt, int32_t&
 
 __device__ __forceinline__ void to_lds(const uint8_t* from, uint8_t* to) {
   __builtin_amdgcn_global_load_lds(from, (lds_void*)to, 16, 0, 0);
+}
+
+// Four results of a row, from column col on.
+__device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t row, int64_t col,
+                                       floatx4 v) {
+  if (p.part != nullptr) {
+    float* to = p.part + (split * p.m + row) * p.n + col;
+    if (p.n % 4 == 0) {
+      if (col < p.n) *reinterpret_cast<floatx4*>(to) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < p.n) to[e] = v[e];
+    }
+    return;
+  }
+  const int64_t at = row * p.ldy + col;
+  if (p.y_vec) {   // rows of whole, aligned fours
+    if (col >= p.n) return;
+    if (p.y_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
+          uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    else
+      *reinterpret_cast<floatx4*>(static_cast<float*>(p.y) + at) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + e >= p.n) continue;
+      if (p.y_bf16) static_cast<uint16_t*>(p.y)[at + e] = to_bf16_rne(v[e]);
+      else static_cast<float*>(p.y)[at + e] = v[e];
+    }
+  }
 }
 
 // y = x w^T on tiles of BM x BN by WM x WN waves. A step is one block of 128
@@ -425,39 +467,33 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
   // where this lane's 16-byte pieces come from
   const int piece_row = lane >> 3;
   const auto piece = [&](int row) { return ((lane & 7) ^ ((row >> 1) & 7)) * 16; };
-  typedef typename std::conditional<kExperts, int64_t, uint32_t>::type Off;
-  Off x_off[kExperts ? kXLoads : 1];
+  int64_t x_off[kExperts ? kXLoads : 1];
   uint32_t w_off[kWLoads];
-  const uint8_t* x = p.x + (kExperts ? 0 : m0 * p.ldx);
+  const uint8_t* x = p.x + (kExperts ? 0 : m0 * 128);
 #pragma unroll
   for (int i = 0; i < (kExperts ? kXLoads : 1); ++i) {
     const int row = (i * kWaves + wave) * 8 + piece_row;
-    if (kExperts) {
-      const int32_t pair = p.order[m0 + (row < rows ? row : 0)];
-      x_off[i] = static_cast<Off>(pair / p.pairs_a_row) * p.ldx + piece(row);
-    } else {
-      x_off[i] = static_cast<Off>(row * p.ldx + piece(row));
-    }
+    const int32_t pair = kExperts ? p.order[m0 + (row < rows ? row : 0)] : 0;
+    x_off[i] = (kExperts ? static_cast<int64_t>(pair / p.pairs_a_row) : row) * 128 + piece(row);
   }
-  w += n0 * p.ldw;
+  w += n0 * 128;
 #pragma unroll
   for (int i = 0; i < kWLoads; ++i) {
     const int row = (i * kWaves + wave) * 8 + piece_row;
     const int64_t at = n0 + row < p.n ? row : p.n - 1 - n0;
-    w_off[i] = static_cast<uint32_t>(at * p.ldw + piece(row));
+    w_off[i] = static_cast<uint32_t>(at * 128 + piece(row));
   }
-  const uint32_t x_step = static_cast<uint32_t>(kWaves * 8 * p.ldx);
   const auto stage = [&](uint8_t* buf, int32_t kb) __attribute__((always_inline)) {
-    const int64_t k = static_cast<int64_t>(kb) * 128;
+    const uint8_t* xk = x + kb * p.x_block;
+    const uint8_t* wk = w + kb * p.w_block;
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const uint64_t off = kExperts ? static_cast<uint64_t>(x_off[kExperts ? i : 0])
-                                    : static_cast<uint64_t>(x_off[0] + i * x_step);
-      to_lds(x + k + off, buf + (i * kWaves + wave) * 1024);
-    }
+    for (int i = 0; i < kXLoads; ++i)   // 32 rows or more on, the pieces lie the same way
+      to_lds(kExperts ? xk + x_off[kExperts ? i : 0]
+                      : xk + (i * kWaves * 1024 + static_cast<uint64_t>(static_cast<uint32_t>(x_off[0]))),
+             buf + (i * kWaves + wave) * 1024);
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      to_lds(w + k + static_cast<uint64_t>(w_off[i]), buf + BM * 128 + (i * kWaves + wave) * 1024);
+      to_lds(wk + static_cast<uint64_t>(w_off[i]), buf + BM * 128 + (i * kWaves + wave) * 1024);
   };
 
   // codes of four steps at once: of the rows of x, and of the weights
@@ -627,36 +663,388 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int64_t col = n0 + wn * TN + j * 16 + q * 4;
-      const floatx4 v = acc[i][j];
-      if (p.part != nullptr) {
-        float* to = p.part + (split * p.m + y_row) * p.n + col;
-        if (p.n % 4 == 0) {
-          if (col < p.n) *reinterpret_cast<floatx4*>(to) = v;
-        } else {
+      store4(p, split, y_row, col, acc[i][j]);
+    }
+  }
+}
+
+// The same on tiles of 192 x 256 by four waves of 96 x 128, one on each SIMD,
+// for products that fill the chip with them. A wave's step is 48 matrix
+// instructions (1536 cycles of the matrix unit) over six operands of x and
+// eight of the weights. They are taken in quarters of three by four, so that an
+// operand's registers are free early and are filled again for the next step
+// while other quarters run. With A and B the halves of the weights' operands
+// and a, b those of x, the quarters of an even and an odd step are
+//   aB aA bA bB  and  aA aB bB bA,
+// each sharing an operand half with its neighbours. A half step's rows (a and
+// the weights that begin; b and the others) have a buffer of their own: the
+// first is read during the last two quarters of the step before, the second
+// during the first two. A barrier before the first and the third quarter says
+// that a half has arrived and that the one read last may be loaded again, with
+// what is read six quarters (2304 cycles) later.
+// A block takes tiles one after the other, and its loads run over their ends:
+// the last steps of a tile load the first ones of the next, and the results
+// are on their way to memory while that one runs. (With a block a tile, its
+// start and end cost as much as ten of its steps.)
+constexpr int kBigM = 192, kBigN = 256;
+constexpr int32_t kBigBlocks = 256;   // one on each CU
+constexpr int kBigStores = 24;        // of a wave's whole tile, at least
+
+template <int kScales>
+__global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
+  constexpr int kWaves = 4, FM = kBigM / 32, HM = FM / 2;
+  constexpr int kHalf = (kBigM + kBigN) / 2 * 128, kXUnits = kBigM / 16, kXLoads = kXUnits / kWaves;
+  // begin and rest of even and of odd steps: named arrays, see gemm_kernel
+  __shared__ __align__(16) uint8_t begin0[kHalf];
+  __shared__ __align__(16) uint8_t rest0[kHalf];
+  __shared__ __align__(16) uint8_t begin1[kHalf];
+  __shared__ __align__(16) uint8_t rest1[kHalf];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4, wm = wave >> 1, wn = wave & 1;
+
+  // This block's tiles: as tile_of numbers them, an XCD's blocks side by side.
+  const int32_t tiles = p.mt * p.nt, work = tiles * p.splits;
+  const int32_t per = work / 8, more = work % 8, xcd = blockIdx.x % 8;
+  const int32_t stride = (static_cast<int32_t>(gridDim.x) + 7 - xcd) / 8;
+  const int32_t behind = xcd * per + (xcd < more ? xcd : more) + per + (xcd < more ? 1 : 0);
+  int32_t id = behind - per - (xcd < more ? 1 : 0) + blockIdx.x / 8;
+  if (id >= behind) return;
+  // steps come in pairs: behind an odd last one x is zeros, and w is read again
+  const int32_t end = (p.kb + 1) & ~1, last = p.kb - 1;
+
+  struct Tile {
+    int32_t mt, nt, split, kb0, kb1;
+  };
+  const auto tile_at = [&](int32_t at) __attribute__((always_inline)) {
+    Tile t;
+    t.split = at / tiles;
+    at -= t.split * tiles;
+    constexpr int32_t kGroup = 8;
+    const int32_t group = at / (kGroup * p.nt), first = group * kGroup;
+    const int32_t high = p.mt - first < kGroup ? p.mt - first : kGroup;
+    at -= group * kGroup * p.nt;
+    t.mt = first + at % high;
+    t.nt = at / high;
+    t.kb0 = t.split * p.per_split;
+    t.kb1 = t.kb0 + p.per_split < end ? t.kb0 + p.per_split : end;
+    return t;
+  };
+
+  // a load: eight rows of 128 bytes, unit by unit; a wave has every fourth
+  // unit. Offsets from a step's blocks on, of x and of the weights' two halves.
+  const int piece_row = lane >> 3;
+  const uint32_t piece = ((lane & 7) ^ ((wave * 4 + (piece_row >> 1)) & 7)) * 16;
+  uint32_t x_off[kXLoads], w_off[2][4];   // x's second half is kBigM / 4 rows further
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < p.n) to[e] = v[e];
-        }
-        continue;
+  for (int i = 0; i < kXLoads; ++i) {
+    const int u = i * kWaves + wave;
+    x_off[i] = (u / (kXUnits / 2) * (kBigM / 2) + u % (kXUnits / 2) * 8 + piece_row) * 128 + piece;
+  }
+  // Loads kFrom .. kTo - 1 of a half's seven.
+  const auto stage = [&](uint8_t* buf, const uint8_t* x, const uint8_t* w, auto x_half, auto w_half,
+                         auto from, auto to) __attribute__((always_inline)) {
+    constexpr int xh = decltype(x_half)::value, wh = decltype(w_half)::value;
+#pragma unroll
+    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
+      to_lds(i < kXLoads ? x + xh * (kBigM / 4) * 128 + static_cast<uint64_t>(x_off[i < kXLoads ? i : 0])
+                         : w + static_cast<uint64_t>(w_off[wh][i < kXLoads ? 0 : i - kXLoads]),
+             buf + (i * kWaves + wave) * 1024);
+  };
+
+  // codes of two steps at once
+  constexpr int kCodes = kScales == kWide ? 1 : FM, kRowCodes = kScales == kRowCode ? 8 : 1;
+  uint32_t xc[kCodes], xc_next[kCodes], wc[kRowCodes], wc_next[kRowCodes];
+  float wf[2], wf_next[2];
+  uint32_t xc_off[kCodes], wc_off[kRowCodes];
+#pragma unroll
+  for (int i = 0; i < kCodes; ++i) xc_off[i] = static_cast<uint32_t>((wm * (kBigM / 2) + i * 16 + r) * p.ld_xc);
+
+  // What is loaded next: two steps' blocks, codes and scales.
+  struct Ahead {
+    const uint8_t *x, *w, *x_codes, *w_scales;
+    int32_t kb, kb1;
+  } ahead;
+  constexpr int kScaleBytes = kScales == kBlockF32 ? 4 : 1;
+  const auto begin_tile = [&](const Tile& t) __attribute__((always_inline)) {
+    const int64_t m0 = static_cast<int64_t>(t.mt) * kBigM, n0 = static_cast<int64_t>(t.nt) * kBigN;
+    ahead.kb = t.kb0;
+    ahead.kb1 = t.kb1;
+    ahead.x = p.x + m0 * 128 + t.kb0 * p.x_block;
+    ahead.w = p.w + n0 * 128 + t.kb0 * p.w_block;
+    ahead.x_codes = p.x_codes + m0 * p.ld_xc + t.kb0;
+    const int32_t w_last = static_cast<int32_t>(p.n - 1 - n0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = i * kWaves + wave;
+        const int32_t row = (u >> 3) * 128 + h * 64 + (u & 7) * 8 + piece_row;
+        w_off[h][i] = static_cast<uint32_t>((row < w_last ? row : w_last) * 128) + piece;
       }
-      const int64_t at = y_row * p.ldy + col;
-      if (p.y_vec) {   // rows of whole, aligned fours
-        if (col >= p.n) continue;
-        if (p.y_bf16)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
-              uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        else
-          *reinterpret_cast<floatx4*>(static_cast<float*>(p.y) + at) = v;
-      } else {
+    ahead.w_scales = static_cast<const uint8_t*>(p.w_scales);
+    if (kScales == kRowCode) {
+      ahead.w_scales += n0 * p.ld_ws + t.kb0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (col + e >= p.n) continue;
-          if (p.y_bf16) static_cast<uint16_t*>(p.y)[at + e] = to_bf16_rne(v[e]);
-          else static_cast<float*>(p.y)[at + e] = v[e];
+      for (int j = 0; j < kRowCodes; ++j) {
+        const int32_t row = wn * 128 + j * 16 + r;
+        wc_off[j] = static_cast<uint32_t>((row < w_last ? row : w_last) * p.ld_ws);
+      }
+    } else if (kScales != kWide) {
+      const int64_t n1 = n0 + wn * 128;
+      ahead.w_scales += ((n1 < p.n ? n1 : p.n - 1) / 128 * p.ld_ws + t.kb0) * kScaleBytes;
+    }
+  };
+  const auto request = [&]() __attribute__((always_inline)) {
+    if (kScales == kWide) return;
+#pragma unroll
+    for (int i = 0; i < kCodes; ++i)
+      xc_next[i] = *reinterpret_cast<const uint16_t*>(ahead.x_codes + static_cast<uint64_t>(xc_off[i]));
+    if (kScales == kRowCode) {
+#pragma unroll
+      for (int j = 0; j < kRowCodes; ++j)
+        wc_next[j] = *reinterpret_cast<const uint16_t*>(ahead.w_scales + static_cast<uint64_t>(wc_off[j]));
+    } else if (kScales == kBlockCode) {
+      wc_next[0] = *reinterpret_cast<const uint16_t*>(ahead.w_scales);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) wf_next[j] = reinterpret_cast<const float*>(ahead.w_scales)[j];
+    }
+  };
+  const auto use_next = [&](int32_t kb) __attribute__((always_inline)) {
+    // not before the loads of two steps have been sent
+    if (kScales == kBlockCode) asm volatile("" : "+v"(wc_next[0]));
+    if (kScales == kBlockF32) asm volatile("" : "+v"(wf_next[0]), "+v"(wf_next[1]));
+    // behind an odd last block: any finite scale
+    if (kScales == kBlockCode) wc_next[0] = kb < last ? wc_next[0] : (wc_next[0] & 0xFFu) | 0x7F00u;
+    if (kScales == kBlockF32) wf_next[1] = kb < last ? wf_next[1] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCodes; ++i) xc[i] = xc_next[i];
+#pragma unroll
+    for (int j = 0; j < kRowCodes; ++j) wc[j] = wc_next[j];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) wf[j] = wf_next[j];
+  };
+
+  floatx4 acc[FM][8];
+  int8v xv[FM], wv[8];
+  const auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+
+  const uint32_t at0 = r * 128 + ((q ^ ((r >> 1) & 7)) << 4), at1 = at0 ^ 64;
+  const auto operand = [&](const uint8_t* rows16) __attribute__((always_inline)) {
+    const int4v a = *reinterpret_cast<const int4v*>(rows16 + at0);
+    const int4v b = *reinterpret_cast<const int4v*>(rows16 + at1);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  // Operands from .. to - 1 of a half.
+  const auto read_x = [&](const uint8_t* buf, auto half, auto from, auto to) __attribute__((always_inline)) {
+    constexpr int h = decltype(half)::value * HM;
+#pragma unroll
+    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
+      xv[h + i] = operand(buf + (wm * (kBigM / 4) + i * 16) * 128);
+  };
+  const auto read_w = [&](const uint8_t* buf, auto half, auto from, auto to) __attribute__((always_inline)) {
+    constexpr int h = decltype(half)::value * 4;
+#pragma unroll
+    for (int j = decltype(from)::value; j < decltype(to)::value; ++j)
+      wv[h + j] = operand(buf + (kBigM / 2 + wn * 64 + j * 16) * 128);
+  };
+  // A third of a quarter: one operand of x by four of the weights. Nothing is
+  // moved over its end, so that the accesses of LDS written before a third
+  // stay between the products of their neighbours.
+  const auto third = [&](auto x_half, auto w_half, auto row, auto step) __attribute__((always_inline)) {
+    constexpr int kStep = decltype(step)::value, wh = decltype(w_half)::value * 4,
+                  i = decltype(x_half)::value * HM + decltype(row)::value;
+#pragma unroll
+    for (int j = wh; j < wh + 4; ++j) {
+      if constexpr (kScales == kWide) {
+        const int8v a = wv[j], b = xv[i];
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, a, 0, 1, 2, 3)),
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(b, b, 0, 1, 2, 3)), acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, a, 4, 5, 6, 7)),
+            __builtin_bit_cast(bf16x8, __builtin_shufflevector(b, b, 4, 5, 6, 7)), acc[i][j], 0, 0, 0);
+      } else if constexpr (kScales == kBlockF32) {
+        const floatx4 sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            wv[j], xv[i], (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep,
+            static_cast<int>(xc[i]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(wf[kStep], sum[e], acc[i][j][e]);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            wv[j], xv[i], acc[i][j], 0, 0, kStep,
+            static_cast<int>(wc[kScales == kRowCode ? j : 0]), kStep, static_cast<int>(xc[i]));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<int, 0> c0;
+  const std::integral_constant<int, 1> c1;
+  const std::integral_constant<int, 2> c2;
+  const std::integral_constant<int, 3> c3;
+  const std::integral_constant<int, 4> c4;
+  const std::integral_constant<int, 5> c5;
+  const std::integral_constant<int, 7> c7;
+  // All but the newest two halves' loads (7 each) have arrived, this wave's
+  // reads are done, and so are the other waves'. behind_stores: a tile's
+  // results were sent after the loads that are waited for.
+  const auto arrived = [&](auto behind_stores) __attribute__((always_inline)) {
+    constexpr int n = 14 + (decltype(behind_stores)::value ? kBigStores : 0);
+    static_assert(n < 64, "vmcnt");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4 << 14));   // vmcnt(n) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // A step: its products, the reads for the next one, and the loads of the
+  // step after that, from x and w on.
+  const auto one = [&](auto step, auto first, auto other, auto stores1, auto stores2, uint8_t* begin,
+                       uint8_t* rest, const uint8_t* next, const uint8_t* x, const uint8_t* w)
+      __attribute__((always_inline)) {
+    arrived(stores1);                  // rest; begin has been read
+    read_w(rest, other, c0, c2);
+    third(c0, first, c0, step);
+    read_w(rest, other, c2, c4);
+    third(c0, first, c1, step);
+    stage(begin, x, w, c0, first, c0, c1);
+    third(c0, first, c2, step);
+    read_x(rest, c1, c0, c2);
+    stage(begin, x, w, c0, first, c1, c3);
+    third(c0, other, c0, step);
+    read_x(rest, c1, c2, c3);
+    stage(begin, x, w, c0, first, c3, c5);
+    third(c0, other, c1, step);
+    stage(begin, x, w, c0, first, c5, c7);
+    third(c0, other, c2, step);
+    arrived(stores2);                  // the next step's begin; rest has been read
+    read_x(next, c0, c0, c1);
+    third(c1, other, c0, step);
+    read_x(next, c0, c1, c2);
+    third(c1, other, c1, step);
+    read_x(next, c0, c2, c3);
+    stage(rest, x, w, c1, other, c0, c1);
+    third(c1, other, c2, step);
+    read_w(next, other, c0, c2);
+    stage(rest, x, w, c1, other, c1, c3);
+    third(c1, first, c0, step);
+    read_w(next, other, c2, c4);
+    stage(rest, x, w, c1, other, c3, c5);
+    third(c1, first, c1, step);
+    stage(rest, x, w, c1, other, c5, c7);
+    third(c1, first, c2, step);
+  };
+
+  // Two steps, with the loads of the two that follow.
+  const auto pair = [&](auto stores) __attribute__((always_inline)) {
+    request();
+    one(c0, c1, c0, stores, stores, begin0, rest0, begin1, ahead.x, ahead.w);
+    one(c1, c0, c1, stores, c0, begin1, rest1, begin0, ahead.x + p.x_block,
+        ahead.w + (ahead.kb < last ? p.w_block : 0));
+    use_next(ahead.kb);
+  };
+
+  int32_t ahead_id = id;
+  // Behind the last tile's steps: the last two again, which nothing reads.
+  const auto go_on = [&]() __attribute__((always_inline)) {
+    if (ahead.kb + 2 < ahead.kb1) {
+      ahead.kb += 2;
+      ahead.x += 2 * p.x_block;
+      ahead.w += 2 * p.w_block;
+      ahead.x_codes += 2;
+      ahead.w_scales += 2 * kScaleBytes;
+    } else if (ahead_id + stride < behind) {
+      ahead_id += stride;
+      begin_tile(tile_at(ahead_id));
+    }
+  };
+
+  begin_tile(tile_at(id));
+  request();
+  const uint8_t* w1 = ahead.w + (ahead.kb < last ? p.w_block : 0);
+  stage(begin0, ahead.x, ahead.w, c0, c1, c0, c7);
+  stage(rest0, ahead.x, ahead.w, c1, c0, c0, c7);
+  stage(begin1, ahead.x + p.x_block, w1, c0, c0, c0, c7);
+  stage(rest1, ahead.x + p.x_block, w1, c1, c1, c0, c7);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the first waits count none of these
+  arrived(c0);
+  use_next(ahead.kb);
+  go_on();
+  read_x(begin0, c0, c0, c3);
+  read_w(begin0, c1, c0, c4);
+  clear();
+  for (;;) {
+    const Tile now = tile_at(id);
+    pair(c1);
+    for (int32_t kb = now.kb0 + 2; kb < now.kb1; kb += 2) {
+      go_on();
+      pair(c0);
+    }
+    go_on();
+
+    // a lane: row i * 16 + r, columns j * 16 + 4 q .. + 3
+    const int64_t m0 = static_cast<int64_t>(now.mt) * kBigM + wm * (kBigM / 2);
+    const int64_t n0 = static_cast<int64_t>(now.nt) * kBigN + wn * 128;
+    const bool whole = m0 + kBigM / 2 <= p.m && n0 + 128 <= p.n;
+    const bool wide = p.part == nullptr && p.y_bf16 && p.y_vec;
+    const bool fours = p.part != nullptr ? p.n % 4 == 0 : p.y_vec && !p.y_bf16;
+    float* to = p.part != nullptr ? p.part + now.split * p.m * p.n : static_cast<float*>(p.y);
+    const int64_t ld = p.part != nullptr ? p.n : p.ldy;
+    if (wide) {
+      // the halves of two operands' results change places between lanes 16
+      // apart: eight columns a lane, 64 bytes of a row side by side
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int64_t row = m0 + i * 16 + r;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const floatx4 a = acc[i][j], b = acc[i][j + 1];
+          const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1]),
+                                                           false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(a[2], a[3]), pack_bf16(b[2], b[3]),
+                                                           false, false);
+          const int64_t col = n0 + (j + (q & 1)) * 16 + (q & 2) * 4;
+          if (whole || (row < p.m && col < p.n))
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + row * p.ldy + col) =
+                uint4{lo[0], hi[0], lo[1], hi[1]};
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int64_t row = m0 + i * 16 + r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t col = n0 + j * 16 + q * 4;
+          const floatx4 v = acc[i][j];
+          if (row >= p.m) continue;
+          if (fours) {
+            if (col < p.n) *reinterpret_cast<floatx4*>(to + row * ld + col) = v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (col + e >= p.n) continue;
+              if (p.part == nullptr && p.y_bf16)
+                static_cast<uint16_t*>(p.y)[row * ld + col + e] = to_bf16_rne(v[e]);
+              else
+                to[row * ld + col + e] = v[e];
+            }
+          }
         }
       }
     }
+    // fewer or more stores than are counted on
+    if (!whole || !(wide || fours)) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    id += stride;
+    if (id >= behind) break;
+    clear();
   }
+  // no load into LDS may be on its way when the block gives it back
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 }
 
 // The splits' sums, in their order.
@@ -691,7 +1079,7 @@ struct SmallArgs {
   const uint8_t* w;
   const void* w_scales;
   void* y;
-  int64_t ldx, ldw, ldy, n, k;
+  int64_t ldx, ldy, n, k;
   int32_t m, ld_ws;
   bool y_bf16;
   const int32_t* idx;     // experts
@@ -740,7 +1128,7 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int64_t row = n0 + i * 16 + r;
-    w_row[i] = w + (row < p.n ? row : p.n - 1) * p.ldw + q * 16;
+    w_row[i] = w + (row < p.n ? row : p.n - 1) * 128 + q * 16;
     const int64_t first = n0 + i * 16 < p.n ? n0 + i * 16 : p.n - 1;
     s_row[i] = expert * p.s_next + first / 128 * p.ld_ws;
   }
@@ -756,8 +1144,8 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
       const int64_t k = static_cast<int64_t>(b) * 128;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
-        wn[i][0] = *reinterpret_cast<const uint4*>(w_row[i] + k);
-        wn[i][1] = *reinterpret_cast<const uint4*>(w_row[i] + k + 64);
+        wn[i][0] = *reinterpret_cast<const uint4*>(w_row[i] + b * p.n * 128);
+        wn[i][1] = *reinterpret_cast<const uint4*>(w_row[i] + b * p.n * 128 + 64);
       }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -912,10 +1300,10 @@ constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 // Tiles and splits of a product of m x n outputs over kb blocks.
 Plan plan_of(int64_t m, int64_t n, int64_t kb, bool exact) {
   Plan q;
-  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t big = ((m + kBigM - 1) / kBigM) * ((n + kBigN - 1) / kBigN);
   if (m <= 32) q.bm = 32, q.bn = 128;
   else if (m <= 64) q.bm = 64, q.bn = 128;
-  else if (!exact && big >= 192) q.bm = 256, q.bn = 256;
+  else if (!exact && big >= 192) q.bm = kBigM, q.bn = kBigN;
   else q.bm = 128, q.bn = 128;
   const int64_t tiles = ((m + q.bm - 1) / q.bm) * ((n + q.bn - 1) / q.bn);
   int64_t splits = tiles >= 192 ? 1 : 512 / tiles;
@@ -950,7 +1338,8 @@ void launch_gemm(const GemmArgs& p, const Plan& q, bool exact, hipStream_t st) {
     if (exact) BINADE_F8_LAUNCH(128, 128, 2, 2, true);
     else BINADE_F8_LAUNCH(128, 128, 2, 2, false);
   } else if constexpr (!kExperts) {
-    BINADE_F8_LAUNCH(256, 256, 2, 4, false);
+    hipLaunchKernelGGL(big_kernel<kScales>, dim3(grid.x < kBigBlocks ? grid.x : kBigBlocks), dim3(256), 0,
+                       st, p);
   }
 #undef BINADE_F8_LAUNCH
 }
@@ -962,16 +1351,19 @@ void launch_kind(int kind, const GemmArgs& p, const Plan& q, bool exact, hipStre
 }
 
 // Rows of a quantised operand: a tile of it is read whole.
-int64_t tile_rows(int64_t m) { return (m + 255) / 256 * 256; }
+int64_t tile_rows(int64_t m) {
+  const int64_t a = (m + 127) / 128 * 128, b = (m + kBigM - 1) / kBigM * kBigM;
+  return a > b ? a : b;
+}
 
 uint32_t some_blocks(int64_t n) {
   return static_cast<uint32_t>(n < 1 ? 1 : n > 16384 ? 16384 : n);
 }
 
-struct Side {   // a quantised operand
+struct Side {   // an operand: its blocks, rows of one, and its codes or scales
   const uint8_t* q;
   const void* scales;
-  int64_t ld;
+  int64_t rows;
   int32_t ld_scales;
 };
 
@@ -986,8 +1378,8 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   p.w_scales = w.scales;
   p.y = y;
   p.part = q.splits > 1 ? part : nullptr;
-  p.ldx = x.ld;
-  p.ldw = w.ld;
+  p.x_block = x.rows * 128;
+  p.w_block = w.rows * 128;
   p.ldy = ldy;
   p.m = m;
   p.n = n;
@@ -999,7 +1391,8 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   p.mt = static_cast<int32_t>((m + q.bm - 1) / q.bm);
   p.nt = static_cast<int32_t>((n + q.bn - 1) / q.bn);
   p.y_bf16 = y_bf16;
-  p.y_vec = n % 4 == 0 && ldy % 4 == 0 && aligned16(y);
+  const int whole = q.bm == kBigM && y_bf16 ? 8 : 4;   // results that a lane stores together
+  p.y_vec = n % whole == 0 && ldy % whole == 0 && aligned16(y);
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
   launch_kind(kind, p, q, !y_bf16, st);
   if (q.splits > 1)
@@ -1013,7 +1406,7 @@ int64_t part_bytes(int64_t m, int64_t n, int64_t k, bool exact) {
   return q.splits > 1 ? up16(4 * q.splits * m * n) : 0;
 }
 int64_t side_bytes(int64_t rows, int64_t cols) {
-  return tile_rows(rows) * padded(cols) + up16(tile_rows(rows) * codes_of(cols));
+  return tile_rows(rows) * paired(cols) + up16(tile_rows(rows) * codes_of(cols));
 }
 
 int32_t check_f8(const binade_f8* w, bool turned) {
@@ -1097,14 +1490,14 @@ extern "C" int32_t binade_f8_pack(const uint16_t* w, binade_f8* out, void* strea
   p.codes = static_cast<uint8_t*>(const_cast<void*>(out->scales));
   p.qt = const_cast<uint8_t*>(out->values_t);
   p.codes_t = static_cast<uint8_t*>(const_cast<void*>(out->scales_t));
-  p.ldq = padded(p.n);
+  p.m_pad = p.m;
+  p.n_pad = p.n;
   p.ldc = codes_of(p.n);
-  p.ldqt = padded(p.m);
   p.ldct = codes_of(p.m);
   p.v_next = p.m * p.n;
-  p.q_next = p.m * p.ldq;
+  p.q_next = p.m * padded(p.n);
   p.c_next = nb * p.ldc;
-  p.qt_next = p.n * p.ldqt;
+  p.qt_next = p.n * padded(p.m);
   p.ct_next = kb * p.ldct;
   p.vec = true;
   hipLaunchKernelGGL((quantise_tile_kernel<false, true>),
@@ -1122,25 +1515,19 @@ extern "C" int32_t binade_f8_layout(const uint8_t* values, const void* scales, b
   if (!aligned16(values)) return BINADE_EUNSUPPORTED;
   if (out->scale_dtype == BINADE_F32 && (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
     return BINADE_EUNSUPPORTED;
-  const bool same = out->values == values;
-  if (same && out->cols % 128 != 0) return BINADE_EINVAL;
   const int64_t nb = blocks_of(out->rows), kb = blocks_of(out->cols);
   if (nb * kb * out->count >= (1ll << 24) || nb > 65535) return BINADE_EUNSUPPORTED;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!same || out->values_t != nullptr) {
-    LayoutArgs p{};
-    p.v = values;
-    p.q = same ? nullptr : const_cast<uint8_t*>(out->values);
-    p.qt = const_cast<uint8_t*>(out->values_t);
-    p.rows = out->rows;
-    p.cols = out->cols;
-    p.ldq = padded(out->cols);
-    p.ldqt = padded(out->rows);
-    hipLaunchKernelGGL(layout_kernel,
-                       dim3(static_cast<uint32_t>(kb), static_cast<uint32_t>(nb),
-                            static_cast<uint32_t>(out->count)),
-                       dim3(256), 0, st, p);
-  }
+  LayoutArgs p{};
+  p.v = values;
+  p.q = const_cast<uint8_t*>(out->values);
+  p.qt = const_cast<uint8_t*>(out->values_t);
+  p.rows = out->rows;
+  p.cols = out->cols;
+  hipLaunchKernelGGL(layout_kernel,
+                     dim3(static_cast<uint32_t>(kb), static_cast<uint32_t>(nb),
+                          static_cast<uint32_t>(out->count)),
+                     dim3(256), 0, st, p);
   const dim3 grid(some_blocks((nb * kb * out->count + 255) / 256));
   if (out->scale_dtype == BINADE_E8M0)
     hipLaunchKernelGGL(layout_scales_kernel<uint8_t>, grid, dim3(256), 0, st,
@@ -1179,7 +1566,6 @@ extern "C" int32_t binade_f8_gemm(const binade_f8* w, const uint16_t* x, int64_t
     p.w_scales = w->scales;
     p.y = y;
     p.ldx = ldx;
-    p.ldw = padded(k);
     p.ldy = ldy;
     p.n = n;
     p.k = k;
@@ -1193,12 +1579,12 @@ extern "C" int32_t binade_f8_gemm(const binade_f8* w, const uint16_t* x, int64_t
     return BINADE_ENOSPACE;
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   uint8_t* q = static_cast<uint8_t*>(workspace);
-  uint8_t* codes = q + tile_rows(m) * padded(k);
+  uint8_t* codes = q + tile_rows(m) * paired(k);
   float* part = reinterpret_cast<float*>(q + side_bytes(m, k));
-  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * blocks_of(k) + 15) / 16)), dim3(256),
-                     0, st, x, ldx, m, k, true, q, padded(k), codes, codes_of(k));
-  return run_product({q, codes, padded(k), static_cast<int32_t>(codes_of(k))},
-                     {w->values, w->scales, padded(k), static_cast<int32_t>(codes_of(k))}, kind_of(w),
+  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * paired(k) / 128 + 15) / 16)), dim3(256),
+                     0, st, x, ldx, m, k, true, q, tile_rows(m), codes, codes_of(k));
+  return run_product({q, codes, tile_rows(m), static_cast<int32_t>(codes_of(k))},
+                     {w->values, w->scales, n, static_cast<int32_t>(codes_of(k))}, kind_of(w),
                      m, n, k, y, ldy, y_dtype == BINADE_BF16, part, st);
 }
 
@@ -1252,7 +1638,7 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   const auto take = [&](int64_t rows, int64_t cols) {
-    Side s{at, at + tile_rows(rows) * padded(cols), padded(cols), static_cast<int32_t>(codes_of(cols))};
+    Side s{at, at + tile_rows(rows) * paired(cols), tile_rows(rows), static_cast<int32_t>(codes_of(cols))};
     at += side_bytes(rows, cols);
     return s;
   };
@@ -1273,14 +1659,14 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
     p.n = cols;
     p.qt = const_cast<uint8_t*>(cols_side.q);
     p.codes_t = static_cast<uint8_t*>(const_cast<void*>(cols_side.scales));
-    p.ldqt = cols_side.ld;
+    p.n_pad = cols_side.rows;
     p.ldct = cols_side.ld_scales;
     p.vec = v8;
-    const dim3 grid(static_cast<uint32_t>(blocks_of(cols)), static_cast<uint32_t>(blocks_of(m)), 1);
+    const dim3 grid(static_cast<uint32_t>(paired(cols) / 128), static_cast<uint32_t>(paired(m) / 128), 1);
     if (rows_side != nullptr) {
       p.q = const_cast<uint8_t*>(rows_side->q);
       p.codes = static_cast<uint8_t*>(const_cast<void*>(rows_side->scales));
-      p.ldq = rows_side->ld;
+      p.m_pad = rows_side->rows;
       p.ldc = rows_side->ld_scales;
       hipLaunchKernelGGL((quantise_tile_kernel<true, false>), grid, dim3(256), 0, st, p);
     } else {
@@ -1291,15 +1677,15 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
     turn(dy, ld_dy, n, vec, need_dx ? &dy_rows : nullptr, dy_cols);
     turn(x, ldx, k, true, nullptr, x_cols);
   } else {
-    hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * blocks_of(n) + 15) / 16)), dim3(256),
-                       0, st, dy, ld_dy, m, n, vec, const_cast<uint8_t*>(dy_rows.q), dy_rows.ld,
+    hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * paired(n) / 128 + 15) / 16)), dim3(256),
+                       0, st, dy, ld_dy, m, n, vec, const_cast<uint8_t*>(dy_rows.q), dy_rows.rows,
                        static_cast<uint8_t*>(const_cast<void*>(dy_rows.scales)),
                        static_cast<int64_t>(dy_rows.ld_scales));
   }
   int32_t status = launch_status();
   if (status != BINADE_OK) return status;
   if (need_dx) {
-    status = run_product(dy_rows, {w->values_t, w->scales_t, padded(n), static_cast<int32_t>(codes_of(n))},
+    status = run_product(dy_rows, {w->values_t, w->scales_t, k, static_cast<int32_t>(codes_of(n))},
                          kind_of(w), m, k, n, dx, ld_dx, true, part, st);
     if (status != BINADE_OK) return status;
   }
@@ -1363,7 +1749,6 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
     p.w_scales = experts->scales;
     p.y = y;
     p.ldx = ldx;
-    p.ldw = padded(k);
     p.ldy = ldy;
     p.n = n;
     p.k = k;
@@ -1386,7 +1771,7 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   const ExpertSpace space = expert_space(rows, pairs, k, experts->count);
   uint8_t* at = static_cast<uint8_t*>(workspace);
-  uint8_t* codes = at + tile_rows(rows) * padded(k);
+  uint8_t* codes = at + tile_rows(rows) * paired(k);
   Plan q{};
   q.bm = expert_tile(pairs, experts->count);
   q.bn = 128;
@@ -1399,8 +1784,8 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   p.nt = static_cast<int32_t>((n + 127) / 128);
   p.splits = 1;
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
-  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((rows * blocks_of(k) + 15) / 16)), dim3(256),
-                     0, st, x, ldx, rows, k, true, at, padded(k), codes, codes_of(k));
+  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((rows * paired(k) / 128 + 15) / 16)), dim3(256),
+                     0, st, x, ldx, rows, k, true, at, tile_rows(rows), codes, codes_of(k));
   hipLaunchKernelGGL(sort_pairs_kernel, dim3(1), dim3(1024), 0, st, idx, static_cast<int32_t>(pairs),
                      experts->count, q.bm, const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles),
                      const_cast<int32_t*>(p.n_tiles), dev_status);
@@ -1409,8 +1794,8 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   p.w = experts->values;
   p.w_scales = experts->scales;
   p.y = y;
-  p.ldx = padded(k);
-  p.ldw = padded(k);
+  p.x_block = tile_rows(rows) * 128;
+  p.w_block = n * 128;
   p.ldy = ldy;
   p.m = pairs;
   p.n = n;

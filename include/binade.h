@@ -758,8 +758,9 @@ int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
 /* Weights in 8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, no
  * infinity, largest 448) with a scale for each block of 128 x 128 (device
  * pointers): count matrices [rows = N, cols = K], such as a layer's experts.
- *   values    u8 [count, rows, P(cols)], zeros behind cols; P(v) is v
- *             rounded up to a multiple of 128
+ *   values    u8 [count, P(cols) / 128, rows, 128]: blocks of 128 columns,
+ *             a block's rows one behind the other, zeros behind cols; P(v) is
+ *             v rounded up to a multiple of 128
  *   scales    u8 or fp32 per scale_dtype (BINADE_E8M0 or BINADE_F32)
  *             [count, P(rows) / 128, P(cols) / 128 rounded up to a multiple
  *             of 4]; entries behind the last block are not used
@@ -802,8 +803,7 @@ int32_t binade_f8_pack(const uint16_t *w, binade_f8 *out, void *stream);
 /* A checkpoint's 8-bit weights into the layout above: values u8 [count,
  * rows, cols] and scales [count, P(rows) / 128, P(cols) / 128] of
  * out->scale_dtype (device, contiguous, values 16-byte aligned). out as for
- * binade_f8_pack; out->values may be values itself where cols % 128 == 0
- * (then only scales and the transposed planes are written). */
+ * binade_f8_pack. */
 int32_t binade_f8_layout(const uint8_t *values, const void *scales,
                          binade_f8 *out, void *stream);
 

@@ -221,8 +221,8 @@ def test_pack_is_the_definition(count, n, k):
         w = w[0]
     p = B.f8_pack(w.to(DEV), train=True)
     K, N = blocks(k) * 128, blocks(n) * 128
-    v = p.values.cpu().view(E4M3).view(count, n, K).float().double()
-    vt = p.values_t.cpu().view(E4M3).view(count, k, N).float().double()
+    v = p.values.cpu().view(E4M3).view(count, K // 128, n, 128).transpose(1, 2).reshape(count, n, K).float().double()
+    vt = p.values_t.cpu().view(E4M3).view(count, N // 128, k, 128).transpose(1, 2).reshape(count, k, N).float().double()
     nb, kb = blocks(n), blocks(k)
     s = p.scales.cpu().view(count, nb, -1)[:, :, :kb]
     st = p.scales_t.cpu().view(count, kb, -1)[:, :, :nb]
