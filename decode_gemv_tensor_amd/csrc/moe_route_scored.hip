@@ -4,12 +4,14 @@
 // moe_route.hip: a row belongs to G lanes with V adjacent experts each.
 //
 // Choice. What is compared is score + bias in fp64. Nearly every row is
-// settled in fp32: a value and its expert make one whole-number key, the keys
-// are sorted, and the row counts as settled if every gap that decides
-// something (between the slots, to the best expert left out, between the last
-// group taken and the first left out) is larger than the fp32 values can be
-// off. A wave with a row that is not settled works its rows out again in
-// fp64. Without bias the logits themselves are the order, which is exact.
+// settled in fp32: its values become 32-bit keys that max and min alone sort,
+// and the row counts as settled if every gap that decides something (between
+// the slots, to the best expert left out, between the last group taken and the
+// first left out) is larger than the fp32 values can be off. A wave with a row
+// that is not settled works its rows out again in fp64. Without bias the
+// logits themselves are the order, which is exact: bf16 ones with the expert
+// in the key's other half, so that ties are settled too. The slots' experts
+// are found by their values: a lane looks for its own among the sorted ones.
 //
 // Scores relative to the row's largest: sigmoid(x) = exp(min(x, 0)) / (1 +
 // exp(-|x|)), and quotients of scores do not change when exp(min(x, 0)) is
@@ -28,6 +30,8 @@ struct ScoredArgs {
   RouteArgs r;
   const float* bias;
   int32_t groups, group_size, top_groups, group_best;
+  int32_t lanes_a_group;   // a power of two of whole lanes, or 0
+  int32_t parts;           // otherwise: lanes that look through a group in LDS
   float scale;
   bool sigmoid;
 };
@@ -35,74 +39,217 @@ struct ScoredArgs {
 // 1 / v for v >= 1/2 here; and exp(-|x|).
 __device__ __forceinline__ float low_exp(float x) { return exp_of(-fabsf(x)); }
 
-// KeyF32's key of any value: rising with it, -0 as +0; NaN and -inf as 0
-// (never taken); among equal values larger for the smaller expert.
-__device__ __forceinline__ uint64_t key_of(float v, int32_t expert) {
+// KeyF32's order of any value: rising with it, -0 as +0; NaN and -inf as 0
+// (never taken).
+__device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v);
   const uint32_t neg = static_cast<uint32_t>(static_cast<int32_t>(b) >> 31);
   const uint32_t o = (b ^ neg) + ((neg & 1u) | (~neg & 0x80000000u));
-  return v > -__builtin_inff() ? (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(expert))
-                               : 0u;
+  return v > -__builtin_inff() ? o : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o - 0x80000000u : 0u - o);
 }
 
-// How far apart two fp32 values have to be for their order to be the exact
-// one. A sigmoid is within 4 u of its value (u = 2^-24: the exponential's
-// product and result, the sum and its inverse, the product), at most 4 u; a
-// softmax p within (|d| + 9) u p <= 10 u; the bias's addition rounds by u |v|.
-// Twice that for two values is less than 32 u (1 + |v|); sums of two of them
-// twice that again.
-__device__ __forceinline__ float apart(float v) { return 1.9073486e-6f * (1.0f + fabsf(v)); }
+// How far apart two fp32 values of at most |v| have to be for their order to
+// be the exact one. u = 2^-24. A sigmoid errs by at most 3 u (the exponential,
+// of at most (|x| + 2) u relative, moves it by less than 1 u; the sum, its
+// inverse and the product), a softmax p by (|d| + 6) u p < 7 u, the bias's
+// addition by u |v| / 2: 16 u + 2 u |v| covers two of them. Scores of groups
+// are sums of two: twice that and their own rounding.
+__device__ __forceinline__ float apart(float v) { return 9.5367432e-7f + 1.1920929e-7f * fabsf(v); }
 
-// The groups taken, as bits. row: the row's values in LDS; score: 64 places a
-// row. kF32: says in `sure` whether rounding could have changed the answer.
-template <int G, typename T>
-__device__ __forceinline__ uint64_t groups_taken(const ScoredArgs& p, const T* row, T* score, int l,
-                                                 bool exact, bool& sure) {
-  constexpr int kTurns = kMaxGroups / G > 0 ? kMaxGroups / G : 1;
-  const T none = -static_cast<T>(__builtin_inff());
-#pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    const int32_t g = l + i * G;
-    if (g >= p.groups) break;
-    T a = none, b = none;
-    const T* from = row + g * p.group_size;
-    int32_t z = l % p.group_size;          // lanes start apart: other banks
-    for (int32_t n = 0; n < p.group_size; ++n) {
-      const T t = from[z];
-      b = t > a ? a : t > b ? t : b;
-      a = t > a ? t : a;
-      z = z + 1 == p.group_size ? 0 : z + 1;
-    }
-    score[g] = p.group_best == 2 && b > none ? a + b : a;
+// The two largest of a lane's and its partner's two.
+template <int kStep, typename T>
+__device__ __forceinline__ void join_two(T& a, T& b) {
+  T a0, a1, b0, b1;
+  if constexpr (sizeof(T) == 4) {
+    uint32_t x, y;
+    pair_of<kStep>(__builtin_bit_cast(uint32_t, a), x, y);
+    a0 = __builtin_bit_cast(T, x), a1 = __builtin_bit_cast(T, y);
+    pair_of<kStep>(__builtin_bit_cast(uint32_t, b), x, y);
+    b0 = __builtin_bit_cast(T, x), b1 = __builtin_bit_cast(T, y);
+  } else {
+    uint64_t x, y;
+    pair_of<kStep>(__builtin_bit_cast(uint64_t, a), x, y);
+    a0 = __builtin_bit_cast(T, x), a1 = __builtin_bit_cast(T, y);
+    pair_of<kStep>(__builtin_bit_cast(uint64_t, b), x, y);
+    b0 = __builtin_bit_cast(T, x), b1 = __builtin_bit_cast(T, y);
+  }
+  const T low = a0 > a1 ? a1 : a0, second = b0 > b1 ? b0 : b1;
+  a = a0 > a1 ? a0 : a1;
+  b = low > second ? low : second;
+}
+
+// Whether the group `mine` of this lane, of the score `of_mine`, is taken; its
+// lane `first` leaves the score in LDS. sure: rounding cannot have decided it.
+template <typename T>
+__device__ __forceinline__ bool taken(const ScoredArgs& p, T* score, int32_t mine, bool first, T of_mine,
+                                      bool exact, bool& sure) {
+  if (first && mine < p.groups) score[mine] = of_mine;
+  wave_sync();
+  const T d = exact ? static_cast<T>(0) : static_cast<T>(3.0f * apart(static_cast<float>(of_mine)));
+  int32_t before = 0, over = 0, near = 0;
+#pragma unroll 4
+  for (int32_t h = 0; h < p.groups; ++h) {
+    const T s = score[h];
+    before += s > of_mine || (s == of_mine && h < mine) ? 1 : 0;
+    over += s > of_mine + d ? 1 : 0;
+    near += h != mine && s >= of_mine - d ? 1 : 0;
   }
   wave_sync();
-  uint64_t taken = 0;
-#pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    if (i * G >= p.groups) break;
-    const int32_t g = l + i * G;
-    bool keep = false;
-    if (g < p.groups) {
-      const T mine = score[g];
-      if (mine > none) {
-        const T d = exact ? static_cast<T>(0) : static_cast<T>(2.0f * apart(static_cast<float>(mine)));
-        int32_t before = 0, over = 0, near = 0;
-        for (int32_t h = 0; h < p.groups; ++h) {
-          const T s = score[h];
-          before += s > mine || (s == mine && h < g) ? 1 : 0;
-          over += s > mine + d ? 1 : 0;
-          near += h != g && s >= mine - d ? 1 : 0;
-        }
-        keep = before < p.top_groups;
-        if (!exact && !(near < p.top_groups || over >= p.top_groups)) sure = false;
+  const bool open = of_mine > -static_cast<T>(__builtin_inff());
+  if (!exact && open && mine < p.groups && !(near < p.top_groups || over >= p.top_groups)) sure = false;
+  return open && before < p.top_groups;
+}
+
+// The groups taken, as bits, of values in a row of LDS: a group by as many
+// lanes as there are for all of them (more groups than lanes: several turns).
+template <int G, typename T>
+__device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t parts, const T* row, T* score,
+                                                  int l, bool exact, bool& sure) {
+  const T none = -static_cast<T>(__builtin_inff());
+  const int32_t turns = (p.groups * parts + G - 1) / G;
+  for (int32_t i = 0; i < turns; ++i) {
+    const int32_t g = (l + i * G) / parts, part = l % parts;
+    T a = none, b = none;
+    if (g < p.groups)
+#pragma unroll 2
+      for (int32_t z = part; z < p.group_size; z += parts) {
+        const T t = row[g * p.group_size + z];
+        b = t > a ? a : t > b ? t : b;
+        a = t > a ? t : a;
       }
-    }
-    const uint64_t bits = __ballot(keep);
-    const int base = (threadIdx.x & 63) & ~(G - 1);
-    const uint64_t mine = G == 64 ? bits : (bits >> base) & ((1ull << (G & 63)) - 1);
-    taken |= mine << (i * G & 63);
+    butterfly<G>([&](auto step) {
+      constexpr int kStep = decltype(step)::value;
+      if (kStep < parts) join_two<kStep>(a, b);
+    });
+    if (g < p.groups && part == 0) score[g] = p.group_best == 2 && b > none ? a + b : a;
   }
-  return taken;
+  wave_sync();
+  uint64_t bits = 0;
+  for (int32_t i = 0; i * G < p.groups; ++i) {
+    const int32_t g = l + i * G;
+    const bool keep = taken(p, score, g, false, g < p.groups ? score[g] : none, exact, sure);
+    const uint64_t all = __ballot(keep) >> ((threadIdx.x & 63) & ~(G - 1));
+    bits |= (G == 64 ? all : all & ((1ull << (G & 63)) - 1)) << (i * G & 63);
+  }
+  return bits;
+}
+
+// Leaves only the values of the groups taken. A group of whole lanes, a power
+// of two, is joined in registers, others through the row in LDS.
+template <int G, int V>
+__device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], const float (&from)[V],
+                                            float* row, float* score, int l, bool exact, bool& sure) {
+  const float none = -__builtin_inff();
+  if (p.lanes_a_group != 0) {
+    float a = none, b = none;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float t = from[j];
+      b = t > a ? a : t > b ? t : b;
+      a = t > a ? t : a;
+    }
+    butterfly<G>([&](auto step) {
+      constexpr int kStep = decltype(step)::value;
+      if (kStep < p.lanes_a_group) join_two<kStep>(a, b);
+    });
+    const float of_mine = p.group_best == 2 && b > none ? a + b : a;
+    const int32_t mine = l / p.lanes_a_group;
+    const bool keep = taken(p, score, mine, l % p.lanes_a_group == 0, of_mine, exact, sure);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = keep ? v[j] : none;
+    return;
+  }
+  const int32_t e0 = l * V;
+#pragma unroll
+  for (int j = 0; j < V; ++j) row[e0 + j] = from[j];
+  wave_sync();
+  const uint64_t bits = groups_of_row<G>(p, p.parts, row, score, l, exact, sure);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t g = static_cast<uint32_t>(e0 + j) / static_cast<uint32_t>(p.group_size);
+    v[j] = g < 64u && ((bits >> g) & 1) ? v[j] : none;
+  }
+}
+
+// A row's choice in fp64, by the whole wave: a lane has every 64th expert.
+// Leaves the slots' experts in LDS.
+template <int kExperts, bool kBf16>
+__device__ __forceinline__ void settle(const ScoredArgs& p, int64_t row, float top, bool plain,
+                                       bool exact_groups, double* values, double* score, int32_t* slots) {
+  constexpr int kE = kExperts / 64;
+  const int lane = threadIdx.x & 63;
+  const int32_t n_experts = p.r.n_experts;
+  const double nothing = -static_cast<double>(__builtin_inff());
+  float x[kE];
+  double v[kE], all = 0.0;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) {
+    const int32_t e = lane + 64 * i;
+    x[i] = -__builtin_inff();
+    if (e < n_experts)
+      x[i] = kBf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.r.logits)[row + e]) << 16)
+                   : static_cast<const float*>(p.r.logits)[row + e];
+    const double xv = x[i];
+    v[i] = p.sigmoid ? (xv < 0.0 ? exp(xv) : 1.0) / (1.0 + exp(-fabs(xv)))
+                     : exp(xv - static_cast<double>(top));
+    all += v[i];
+  }
+  butterfly<64>([&](auto step) {
+    uint64_t c, d;
+    pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, all), c, d);
+    all = __builtin_bit_cast(double, c) + __builtin_bit_cast(double, d);
+  });
+  const bool grouped = p.groups > 1 && p.top_groups < p.groups;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) {
+    const int32_t e = lane + 64 * i;
+    const bool open = x[i] > -__builtin_inff();
+    const double bias = p.bias != nullptr && e < n_experts ? p.bias[e] : 0.0f;
+    const double s = (p.sigmoid ? v[i] : v[i] / all) + bias;
+    if (grouped) {
+      const double g = exact_groups ? static_cast<double>(x[i]) : s;
+      values[e] = open && g > nothing ? g : nothing;
+    }
+    v[i] = plain ? static_cast<double>(x[i]) : s;
+    if (!open || !(v[i] > nothing)) v[i] = nothing;
+  }
+  if (grouped) {
+    wave_sync();
+    int32_t parts = 1;
+    while (2 * parts * p.groups <= 64) parts *= 2;
+    bool sure = true;
+    const uint64_t bits = groups_of_row<64>(p, parts, values, score, lane, true, sure);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const uint32_t g = static_cast<uint32_t>(lane + 64 * i) / static_cast<uint32_t>(p.group_size);
+      v[i] = g < 64u && ((bits >> g) & 1) ? v[i] : nothing;
+    }
+  }
+  for (int32_t n = 0; n < p.r.top_k; ++n) {
+    double best = v[0];
+    uint32_t at = lane;
+#pragma unroll
+    for (int i = 1; i < kE; ++i) {
+      at = v[i] > best ? lane + 64 * i : at;
+      best = v[i] > best ? v[i] : best;
+    }
+    butterfly<64>([&](auto step) {
+      uint64_t c, d;
+      uint32_t ac, ad;
+      pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, best), c, d);
+      pair_of<decltype(step)::value>(at, ac, ad);
+      const double bc = __builtin_bit_cast(double, c), bd = __builtin_bit_cast(double, d);
+      const bool second = bd > bc || (bd == bc && ad < ac);
+      best = second ? bd : bc;
+      at = second ? ad : ac;
+    });
+#pragma unroll
+    for (int i = 0; i < kE; ++i) v[i] = at == static_cast<uint32_t>(lane + 64 * i) ? nothing : v[i];
+    if (lane == 0) slots[n] = best > nothing ? static_cast<int32_t>(at) : -1;
+  }
 }
 
 template <int G, int V, bool kBf16, bool kSort>
@@ -111,9 +258,10 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
   constexpr int kHeld = kSort ? 1 : kMaxTopK / G;
   __shared__ int32_t counts[kExperts + 1];
   __shared__ double red[kWavesABlock];
-  __shared__ __align__(16) float x_s[kWavesABlock][kRows][kExperts];
-  __shared__ __align__(16) double v_s[kWavesABlock][kRows][kExperts];
+  // a row's logits and values; in fp64, values over both
+  __shared__ __align__(16) double row_s[kWavesABlock][kRows][kExperts];
   __shared__ double g_s[kWavesABlock][kRows][kMaxGroups];
+  __shared__ int32_t slot_s[kWavesABlock][kRows][kSort ? kSorted : kMaxTopK];
   const RouteArgs& p = a.r;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (G - 1), mine = lane / G;
@@ -123,19 +271,22 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     for (int32_t e = threadIdx.x; e <= p.n_experts; e += blockDim.x) counts[e] = 0;
     __syncthreads();
   }
-  const bool by_logit = a.bias == nullptr, grouped = a.groups > 1 && a.top_groups < a.groups;
+  const bool grouped = a.groups > 1 && a.top_groups < a.groups;
   float bias[V], sums[V];
-  uint32_t group[V];
+  bool zero = true;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    bias[j] = !by_logit && e0 + j < p.n_experts ? a.bias[e0 + j] : 0.0f;
-    group[j] = grouped ? static_cast<uint32_t>(e0 + j) / static_cast<uint32_t>(a.group_size) & 63u : 0u;
+    bias[j] = a.bias != nullptr && e0 + j < p.n_experts ? a.bias[e0 + j] : 0.0f;
+    zero &= bias[j] == 0.0f;
     sums[j] = 0.0f;
   }
-  float* x_row = x_s[wave][mine];
-  double* v_row = v_s[wave][mine];
-  float* vf_row = reinterpret_cast<float*>(v_row);
+  // a bias of zeros is none
+  const bool by_logit = __ballot(!zero) == 0;
+  double* d_row = row_s[wave][mine];
+  float* x_row = reinterpret_cast<float*>(d_row);
+  float* v_row = x_row + kExperts;
   double* g_row = g_s[wave][mine];
+  int32_t* slot_row = slot_s[wave][mine];
   const float none = -__builtin_inff();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesABlock * kRows;
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWavesABlock + wave) * kRows; t0 < p.n_tokens;
@@ -152,156 +303,167 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     // scores relative to exp(shift), and their sum
     const float shift = a.sigmoid ? fminf(top, 0.0f) : top;
     float s[V], total = 0.0f;
+    if (a.sigmoid) {
+      const bool low = __ballot(shift < 0.0f) != 0;   // then a second exponential
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float xv = x.value(j);
-      if (a.sigmoid) {
-        s[j] = exp_of(fminf(xv, 0.0f) - shift) * inverse(1.0f + low_exp(xv));
+      for (int j = 0; j < V; ++j) {
+        const float xv = x.value(j), e = low_exp(xv);
+        s[j] = (xv >= 0.0f ? 1.0f : low ? exp_of(xv - shift) : e) * inverse(1.0f + e);
         if (xv != xv) s[j] = xv;
-      } else {
-        s[j] = exp_of(xv - top);
       }
-      x_row[e0 + j] = xv;
-      total += s[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = exp_of(x.value(j) - top);
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) total += s[j];
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<float4*>(x_row + e0 + j) =
+          float4{x.value(j), x.value(j + 1), x.value(j + 2), x.value(j + 3)};
     total = group_sum<G>(total);
     const float inv = inverse(total);
     // what is compared
-    const bool plain = by_logit || (!a.sigmoid && total != total);
+    const bool no_numbers = !a.sigmoid && total != total, plain = by_logit || no_numbers;
+    const bool exact_groups = plain && (a.group_best == 1 || no_numbers);
+    const float whole = a.sigmoid ? (shift < 0.0f ? exp_of(shift) : 1.0f) : inv;
     float v[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float xv = x.value(j);
-      const float abs = a.sigmoid ? s[j] * (shift < 0.0f ? exp_of(shift) : 1.0f) : s[j] * inv;
-      v[j] = !(xv > none) ? none : plain ? xv : abs + bias[j];
-      if (grouped) vf_row[e0 + j] = !(xv > none) ? none
-                                    : plain && (a.group_best == 1 || total != total) ? xv : abs + bias[j];
+      v[j] = !(xv > none) ? none : plain ? xv : __builtin_fmaf(s[j], whole, bias[j]);
     }
-    wave_sync();
     bool sure = true;
     if (grouped) {
-      const uint64_t taken = groups_taken<G, float>(a, vf_row, reinterpret_cast<float*>(g_row), l,
-                                                    plain && (a.group_best == 1 || total != total), sure);
+      float from[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = (taken >> group[j]) & 1 ? v[j] : none;
+      for (int j = 0; j < V; ++j)
+        from[j] = exact_groups || !(x.value(j) > none) ? v[j] : __builtin_fmaf(s[j], whole, bias[j]);
+      keep_groups<G, V>(a, v, from, v_row, reinterpret_cast<float*>(g_row), l, exact_groups, sure);
     }
-    uint64_t key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = key_of(v[j], e0 + j);
     // lane l of the row: slots l, l + G, ..; -1 where none is left
     int32_t slot[kHeld];
-    float first = 0.0f;
-    uint64_t last;
-    if (kSort) {
-      uint64_t best[8];
+    const bool keyed = kBf16 && kSort && __ballot(!plain) == 0;   // the expert is in the key
+    if constexpr (kSort) {
+      uint32_t key[V], best[8];
+      if (keyed) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const uint32_t o = order_of(v[j]);
+          key[j] = o == 0 ? 0u : (o & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(e0 + j));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = order_of(v[j]);
+      }
       best8<G, V>(key, best);
       slot[0] = -1;
-      last = best[0];
+      if (keyed) {
 #pragma unroll
-      for (int j = 0; j < kSorted; ++j) {
-        if (l == j && best[j] != 0) slot[0] = KeyF32::expert(best[j]);
-        if (j >= p.top_k) continue;
-        last = best[j];
-        if (!plain && j > 0 && best[j] != 0) {
-          const float b = KeyF32::value(best[j]);
-          sure &= KeyF32::value(best[j - 1]) - b > apart(b) + apart(first);
+        for (int j = 0; j < kSorted; ++j)
+          if (l == j && best[j] != 0) slot[0] = static_cast<int32_t>(0xFFFFu - (best[j] & 0xFFFFu));
+      } else {
+        // gaps between the slots and to the best left out
+        const float first = value_of(best[0]);
+        uint32_t last = best[0];
+#pragma unroll
+        for (int j = 1; j < kSorted; ++j) {
+          if (j >= p.top_k) break;
+          last = best[j];
+          const float b = value_of(best[j]), gap = value_of(best[j - 1]) - b;
+          if (best[j] != 0) sure &= plain ? gap > 0.0f : gap > apart(fmaxf(fabsf(b), fabsf(first)));
         }
-        if (j == 0) first = KeyF32::value(best[0]);
+        uint32_t next = 0, equal = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          next = key[j] < last && key[j] > next ? key[j] : next;
+          equal += key[j] == last ? 1u : 0u;
+        }
+        next = group_max_key<G>(next);
+        if (last != 0) {
+          const float b = value_of(next), gap = value_of(last) - b;
+          if (next != 0) sure &= plain || gap > apart(fmaxf(fabsf(b), fabsf(first)));
+          // the last slot's value once in the row (a butterfly of counts, as floats)
+          sure &= group_sum<G>(static_cast<float>(equal)) == 1.0f;
+        }
+        // each lane's own experts among the slots
+        uint32_t own = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) own |= key[j] >= last && key[j] != 0 ? 1u << j : 0u;
+        if (l < kSorted) slot_row[l] = -1;
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(v_row) + e0 + j) =
+              uint4{key[j], key[j + 1], key[j + 2], key[j + 3]};
+        wave_sync();
+        while (own != 0) {
+          const int j = __builtin_ctz(own);
+          own &= own - 1;
+          const uint32_t k = reinterpret_cast<const uint32_t*>(v_row)[e0 + j];
+          int32_t n = 0;
+#pragma unroll
+          for (int q = 0; q < kSorted; ++q) n += best[q] > k ? 1 : 0;
+          if (n < kSorted) slot_row[n] = e0 + j;
+        }
+        wave_sync();
+        if (l < kSorted) slot[0] = slot_row[l];
       }
     } else {
+      uint64_t key[V], last = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint32_t o = order_of(v[j]);
+        key[j] = o == 0 ? 0u : (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e0 + j));
+      }
       int32_t n = 0;
-      last = 0;
-      float before = 0.0f;
+      float first = 0.0f, before = 0.0f;
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
         slot[h] = -1;
-        for (int j = 0; j < G && n < p.top_k; ++j, ++n) {
+        for (int j = 0; j < G && n <= p.top_k; ++j, ++n) {   // one more: the best left out
           last = key[0];
 #pragma unroll
           for (int q = 1; q < V; ++q) last = key[q] > last ? key[q] : last;
           last = group_max_key<G>(last);
 #pragma unroll
           for (int q = 0; q < V; ++q) key[q] = key[q] == last ? 0 : key[q];
-          if (l == j && last != 0) slot[h] = KeyF32::expert(last);
+          if (l == j && last != 0 && n < p.top_k) slot[h] = KeyF32::expert(last);
           const float b = KeyF32::value(last);
           if (n == 0) first = b;
-          if (!plain && n > 0 && last != 0) sure &= before - b > apart(b) + apart(first);
+          if (!plain && n > 0 && last != 0) sure &= before - b > apart(fmaxf(fabsf(b), fabsf(first)));
           before = b;
         }
       }
+      // 64 slots leave no turn for the best left out
+      if (!plain && n <= p.top_k && last != 0) sure = false;
     }
-    if (!plain && last != 0) {   // the best one left out
-      uint64_t next = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) next = key[j] < last && key[j] > next ? key[j] : next;
-      next = group_max_key<G>(next);
-      if (next != 0) {
-        const float b = KeyF32::value(next);
-        sure &= KeyF32::value(last) - b > apart(b) + apart(first);
-      }
-    }
-    if (__ballot(!sure && valid) != 0) {   // rare: these rows in fp64
-      double w[V], all = 0.0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const double xv = x.value(j);
-        w[j] = a.sigmoid ? (xv < 0.0 ? exp(xv) : 1.0) / (1.0 + exp(-fabs(xv))) : exp(xv - static_cast<double>(top));
-        all += w[j];
-      }
-      butterfly<G>([&](auto step) {
-        uint64_t c, d;
-        pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, all), c, d);
-        all = __builtin_bit_cast(double, c) + __builtin_bit_cast(double, d);
-      });
+    const uint64_t unsettled = __ballot(!sure && valid);
+    if (unsettled != 0) {   // rare: these rows in fp64
       wave_sync();
-      const double nothing = -static_cast<double>(__builtin_inff());
+#pragma unroll 1
+      for (int row = 0; row < kRows; ++row) {
+        const int at = row * G;
+        if (((unsettled >> at) & (G == 64 ? ~0ull : (1ull << (G & 63)) - 1)) == 0) continue;
+        settle<kExperts, kBf16>(a, (t0 + row) * p.ld, __shfl(top, at, 64), __shfl(plain ? 1 : 0, at, 64) != 0,
+                                __shfl(exact_groups ? 1 : 0, at, 64) != 0, row_s[wave][row], g_s[wave][row],
+                                slot_s[wave][row]);
+        wave_sync();
+        if (mine == row) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const double xv = x.value(j), score = (a.sigmoid ? w[j] : w[j] / all) + static_cast<double>(bias[j]);
-        const bool open = x.value(j) > none;
-        v_row[e0 + j] = !open ? nothing : plain && (a.group_best == 1 || total != total) ? xv : score;
-        w[j] = !open ? nothing : plain ? xv : score;
-        if (!(w[j] > nothing)) w[j] = nothing;
-      }
-      wave_sync();
-      if (grouped) {
-        const uint64_t taken = groups_taken<G, double>(a, v_row, g_row, l, true, sure);
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = (taken >> group[j]) & 1 ? w[j] : nothing;
-      }
-      int32_t n = 0;
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h) {
-        slot[h] = -1;
-        for (int q = 0; q < G && n < p.top_k; ++q, ++n) {
-          double best = w[0];
-          uint32_t at = e0;
-#pragma unroll
-          for (int j = 1; j < V; ++j) {
-            at = w[j] > best ? e0 + j : at;
-            best = w[j] > best ? w[j] : best;
-          }
-          butterfly<G>([&](auto step) {
-            uint64_t c, d;
-            uint32_t ac, ad;
-            pair_of<decltype(step)::value>(__builtin_bit_cast(uint64_t, best), c, d);
-            pair_of<decltype(step)::value>(at, ac, ad);
-            const double bc = __builtin_bit_cast(double, c), bd = __builtin_bit_cast(double, d);
-            const bool second = bd > bc || (bd == bc && ad < ac);
-            best = second ? bd : bc;
-            at = second ? ad : ac;
-          });
-#pragma unroll
-          for (int j = 0; j < V; ++j) w[j] = at == static_cast<uint32_t>(e0 + j) ? nothing : w[j];
-          if (l == q && best > nothing) slot[h] = static_cast<int32_t>(at);
+          for (int h = 0; h < kHeld; ++h)
+            slot[h] = l + h * G < p.top_k ? slot_row[l + h * G] : -1;
         }
       }
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < V; ++j) x_row[e0 + j] = x.value(j);
+      wave_sync();
     }
     // weights of the slots
     float e[kHeld], xs[kHeld], high = none, taken = 0.0f;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-      if ((kSort && l >= kSorted) || l + h * G >= p.top_k) slot[h] = -1;
+      if (l + h * G >= p.top_k) slot[h] = -1;
       xs[h] = slot[h] >= 0 ? x_row[slot[h]] : none;
       high = fmaxf(high, xs[h]);
     }
@@ -318,8 +480,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     }
     if (p.renorm) taken = group_sum<G>(taken);
     // a NaN among the logits is one of every softmax weight
-    const float f = !a.sigmoid && total != total ? total
-                    : p.renorm ? inverse(taken) : a.sigmoid ? 1.0f : inv;
+    const float f = no_numbers ? total : p.renorm ? inverse(taken) : a.sigmoid ? 1.0f : inv;
     if (stats) {
 #pragma unroll
       for (int j = 0; j < V; ++j) sums[j] = counted ? __builtin_fmaf(s[j], inv, sums[j]) : sums[j];
@@ -341,7 +502,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
   if (!stats) return;
   __syncthreads();
   // the wave's rows, then the block's waves, in a fixed order
-  float(*prob)[kExperts] = reinterpret_cast<float(*)[kExperts]>(&x_s[0][0][0]);
+  float(*prob)[kExperts] = reinterpret_cast<float(*)[kExperts]>(&row_s[0][0][0]);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     float s = sums[j];
@@ -582,8 +743,9 @@ __global__ __launch_bounds__(256) void scored_grad_kernel(ScoredGradArgs p) {
 }
 
 // ------------------------------------------------------------------- hosts
+// Lanes a row, of 8 experts each up to 64 of them and 16 beyond.
 int32_t scored_lanes(int32_t n_experts) {
-  return n_experts <= 64 ? 8 : n_experts <= 128 ? 16 : n_experts <= 256 ? 32 : 64;
+  return n_experts <= 128 ? 8 : n_experts <= 256 ? 16 : n_experts <= 512 ? 32 : 64;
 }
 
 uint32_t scored_blocks(int64_t n_tokens, int32_t n_experts) {
@@ -676,13 +838,18 @@ extern "C" int32_t binade_moe_route_scored(const void* logits, int32_t dtype, in
   a.group_size = n_experts / rule->groups;
   a.top_groups = rule->top_groups;
   a.group_best = rule->group_best;
+  const int32_t lanes = scored_lanes(n_experts), each = n_experts <= 64 ? 8 : 16;
+  const int32_t whole = a.group_size % each == 0 ? a.group_size / each : 0;
+  a.lanes_a_group = (whole & (whole - 1)) == 0 ? whole : 0;
+  a.parts = 1;
+  while (2 * a.parts * a.groups <= lanes) a.parts *= 2;
   a.scale = rule->scale;
   a.sigmoid = rule->score == BINADE_SIGMOID;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (n_experts <= 64) launch_scored<8, 8>(a, blocks, bf16, st);
-  else if (n_experts <= 128) launch_scored<16, 8>(a, blocks, bf16, st);
-  else if (n_experts <= 256) launch_scored<32, 8>(a, blocks, bf16, st);
-  else if (n_experts <= 512) launch_scored<64, 8>(a, blocks, bf16, st);
+  else if (n_experts <= 128) launch_scored<8, 16>(a, blocks, bf16, st);
+  else if (n_experts <= 256) launch_scored<16, 16>(a, blocks, bf16, st);
+  else if (n_experts <= 512) launch_scored<32, 16>(a, blocks, bf16, st);
   else launch_scored<64, 16>(a, blocks, bf16, st);
   if (stats && blocks > 1)
     hipLaunchKernelGGL(route_stats_kernel, dim3(static_cast<uint32_t>((n_experts + 63) / 64)),
