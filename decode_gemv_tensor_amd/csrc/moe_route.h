@@ -57,6 +57,14 @@ __device__ __forceinline__ void pair_of(uint64_t v, uint64_t& a, uint64_t& b) {
   b = (static_cast<uint64_t>(b1) << 32) | b0;
 }
 
+template <int kStep>
+__device__ __forceinline__ void pair_of(int32_t v, int32_t& a, int32_t& b) {
+  uint32_t c, d;
+  pair_of<kStep>(static_cast<uint32_t>(v), c, d);
+  a = static_cast<int32_t>(c);
+  b = static_cast<int32_t>(d);
+}
+
 template <int G, int kStep = 1, typename F>
 __device__ __forceinline__ void butterfly(F f) {
   if constexpr (kStep < G) {

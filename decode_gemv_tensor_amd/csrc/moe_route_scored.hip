@@ -23,7 +23,7 @@ namespace binade {
 namespace {
 
 constexpr int kWavesABlock = 4;
-constexpr int32_t kScoredBlocks = 1024;   // at most: each leaves one row of partial sums
+constexpr int32_t kScoredBlocks = 512;   // at most: each leaves one row of partial sums
 constexpr int kMaxGroups = 64;
 
 struct ScoredArgs {
@@ -47,8 +47,15 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t o = (b ^ neg) + ((neg & 1u) | (~neg & 0x80000000u));
   return v > -__builtin_inff() ? o : 0u;
 }
-__device__ __forceinline__ float value_of(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o - 0x80000000u : 0u - o);
+// A value's bits as a whole number of the same order, and back. (-0 lies below
+// +0: such a row is not settled, their gap is nothing.) -inf is the least.
+constexpr int32_t kNone = static_cast<int32_t>(0x807FFFFFu);   // of -inf
+__device__ __forceinline__ int32_t ordered(float v) {
+  const int32_t b = __float_as_int(v);
+  return b ^ static_cast<int32_t>(static_cast<uint32_t>(b >> 31) >> 1);
+}
+__device__ __forceinline__ float value_of(int32_t o) {
+  return __int_as_float(o ^ static_cast<int32_t>(static_cast<uint32_t>(o >> 31) >> 1));
 }
 
 // How far apart two fp32 values of at most |v| have to be for their order to
@@ -147,9 +154,8 @@ __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], 
     float a = none, b = none;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float t = from[j];
-      b = t > a ? a : t > b ? t : b;
-      a = t > a ? t : a;
+      b = __builtin_amdgcn_fmed3f(a, b, from[j]);
+      a = from[j] > a ? from[j] : a;
     }
     butterfly<G>([&](auto step) {
       constexpr int kStep = decltype(step)::value;
@@ -296,24 +302,31 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     const bool valid = in && (p.valid == nullptr || p.valid[t] != 0);
     Logits<V, kBf16> x;
     x.load(p.logits, (in ? t : t0) * p.ld, e0, p.n_experts, p.vec);
-    float top = x.value(0);
+    float top = x.value(0), low = top;
 #pragma unroll
-    for (int j = 1; j < V; ++j) top = fmaxf(top, x.value(j));
+    for (int j = 1; j < V; ++j) {
+      top = fmaxf(top, x.value(j));
+      low = fminf(low, x.value(j));
+    }
     top = group_max<G>(top);
     // scores relative to exp(shift), and their sum
     const float shift = a.sigmoid ? fminf(top, 0.0f) : top;
     float s[V], total = 0.0f;
-    if (a.sigmoid) {
-      const bool low = __ballot(shift < 0.0f) != 0;   // then a second exponential
+    if (!a.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = exp_of(x.value(j) - top);
+    } else if (__ballot(shift < 0.0f) == 0) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float xv = x.value(j), e = low_exp(xv);
-        s[j] = (xv >= 0.0f ? 1.0f : low ? exp_of(xv - shift) : e) * inverse(1.0f + e);
-        if (xv != xv) s[j] = xv;
+        s[j] = (xv >= 0.0f ? 1.0f : e) * inverse(1.0f + e);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) s[j] = exp_of(x.value(j) - top);
+      for (int j = 0; j < V; ++j) {
+        const float xv = x.value(j);
+        s[j] = (xv >= 0.0f ? 1.0f : exp_of(xv - shift)) * inverse(1.0f + low_exp(xv));
+      }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) total += s[j];
@@ -328,78 +341,92 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     const bool exact_groups = plain && (a.group_best == 1 || no_numbers);
     const float whole = a.sigmoid ? (shift < 0.0f ? exp_of(shift) : 1.0f) : inv;
     float v[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float xv = x.value(j);
-      v[j] = !(xv > none) ? none : plain ? xv : __builtin_fmaf(s[j], whole, bias[j]);
-    }
     bool sure = true;
-    if (grouped) {
-      float from[V];
+    // closed experts, or no numbers: each value looked at
+    const bool special = __ballot(!(low > none) || total != total) != 0;
+    if (special || by_logit) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        from[j] = exact_groups || !(x.value(j) > none) ? v[j] : __builtin_fmaf(s[j], whole, bias[j]);
-      keep_groups<G, V>(a, v, from, v_row, reinterpret_cast<float*>(g_row), l, exact_groups, sure);
+      for (int j = 0; j < V; ++j) {
+        const float xv = x.value(j), w = plain ? xv : __builtin_fmaf(s[j], whole, bias[j]);
+        v[j] = xv > none && w > none ? w : none;
+      }
+      if (grouped) {
+        float from[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          from[j] = exact_groups || !(v[j] > none) ? v[j] : __builtin_fmaf(s[j], whole, bias[j]);
+        keep_groups<G, V>(a, v, from, v_row, reinterpret_cast<float*>(g_row), l, exact_groups, sure);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(s[j], whole, bias[j]);
+      if (grouped) keep_groups<G, V>(a, v, v, v_row, reinterpret_cast<float*>(g_row), l, false, sure);
     }
     // lane l of the row: slots l, l + G, ..; -1 where none is left
     int32_t slot[kHeld];
     const bool keyed = kBf16 && kSort && __ballot(!plain) == 0;   // the expert is in the key
     if constexpr (kSort) {
-      uint32_t key[V], best[8];
+      slot[0] = -1;
       if (keyed) {
+        uint32_t key[V], best[8];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const uint32_t o = order_of(v[j]);
           key[j] = o == 0 ? 0u : (o & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(e0 + j));
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = order_of(v[j]);
-      }
-      best8<G, V>(key, best);
-      slot[0] = -1;
-      if (keyed) {
+        best8<G, V>(key, best);
 #pragma unroll
         for (int j = 0; j < kSorted; ++j)
           if (l == j && best[j] != 0) slot[0] = static_cast<int32_t>(0xFFFFu - (best[j] & 0xFFFFu));
       } else {
+        int32_t key[V], best[8];
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = ordered(v[j]);
+        best8<G, V>(key, best);
         // gaps between the slots and to the best left out
-        const float first = value_of(best[0]);
-        uint32_t last = best[0];
+        const float first = fabsf(value_of(best[0]));
+        int32_t last = best[0];
+        uint32_t filled = best[0] > kNone ? 1u : 0u;
 #pragma unroll
         for (int j = 1; j < kSorted; ++j) {
           if (j >= p.top_k) break;
           last = best[j];
           const float b = value_of(best[j]), gap = value_of(best[j - 1]) - b;
-          if (best[j] != 0) sure &= plain ? gap > 0.0f : gap > apart(fmaxf(fabsf(b), fabsf(first)));
+          if (best[j] > kNone) {
+            sure &= plain ? gap > 0.0f : gap > apart(fmaxf(fabsf(b), first));
+            ++filled;
+          }
         }
-        uint32_t next = 0, equal = 0;
+        int32_t next = kNone;
+        uint32_t own = 0;   // this lane's experts among the slots
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          next = key[j] < last && key[j] > next ? key[j] : next;
-          equal += key[j] == last ? 1u : 0u;
+          const int32_t left = key[j] < last ? key[j] : kNone;
+          next = left > next ? left : next;
+          own |= key[j] >= last ? 1u << j : 0u;
+        }
+        if (last == kNone) {
+          own = 0;
+#pragma unroll
+          for (int j = 0; j < V; ++j) own |= key[j] > kNone ? 1u << j : 0u;
         }
         next = group_max_key<G>(next);
-        if (last != 0) {
-          const float b = value_of(next), gap = value_of(last) - b;
-          if (next != 0) sure &= plain || gap > apart(fmaxf(fabsf(b), fabsf(first)));
-          // the last slot's value once in the row (a butterfly of counts, as floats)
-          sure &= group_sum<G>(static_cast<float>(equal)) == 1.0f;
+        if (last > kNone && next > kNone && !plain) {
+          const float b = value_of(next);
+          sure &= value_of(last) - b > apart(fmaxf(fabsf(b), first));
         }
-        // each lane's own experts among the slots
-        uint32_t own = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) own |= key[j] >= last && key[j] != 0 ? 1u << j : 0u;
+        // equal values at the end of the slots: more experts than slots
+        sure &= group_sum<G>(static_cast<float>(__builtin_popcount(own))) == static_cast<float>(filled);
         if (l < kSorted) slot_row[l] = -1;
 #pragma unroll
         for (int j = 0; j < V; j += 4)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(v_row) + e0 + j) =
-              uint4{key[j], key[j + 1], key[j + 2], key[j + 3]};
+          *reinterpret_cast<int4*>(reinterpret_cast<int32_t*>(v_row) + e0 + j) =
+              int4{key[j], key[j + 1], key[j + 2], key[j + 3]};
         wave_sync();
         while (own != 0) {
           const int j = __builtin_ctz(own);
           own &= own - 1;
-          const uint32_t k = reinterpret_cast<const uint32_t*>(v_row)[e0 + j];
+          const int32_t k = reinterpret_cast<const int32_t*>(v_row)[e0 + j];
           int32_t n = 0;
 #pragma unroll
           for (int q = 0; q < kSorted; ++q) n += best[q] > k ? 1 : 0;
@@ -482,8 +509,13 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     // a NaN among the logits is one of every softmax weight
     const float f = no_numbers ? total : p.renorm ? inverse(taken) : a.sigmoid ? 1.0f : inv;
     if (stats) {
+      if (__ballot(!counted) == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) sums[j] = counted ? __builtin_fmaf(s[j], inv, sums[j]) : sums[j];
+        for (int j = 0; j < V; ++j) sums[j] = __builtin_fmaf(s[j], inv, sums[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sums[j] = counted ? __builtin_fmaf(s[j], inv, sums[j]) : sums[j];
+      }
       if (counted && l == 0) atomicAdd(&counts[p.n_experts], 1);
     }
     if (in) {
