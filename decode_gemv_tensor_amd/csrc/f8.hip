@@ -145,15 +145,13 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n,
 //
 // Rows of v [m, n] as e4m3, paired(n) / 128 blocks of m_pad rows, with a code
 // for each block of a row: 16 lanes a block, 8 values a lane.
-__global__ __launch_bounds__(256) void quantise_rows_kernel(const uint16_t* v, int64_t ld,
-                                                            int64_t m, int64_t n, bool vec,
-                                                            uint8_t* q, int64_t m_pad, uint8_t* codes,
-                                                            int64_t ldc) {
+__device__ __forceinline__ void quantise_rows(const uint16_t* v, int64_t ld, int64_t m, int64_t n,
+                                              bool vec, uint8_t* q, int64_t m_pad, uint8_t* codes,
+                                              int64_t ldc, int64_t first, int64_t step) {
   const int64_t nb = (n + 255) / 256 * 2, units = m * nb;
   const int l = threadIdx.x & 15;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 16;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4); u < units;
-       u += step) {
+#pragma unroll 2
+  for (int64_t u = first; u < units; u += step) {
     const int64_t row = u / nb, b = u - row * nb;
     uint32_t d[4];
     load8(v + row * ld, b * 128 + l * 8, n, vec, d);
@@ -165,6 +163,15 @@ __global__ __launch_bounds__(256) void quantise_rows_kernel(const uint16_t* v, i
         uint2{to_f8(d[0], d[1], s), to_f8(d[2], d[3], s)};
     if (l == 0) codes[row * ldc + b] = static_cast<uint8_t>(code);
   }
+}
+
+__global__ __launch_bounds__(256) void quantise_rows_kernel(const uint16_t* v, int64_t ld,
+                                                            int64_t m, int64_t n, bool vec,
+                                                            uint8_t* q, int64_t m_pad, uint8_t* codes,
+                                                            int64_t ldc) {
+  quantise_rows(v, ld, m, n, vec, q, m_pad, codes, ldc,
+                static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4),
+                static_cast<int64_t>(gridDim.x) * 16);
 }
 
 // 128 x 128 tiles of v [m, n], turned: qt of n_pad rows with codes for 128
@@ -412,13 +419,8 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t
     return;
   }
   const int64_t at = row * p.ldy + col;
-  if (p.y_vec) {   // rows of whole, aligned fours
-    if (col >= p.n) return;
-    if (p.y_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
-          uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    else
-      *reinterpret_cast<floatx4*>(static_cast<float*>(p.y) + at) = v;
+  if (p.y_vec) {   // rows of whole, aligned fours of fp32
+    if (col < p.n) *reinterpret_cast<floatx4*>(static_cast<float*>(p.y) + at) = v;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -597,19 +599,38 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
       }
     } else {
       int8v wv[FN];
+      floatx4 sum[2][FN], last_sum[FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j) wv[j] = operand(wb + j * 2048);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < (kScales == kBlockF32 ? FM : 0); ++i) {
+        // a row's products while the ones before are scaled and added
+        const int8v xv = operand(xb + i * 2048);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          sum[i % 2][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              wv[j], xv, (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep, static_cast<int>(xc[i]));
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (i > 0) acc[i - 1][j][e] = __builtin_fmaf(wf[kStep], sum[(i + 1) % 2][j][e], acc[i - 1][j][e]);
+            if (i == FM - 1) last_sum[j] = sum[i % 2][j];
+          }
+      }
+      if (kScales == kBlockF32) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[FM - 1][j][e] = __builtin_fmaf(wf[kStep], last_sum[j][e], acc[FM - 1][j][e]);
+      }
+#pragma unroll
+      for (int i = 0; i < (kScales == kBlockF32 ? 0 : FM); ++i) {
         const int8v xv = operand(xb + i * 2048);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          if (kScales == kBlockF32) {
-            const floatx4 sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wv[j], xv, (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep, static_cast<int>(xc[i]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(wf[kStep], sum[e], acc[i][j][e]);
-          } else {
+          {
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 wv[j], xv, acc[i][j], 0, 0, kStep, static_cast<int>(wc[kScales == kRowCode ? j : 0]), kStep,
                 static_cast<int>(xc[i]));
@@ -658,12 +679,27 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int row = wm * TM + i * 16 + r;
-    if (row >= rows) continue;
-    const int64_t y_row = kExperts ? static_cast<int64_t>(p.order[m0 + row]) : m0 + row;
+    const bool live = row < rows;
+    const int64_t y_row = kExperts ? static_cast<int64_t>(p.order[m0 + (live ? row : 0)]) : m0 + row;
+    const int64_t col0 = n0 + wn * TN;
+    if (p.part == nullptr && p.y_bf16 && p.y_vec) {
+      // the halves of two operands' results change places between lanes 16
+      // apart: eight columns a lane, 64 bytes of a row side by side
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t col = n0 + wn * TN + j * 16 + q * 4;
-      store4(p, split, y_row, col, acc[i][j]);
+      for (int j = 0; j < FN; j += 2) {
+        const floatx4 a = acc[i][j], b = acc[i][j + 1];
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1]), false,
+                                                         false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(a[2], a[3]), pack_bf16(b[2], b[3]), false,
+                                                         false);
+        const int64_t col = col0 + (j + (q & 1)) * 16 + (q & 2) * 4;
+        if (live && col < p.n)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + y_row * p.ldy + col) =
+              uint4{lo[0], hi[0], lo[1], hi[1]};
+      }
+    } else if (live) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) store4(p, split, y_row, col0 + j * 16 + q * 4, acc[i][j]);
     }
   }
 }
@@ -1226,32 +1262,51 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
 // ------------------------------------------------------------ pairs by expert
 // One block: counts, the tiles of each expert's pairs (those without expert
 // last, as expert -1), and the pairs in their experts' order (within one in
-// whatever order: a row's result does not depend on its place).
-__global__ __launch_bounds__(1024) void sort_pairs_kernel(const int32_t* idx, int32_t pairs,
-                                                          int32_t n_experts, int32_t bm,
-                                                          int32_t* order, int4* tiles,
-                                                          int32_t* n_tiles, uint32_t* status) {
+// whatever order: a row's result does not depend on its place). The other
+// blocks quantise the rows meanwhile.
+struct SortArgs {
+  const int32_t* idx;
+  int32_t pairs, n_experts, bm;
+  int32_t* order;
+  int4* tiles;
+  int32_t* n_tiles;
+  uint32_t* status;
+};
+
+// Eight ids of a thread, thread by thread; -1 behind the last.
+__device__ __forceinline__ void ids_of(const SortArgs& p, int32_t from, int32_t (&e)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int32_t i = from + j * 1024;
+    e[j] = i < p.pairs ? p.idx[i] : -1;
+  }
+}
+
+__device__ void sort_pairs(const SortArgs& p) {
   __shared__ int32_t cursor[kMaxExperts + 1];
   __shared__ int32_t sums[2][16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  for (int32_t e = t; e <= n_experts; e += 1024) cursor[e] = 0;
+  for (int32_t e = t; e <= p.n_experts; e += 1024) cursor[e] = 0;
   __syncthreads();
   bool bad = false;
-  for (int32_t i = t; i < pairs; i += 1024) {
-    int32_t e = idx[i];
-    if (e < 0 || e >= n_experts) {
-      bad |= e != -1;
-      e = n_experts;
+  for (int32_t from = t; from < p.pairs; from += 8192) {
+    int32_t e[8];
+    ids_of(p, from, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (from + j * 1024 >= p.pairs) continue;
+      const bool none = e[j] < 0 || e[j] >= p.n_experts;
+      bad |= none && e[j] != -1;
+      atomicAdd(&cursor[none ? p.n_experts : e[j]], 1);
     }
-    atomicAdd(&cursor[e], 1);
   }
-  if (bad && status != nullptr) atomicOr(status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
+  if (bad && p.status != nullptr) atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
   __syncthreads();
   // starts: a sum over the experts before, 1024 at a time
   int32_t pair_base = 0, tile_base = 0;
-  for (int32_t e0 = 0; e0 <= n_experts; e0 += 1024) {
+  for (int32_t e0 = 0; e0 <= p.n_experts; e0 += 1024) {
     const int32_t e = e0 + t;
-    const int32_t n = e <= n_experts ? cursor[e] : 0, k = (n + bm - 1) / bm;
+    const int32_t n = e <= p.n_experts ? cursor[e] : 0, k = (n + p.bm - 1) / p.bm;
     int32_t ps = n, ts = k;
     for (int d = 1; d < 64; d <<= 1) {
       const int32_t a = __shfl_up(ps, d, 64), b = __shfl_up(ts, d, 64);
@@ -1275,19 +1330,35 @@ __global__ __launch_bounds__(1024) void sort_pairs_kernel(const int32_t* idx, in
       tile_base += sums[1][v];
     }
     const int32_t start = before_p + ps - n, first = before_t + ts - k;
-    if (e <= n_experts) {
+    if (e <= p.n_experts) {
       cursor[e] = start;
       for (int32_t j = 0; j < k; ++j)
-        tiles[first + j] = int4{e < n_experts ? e : -1, start + j * bm,
-                                n - j * bm < bm ? n - j * bm : bm, 0};
+        p.tiles[first + j] = int4{e < p.n_experts ? e : -1, start + j * p.bm,
+                                  n - j * p.bm < p.bm ? n - j * p.bm : p.bm, 0};
     }
     __syncthreads();
   }
-  if (t == 0) *n_tiles = tile_base;
-  for (int32_t i = t; i < pairs; i += 1024) {
-    const int32_t e = idx[i];
-    order[atomicAdd(&cursor[e < 0 || e >= n_experts ? n_experts : e], 1)] = i;
+  if (t == 0) *p.n_tiles = tile_base;
+  for (int32_t from = t; from < p.pairs; from += 8192) {
+    int32_t e[8], at[8];
+    ids_of(p, from, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      at[j] = from + j * 1024 < p.pairs
+                  ? atomicAdd(&cursor[e[j] < 0 || e[j] >= p.n_experts ? p.n_experts : e[j]], 1) : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at[j] >= 0) p.order[at[j]] = from + j * 1024;
   }
+}
+
+__global__ __launch_bounds__(1024) void prepare_experts_kernel(SortArgs p, const uint16_t* v, int64_t ld,
+                                                               int64_t m, int64_t n, uint8_t* q,
+                                                               int64_t m_pad, uint8_t* codes, int64_t ldc) {
+  if (blockIdx.x == 0) sort_pairs(p);
+  else quantise_rows(v, ld, m, n, true, q, m_pad, codes, ldc,
+                     (static_cast<int64_t>(blockIdx.x) - 1) * 64 + (threadIdx.x >> 4),
+                     (static_cast<int64_t>(gridDim.x) - 1) * 64);
 }
 
 // ------------------------------------------------------------------- hosts
@@ -1391,7 +1462,7 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   p.mt = static_cast<int32_t>((m + q.bm - 1) / q.bm);
   p.nt = static_cast<int32_t>((n + q.bn - 1) / q.bn);
   p.y_bf16 = y_bf16;
-  const int whole = q.bm == kBigM && y_bf16 ? 8 : 4;   // results that a lane stores together
+  const int whole = y_bf16 ? 8 : 4;   // results that a lane stores together
   p.y_vec = n % whole == 0 && ldy % whole == 0 && aligned16(y);
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
   launch_kind(kind, p, q, !y_bf16, st);
@@ -1784,11 +1855,12 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   p.nt = static_cast<int32_t>((n + 127) / 128);
   p.splits = 1;
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
-  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((rows * paired(k) / 128 + 15) / 16)), dim3(256),
-                     0, st, x, ldx, rows, k, true, at, tile_rows(rows), codes, codes_of(k));
-  hipLaunchKernelGGL(sort_pairs_kernel, dim3(1), dim3(1024), 0, st, idx, static_cast<int32_t>(pairs),
-                     experts->count, q.bm, const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles),
-                     const_cast<int32_t*>(p.n_tiles), dev_status);
+  const SortArgs sort{idx, static_cast<int32_t>(pairs), experts->count, q.bm,
+                      const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles),
+                      const_cast<int32_t*>(p.n_tiles), dev_status};
+  const int64_t blocks = (rows * paired(k) / 128 + 127) / 128;   // two blocks of a row a thread
+  hipLaunchKernelGGL(prepare_experts_kernel, dim3(1 + some_blocks(blocks)), dim3(1024), 0, st, sort, x, ldx,
+                     rows, k, at, tile_rows(rows), codes, codes_of(k));
   p.x = at;
   p.x_codes = codes;
   p.w = experts->values;
@@ -1804,7 +1876,8 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   p.kb = static_cast<int32_t>(blocks_of(k));
   p.per_split = (p.kb + 3) / 4 * 4;
   p.y_bf16 = y_dtype == BINADE_BF16;
-  p.y_vec = n % 4 == 0 && ldy % 4 == 0 && aligned16(y);
+  const int whole = p.y_bf16 ? 8 : 4;
+  p.y_vec = n % whole == 0 && ldy % whole == 0 && aligned16(y);
   p.w_next = w_next;
   p.s_next = s_next;
   p.pairs_a_row = per_row;
