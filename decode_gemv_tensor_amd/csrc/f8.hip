@@ -375,8 +375,7 @@ struct GemmArgs {
   bool y_bf16, y_vec;
   // experts: pairs by expert, tiles of them, and a matrix's size
   const int32_t* order;
-  const int4* tiles;       // expert (-1: none), first pair, pairs
-  const int32_t* n_tiles;
+  const int4* tiles;       // expert (-1: none, -2: no tile), first pair, pairs
   int64_t w_next, s_next;
   int32_t pairs_a_row;
 };
@@ -439,6 +438,17 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t
 // every bank once; the swizzle is in the addresses that the lanes load from.
 // The weights are the instruction's first operand: a lane's four results lie
 // side by side in a row of y.
+// Experts' tiles: an XCD's share of the places (p.mt), in columns of eight.
+__device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, int32_t& nt) {
+  const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+  constexpr int32_t kGroup = 8;
+  const int32_t group = local / (kGroup * p.nt), first = group * kGroup;
+  const int32_t high = p.mt - first < kGroup ? p.mt - first : kGroup;
+  const int32_t at = local - group * kGroup * p.nt;
+  mt = xcd * p.mt + first + at % high;
+  nt = at / high;
+}
+
 template <int BM, int BN, int WM, int WN, bool kExact, int kScales, bool kExperts>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
   constexpr int kWaves = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -450,14 +460,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
   int32_t mt, nt, split;
-  if (!tile_of(p, mt, nt, split)) return;
+  if (kExperts) {
+    expert_tile_of(p, mt, nt);
+    split = blockIdx.y;   // 0
+  } else if (!tile_of(p, mt, nt, split)) {
+    return;
+  }
   const int64_t n0 = static_cast<int64_t>(nt) * BN;
   int64_t m0 = static_cast<int64_t>(mt) * BM, rows = p.m - m0;
   const uint8_t* w = p.w;
   int64_t expert = 0;
   if (kExperts) {
-    if (mt >= *p.n_tiles) return;
     const int4 tile = p.tiles[mt];
+    if (tile.x == -2) return;
     expert = tile.x;
     m0 = tile.y;
     rows = tile.z;
@@ -1260,49 +1275,94 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
 }
 
 // ------------------------------------------------------------ pairs by expert
-// One block: counts, the tiles of each expert's pairs (those without expert
-// last, as expert -1), and the pairs in their experts' order (within one in
-// whatever order: a row's result does not depend on its place). The other
-// blocks quantise the rows meanwhile.
+// One block: counts, the tiles of each expert's pairs, and the pairs in their
+// experts' order, those without expert last (within one expert in whatever
+// order: a row's result does not depend on its place). The other blocks
+// quantise the rows meanwhile. Tiles lie as the product's blocks take them: an
+// eighth for each XCD, with its share of the tiles that have an expert,
+// connected, then its share of the others (expert -1: zeros), then none (-2).
 struct SortArgs {
   const int32_t* idx;
-  int32_t pairs, n_experts, bm;
+  int32_t pairs, n_experts, bm, share;   // share: places of tiles of an XCD
   int32_t* order;
   int4* tiles;
-  int32_t* n_tiles;
   uint32_t* status;
 };
 
-// Eight ids of a thread, thread by thread; -1 behind the last.
-__device__ __forceinline__ void ids_of(const SortArgs& p, int32_t from, int32_t (&e)[8]) {
+// Eight ids of a thread, thread by thread: an expert, n_experts for none, -1
+// behind the last pair.
+__device__ __forceinline__ bool ids_of(const SortArgs& p, int32_t from, int32_t (&e)[8]) {
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int32_t i = from + j * 1024;
-    e[j] = i < p.pairs ? p.idx[i] : -1;
+    e[j] = i < p.pairs ? p.idx[i] : INT32_MIN;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool none = e[j] < 0 || e[j] >= p.n_experts, in = from + j * 1024 < p.pairs;
+    bad |= in && none && e[j] != -1;
+    e[j] = !in ? -1 : none ? p.n_experts : e[j];
+  }
+  return bad;
+}
+
+// Counts eight ids a lane. Pairs without expert are many where tokens are
+// padded: one addition a wave for them.
+__device__ __forceinline__ void count_behind(int32_t* cursor, const int32_t (&e)[8], int32_t none, int lane) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint64_t nones = __ballot(e[j] == none);
+    if (e[j] == none ? (nones & ((1ull << lane) - 1)) == 0 : e[j] >= 0)
+      atomicAdd(&cursor[e[j]], e[j] == none ? __popcll(nones) : 1);
+  }
+}
+// And gives each its place.
+__device__ __forceinline__ void place_behind(int32_t* cursor, const int32_t (&e)[8], int32_t none, int lane,
+                                             int32_t (&at)[8]) {
+  uint64_t nones[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    nones[j] = __ballot(e[j] == none);
+    at[j] = 0;
+    if (e[j] == none ? (nones[j] & ((1ull << lane) - 1)) == 0 : e[j] >= 0)
+      at[j] = atomicAdd(&cursor[e[j]], e[j] == none ? __popcll(nones[j]) : 1);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int32_t first = __shfl(at[j], nones[j] != 0 ? __builtin_ctzll(nones[j]) : 0, 64);
+    if (e[j] == none) at[j] = first + __popcll(nones[j] & ((1ull << lane) - 1));
   }
 }
 
 __device__ void sort_pairs(const SortArgs& p) {
-  __shared__ int32_t cursor[kMaxExperts + 1];
+  __shared__ int32_t cursor[kMaxExperts + 1], first_tile[kMaxExperts + 1];
   __shared__ int32_t sums[2][16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  for (int32_t e = t; e <= p.n_experts; e += 1024) cursor[e] = 0;
-  __syncthreads();
+  const bool few = p.pairs <= 32768;   // then ids stay in registers
+  int32_t held[4][8];
   bool bad = false;
-  for (int32_t from = t; from < p.pairs; from += 8192) {
-    int32_t e[8];
-    ids_of(p, from, e);
+  if (few) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (from + j * 1024 >= p.pairs) continue;
-      const bool none = e[j] < 0 || e[j] >= p.n_experts;
-      bad |= none && e[j] != -1;
-      atomicAdd(&cursor[none ? p.n_experts : e[j]], 1);
+    for (int b = 0; b < 4; ++b) bad |= ids_of(p, t + b * 8192, held[b]);
+  }
+  for (int32_t e = t; e <= p.n_experts; e += 1024) cursor[e] = 0;
+  for (int32_t i = t; i < 8 * p.share; i += 1024) p.tiles[i] = int4{-2, 0, 0, 0};
+  __syncthreads();
+  if (few) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) count_behind(cursor, held[b], p.n_experts, lane);
+  } else {
+    for (int32_t from = t; from - t < p.pairs; from += 8192) {
+      int32_t e[8];
+      bad |= ids_of(p, from, e);
+      count_behind(cursor, e, p.n_experts, lane);
     }
   }
   if (bad && p.status != nullptr) atomicOr(p.status, static_cast<uint32_t>(BINADE_DEV_BAD_INDEX));
   __syncthreads();
-  // starts: a sum over the experts before, 1024 at a time
+  // starts: sums over the experts before, 1024 at a time. A start replaces the
+  // count; the next start, or the pairs' number, ends it.
   int32_t pair_base = 0, tile_base = 0;
   for (int32_t e0 = 0; e0 <= p.n_experts; e0 += 1024) {
     const int32_t e = e0 + t;
@@ -1329,26 +1389,50 @@ __device__ void sort_pairs(const SortArgs& p) {
       pair_base += sums[0][v];
       tile_base += sums[1][v];
     }
-    const int32_t start = before_p + ps - n, first = before_t + ts - k;
     if (e <= p.n_experts) {
-      cursor[e] = start;
-      for (int32_t j = 0; j < k; ++j)
-        p.tiles[first + j] = int4{e < p.n_experts ? e : -1, start + j * p.bm,
-                                  n - j * p.bm < p.bm ? n - j * p.bm : p.bm, 0};
+      cursor[e] = before_p + ps - n;
+      first_tile[e] = before_t + ts - k;
     }
     __syncthreads();
   }
-  if (t == 0) *p.n_tiles = tile_base;
-  for (int32_t from = t; from < p.pairs; from += 8192) {
-    int32_t e[8], at[8];
+  const int32_t live = first_tile[p.n_experts], per = live / 8, more = live % 8;
+  for (int32_t e = t; e <= p.n_experts; e += 1024) {
+    const int32_t start = cursor[e], end = e < p.n_experts ? cursor[e + 1] : p.pairs;
+    for (int32_t j = 0; start + j * p.bm < end; ++j) {
+      const int32_t i = first_tile[e] + j;
+      int32_t xcd, place;
+      if (e < p.n_experts) {
+        const int32_t larger = more * (per + 1);   // tiles of the XCDs with one more
+        xcd = i < larger ? i / (per + 1) : more + (i - larger) / per;
+        place = i < larger ? i % (per + 1) : (i - larger) % per;
+      } else {
+        xcd = j % 8;
+        place = per + (xcd < more ? 1 : 0) + j / 8;
+      }
+      p.tiles[xcd * p.share + place] =
+          int4{e < p.n_experts ? e : -1, start + j * p.bm,
+               end - start - j * p.bm < p.bm ? end - start - j * p.bm : p.bm, 0};
+    }
+  }
+  __syncthreads();   // starts are read above and moved on below
+  if (few) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      int32_t to[8];
+      place_behind(cursor, held[b], p.n_experts, lane, to);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (held[b][j] >= 0) p.order[to[j]] = t + b * 8192 + j * 1024;
+    }
+    return;
+  }
+  for (int32_t from = t; from - t < p.pairs; from += 8192) {
+    int32_t e[8], to[8];
     ids_of(p, from, e);
+    place_behind(cursor, e, p.n_experts, lane, to);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      at[j] = from + j * 1024 < p.pairs
-                  ? atomicAdd(&cursor[e[j] < 0 || e[j] >= p.n_experts ? p.n_experts : e[j]], 1) : -1;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at[j] >= 0) p.order[at[j]] = from + j * 1024;
+      if (e[j] >= 0) p.order[to[j]] = from + j * 1024;
   }
 }
 
@@ -1390,12 +1474,12 @@ Plan plan_of(int64_t m, int64_t n, int64_t kb, bool exact) {
 
 // Whether a launch stays below 2^32 threads (of at most 512 a block).
 bool launchable(const GemmArgs& p) {
-  return static_cast<int64_t>(p.mt) * p.nt * p.splits < (1ll << 23);
+  return static_cast<int64_t>(p.mt) * p.nt * (p.order != nullptr ? 8 : p.splits) < (1ll << 23);
 }
 
 template <int kScales, bool kExperts>
 void launch_gemm(const GemmArgs& p, const Plan& q, bool exact, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(p.mt) * p.nt * p.splits));
+  const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(p.mt) * p.nt * (kExperts ? 8 : p.splits)));
 #define BINADE_F8_LAUNCH(BM, BN, WM, WN, EX)                                                     \
   hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, EX, kScales, kExperts>), grid, dim3(64 * WM * WN), \
                      0, st, p)
@@ -1767,18 +1851,17 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
 
 namespace {
 struct ExpertSpace {
-  int64_t order, tiles, count, total;   // bytes before each
-  int64_t n_tiles;                      // at most
+  int64_t order, tiles, total;   // bytes before each, and of all
+  int64_t share;                 // places of tiles of an XCD
 };
 ExpertSpace expert_space(int64_t rows, int64_t pairs, int64_t k, int32_t experts) {
   ExpertSpace s;
   const int32_t bm = expert_tile(pairs, experts);
   const int64_t each = experts + 1 < pairs ? experts + 1 : pairs;   // experts with a part of a tile
-  s.n_tiles = pairs / bm + each;
+  s.share = (pairs / bm + each) / 8 + 2;   // two parts, each rounded up
   s.order = side_bytes(rows, k);
   s.tiles = s.order + up16(4 * pairs);
-  s.count = s.tiles + 16 * s.n_tiles;
-  s.total = s.count + 16;
+  s.total = s.tiles + 16 * 8 * s.share;
   return s;
 }
 }  // namespace
@@ -1850,14 +1933,12 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   GemmArgs p{};
   p.order = reinterpret_cast<int32_t*>(at + space.order);
   p.tiles = reinterpret_cast<int4*>(at + space.tiles);
-  p.n_tiles = reinterpret_cast<int32_t*>(at + space.count);
-  p.mt = static_cast<int32_t>(space.n_tiles);
+  p.mt = static_cast<int32_t>(space.share);
   p.nt = static_cast<int32_t>((n + 127) / 128);
   p.splits = 1;
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
-  const SortArgs sort{idx, static_cast<int32_t>(pairs), experts->count, q.bm,
-                      const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles),
-                      const_cast<int32_t*>(p.n_tiles), dev_status};
+  const SortArgs sort{idx, static_cast<int32_t>(pairs), experts->count, q.bm, p.mt,
+                      const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles), dev_status};
   const int64_t blocks = (rows * paired(k) / 128 + 127) / 128;   // two blocks of a row a thread
   hipLaunchKernelGGL(prepare_experts_kernel, dim3(1 + some_blocks(blocks)), dim3(1024), 0, st, sort, x, ldx,
                      rows, k, at, tile_rows(rows), codes, codes_of(k));
