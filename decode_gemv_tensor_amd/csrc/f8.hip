@@ -361,7 +361,7 @@ __global__ __launch_bounds__(256) void layout_scales_kernel(const T* s, T* out, 
 // ------------------------------------------------------------------ product
 // Scales of the weights' side: a code for 128 x 128 values, a code for 128
 // columns of each row, or an fp32 number for 128 x 128 values.
-enum Scales { kBlockCode, kRowCode, kBlockF32, kWide };
+enum Scales { kBlockCode, kRowCode, kBlockF32 };
 
 struct GemmArgs {
   const uint8_t *x, *x_codes, *w;
@@ -450,7 +450,7 @@ __device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, i
 }
 
 template <int BM, int BN, int WM, int WN, bool kExact, int kScales, bool kExperts>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs p) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
   constexpr int kWaves = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int kXLoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;
   static_assert(kXLoads * 8 * kWaves == BM && kWLoads * 8 * kWaves == BN, "whole loads");
@@ -803,7 +803,7 @@ __global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
   };
 
   // codes of two steps at once
-  constexpr int kCodes = kScales == kWide ? 1 : FM, kRowCodes = kScales == kRowCode ? 8 : 1;
+  constexpr int kCodes = FM, kRowCodes = kScales == kRowCode ? 8 : 1;
   uint32_t xc[kCodes], xc_next[kCodes], wc[kRowCodes], wc_next[kRowCodes];
   float wf[2], wf_next[2];
   uint32_t xc_off[kCodes], wc_off[kRowCodes];
@@ -840,13 +840,12 @@ __global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
         const int32_t row = wn * 128 + j * 16 + r;
         wc_off[j] = static_cast<uint32_t>((row < w_last ? row : w_last) * p.ld_ws);
       }
-    } else if (kScales != kWide) {
+    } else {
       const int64_t n1 = n0 + wn * 128;
       ahead.w_scales += ((n1 < p.n ? n1 : p.n - 1) / 128 * p.ld_ws + t.kb0) * kScaleBytes;
     }
   };
   const auto request = [&]() __attribute__((always_inline)) {
-    if (kScales == kWide) return;
 #pragma unroll
     for (int i = 0; i < kCodes; ++i)
       xc_next[i] = *reinterpret_cast<const uint16_t*>(ahead.x_codes + static_cast<uint64_t>(xc_off[i]));
@@ -912,15 +911,7 @@ __global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
                   i = decltype(x_half)::value * HM + decltype(row)::value;
 #pragma unroll
     for (int j = wh; j < wh + 4; ++j) {
-      if constexpr (kScales == kWide) {
-        const int8v a = wv[j], b = xv[i];
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, a, 0, 1, 2, 3)),
-            __builtin_bit_cast(bf16x8, __builtin_shufflevector(b, b, 0, 1, 2, 3)), acc[i][j], 0, 0, 0);
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, a, 4, 5, 6, 7)),
-            __builtin_bit_cast(bf16x8, __builtin_shufflevector(b, b, 4, 5, 6, 7)), acc[i][j], 0, 0, 0);
-      } else if constexpr (kScales == kBlockF32) {
+      if constexpr (kScales == kBlockF32) {
         const floatx4 sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
             wv[j], xv[i], (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep,
             static_cast<int>(xc[i]));
@@ -1098,17 +1089,24 @@ __global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 }
 
-// The splits' sums, in their order.
-__global__ __launch_bounds__(256) void join_kernel(const float* part, int32_t splits, int64_t m,
-                                                   int64_t n, void* y, int64_t ldy, bool y_bf16) {
-  const int64_t total = m * n;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    float s = part[i];
-    for (int32_t k = 1; k < splits; ++k) s += part[k * total + i];
-    const int64_t row = i / n, at = row * ldy + (i - row * n);
-    if (y_bf16) static_cast<uint16_t*>(y)[at] = to_bf16_rne(s);
-    else static_cast<float*>(y)[at] = s;
+// The splits' sums, in their order. Only outputs of fewer than 128 tiles are
+// split: m * n fits 32 bits.
+template <int kEach>
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int32_t splits, uint32_t total,
+                                                   uint32_t n, void* y, int64_t ldy, bool y_bf16) {
+  typedef float values __attribute__((ext_vector_type(kEach)));
+  for (uint32_t i = (blockIdx.x * 256 + threadIdx.x) * kEach; i < total; i += gridDim.x * 256 * kEach) {
+    values s = *reinterpret_cast<const values*>(part + i);
+#pragma unroll 4
+    for (int32_t k = 1; k < splits; ++k)
+      s += *reinterpret_cast<const values*>(part + static_cast<int64_t>(k) * total + i);
+    const uint32_t row = i / n;
+    const int64_t at = row * ldy + (i - row * n);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (y_bf16) static_cast<uint16_t*>(y)[at + e] = to_bf16_rne(s[e]);
+      else static_cast<float*>(y)[at + e] = s[e];
+    }
   }
 }
 
@@ -1452,7 +1450,17 @@ struct Plan {
 
 constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 
-// Tiles and splits of a product of m x n outputs over kb blocks.
+// Tiles and splits of a product of m x n outputs over kb blocks. Measured, us
+// for m x n x k with bf16 results (fp32 ones alike):
+//   large tiles from 192 of them on (4096 x 15360 x 3840: 227, 128 x 128 tiles
+//   320; below, a third of the CUs or more would stand idle);
+//   one split from 128 tiles on (512 x 4096 x 2048, 128 tiles: 17, four splits
+//   32; 512 x 2048 x 4096, 64 tiles: 28 with one, 26 with four), and with up
+//   to eight blocks from 64 on (256 x 4096 x 1024: 13, with four 17): a step
+//   takes less than joining;
+//   else splits for 256 blocks, or 512 of the tiles of 32 rows, of which four
+//   fit a CU (61 x 3840 x 15360, 30 tiles of 64: 22.5 with 8, 23.3 with 15;
+//   20 x 4096 x 4096: 16.6 with 8, 14.9 with 16).
 Plan plan_of(int64_t m, int64_t n, int64_t kb, bool exact) {
   Plan q;
   const int64_t big = ((m + kBigM - 1) / kBigM) * ((n + kBigN - 1) / kBigN);
@@ -1461,7 +1469,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t kb, bool exact) {
   else if (!exact && big >= 192) q.bm = kBigM, q.bn = kBigN;
   else q.bm = 128, q.bn = 128;
   const int64_t tiles = ((m + q.bm - 1) / q.bm) * ((n + q.bn - 1) / q.bn);
-  int64_t splits = tiles >= 192 ? 1 : 512 / tiles;
+  int64_t splits = tiles >= 128 || (tiles >= 64 && kb <= 8) ? 1 : (q.bm == 32 ? 512 : 256) / tiles;
   if (splits > kb / 4) splits = kb / 4;
   if (splits < 1) splits = 1;
   int64_t per = (kb + splits - 1) / splits;
@@ -1550,9 +1558,15 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   p.y_vec = n % whole == 0 && ldy % whole == 0 && aligned16(y);
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
   launch_kind(kind, p, q, !y_bf16, st);
-  if (q.splits > 1)
-    hipLaunchKernelGGL(join_kernel, dim3(some_blocks((m * n + 255) / 256)), dim3(256), 0, st, part,
-                       q.splits, m, n, y, ldy, y_bf16);
+  if (q.splits > 1) {
+    const uint32_t total = static_cast<uint32_t>(m * n), cols = static_cast<uint32_t>(n);
+    if (n % 4 == 0)
+      hipLaunchKernelGGL(join_kernel<4>, dim3(some_blocks((total / 4 + 255) / 256)), dim3(256), 0, st, part,
+                         q.splits, total, cols, y, ldy, y_bf16);
+    else
+      hipLaunchKernelGGL(join_kernel<1>, dim3(some_blocks((total + 255) / 256)), dim3(256), 0, st, part,
+                         q.splits, total, cols, y, ldy, y_bf16);
+  }
   return launch_status();
 }
 
