@@ -438,6 +438,18 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t
 // every bank once; the swizzle is in the addresses that the lanes load from.
 // The weights are the instruction's first operand: a lane's four results lie
 // side by side in a row of y.
+// Every variant is held to two waves a SIMD (256 registers): the few that took
+// more by themselves lost more from waiting alone than from what they spill
+// (2048 x 4096 x 4096 with fp32 results and scales 108 -> 87 us, experts of
+// 4096 x 8 pairs alike 387 -> 257 us).
+// Exact products convert both operands beside the matrix instructions: 15360 x
+// 3840 x 8192 (a weight's gradient) 0.83 to 0.93 ms, 1.04 to 1.16 PFLOP/s,
+// against 1.6 of a large bf16 library product (tiles of 256 rows, a wave's 128
+// or 64 of them: 1.13 and 0.97 ms). With experts and few blocks of
+// K the ends of the tiles count: 32768 pairs of 128 experts, 2816 x 704, 164 us
+// of which 36 go without the stores and 41 without the weights' loads, for 513
+// MB (101 us at a copy's rate). Runs of two to six tiles a block, the next
+// one's loads under way over an end, spill and take 157 to 161 us.
 // Experts' tiles: an XCD's share of the places (p.mt), in columns of eight.
 __device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, int32_t& nt) {
   const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
@@ -733,6 +745,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
 // during the first two. A barrier before the first and the third quarter says
 // that a half has arrived and that the one read last may be loaded again, with
 // what is read six quarters (2304 cycles) later.
+// 4096 x 15360 x 3840: 218 us, 2.2 PFLOP/s, 70% of a large library product's
+// rate; a step takes 1.12 us, of which the matrix instructions alone 0.71: reads
+// of LDS and loads into it contend for it.
 // A block takes tiles one after the other, and its loads run over their ends:
 // the last steps of a tile load the first ones of the next, and the results
 // are on their way to memory while that one runs. (With a block a tile, its
@@ -1090,7 +1105,7 @@ __global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
 }
 
 // The splits' sums, in their order. Only outputs of fewer than 128 tiles are
-// split: m * n fits 32 bits.
+// split: m * n fits 32 bits. 8 splits of 61 x 3840: 3.0 us, the launch itself.
 template <int kEach>
 __global__ __launch_bounds__(256) void join_kernel(const float* part, int32_t splits, uint32_t total,
                                                    uint32_t n, void* y, int64_t ldy, bool y_bf16) {
@@ -1117,7 +1132,9 @@ __global__ __launch_bounds__(256) void zero_kernel(uint32_t* p, int64_t words) {
 }
 
 // ------------------------------------------------------------ few-row product
-// Up to 16 rows of x at a time: what counts is reading the weights. A block
+// Up to 16 rows of x at a time: what counts is reading the weights (15360 x
+// 3840, one row: 16.3 us, 3.6 TB/s, of which the launch and the ends about 5;
+// 64 pairs of 128 experts, 704 x 2816: 22 us, 5.1 TB/s). A block
 // has 16 NR rows of w; its waves take blocks of 128 columns in turn, weights
 // and rows of x straight into the operands' registers (lane: row l % 16,
 // columns 16 q .. and 64 + 16 q ..; x in the same order), x quantised there.
@@ -1279,6 +1296,10 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
 // quantise the rows meanwhile. Tiles lie as the product's blocks take them: an
 // eighth for each XCD, with its share of the tiles that have an expert,
 // connected, then its share of the others (expert -1: zeros), then none (-2).
+// (With tiles numbered through, the last XCDs have few that are in use: 32768
+// pairs of 128 experts 204 us instead of 164.)
+// 32768 pairs take 26 us, a chain of loads, LDS atomics and sums over experts
+// that the rows' quantising (46 MB) hides about half of.
 struct SortArgs {
   const int32_t* idx;
   int32_t pairs, n_experts, bm, share;   // share: places of tiles of an XCD
@@ -1452,8 +1473,8 @@ constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 
 // Tiles and splits of a product of m x n outputs over kb blocks. Measured, us
 // for m x n x k with bf16 results (fp32 ones alike):
-//   large tiles from 192 of them on (4096 x 15360 x 3840: 227, 128 x 128 tiles
-//   320; below, a third of the CUs or more would stand idle);
+//   large tiles from 192 of them on (4096 x 15360 x 3840: 241, 128 x 128 tiles
+//   285; below, more than a quarter of the CUs would stand idle);
 //   one split from 128 tiles on (512 x 4096 x 2048, 128 tiles: 17, four splits
 //   32; 512 x 2048 x 4096, 64 tiles: 28 with one, 26 with four), and with up
 //   to eight blocks from 64 on (256 x 4096 x 1024: 13, with four 17): a step

@@ -13,6 +13,11 @@
 // in the key's other half, so that ties are settled too. The slots' experts
 // are found by their values: a lane looks for its own among the sorted ones.
 //
+// Bound by vector instructions: 1346 for four rows of 256 experts (16 scores, a
+// sort of 16 and four merges of eight a lane, groups, the checks of gaps);
+// 65536 rows 63 us, of which 71 MB are 14. Three waves a SIMD instead of two
+// (168 registers, with spills) take as long.
+//
 // Scores relative to the row's largest: sigmoid(x) = exp(min(x, 0)) / (1 +
 // exp(-|x|)), and quotients of scores do not change when exp(min(x, 0)) is
 // taken as exp(min(x, 0) - c) with c = min(0, the largest x); so neither sums
@@ -591,7 +596,8 @@ struct ScoredGradArgs {
 // expert's slots and f the loss's share: the weights give t (u - h sum u t) or
 // s u, the loss q (f - sum f q), each times 1 - s for a sigmoid; a softmax that
 // is not renormalised p (u - sum u p). The slots' gradients reach their
-// experts' lanes through rows of LDS, as in moe_route.hip.
+// experts' lanes through rows of LDS, as in moe_route.hip. 65536 rows of 256
+// experts: 43 us for 138 MB, 27 of them at a copy's rate.
 template <int G, int V, bool kBf16, bool kOutBf16>
 __global__ __launch_bounds__(256) void scored_grad_kernel(ScoredGradArgs p) {
   constexpr int kRows = 64 / G, kExperts = G * V, kHeld = kMaxTopK / G;

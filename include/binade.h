@@ -620,7 +620,8 @@ int32_t binade_moe_route_grad(const void *logits, int32_t dtype, int64_t ld,
  *   s[e] = sigmoid(logits[t, e]), or softmax(logits[t])[e];
  *   v[e] = s[e] + bias[e] (bias: device fp32 [n_experts]; it moves load
  *   between experts and has no part in the weights or gradients), in fp64.
- *   Without bias (NULL) the order of the logits is v's;
+ *   Without bias (NULL, or zeros alone) the order of the logits is v's, also
+ *   where two scores round to one number;
  *   groups: the experts in that many equal runs; a group's score is the sum
  *   of its group_best (1 or 2) largest v, or its one v where no other of it
  *   can be taken; only experts of the top_groups groups of largest score,
@@ -766,9 +767,11 @@ int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *             of 4]; entries behind the last block are not used
  *   values_t, scales_t   the same of the transposed matrices [cols, rows],
  *             for binade_f8_gemm_grad's dx; or NULL
- * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. cols % 32 == 0, rows
- * and cols at most 2^22, count at most 65535; planes 16-byte aligned, else
- * BINADE_EUNSUPPORTED. */
+ * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. Products that are
+ * called exact below take a weight with a power of two as bf16 holds it: under
+ * 2^-133 (codes 0 to 2) rounded to its steps, over its largest (codes from 247
+ * on) infinite. cols % 32 == 0, rows and cols at most 2^22, count at most
+ * 65535; planes 16-byte aligned, else BINADE_EUNSUPPORTED. */
 typedef struct binade_f8 {
   int64_t rows, cols;
   int32_t count, scale_dtype;
@@ -861,7 +864,9 @@ int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  * not NULL) and counts as -1. Each used expert is read about once (once for
  * each 128 of its pairs); arithmetic as in binade_f8_gemm, exact products up
  * to 256 pairs; a pair's result does not depend on the other pairs' order.
- * top_k in 1..64, count at most 4096, n_tokens * top_k at most 2^24.
+ * top_k in 1..64, count at most 4096, n_tokens * top_k at most 2^24, pairs * N
+ * at most 2^36 and 2^23 tiles of outputs, else EUNSUPPORTED. Experts that are
+ * trained take binade_f8_gemm_grad of their own rows, expert by expert.
  * workspace: binade_f8_moe_workspace_bytes (0 for few pairs). */
 int32_t binade_f8_moe_gemm(const binade_f8 *experts, const uint16_t *x,
                            int64_t ldx, int32_t x_per_slot,

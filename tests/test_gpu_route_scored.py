@@ -333,3 +333,26 @@ def test_bad_index_strides_and_repeats():
     idx[5, 1] = idx[6, 2] = -1
     ref, big = ref_grad(x, idx, dw, None, 0.0, True, "sigmoid", 2.0)
     assert torch.all((d - ref).abs() <= (8 * 16 + 128) * U * big + 1e-38)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_no_tokens(score):
+    E = 24
+    none = torch.empty(0, E, device=DEV)
+    r = B.moe_route(none, 3, score=score, bias=torch.ones(E, device=DEV), groups=4, top_groups=2)
+    assert r.idx.shape == (0, 3) and not bool(r.counts.any()) and not bool(r.prob_sum.any()) and float(r.loss) == 0
+    d = B.moe_route_grad(none, r.idx, counts=r.counts, dloss=torch.ones(1, device=DEV), score=score, scale=2.0)
+    assert d.shape == (0, E)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(700, 60, 4), (5000, 256, 8), (90, 1024, 20)])
+def test_gradient_over_the_logits_themselves(T, E, k, score):
+    x = make(T, E, 3, F32).to(DEV)
+    r = B.moe_route(x, k, score=score, scale=1.5)
+    dw, one = torch.randn(T, k, generator=gen(4)).to(DEV), torch.ones(1, device=DEV)
+    args = dict(dweights=dw, counts=r.counts, dloss=one, score=score, scale=1.5)
+    want = B.moe_route_grad(x, r.idx, **args)
+    over = x.clone()
+    assert B.moe_route_grad(over, r.idx, dlogits=over, **args) is over
+    assert torch.equal(over, want)
