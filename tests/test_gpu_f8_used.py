@@ -504,3 +504,65 @@ def test_bindings_refuse():
     odd = torch.zeros(4, 70, dtype=BF, device=DEV)
     odd[:, 3:67] = x
     assert torch.equal(B.f8_gemm(odd[:, 3:67], w), B.f8_gemm(x, w))
+
+
+# ------------------------------------------------------------- far offsets
+@pytest.mark.parametrize("m,n,k,out", [(1 << 20, 16, 4224, BF), (1 << 20, 16, 4224, F32), (1 << 20, 4200, 32, F32)])
+def test_rows_past_32_bits_of_bytes(m, n, k, out):
+    """Rows that repeat: every period's results are those of the first rows alone."""
+    say("far rows", m, n, k, out)
+    base = whole(4096, k, 1)
+    v, s = whole_w(1, n, k, 2)
+    w = B.f8_weight(v.to(DEV), s.to(DEV))
+    want = (base.double() @ dense(v, s).T).to(out).to(DEV)
+    x = base.to(DEV).repeat(m // 4096, 1)
+    assert x.numel() * 2 > 1 << 32 or m * n * 4 > 1 << 32
+    y = B.f8_gemm(x, w, out_dtype=out).view(-1, 4096, n)
+    assert all(torch.equal(y[i], want) for i in range(y.shape[0]))
+
+
+def test_gradients_past_32_bits_of_bytes():
+    m, n, k = 1 << 20, 32, 4224
+    base, dyb = whole(4096, k, 1, 1), whole(4096, n, 2, 1)
+    v, s = whole_w(1, n, k, 3)
+    w = B.f8_weight(v.to(DEV), s.to(DEV), train=True)
+    x, dy = base.to(DEV).repeat(m // 4096, 1), dyb.to(DEV).repeat(m // 4096, 1)
+    dx, dw = B.f8_gemm_grad(x, w, dy)
+    want = (dyb.double() @ dense(v, s)).to(BF).to(DEV)
+    assert all(torch.equal(part, want) for part in dx.view(-1, 4096, k))
+    assert torch.equal(dw.cpu(), ((dyb.double().T @ base.double()) * (m // 4096)).float())   # below 2^24
+
+
+def test_experts_past_32_bits_of_bytes():
+    E, n, k = 280, 4096, 4096
+    few = torch.randint(-4, 5, (7, n, k), generator=gen(1)).float().to(E4M3).view(torch.uint8).to(DEV)
+    v = few.repeat(E // 7, 1, 1)
+    s = torch.full((E, n // 128, k // 128), 127, dtype=torch.uint8, device=DEV)
+    w = B.f8_weight(v, s)
+    del v
+    one = [B.f8_weight(few[e], s[e]) for e in range(7)]
+    for tokens in (4, 300):
+        x = whole(tokens, k, 2, 1).to(DEV)
+        idx = torch.randint(E - 9, E, (tokens, 2), generator=gen(3)).int().to(DEV)
+        y = B.f8_moe_gemm(x, w, idx).view(tokens, 2, n)
+        for e in range(7):
+            mine = B.f8_gemm(x, one[e])
+            for slot in range(2):
+                at = idx[:, slot] % 7 == e
+                assert torch.equal(y[:, slot][at], mine[at])
+
+
+def test_one_pair_more_than_the_registers_hold():
+    """32768 pairs stay in registers while they are sorted, more are read twice."""
+    E, n, k = 50, 32, 32
+    v, s = whole_w(E, n, k, 1)
+    wd = dense(v, s)
+    w = B.f8_weight(v.to(DEV), s.to(DEV))
+    for pairs in (32767, 32768, 32769, 50001):
+        x = whole(pairs, k, 2)
+        idx = torch.randint(-1, E, (pairs, 1), generator=gen(pairs)).int()
+        y = B.f8_moe_gemm(x.to(DEV), w, idx.to(DEV))
+        pick = wd[idx.flatten().clamp(min=0).long()]
+        want = torch.bmm(pick, x.double().unsqueeze(-1)).squeeze(-1)
+        want[idx.flatten() < 0] = 0
+        assert torch.equal(y.cpu(), want.float()), pairs
