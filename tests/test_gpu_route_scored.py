@@ -356,3 +356,28 @@ def test_gradient_over_the_logits_themselves(T, E, k, score):
     over = x.clone()
     assert B.moe_route_grad(over, r.idx, dlogits=over, **args) is over
     assert torch.equal(over, want)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,groups,top,best", [(64, 8, 8, 3, 2), (256, 8, 8, 4, 2), (60, 4, 6, 2, 1), (128, 12, 4, 2, 2),
+                                                 (32, 4, 1, 1, 2)])
+def test_special_biases_in_groups(E, k, groups, top, best, score):
+    """A bias that is infinite or NaN: +inf comes first (equal ones, and groups
+    that hold one, by rising number), -inf and NaN are never taken."""
+    g = gen(11)
+    for T, n_special in ((40, 1), (70, 5)):
+        x = make(T, E, 12, F32)
+        bias = torch.randn(E, generator=g) * 0.2
+        at = torch.randperm(E, generator=g)
+        bias[at[:n_special]] = INF
+        bias[at[n_special:2 * n_special]] = -INF
+        bias[at[2 * n_special:3 * n_special]] = math.nan
+        bias[at[3 * n_special]] = -math.nan
+        rule = dict(score=score, groups=groups, top_groups=top)
+        r = B.moe_route(x.to(DEV), k, bias=bias.to(DEV), group_best=best, **rule)
+        want = ref_choice(x, k, bias=bias, best=best, **rule)
+        idx = r.idx.cpu().tolist()
+        for t in range(T):
+            assert idx[t] == want[t] + [-1] * (k - len(want[t])), (t, idx[t], want[t])
+        assert torch.isfinite(r.weights).all()
+        assert int(r.counts[:E].sum()) == sum(len(w) for w in want)
