@@ -781,13 +781,22 @@ __global__ __launch_bounds__(256) void scored_grad_kernel(ScoredGradArgs p) {
 }
 
 // ------------------------------------------------------------------- hosts
-// Lanes a row, of 8 experts each up to 64 of them and 16 beyond.
-int32_t scored_lanes(int32_t n_experts) {
-  return n_experts <= 128 ? 8 : n_experts <= 256 ? 16 : n_experts <= 512 ? 32 : 64;
+// Experts a lane, and lanes a row. With few tokens the chain of one row's
+// instructions counts, and eight experts a lane make it shorter; with many
+// their number does: sixteen (more than 512 experts take a whole wave's). In a
+// graph, 8 of 256 fp32 experts in groups, us: one token 7.0 and 8.9, 256 of
+// them 7.8 and 9.7, 2049 9.5 and 15.5 (bf16 13.6 and 10.1), 4096 13.6 and 10.2.
+constexpr int64_t kFewTokens = 512;
+int32_t scored_each(int64_t n_tokens, int32_t n_experts) {
+  return n_experts <= 64 || (n_experts <= 512 && n_tokens <= kFewTokens) ? 8 : 16;
+}
+int32_t scored_lanes(int64_t n_tokens, int32_t n_experts) {
+  const int32_t held = 8 * scored_each(n_tokens, n_experts);   // of the fewest lanes
+  return n_experts <= held ? 8 : n_experts <= 2 * held ? 16 : n_experts <= 4 * held ? 32 : 64;
 }
 
 uint32_t scored_blocks(int64_t n_tokens, int32_t n_experts) {
-  const int64_t rows = kWavesABlock * (64 / scored_lanes(n_experts));
+  const int64_t rows = kWavesABlock * (64 / scored_lanes(n_tokens, n_experts));
   const int64_t b = (n_tokens + rows - 1) / rows;
   return static_cast<uint32_t>(b < 1 ? 1 : b > kScoredBlocks ? kScoredBlocks : b);
 }
@@ -876,7 +885,7 @@ extern "C" int32_t binade_moe_route_scored(const void* logits, int32_t dtype, in
   a.group_size = n_experts / rule->groups;
   a.top_groups = rule->top_groups;
   a.group_best = rule->group_best;
-  const int32_t lanes = scored_lanes(n_experts), each = n_experts <= 64 ? 8 : 16;
+  const int32_t lanes = scored_lanes(n_tokens, n_experts), each = scored_each(n_tokens, n_experts);
   const int32_t whole = a.group_size % each == 0 ? a.group_size / each : 0;
   a.lanes_a_group = (whole & (whole - 1)) == 0 ? whole : 0;
   a.parts = 1;
@@ -884,11 +893,17 @@ extern "C" int32_t binade_moe_route_scored(const void* logits, int32_t dtype, in
   a.scale = rule->scale;
   a.sigmoid = rule->score == BINADE_SIGMOID;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (n_experts <= 64) launch_scored<8, 8>(a, blocks, bf16, st);
-  else if (n_experts <= 128) launch_scored<8, 16>(a, blocks, bf16, st);
-  else if (n_experts <= 256) launch_scored<16, 16>(a, blocks, bf16, st);
-  else if (n_experts <= 512) launch_scored<32, 16>(a, blocks, bf16, st);
-  else launch_scored<64, 16>(a, blocks, bf16, st);
+  if (each == 8) {
+    if (lanes == 8) launch_scored<8, 8>(a, blocks, bf16, st);
+    else if (lanes == 16) launch_scored<16, 8>(a, blocks, bf16, st);
+    else if (lanes == 32) launch_scored<32, 8>(a, blocks, bf16, st);
+    else launch_scored<64, 8>(a, blocks, bf16, st);
+  } else {
+    if (lanes == 8) launch_scored<8, 16>(a, blocks, bf16, st);
+    else if (lanes == 16) launch_scored<16, 16>(a, blocks, bf16, st);
+    else if (lanes == 32) launch_scored<32, 16>(a, blocks, bf16, st);
+    else launch_scored<64, 16>(a, blocks, bf16, st);
+  }
   if (stats && blocks > 1)
     hipLaunchKernelGGL(route_stats_kernel, dim3(static_cast<uint32_t>((n_experts + 63) / 64)),
                        dim3(1024), 0, st, p, static_cast<int32_t>(blocks));

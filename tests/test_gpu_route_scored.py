@@ -381,3 +381,46 @@ def test_special_biases_in_groups(E, k, groups, top, best, score):
             assert idx[t] == want[t] + [-1] * (k - len(want[t])), (t, idx[t], want[t])
         assert torch.isfinite(r.weights).all()
         assert int(r.counts[:E].sum()) == sum(len(w) for w in want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups,best", [
+    (513, 128, 6, 8, 3, 2), (600, 256, 8, 8, 4, 2), (520, 300, 10, 3, 2, 1), (700, 512, 8, 16, 4, 2),
+    (515, 160, 16, 8, 3, 1), (1000, 65, 5, 5, 2, 2), (512, 512, 33, 8, 6, 2), (530, 96, 8, 1, 1, 2)])
+def test_route_of_many_tokens(T, E, k, groups, top_groups, best, score, dtype):
+    """From 513 tokens on a lane has sixteen experts instead of eight: rows that
+    repeat, against the first ones by the formulas; plain values, and ties."""
+    say("many", T, E, k, groups, top_groups, best, score, dtype)
+    rows = 43
+    times = -(-T // rows)
+    valid = torch.rand(rows, generator=gen(2)) < 0.9
+    coarse = (torch.rand(E, generator=gen(3)) * 4).round() / 4
+    for b, ties in ((torch.randn(E, generator=gen(1)) * 0.2, False), (None, False), (coarse, True)):
+        x = make(rows, E, T + E, dtype, closed=E // 9, coarse=ties)
+        rule = dict(score=score, groups=groups, top_groups=top_groups)
+        r = B.moe_route(x.repeat(times, 1).to(DEV), k, bias=None if b is None else b.to(DEV),
+                        valid=valid.repeat(times).to(DEV), group_best=best, scale=2.5, **rule)
+        idx, w, counts, ps, loss = ref_route(x, k, True, 2.5, valid, bias=b, best=best, **rule)
+        assert torch.equal(r.idx.cpu().long(), idx.repeat(times, 1))
+        fin = torch.where(x > -INF, x, 0.0).double()
+        tol = (4 * (float((fin.amax(1) - fin.amin(1)).max()) + float(fin.abs().max())) + 64) * U
+        assert torch.all((r.weights.cpu().double() - w.repeat(times, 1)).abs() <= tol * w.abs().repeat(times, 1) + 1e-37)
+        assert torch.equal(r.counts.cpu().long(), counts * times)
+        assert torch.all((r.prob_sum.cpu().double() - ps * times).abs() <= (tol + 64 * U) * ps * times + 1e-37)
+        assert abs(float(r.loss) - loss) <= (tol + 64 * U) * loss + 1e-37
+
+
+def test_near_ties_of_many_tokens():
+    """Row by row the same choice as of few tokens, where neighbours' scores
+    differ by less than fp32 resolves."""
+    E, k = 256, 8
+    base = torch.randn(90, 1, generator=gen(5)) + torch.randint(0, 40, (90, E), generator=gen(6)) * 2.0 ** -22
+    x = base.to(DEV)
+    bias = (torch.randint(0, 3, (E,), generator=gen(7)) * 2.0 ** -24).to(DEV)
+    rule = dict(score="sigmoid", groups=8, top_groups=4)
+    few = B.moe_route(x, k, bias=bias, **rule)
+    many = B.moe_route(x.repeat(7, 1), k, bias=bias, **rule)
+    assert torch.equal(many.idx.view(7, 90, k), few.idx.expand(7, 90, k))
+    want = ref_choice(base, k, bias=bias.cpu(), best=2, **rule)
+    assert few.idx.cpu().tolist() == want
