@@ -1430,8 +1430,7 @@ def _f8_arg(w: F8Weight, device):
 def f8_gemm(x: torch.Tensor, w: F8Weight, out_dtype=torch.float32, y: torch.Tensor | None = None,
             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """binade_f8_gemm: Q(x) W^T of bf16 x [m, K], x quantised in blocks of 128
-    along K. A bf16 result of more than 16 rows takes the 8-bit matrix
-    instruction, an fp32 one exact products at half its rate."""
+    along K, summed in fp32; a bf16 result is that sum rounded once."""
     code = _dtype_code(out_dtype)
     dev = x.device
     d = _f8_arg(w, dev)

@@ -31,17 +31,12 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-Wall", "-Wno-unused-function",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
-# f8.hip: accumulators of matrix instructions in vector registers, so that the
-# operands alone use the accumulation registers; with the sums there, the large
-# tile's loop has 208 register copies for its 96 matrix instructions.
-EXTRA = {"f8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
-
 
 def _compile(src: str) -> str:
     path = os.path.join(CSRC, src)
     obj = os.path.join(OUT, src + ".o")
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    cmd = [HIPCC] + FLAGS + EXTRA.get(src, []) + lang + ["-c", path, "-o", obj]
+    cmd = [HIPCC] + FLAGS + lang + ["-c", path, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stderr}")

@@ -3,20 +3,18 @@
 // of the experts that a router chose.
 //
 // A block's scale is a power of two for everything that is quantised here, so
-// that v 2^-e is exact and the only rounding is the one to e4m3; it is also
-// what the matrix instruction takes beside its operands (one code for 32
-// values: four times the same). Weights of a checkpoint may come with any
-// fp32 scale for 128 x 128 values: then each block's 128 columns are summed
-// from zero and added with one fma.
+// that v 2^-e is exact and the only rounding is the one to e4m3. Weights of a
+// checkpoint may come with any fp32 scale for 128 x 128 values: then each
+// block's 128 columns are summed from zero and added with one fma.
 //
-// Two matrix instructions. The 8-bit one (16x16x128) runs at twice the rate
-// of the bf16 one, but adds each eight products after cutting them to about
-// 13 bits below the largest: measured, 1.4e-5 of the result's norm for normal
-// data, 5e-5 for values spread over the whole range. A bf16 output rounds to
-// 1.7e-3 and takes it. An fp32 output does not: there the operands (e4m3 times
-// a power of two is exact in bf16) go through v_mfma_f32_16x16x32_bf16, whose
-// products are exact and whose sums are fp32's. So do the few-row kernels, at
-// either type, which wait for the weights anyway.
+// The operands (e4m3 times a power of two is exact in bf16) go through
+// v_mfma_f32_16x16x32_bf16, whose products are exact and whose sums are fp32's.
+// The instructions on 8-bit operands are not used: they add eight products
+// after cutting them to 13 bits below the largest (1.4e-5 of the result's norm
+// for normal data, 5e-5 for values spread over the whole range, where this one
+// has 1e-8 and 8e-8; up to 2% of the results round to another bf16). The one
+// of 16x16x128 would run at twice the rate (4.3 against 2.3 PFLOP/s), the one
+// of 16x16x32, which cuts alike, at the same.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -430,6 +428,17 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t
   }
 }
 
+// Experts' tiles: an XCD's share of the places (p.mt), in columns of eight.
+__device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, int32_t& nt) {
+  const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+  constexpr int32_t kGroup = 8;
+  const int32_t group = local / (kGroup * p.nt), first = group * kGroup;
+  const int32_t high = p.mt - first < kGroup ? p.mt - first : kGroup;
+  const int32_t at = local - group * kGroup * p.nt;
+  mt = xcd * p.mt + first + at % high;
+  nt = at / high;
+}
+
 // y = x w^T on tiles of BM x BN by WM x WN waves. A step is one block of 128
 // columns: its BM + BN rows of 128 bytes go straight to LDS, one step ahead of
 // their use, into two buffers (named arrays: the compiler then sees that reads
@@ -442,26 +451,16 @@ __device__ __forceinline__ void store4(const GemmArgs& p, int32_t split, int64_t
 // more by themselves lost more from waiting alone than from what they spill
 // (2048 x 4096 x 4096 with fp32 results and scales 108 -> 87 us, experts of
 // 4096 x 8 pairs alike 387 -> 257 us).
-// Exact products convert both operands beside the matrix instructions: 15360 x
-// 3840 x 8192 (a weight's gradient) 0.83 to 0.93 ms, 1.04 to 1.16 PFLOP/s,
-// against 1.6 of a large bf16 library product (tiles of 256 rows, a wave's 128
-// or 64 of them: 1.13 and 0.97 ms). With experts and few blocks of
-// K the ends of the tiles count: 32768 pairs of 128 experts, 2816 x 704, 164 us
-// of which 36 go without the stores and 41 without the weights' loads, for 513
-// MB (101 us at a copy's rate). Runs of two to six tiles a block, the next
-// one's loads under way over an end, spill and take 157 to 161 us.
-// Experts' tiles: an XCD's share of the places (p.mt), in columns of eight.
-__device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, int32_t& nt) {
-  const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
-  constexpr int32_t kGroup = 8;
-  const int32_t group = local / (kGroup * p.nt), first = group * kGroup;
-  const int32_t high = p.mt - first < kGroup ? p.mt - first : kGroup;
-  const int32_t at = local - group * kGroup * p.nt;
-  mt = xcd * p.mt + first + at % high;
-  nt = at / high;
-}
-
-template <int BM, int BN, int WM, int WN, bool kExact, int kScales, bool kExperts>
+// Bound by vector instructions beside the matrix ones: both operands become
+// bf16 here, two conversions for each matrix instruction of a wave's 64 x 64,
+// 3.7 instructions with everything. Two are hidden behind a matrix instruction
+// (7.2 ns a slot of a SIMD with one, 7.8 with two, 11.4 with four). 4096 x
+// 15360 x 3840: 388 us, 1.25 PFLOP/s; 15360 x 3840 x 8192 (a weight's gradient)
+// 0.83 to 0.93 ms, 1.04 to 1.16; a large bf16 library product has 1.6 (tiles of
+// 256 rows, a wave's 128 or 64 of them: 1.13 and 0.97 ms). With experts and few
+// blocks of K the ends of the tiles count too: runs of two to six tiles a
+// block, the next one's loads under way over an end, spill and gain nothing.
+template <int BM, int BN, int WM, int WN, int kScales, bool kExperts>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
   constexpr int kWaves = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int kXLoads = BM / 8 / kWaves, kWLoads = BN / 8 / kWaves;
@@ -592,76 +591,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
     constexpr int kStep = decltype(step)::value;
     const uint8_t* xb = buf + wm * TM * 128;
     const uint8_t* wb = buf + (BM + wn * TN) * 128;
-    if (kExact) {
-      bf16x8 wv[FN][4];
+    bf16x8 wv[FN][4];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int8v v = operand(wb + j * 2048);
+      const uint32_t c = kScales == kBlockF32 ? 127u : (wc[kScales == kRowCode ? j : 0] >> (8 * kStep)) & 255u;
+      const float s = kScales == kBlockCode ? scale_of_any_code(c) : scale_of_code(c);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) wv[j][h] = from_f8(v[2 * h], v[2 * h + 1], s);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int8v v = operand(xb + i * 2048);
+      const float s = scale_of_code((xc[i] >> (8 * kStep)) & 255u);
+      bf16x8 xv[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) xv[h] = from_f8(v[2 * h], v[2 * h + 1], s);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int8v v = operand(wb + j * 2048);
-        const uint32_t c = kScales == kBlockF32 ? 127u
-                                                : (wc[kScales == kRowCode ? j : 0] >> (8 * kStep)) & 255u;
-        const float s = kScales == kBlockCode ? scale_of_any_code(c) : scale_of_code(c);
+        floatx4 sum = kScales == kBlockF32 ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) wv[j][h] = from_f8(v[2 * h], v[2 * h + 1], s);
-      }
+        for (int h = 0; h < 4; ++h)
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j][h], xv[h], sum, 0, 0, 0);
+        if (kScales == kBlockF32) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int8v v = operand(xb + i * 2048);
-        const float s = scale_of_code((xc[i] >> (8 * kStep)) & 255u);
-        bf16x8 xv[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) xv[h] = from_f8(v[2 * h], v[2 * h + 1], s);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          floatx4 sum = kScales == kBlockF32 ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[j][h], xv[h], sum, 0, 0, 0);
-          if (kScales == kBlockF32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(wf[kStep], sum[e], acc[i][j][e]);
-          } else {
-            acc[i][j] = sum;
-          }
-        }
-      }
-    } else {
-      int8v wv[FN];
-      floatx4 sum[2][FN], last_sum[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) wv[j] = operand(wb + j * 2048);
-#pragma unroll
-      for (int i = 0; i < (kScales == kBlockF32 ? FM : 0); ++i) {
-        // a row's products while the ones before are scaled and added
-        const int8v xv = operand(xb + i * 2048);
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          sum[i % 2][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              wv[j], xv, (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep, static_cast<int>(xc[i]));
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (i > 0) acc[i - 1][j][e] = __builtin_fmaf(wf[kStep], sum[(i + 1) % 2][j][e], acc[i - 1][j][e]);
-            if (i == FM - 1) last_sum[j] = sum[i % 2][j];
-          }
-      }
-      if (kScales == kBlockF32) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[FM - 1][j][e] = __builtin_fmaf(wf[kStep], last_sum[j][e], acc[FM - 1][j][e]);
-      }
-#pragma unroll
-      for (int i = 0; i < (kScales == kBlockF32 ? 0 : FM); ++i) {
-        const int8v xv = operand(xb + i * 2048);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          {
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wv[j], xv, acc[i][j], 0, 0, kStep, static_cast<int>(wc[kScales == kRowCode ? j : 0]), kStep,
-                static_cast<int>(xc[i]));
-          }
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(wf[kStep], sum[e], acc[i][j][e]);
+        } else {
+          acc[i][j] = sum;
         }
       }
     }
@@ -729,379 +685,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
       for (int j = 0; j < FN; ++j) store4(p, split, y_row, col0 + j * 16 + q * 4, acc[i][j]);
     }
   }
-}
-
-// The same on tiles of 192 x 256 by four waves of 96 x 128, one on each SIMD,
-// for products that fill the chip with them. A wave's step is 48 matrix
-// instructions (1536 cycles of the matrix unit) over six operands of x and
-// eight of the weights. They are taken in quarters of three by four, so that an
-// operand's registers are free early and are filled again for the next step
-// while other quarters run. With A and B the halves of the weights' operands
-// and a, b those of x, the quarters of an even and an odd step are
-//   aB aA bA bB  and  aA aB bB bA,
-// each sharing an operand half with its neighbours. A half step's rows (a and
-// the weights that begin; b and the others) have a buffer of their own: the
-// first is read during the last two quarters of the step before, the second
-// during the first two. A barrier before the first and the third quarter says
-// that a half has arrived and that the one read last may be loaded again, with
-// what is read six quarters (2304 cycles) later.
-// 4096 x 15360 x 3840: 218 us, 2.2 PFLOP/s, 70% of a large library product's
-// rate; a step takes 1.12 us, of which the matrix instructions alone 0.71: reads
-// of LDS and loads into it contend for it.
-// A block takes tiles one after the other, and its loads run over their ends:
-// the last steps of a tile load the first ones of the next, and the results
-// are on their way to memory while that one runs. (With a block a tile, its
-// start and end cost as much as ten of its steps.)
-constexpr int kBigM = 192, kBigN = 256;
-constexpr int32_t kBigBlocks = 256;   // one on each CU
-constexpr int kBigStores = 24;        // of a wave's whole tile, at least
-
-template <int kScales>
-__global__ __launch_bounds__(256, 1) void big_kernel(GemmArgs p) {
-  constexpr int kWaves = 4, FM = kBigM / 32, HM = FM / 2;
-  constexpr int kHalf = (kBigM + kBigN) / 2 * 128, kXUnits = kBigM / 16, kXLoads = kXUnits / kWaves;
-  // begin and rest of even and of odd steps: named arrays, see gemm_kernel
-  __shared__ __align__(16) uint8_t begin0[kHalf];
-  __shared__ __align__(16) uint8_t rest0[kHalf];
-  __shared__ __align__(16) uint8_t begin1[kHalf];
-  __shared__ __align__(16) uint8_t rest1[kHalf];
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4, wm = wave >> 1, wn = wave & 1;
-
-  // This block's tiles: as tile_of numbers them, an XCD's blocks side by side.
-  const int32_t tiles = p.mt * p.nt, work = tiles * p.splits;
-  const int32_t per = work / 8, more = work % 8, xcd = blockIdx.x % 8;
-  const int32_t stride = (static_cast<int32_t>(gridDim.x) + 7 - xcd) / 8;
-  const int32_t behind = xcd * per + (xcd < more ? xcd : more) + per + (xcd < more ? 1 : 0);
-  int32_t id = behind - per - (xcd < more ? 1 : 0) + blockIdx.x / 8;
-  if (id >= behind) return;
-  // steps come in pairs: behind an odd last one x is zeros, and w is read again
-  const int32_t end = (p.kb + 1) & ~1, last = p.kb - 1;
-
-  struct Tile {
-    int32_t mt, nt, split, kb0, kb1;
-  };
-  const auto tile_at = [&](int32_t at) __attribute__((always_inline)) {
-    Tile t;
-    t.split = at / tiles;
-    at -= t.split * tiles;
-    constexpr int32_t kGroup = 8;
-    const int32_t group = at / (kGroup * p.nt), first = group * kGroup;
-    const int32_t high = p.mt - first < kGroup ? p.mt - first : kGroup;
-    at -= group * kGroup * p.nt;
-    t.mt = first + at % high;
-    t.nt = at / high;
-    t.kb0 = t.split * p.per_split;
-    t.kb1 = t.kb0 + p.per_split < end ? t.kb0 + p.per_split : end;
-    return t;
-  };
-
-  // a load: eight rows of 128 bytes, unit by unit; a wave has every fourth
-  // unit. Offsets from a step's blocks on, of x and of the weights' two halves.
-  const int piece_row = lane >> 3;
-  const uint32_t piece = ((lane & 7) ^ ((wave * 4 + (piece_row >> 1)) & 7)) * 16;
-  uint32_t x_off[kXLoads], w_off[2][4];   // x's second half is kBigM / 4 rows further
-#pragma unroll
-  for (int i = 0; i < kXLoads; ++i) {
-    const int u = i * kWaves + wave;
-    x_off[i] = (u / (kXUnits / 2) * (kBigM / 2) + u % (kXUnits / 2) * 8 + piece_row) * 128 + piece;
-  }
-  // Loads kFrom .. kTo - 1 of a half's seven.
-  const auto stage = [&](uint8_t* buf, const uint8_t* x, const uint8_t* w, auto x_half, auto w_half,
-                         auto from, auto to) __attribute__((always_inline)) {
-    constexpr int xh = decltype(x_half)::value, wh = decltype(w_half)::value;
-#pragma unroll
-    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
-      to_lds(i < kXLoads ? x + xh * (kBigM / 4) * 128 + static_cast<uint64_t>(x_off[i < kXLoads ? i : 0])
-                         : w + static_cast<uint64_t>(w_off[wh][i < kXLoads ? 0 : i - kXLoads]),
-             buf + (i * kWaves + wave) * 1024);
-  };
-
-  // codes of two steps at once
-  constexpr int kCodes = FM, kRowCodes = kScales == kRowCode ? 8 : 1;
-  uint32_t xc[kCodes], xc_next[kCodes], wc[kRowCodes], wc_next[kRowCodes];
-  float wf[2], wf_next[2];
-  uint32_t xc_off[kCodes], wc_off[kRowCodes];
-#pragma unroll
-  for (int i = 0; i < kCodes; ++i) xc_off[i] = static_cast<uint32_t>((wm * (kBigM / 2) + i * 16 + r) * p.ld_xc);
-
-  // What is loaded next: two steps' blocks, codes and scales.
-  struct Ahead {
-    const uint8_t *x, *w, *x_codes, *w_scales;
-    int32_t kb, kb1;
-  } ahead;
-  constexpr int kScaleBytes = kScales == kBlockF32 ? 4 : 1;
-  const auto begin_tile = [&](const Tile& t) __attribute__((always_inline)) {
-    const int64_t m0 = static_cast<int64_t>(t.mt) * kBigM, n0 = static_cast<int64_t>(t.nt) * kBigN;
-    ahead.kb = t.kb0;
-    ahead.kb1 = t.kb1;
-    ahead.x = p.x + m0 * 128 + t.kb0 * p.x_block;
-    ahead.w = p.w + n0 * 128 + t.kb0 * p.w_block;
-    ahead.x_codes = p.x_codes + m0 * p.ld_xc + t.kb0;
-    const int32_t w_last = static_cast<int32_t>(p.n - 1 - n0);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = i * kWaves + wave;
-        const int32_t row = (u >> 3) * 128 + h * 64 + (u & 7) * 8 + piece_row;
-        w_off[h][i] = static_cast<uint32_t>((row < w_last ? row : w_last) * 128) + piece;
-      }
-    ahead.w_scales = static_cast<const uint8_t*>(p.w_scales);
-    if (kScales == kRowCode) {
-      ahead.w_scales += n0 * p.ld_ws + t.kb0;
-#pragma unroll
-      for (int j = 0; j < kRowCodes; ++j) {
-        const int32_t row = wn * 128 + j * 16 + r;
-        wc_off[j] = static_cast<uint32_t>((row < w_last ? row : w_last) * p.ld_ws);
-      }
-    } else {
-      const int64_t n1 = n0 + wn * 128;
-      ahead.w_scales += ((n1 < p.n ? n1 : p.n - 1) / 128 * p.ld_ws + t.kb0) * kScaleBytes;
-    }
-  };
-  const auto request = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kCodes; ++i)
-      xc_next[i] = *reinterpret_cast<const uint16_t*>(ahead.x_codes + static_cast<uint64_t>(xc_off[i]));
-    if (kScales == kRowCode) {
-#pragma unroll
-      for (int j = 0; j < kRowCodes; ++j)
-        wc_next[j] = *reinterpret_cast<const uint16_t*>(ahead.w_scales + static_cast<uint64_t>(wc_off[j]));
-    } else if (kScales == kBlockCode) {
-      wc_next[0] = *reinterpret_cast<const uint16_t*>(ahead.w_scales);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) wf_next[j] = reinterpret_cast<const float*>(ahead.w_scales)[j];
-    }
-  };
-  const auto use_next = [&](int32_t kb) __attribute__((always_inline)) {
-    // not before the loads of two steps have been sent
-    if (kScales == kBlockCode) asm volatile("" : "+v"(wc_next[0]));
-    if (kScales == kBlockF32) asm volatile("" : "+v"(wf_next[0]), "+v"(wf_next[1]));
-    // behind an odd last block: any finite scale
-    if (kScales == kBlockCode) wc_next[0] = kb < last ? wc_next[0] : (wc_next[0] & 0xFFu) | 0x7F00u;
-    if (kScales == kBlockF32) wf_next[1] = kb < last ? wf_next[1] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kCodes; ++i) xc[i] = xc_next[i];
-#pragma unroll
-    for (int j = 0; j < kRowCodes; ++j) wc[j] = wc_next[j];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) wf[j] = wf_next[j];
-  };
-
-  floatx4 acc[FM][8];
-  int8v xv[FM], wv[8];
-  const auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  };
-
-  const uint32_t at0 = r * 128 + ((q ^ ((r >> 1) & 7)) << 4), at1 = at0 ^ 64;
-  const auto operand = [&](const uint8_t* rows16) __attribute__((always_inline)) {
-    const int4v a = *reinterpret_cast<const int4v*>(rows16 + at0);
-    const int4v b = *reinterpret_cast<const int4v*>(rows16 + at1);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  // Operands from .. to - 1 of a half.
-  const auto read_x = [&](const uint8_t* buf, auto half, auto from, auto to) __attribute__((always_inline)) {
-    constexpr int h = decltype(half)::value * HM;
-#pragma unroll
-    for (int i = decltype(from)::value; i < decltype(to)::value; ++i)
-      xv[h + i] = operand(buf + (wm * (kBigM / 4) + i * 16) * 128);
-  };
-  const auto read_w = [&](const uint8_t* buf, auto half, auto from, auto to) __attribute__((always_inline)) {
-    constexpr int h = decltype(half)::value * 4;
-#pragma unroll
-    for (int j = decltype(from)::value; j < decltype(to)::value; ++j)
-      wv[h + j] = operand(buf + (kBigM / 2 + wn * 64 + j * 16) * 128);
-  };
-  // A third of a quarter: one operand of x by four of the weights. Nothing is
-  // moved over its end, so that the accesses of LDS written before a third
-  // stay between the products of their neighbours.
-  const auto third = [&](auto x_half, auto w_half, auto row, auto step) __attribute__((always_inline)) {
-    constexpr int kStep = decltype(step)::value, wh = decltype(w_half)::value * 4,
-                  i = decltype(x_half)::value * HM + decltype(row)::value;
-#pragma unroll
-    for (int j = wh; j < wh + 4; ++j) {
-      if constexpr (kScales == kBlockF32) {
-        const floatx4 sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            wv[j], xv[i], (floatx4{0.0f, 0.0f, 0.0f, 0.0f}), 0, 0, 0, 127, kStep,
-            static_cast<int>(xc[i]));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(wf[kStep], sum[e], acc[i][j][e]);
-      } else {
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            wv[j], xv[i], acc[i][j], 0, 0, kStep,
-            static_cast<int>(wc[kScales == kRowCode ? j : 0]), kStep, static_cast<int>(xc[i]));
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  const std::integral_constant<int, 0> c0;
-  const std::integral_constant<int, 1> c1;
-  const std::integral_constant<int, 2> c2;
-  const std::integral_constant<int, 3> c3;
-  const std::integral_constant<int, 4> c4;
-  const std::integral_constant<int, 5> c5;
-  const std::integral_constant<int, 7> c7;
-  // All but the newest two halves' loads (7 each) have arrived, this wave's
-  // reads are done, and so are the other waves'. behind_stores: a tile's
-  // results were sent after the loads that are waited for.
-  const auto arrived = [&](auto behind_stores) __attribute__((always_inline)) {
-    constexpr int n = 14 + (decltype(behind_stores)::value ? kBigStores : 0);
-    static_assert(n < 64, "vmcnt");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4 << 14));   // vmcnt(n) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  // A step: its products, the reads for the next one, and the loads of the
-  // step after that, from x and w on.
-  const auto one = [&](auto step, auto first, auto other, auto stores1, auto stores2, uint8_t* begin,
-                       uint8_t* rest, const uint8_t* next, const uint8_t* x, const uint8_t* w)
-      __attribute__((always_inline)) {
-    arrived(stores1);                  // rest; begin has been read
-    read_w(rest, other, c0, c2);
-    third(c0, first, c0, step);
-    read_w(rest, other, c2, c4);
-    third(c0, first, c1, step);
-    stage(begin, x, w, c0, first, c0, c1);
-    third(c0, first, c2, step);
-    read_x(rest, c1, c0, c2);
-    stage(begin, x, w, c0, first, c1, c3);
-    third(c0, other, c0, step);
-    read_x(rest, c1, c2, c3);
-    stage(begin, x, w, c0, first, c3, c5);
-    third(c0, other, c1, step);
-    stage(begin, x, w, c0, first, c5, c7);
-    third(c0, other, c2, step);
-    arrived(stores2);                  // the next step's begin; rest has been read
-    read_x(next, c0, c0, c1);
-    third(c1, other, c0, step);
-    read_x(next, c0, c1, c2);
-    third(c1, other, c1, step);
-    read_x(next, c0, c2, c3);
-    stage(rest, x, w, c1, other, c0, c1);
-    third(c1, other, c2, step);
-    read_w(next, other, c0, c2);
-    stage(rest, x, w, c1, other, c1, c3);
-    third(c1, first, c0, step);
-    read_w(next, other, c2, c4);
-    stage(rest, x, w, c1, other, c3, c5);
-    third(c1, first, c1, step);
-    stage(rest, x, w, c1, other, c5, c7);
-    third(c1, first, c2, step);
-  };
-
-  // Two steps, with the loads of the two that follow.
-  const auto pair = [&](auto stores) __attribute__((always_inline)) {
-    request();
-    one(c0, c1, c0, stores, stores, begin0, rest0, begin1, ahead.x, ahead.w);
-    one(c1, c0, c1, stores, c0, begin1, rest1, begin0, ahead.x + p.x_block,
-        ahead.w + (ahead.kb < last ? p.w_block : 0));
-    use_next(ahead.kb);
-  };
-
-  int32_t ahead_id = id;
-  // Behind the last tile's steps: the last two again, which nothing reads.
-  const auto go_on = [&]() __attribute__((always_inline)) {
-    if (ahead.kb + 2 < ahead.kb1) {
-      ahead.kb += 2;
-      ahead.x += 2 * p.x_block;
-      ahead.w += 2 * p.w_block;
-      ahead.x_codes += 2;
-      ahead.w_scales += 2 * kScaleBytes;
-    } else if (ahead_id + stride < behind) {
-      ahead_id += stride;
-      begin_tile(tile_at(ahead_id));
-    }
-  };
-
-  begin_tile(tile_at(id));
-  request();
-  const uint8_t* w1 = ahead.w + (ahead.kb < last ? p.w_block : 0);
-  stage(begin0, ahead.x, ahead.w, c0, c1, c0, c7);
-  stage(rest0, ahead.x, ahead.w, c1, c0, c0, c7);
-  stage(begin1, ahead.x + p.x_block, w1, c0, c0, c0, c7);
-  stage(rest1, ahead.x + p.x_block, w1, c1, c1, c0, c7);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the first waits count none of these
-  arrived(c0);
-  use_next(ahead.kb);
-  go_on();
-  read_x(begin0, c0, c0, c3);
-  read_w(begin0, c1, c0, c4);
-  clear();
-  for (;;) {
-    const Tile now = tile_at(id);
-    pair(c1);
-    for (int32_t kb = now.kb0 + 2; kb < now.kb1; kb += 2) {
-      go_on();
-      pair(c0);
-    }
-    go_on();
-
-    // a lane: row i * 16 + r, columns j * 16 + 4 q .. + 3
-    const int64_t m0 = static_cast<int64_t>(now.mt) * kBigM + wm * (kBigM / 2);
-    const int64_t n0 = static_cast<int64_t>(now.nt) * kBigN + wn * 128;
-    const bool whole = m0 + kBigM / 2 <= p.m && n0 + 128 <= p.n;
-    const bool wide = p.part == nullptr && p.y_bf16 && p.y_vec;
-    const bool fours = p.part != nullptr ? p.n % 4 == 0 : p.y_vec && !p.y_bf16;
-    float* to = p.part != nullptr ? p.part + now.split * p.m * p.n : static_cast<float*>(p.y);
-    const int64_t ld = p.part != nullptr ? p.n : p.ldy;
-    if (wide) {
-      // the halves of two operands' results change places between lanes 16
-      // apart: eight columns a lane, 64 bytes of a row side by side
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t row = m0 + i * 16 + r;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const floatx4 a = acc[i][j], b = acc[i][j + 1];
-          const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(a[0], a[1]), pack_bf16(b[0], b[1]),
-                                                           false, false);
-          const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(a[2], a[3]), pack_bf16(b[2], b[3]),
-                                                           false, false);
-          const int64_t col = n0 + (j + (q & 1)) * 16 + (q & 2) * 4;
-          if (whole || (row < p.m && col < p.n))
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + row * p.ldy + col) =
-                uint4{lo[0], hi[0], lo[1], hi[1]};
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t row = m0 + i * 16 + r;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t col = n0 + j * 16 + q * 4;
-          const floatx4 v = acc[i][j];
-          if (row >= p.m) continue;
-          if (fours) {
-            if (col < p.n) *reinterpret_cast<floatx4*>(to + row * ld + col) = v;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (col + e >= p.n) continue;
-              if (p.part == nullptr && p.y_bf16)
-                static_cast<uint16_t*>(p.y)[row * ld + col + e] = to_bf16_rne(v[e]);
-              else
-                to[row * ld + col + e] = v[e];
-            }
-          }
-        }
-      }
-    }
-    // fewer or more stores than are counted on
-    if (!whole || !(wide || fours)) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-    id += stride;
-    if (id >= behind) break;
-    clear();
-  }
-  // no load into LDS may be on its way when the block gives it back
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 }
 
 // The splits' sums, in their order. Only outputs of fewer than 128 tiles are
@@ -1482,13 +1065,10 @@ constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 //   else splits for 256 blocks, or 512 of the tiles of 32 rows, of which four
 //   fit a CU (61 x 3840 x 15360, 30 tiles of 64: 22.5 with 8, 23.3 with 15;
 //   20 x 4096 x 4096: 16.6 with 8, 14.9 with 16).
-Plan plan_of(int64_t m, int64_t n, int64_t kb, bool exact) {
+Plan plan_of(int64_t m, int64_t n, int64_t kb) {
   Plan q;
-  const int64_t big = ((m + kBigM - 1) / kBigM) * ((n + kBigN - 1) / kBigN);
-  if (m <= 32) q.bm = 32, q.bn = 128;
-  else if (m <= 64) q.bm = 64, q.bn = 128;
-  else if (!exact && big >= 192) q.bm = kBigM, q.bn = kBigN;
-  else q.bm = 128, q.bn = 128;
+  q.bm = m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  q.bn = 128;
   const int64_t tiles = ((m + q.bm - 1) / q.bm) * ((n + q.bn - 1) / q.bn);
   int64_t splits = tiles >= 128 || (tiles >= 64 && kb <= 8) ? 1 : (q.bm == 32 ? 512 : 256) / tiles;
   if (splits > kb / 4) splits = kb / 4;
@@ -1507,36 +1087,26 @@ bool launchable(const GemmArgs& p) {
 }
 
 template <int kScales, bool kExperts>
-void launch_gemm(const GemmArgs& p, const Plan& q, bool exact, hipStream_t st) {
+void launch_gemm(const GemmArgs& p, const Plan& q, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(p.mt) * p.nt * (kExperts ? 8 : p.splits)));
-#define BINADE_F8_LAUNCH(BM, BN, WM, WN, EX)                                                     \
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, EX, kScales, kExperts>), grid, dim3(64 * WM * WN), \
-                     0, st, p)
-  if (q.bm == 32) {
-    if (exact) BINADE_F8_LAUNCH(32, 128, 1, 4, true);
-    else BINADE_F8_LAUNCH(32, 128, 1, 4, false);
-  } else if (q.bm == 64) {
-    if (exact) BINADE_F8_LAUNCH(64, 128, 1, 4, true);
-    else BINADE_F8_LAUNCH(64, 128, 1, 4, false);
-  } else if (q.bm == 128) {
-    if (exact) BINADE_F8_LAUNCH(128, 128, 2, 2, true);
-    else BINADE_F8_LAUNCH(128, 128, 2, 2, false);
-  } else if constexpr (!kExperts) {
-    hipLaunchKernelGGL(big_kernel<kScales>, dim3(grid.x < kBigBlocks ? grid.x : kBigBlocks), dim3(256), 0,
-                       st, p);
-  }
+#define BINADE_F8_LAUNCH(BM, BN, WM, WN)                                                              \
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, kScales, kExperts>), grid, dim3(64 * WM * WN), 0, st, p)
+  if (q.bm == 32) BINADE_F8_LAUNCH(32, 128, 1, 4);
+  else if (q.bm == 64) BINADE_F8_LAUNCH(64, 128, 1, 4);
+  else BINADE_F8_LAUNCH(128, 128, 2, 2);
 #undef BINADE_F8_LAUNCH
 }
 
-void launch_kind(int kind, const GemmArgs& p, const Plan& q, bool exact, hipStream_t st) {
-  if (kind == kBlockCode) launch_gemm<kBlockCode, false>(p, q, exact, st);
-  else if (kind == kRowCode) launch_gemm<kRowCode, false>(p, q, exact, st);
-  else launch_gemm<kBlockF32, false>(p, q, exact, st);
+void launch_kind(int kind, const GemmArgs& p, const Plan& q, hipStream_t st) {
+  if (kind == kBlockCode) launch_gemm<kBlockCode, false>(p, q, st);
+  else if (kind == kRowCode) launch_gemm<kRowCode, false>(p, q, st);
+  else launch_gemm<kBlockF32, false>(p, q, st);
 }
 
-// Rows of a quantised operand: a tile of it is read whole.
+// Rows of a quantised operand: tiles of it are read whole. (Of 192 too: the
+// workspace's sizes stay what they were.)
 int64_t tile_rows(int64_t m) {
-  const int64_t a = (m + 127) / 128 * 128, b = (m + kBigM - 1) / kBigM * kBigM;
+  const int64_t a = (m + 127) / 128 * 128, b = (m + 191) / 192 * 192;
   return a > b ? a : b;
 }
 
@@ -1554,7 +1124,7 @@ struct Side {   // an operand: its blocks, rows of one, and its codes or scales
 int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n, int64_t k, void* y,
                     int64_t ldy, bool y_bf16, float* part, hipStream_t st) {
   const int64_t kb = blocks_of(k);
-  const Plan q = plan_of(m, n, kb, !y_bf16);
+  const Plan q = plan_of(m, n, kb);
   GemmArgs p{};
   p.x = x.q;
   p.x_codes = static_cast<const uint8_t*>(x.scales);
@@ -1578,7 +1148,7 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   const int whole = y_bf16 ? 8 : 4;   // results that a lane stores together
   p.y_vec = n % whole == 0 && ldy % whole == 0 && aligned16(y);
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
-  launch_kind(kind, p, q, !y_bf16, st);
+  launch_kind(kind, p, q, st);
   if (q.splits > 1) {
     const uint32_t total = static_cast<uint32_t>(m * n), cols = static_cast<uint32_t>(n);
     if (n % 4 == 0)
@@ -1591,8 +1161,8 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   return launch_status();
 }
 
-int64_t part_bytes(int64_t m, int64_t n, int64_t k, bool exact) {
-  const Plan q = plan_of(m, n, blocks_of(k), exact);
+int64_t part_bytes(int64_t m, int64_t n, int64_t k) {
+  const Plan q = plan_of(m, n, blocks_of(k));
   return q.splits > 1 ? up16(4 * q.splits * m * n) : 0;
 }
 int64_t side_bytes(int64_t rows, int64_t cols) {
@@ -1732,9 +1302,9 @@ extern "C" int32_t binade_f8_layout(const uint8_t* values, const void* scales, b
   return launch_status();
 }
 
-extern "C" int64_t binade_f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t y_dtype) {
+extern "C" int64_t binade_f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t) {
   if (m <= kSmallRows || n < 1 || k < 1 || m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
-  return side_bytes(m, k) + part_bytes(m, n, k, y_dtype == BINADE_F32);
+  return side_bytes(m, k) + part_bytes(m, n, k);
 }
 
 extern "C" int32_t binade_f8_gemm(const binade_f8* w, const uint16_t* x, int64_t m, int64_t ldx,
@@ -1779,17 +1349,16 @@ extern "C" int32_t binade_f8_gemm(const binade_f8* w, const uint16_t* x, int64_t
 }
 
 extern "C" int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
-                                                       int32_t need_dx, int32_t need_dw,
-                                                       int32_t dw_dtype) {
+                                                       int32_t need_dx, int32_t need_dw, int32_t) {
   if (m < 1 || n < 1 || k < 1 || m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
   int64_t bytes = 0, part = 0;
   if (need_dx) {
     bytes += side_bytes(m, n);
-    part = part_bytes(m, k, n, false);
+    part = part_bytes(m, k, n);
   }
   if (need_dw) {
     bytes += side_bytes(n, m) + side_bytes(k, m);
-    const int64_t b = part_bytes(n, k, m, dw_dtype == BINADE_F32);
+    const int64_t b = part_bytes(n, k, m);
     part = b > part ? b : part;
   }
   return bytes + part;
@@ -1997,7 +1566,7 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   p.w_next = w_next;
   p.s_next = s_next;
   p.pairs_a_row = per_row;
-  if (kind_of(experts) == kBlockCode) launch_gemm<kBlockCode, true>(p, q, y_dtype == BINADE_F32, st);
-  else launch_gemm<kBlockF32, true>(p, q, y_dtype == BINADE_F32, st);
+  if (kind_of(experts) == kBlockCode) launch_gemm<kBlockCode, true>(p, q, st);
+  else launch_gemm<kBlockF32, true>(p, q, st);
   return launch_status();
 }

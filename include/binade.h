@@ -767,10 +767,10 @@ int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *             of 4]; entries behind the last block are not used
  *   values_t, scales_t   the same of the transposed matrices [cols, rows],
  *             for binade_f8_gemm_grad's dx; or NULL
- * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. Products that are
- * called exact below take a weight with a power of two as bf16 holds it: under
- * 2^-133 (codes 0 to 2) rounded to its steps, over its largest (codes from 247
- * on) infinite. cols % 32 == 0, rows and cols at most 2^22, count at most
+ * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. The products take a
+ * weight with a power of two as bf16 holds it: under 2^-133 (codes 0 to 2)
+ * rounded to its steps, over its largest (codes from 247 on) infinite; and so
+ * a quantised x or dy: a value that rounds to 2^128 is infinite. cols % 32 == 0, rows and cols at most 2^22, count at most
  * 65535; planes 16-byte aligned, else BINADE_EUNSUPPORTED. */
 typedef struct binade_f8 {
   int64_t rows, cols;
@@ -815,12 +815,9 @@ int32_t binade_f8_layout(const uint8_t *values, const void *scales,
  * (ldx >= K, a multiple of 8, at most 2^24; 16-byte aligned). Y: fp32 or bf16
  * per y_dtype, row stride ldy >= N, at most 2^24. m from 0 to 2^22, m * N at
  * most 2^36.
- * Arithmetic: an fp32 Y, and up to 16 rows of either type, add exact products
- * in fp32. A bf16 Y of more rows goes through the 8-bit matrix instruction,
- * at twice the rate: it adds eight products at a time, cut to about 13 bits
- * below the largest, in fp32 sums (1.4e-5 of Y's norm for normal data, less
- * than 1/100 of the output's own rounding). The order depends on m, N and K:
- * the same call gives the same bits. A NaN in a row of X, or in a row or a
+ * Arithmetic: exact products of 8-bit values are added in fp32, and a bf16 Y is
+ * that sum rounded once. The order depends on m, N and K: the same call gives
+ * the same bits, another m may add in another order. A NaN in a row of X, or in a row or a
  * scale of W, gives NaN in that row or column (block) of Y alone.
  * workspace: device, 16-byte aligned, binade_f8_gemm_workspace_bytes (0 for m
  * <= 16: may be NULL), not read before written; calls that overlap need their
@@ -841,7 +838,7 @@ int64_t binade_f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *              [N, K] contiguous; blocks of 128 rows t of a column
  * dx (row stride ld_dx >= K) or dw may be NULL: not computed. dx needs w's
  * transposed planes, dw needs x (as in binade_f8_gemm; otherwise x may be
- * NULL) and of w the sizes alone. Arithmetic by the output's type as above.
+ * NULL) and of w the sizes alone. Arithmetic as in binade_f8_gemm.
  * m = 0 leaves dw zeros. workspace: binade_f8_gemm_grad_workspace_bytes with
  * need_dx, need_dw 0 or 1. */
 int32_t binade_f8_gemm_grad(const binade_f8 *w, const uint16_t *x, int64_t m,
@@ -861,9 +858,9 @@ int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  * int32 [n_tokens * top_k]. y: fp32 or bf16 per y_dtype, pair p at y + p*ldy.
  * A pair of index -1 has no expert (a padded token's slot): its row is zeros.
  * An index outside [-1, count) sets BINADE_DEV_BAD_INDEX in dev_status (if
- * not NULL) and counts as -1. Each used expert is read about once (once for
- * each 128 of its pairs); arithmetic as in binade_f8_gemm, exact products up
- * to 256 pairs; a pair's result does not depend on the other pairs' order.
+ * not NULL) and counts as -1. Each used expert is read once for each tile of
+ * 16 (few pairs) to 128 of its pairs; arithmetic as in binade_f8_gemm; a
+ * pair's result does not depend on the other pairs' order.
  * top_k in 1..64, count at most 4096, n_tokens * top_k at most 2^24, pairs * N
  * at most 2^36 and 2^23 tiles of outputs, else EUNSUPPORTED. Experts that are
  * trained take binade_f8_gemm_grad of their own rows, expert by expert.
