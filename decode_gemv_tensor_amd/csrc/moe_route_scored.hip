@@ -67,8 +67,7 @@ __device__ __forceinline__ float value_of(int32_t o) {
 // be the exact one. u = 2^-24. A sigmoid errs by at most 3 u (the exponential,
 // of at most (|x| + 2) u relative, moves it by less than 1 u; the sum, its
 // inverse and the product), a softmax p by (|d| + 6) u p < 7 u, the bias's
-// addition by u |v| / 2: 16 u + 2 u |v| covers two of them. Scores of groups
-// are sums of two: twice that and their own rounding.
+// addition by u |v| / 2: 16 u + 2 u |v| covers two of them.
 __device__ __forceinline__ float apart(float v) { return 9.5367432e-7f + 1.1920929e-7f * fabsf(v); }
 
 // The two largest of a lane's and its partner's two.
@@ -93,32 +92,55 @@ __device__ __forceinline__ void join_two(T& a, T& b) {
   b = low > second ? low : second;
 }
 
+// A group's score in fp32, and how far it may be off: by its two terms' errors,
+// which go by their magnitudes, and the sum's rounding, below both together.
+// Terms of opposite sign cancel in the score and not in this.
+struct GroupScore {
+  float v, off;
+};
+__device__ __forceinline__ float number(GroupScore s) { return s.v; }
+__device__ __forceinline__ double number(double s) { return s; }
+
+// The score of a group whose two largest are a >= b (-inf: none). An infinite
+// one is exact; where the sum alone overflows, `off` is infinite.
+__device__ __forceinline__ GroupScore score_of(const ScoredArgs& p, float a, float b, bool exact) {
+  const bool two = p.group_best == 2 && b > -__builtin_inff();
+  return {two ? a + b : a, exact || !(fabsf(a) < __builtin_inff()) ? 0.0f : apart(fabsf(a) + (two ? fabsf(b) : 0.0f))};
+}
+__device__ __forceinline__ double score_of(const ScoredArgs& p, double a, double b, bool) {
+  return p.group_best == 2 && b > -static_cast<double>(__builtin_inff()) ? a + b : a;
+}
+
 // Whether the group `mine` of this lane, of the score `of_mine`, is taken; its
-// lane `first` leaves the score in LDS. sure: rounding cannot have decided it.
-template <typename T>
-__device__ __forceinline__ bool taken(const ScoredArgs& p, T* score, int32_t mine, bool first, T of_mine,
+// lane `first` leaves the score in LDS. sure: rounding cannot have decided it,
+// that is, too few groups may lie above it or enough certainly do.
+template <typename S>
+__device__ __forceinline__ bool taken(const ScoredArgs& p, S* score, int32_t mine, bool first, S of_mine,
                                       bool exact, bool& sure) {
   if (first && mine < p.groups) score[mine] = of_mine;
   wave_sync();
-  const T d = exact ? static_cast<T>(0) : static_cast<T>(3.0f * apart(static_cast<float>(of_mine)));
+  const auto m = number(of_mine);
   int32_t before = 0, over = 0, near = 0;
 #pragma unroll 4
   for (int32_t h = 0; h < p.groups; ++h) {
-    const T s = score[h];
-    before += s > of_mine || (s == of_mine && h < mine) ? 1 : 0;
-    over += s > of_mine + d ? 1 : 0;
-    near += h != mine && s >= of_mine - d ? 1 : 0;
+    const S s = score[h];
+    before += number(s) > m || (number(s) == m && h < mine) ? 1 : 0;
+    if constexpr (std::is_same<S, GroupScore>::value) {
+      const float d = s.off + of_mine.off, t = s.v - m;
+      over += t > d ? 1 : 0;
+      near += h != mine && !(t < -d) ? 1 : 0;
+    }
   }
   wave_sync();
-  const bool open = of_mine > -static_cast<T>(__builtin_inff());
+  const bool open = m > -__builtin_inff();
   if (!exact && open && mine < p.groups && !(near < p.top_groups || over >= p.top_groups)) sure = false;
   return open && before < p.top_groups;
 }
 
 // The groups taken, as bits, of values in a row of LDS: a group by as many
 // lanes as there are for all of them (more groups than lanes: several turns).
-template <int G, typename T>
-__device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t parts, const T* row, T* score,
+template <int G, typename T, typename S>
+__device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t parts, const T* row, S* score,
                                                   int l, bool exact, bool& sure) {
   const T none = -static_cast<T>(__builtin_inff());
   const int32_t turns = (p.groups * parts + G - 1) / G;
@@ -136,13 +158,13 @@ __device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t p
       constexpr int kStep = decltype(step)::value;
       if (kStep < parts) join_two<kStep>(a, b);
     });
-    if (g < p.groups && part == 0) score[g] = p.group_best == 2 && b > none ? a + b : a;
+    if (g < p.groups && part == 0) score[g] = score_of(p, a, b, exact);
   }
   wave_sync();
   uint64_t bits = 0;
   for (int32_t i = 0; i * G < p.groups; ++i) {
     const int32_t g = l + i * G;
-    const bool keep = taken(p, score, g, false, g < p.groups ? score[g] : none, exact, sure);
+    const bool keep = taken(p, score, g, false, g < p.groups ? score[g] : score_of(p, none, none, true), exact, sure);
     const uint64_t all = __ballot(keep) >> ((threadIdx.x & 63) & ~(G - 1));
     bits |= (G == 64 ? all : all & ((1ull << (G & 63)) - 1)) << (i * G & 63);
   }
@@ -153,7 +175,7 @@ __device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t p
 // of two, is joined in registers, others through the row in LDS.
 template <int G, int V>
 __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], const float (&from)[V],
-                                            float* row, float* score, int l, bool exact, bool& sure) {
+                                            float* row, GroupScore* score, int l, bool exact, bool& sure) {
   const float none = -__builtin_inff();
   if (p.lanes_a_group != 0) {
     float a = none, b = none;
@@ -166,9 +188,8 @@ __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], 
       constexpr int kStep = decltype(step)::value;
       if (kStep < p.lanes_a_group) join_two<kStep>(a, b);
     });
-    const float of_mine = p.group_best == 2 && b > none ? a + b : a;
     const int32_t mine = l / p.lanes_a_group;
-    const bool keep = taken(p, score, mine, l % p.lanes_a_group == 0, of_mine, exact, sure);
+    const bool keep = taken(p, score, mine, l % p.lanes_a_group == 0, score_of(p, a, b, exact), exact, sure);
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = keep ? v[j] : none;
     return;
@@ -296,7 +317,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
   double* d_row = row_s[wave][mine];
   float* x_row = reinterpret_cast<float*>(d_row);
   float* v_row = x_row + kExperts;
-  double* g_row = g_s[wave][mine];
+  GroupScore* g_row = reinterpret_cast<GroupScore*>(g_s[wave][mine]);
   int32_t* slot_row = slot_s[wave][mine];
   const float none = -__builtin_inff();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWavesABlock * kRows;
@@ -360,12 +381,12 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
 #pragma unroll
         for (int j = 0; j < V; ++j)
           from[j] = exact_groups || !(v[j] > none) ? v[j] : __builtin_fmaf(s[j], whole, bias[j]);
-        keep_groups<G, V>(a, v, from, v_row, reinterpret_cast<float*>(g_row), l, exact_groups, sure);
+        keep_groups<G, V>(a, v, from, v_row, g_row, l, exact_groups, sure);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(s[j], whole, bias[j]);
-      if (grouped) keep_groups<G, V>(a, v, v, v_row, reinterpret_cast<float*>(g_row), l, false, sure);
+      if (grouped) keep_groups<G, V>(a, v, v, v_row, g_row, l, false, sure);
     }
     // lane l of the row: slots l, l + G, ..; -1 where none is left
     int32_t slot[kHeld];

@@ -1,0 +1,124 @@
+"""GPU tests of choices that fp32 alone cannot make: the router by scores compares
+score + bias in fp64, and a row may only be settled in fp32 where its gaps are
+larger than everything that fp32 rounds. Inputs here bring gaps and roundings of
+like size together; choices have to be those of 64 bits, row by row. (Exactly
+equal values aside, the 64-bit values compared here are more than 2^-49 of the
+larger apart, which fp64 resolves whichever way its sums are ordered: rows that
+are nearer are left out, and have to be few.)"""
+import math
+
+import pytest
+import torch
+
+from decode_gemv_tensor_amd import binade as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+INF = math.inf
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def scores(x, score):
+    x = x.double()
+    return torch.softmax(x, 1) if score == "softmax" else torch.sigmoid(x)
+
+
+def choice(x, bias, k, score, groups=1, top_groups=1, best=2):
+    """(experts [T, k], whether fp64 itself tells the row's values apart)."""
+    T, E = x.shape
+    v = scores(x, score) + bias.double()
+    clear = torch.ones(T, dtype=torch.bool)
+
+    def settle(values, size, n):          # n largest, ties to the lowest; are they clear?
+        s, at = torch.sort(values, dim=1, descending=True, stable=True)
+        m = min(n, values.shape[1] - 1)
+        gap = s[:, :m] - s[:, 1:m + 1]
+        return at[:, :n], ((gap == 0) | (gap > 2.0 ** -49 * size)).all(1)
+
+    if groups > 1:
+        part = torch.sort(v.view(T, groups, -1), dim=2, descending=True).values[:, :, :best]
+        at, ok = settle(part.sum(2), part.abs().sum(2).amax(1, keepdim=True), top_groups)
+        clear &= ok
+        keep = torch.zeros(T, groups, dtype=torch.bool).scatter_(1, at, True)
+        v = torch.where(keep.repeat_interleave(E // groups, 1), v, -INF)
+    fin = torch.where(v > -INF, v, 0.0).abs().amax(1, keepdim=True)
+    at, ok = settle(v, fin, k)
+    return at, clear & ok
+
+
+def agree(name, x, bias, k, few=0.02, **rule):
+    want, clear = choice(x, bias, k, **rule)
+    rule["group_best"] = rule.pop("best", 2)
+    got = B.moe_route(x.to(DEV), k, bias=bias.to(DEV), stats=False, **rule).idx.cpu().long()
+    wrong = ((got != want).any(1) & clear).sum().item()
+    print(name, "wrong", wrong, "unclear", int((~clear).sum()), "of", len(x), flush=True)
+    assert wrong == 0, name
+    assert (~clear).float().mean() <= few
+
+
+def test_a_group_whose_two_best_cancel():
+    """Sums of 1.0197 and 1.0423 in 64 bits, 1.0625 and 1.0 in 32."""
+    x = torch.tensor([[1.7583513, -1.6088977, -0.13181214, 0.30318862]])
+    bias = torch.tensor([1e6, -1e6, 1e6, -1e6])
+    assert choice(x, bias, 1, "sigmoid", 2, 1)[0].item() == 2
+    agree("cancel", x, bias, 1, score="sigmoid", groups=2, top_groups=1)
+
+
+# groups of whole lanes (8 and 16 experts a lane: more than 512 tokens) and others
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,groups,top_groups,k", [
+    (500, 4, 2, 1, 1), (500, 64, 8, 3, 8), (4000, 256, 8, 4, 8), (500, 256, 8, 4, 12), (4000, 96, 8, 2, 4),
+    (500, 60, 6, 2, 10), (4000, 512, 16, 4, 8), (400, 1024, 32, 5, 6)])
+@pytest.mark.parametrize("size", [1.0, 20.0, 50.0, 1e3, 1e6, 1e30])
+def test_large_biases_of_both_signs(T, E, groups, top_groups, k, score, size):
+    """A group's best is far above nothing and its second best as far below."""
+    g = gen(int(size) % 1000 + E)
+    x = torch.randn(T, E, generator=g)
+    near = x * 1e-3                                      # scores close together
+    bias = torch.full((E,), -size)
+    bias[torch.arange(groups) * (E // groups) + torch.randint(0, E // groups, (groups,), generator=g)] = size
+    for name, rows in (("plain", x), ("near", near)):
+        # at 1e30 scores do not move a sum of 64 bits: equal groups everywhere
+        agree(name, rows, bias, k, 0.05 if size < 1e6 else 1.0, score=score, groups=groups, top_groups=top_groups)
+        mixed = torch.where(torch.rand(E, generator=gen(3)) < 0.5, size, -size)
+        agree(name + " mixed", rows, mixed, k, 1.0, score=score, groups=groups, top_groups=top_groups)
+
+
+@pytest.mark.parametrize("T", [300, 3000])
+@pytest.mark.parametrize("E", [64, 256, 1024])
+def test_softmax_totals_that_lose_small_terms(T, E):
+    """One expert near probability 1 beside many that fp32 drops one by one from
+    the row's total, and another whose bias is as large as the first one's
+    probability: gaps of 0 to 60 steps of 2^-24."""
+    u = 2.0 ** -24
+    for first in (0, E // 2 + 1):
+        c = torch.linspace(0.80, 0.999, T)
+        x = torch.full((T, E), 0.0)
+        x += torch.log(c * u)[:, None]
+        x[:, first] = 0.0
+        for j in range(16):
+            bias = torch.zeros(E)
+            bias[E - 1] = 1.0 - (E - 1) * 0.9 * u + (j - 8) * 4 * u
+            agree(f"total {first} {j}", x, bias, 1, score="softmax")
+            agree(f"total {first} {j} in groups", x, bias, 2, score="softmax", groups=4, top_groups=1)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_gaps_of_a_few_steps(score):
+    """Pairs of experts whose values differ by -40 to 40 steps of 2^-24."""
+    E, T = 128, 2000
+    g = gen(7)
+    base = torch.randn(1, E, generator=g) * 1.5
+    x = base + torch.randint(-40, 41, (T, E), generator=g) * 2.0 ** -22
+    s = scores(base, score)[0]
+    bias = (0.5 - s).float()
+    for k in (1, 4, 8, 10):
+        agree(f"k {k}", x, bias, k, score=score)
+        agree(f"k {k} in groups", x, bias, k, score=score, groups=8, top_groups=4)
