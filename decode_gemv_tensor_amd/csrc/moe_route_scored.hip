@@ -64,11 +64,16 @@ __device__ __forceinline__ float value_of(int32_t o) {
 }
 
 // How far apart two fp32 values of at most |v| have to be for their order to
-// be the exact one. u = 2^-24. A sigmoid errs by at most 3 u (the exponential,
-// of at most (|x| + 2) u relative, moves it by less than 1 u; the sum, its
-// inverse and the product), a softmax p by (|d| + 6) u p < 7 u, the bias's
-// addition by u |v| / 2: 16 u + 2 u |v| covers two of them.
-__device__ __forceinline__ float apart(float v) { return 9.5367432e-7f + 1.1920929e-7f * fabsf(v); }
+// be the exact one: `base` for their scores and 2 u |v| for the two additions of
+// a bias. u = 2^-24. A sigmoid errs by at most 4 u (an exponential, of at most
+// (2 |x| + 2) u relative, the sum, its inverse and the product): base is 16 u. A
+// softmax p = exp(d) / total errs by (2 |d| + 2) u p and by its total, which all
+// of the row have in common: 21 u relative from up to 15 additions a lane and
+// 6 across lanes, 11 u from its terms ((2 |d| + 2) u on the average that 1024 of
+// them can bring), 1 u from the inverse. That is below 40 u of the row's largest
+// p: base is 80 u of it, and of 1 / total, which is no less.
+constexpr float kSigmoidBase = 9.5367432e-7f, kSoftmaxBase = 4.7683716e-6f;
+__device__ __forceinline__ float apart(float base, float v) { return base + 1.1920929e-7f * fabsf(v); }
 
 // The two largest of a lane's and its partner's two.
 template <int kStep, typename T>
@@ -103,11 +108,12 @@ __device__ __forceinline__ double number(double s) { return s; }
 
 // The score of a group whose two largest are a >= b (-inf: none). An infinite
 // one is exact; where the sum alone overflows, `off` is infinite.
-__device__ __forceinline__ GroupScore score_of(const ScoredArgs& p, float a, float b, bool exact) {
+__device__ __forceinline__ GroupScore score_of(const ScoredArgs& p, float a, float b, bool exact, float base) {
   const bool two = p.group_best == 2 && b > -__builtin_inff();
-  return {two ? a + b : a, exact || !(fabsf(a) < __builtin_inff()) ? 0.0f : apart(fabsf(a) + (two ? fabsf(b) : 0.0f))};
+  return {two ? a + b : a,
+          exact || !(fabsf(a) < __builtin_inff()) ? 0.0f : apart(base, fabsf(a) + (two ? fabsf(b) : 0.0f))};
 }
-__device__ __forceinline__ double score_of(const ScoredArgs& p, double a, double b, bool) {
+__device__ __forceinline__ double score_of(const ScoredArgs& p, double a, double b, bool, float) {
   return p.group_best == 2 && b > -static_cast<double>(__builtin_inff()) ? a + b : a;
 }
 
@@ -141,7 +147,7 @@ __device__ __forceinline__ bool taken(const ScoredArgs& p, S* score, int32_t min
 // lanes as there are for all of them (more groups than lanes: several turns).
 template <int G, typename T, typename S>
 __device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t parts, const T* row, S* score,
-                                                  int l, bool exact, bool& sure) {
+                                                  int l, bool exact, float base, bool& sure) {
   const T none = -static_cast<T>(__builtin_inff());
   const int32_t turns = (p.groups * parts + G - 1) / G;
   for (int32_t i = 0; i < turns; ++i) {
@@ -158,13 +164,14 @@ __device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t p
       constexpr int kStep = decltype(step)::value;
       if (kStep < parts) join_two<kStep>(a, b);
     });
-    if (g < p.groups && part == 0) score[g] = score_of(p, a, b, exact);
+    if (g < p.groups && part == 0) score[g] = score_of(p, a, b, exact, base);
   }
   wave_sync();
   uint64_t bits = 0;
   for (int32_t i = 0; i * G < p.groups; ++i) {
     const int32_t g = l + i * G;
-    const bool keep = taken(p, score, g, false, g < p.groups ? score[g] : score_of(p, none, none, true), exact, sure);
+    const S of_mine = g < p.groups ? score[g] : score_of(p, none, none, true, 0.0f);
+    const bool keep = taken(p, score, g, false, of_mine, exact, sure);
     const uint64_t all = __ballot(keep) >> ((threadIdx.x & 63) & ~(G - 1));
     bits |= (G == 64 ? all : all & ((1ull << (G & 63)) - 1)) << (i * G & 63);
   }
@@ -175,7 +182,8 @@ __device__ __forceinline__ uint64_t groups_of_row(const ScoredArgs& p, int32_t p
 // of two, is joined in registers, others through the row in LDS.
 template <int G, int V>
 __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], const float (&from)[V],
-                                            float* row, GroupScore* score, int l, bool exact, bool& sure) {
+                                            float* row, GroupScore* score, int l, bool exact, float base,
+                                            bool& sure) {
   const float none = -__builtin_inff();
   if (p.lanes_a_group != 0) {
     float a = none, b = none;
@@ -189,7 +197,8 @@ __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], 
       if (kStep < p.lanes_a_group) join_two<kStep>(a, b);
     });
     const int32_t mine = l / p.lanes_a_group;
-    const bool keep = taken(p, score, mine, l % p.lanes_a_group == 0, score_of(p, a, b, exact), exact, sure);
+    const bool keep = taken(p, score, mine, l % p.lanes_a_group == 0, score_of(p, a, b, exact, base), exact,
+                            sure);
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = keep ? v[j] : none;
     return;
@@ -198,7 +207,7 @@ __device__ __forceinline__ void keep_groups(const ScoredArgs& p, float (&v)[V], 
 #pragma unroll
   for (int j = 0; j < V; ++j) row[e0 + j] = from[j];
   wave_sync();
-  const uint64_t bits = groups_of_row<G>(p, p.parts, row, score, l, exact, sure);
+  const uint64_t bits = groups_of_row<G>(p, p.parts, row, score, l, exact, base, sure);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const uint32_t g = static_cast<uint32_t>(e0 + j) / static_cast<uint32_t>(p.group_size);
@@ -253,7 +262,7 @@ __device__ __forceinline__ void settle(const ScoredArgs& p, int64_t row, float t
     int32_t parts = 1;
     while (2 * parts * p.groups <= 64) parts *= 2;
     bool sure = true;
-    const uint64_t bits = groups_of_row<64>(p, parts, values, score, lane, true, sure);
+    const uint64_t bits = groups_of_row<64>(p, parts, values, score, lane, true, 0.0f, sure);
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const uint32_t g = static_cast<uint32_t>(lane + 64 * i) / static_cast<uint32_t>(p.group_size);
@@ -365,6 +374,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     // what is compared
     const bool no_numbers = !a.sigmoid && total != total, plain = by_logit || no_numbers;
     const bool exact_groups = plain && (a.group_best == 1 || no_numbers);
+    const float base = a.sigmoid ? kSigmoidBase : kSoftmaxBase * inv;
     const float whole = a.sigmoid ? (shift < 0.0f ? exp_of(shift) : 1.0f) : inv;
     float v[V];
     bool sure = true;
@@ -381,12 +391,12 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
 #pragma unroll
         for (int j = 0; j < V; ++j)
           from[j] = exact_groups || !(v[j] > none) ? v[j] : __builtin_fmaf(s[j], whole, bias[j]);
-        keep_groups<G, V>(a, v, from, v_row, g_row, l, exact_groups, sure);
+        keep_groups<G, V>(a, v, from, v_row, g_row, l, exact_groups, base, sure);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = __builtin_fmaf(s[j], whole, bias[j]);
-      if (grouped) keep_groups<G, V>(a, v, v, v_row, g_row, l, false, sure);
+      if (grouped) keep_groups<G, V>(a, v, v, v_row, g_row, l, false, base, sure);
     }
     // lane l of the row: slots l, l + G, ..; -1 where none is left
     int32_t slot[kHeld];
@@ -419,7 +429,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
           last = best[j];
           const float b = value_of(best[j]), gap = value_of(best[j - 1]) - b;
           if (best[j] > kNone) {
-            sure &= plain ? gap > 0.0f : gap > apart(fmaxf(fabsf(b), first));
+            sure &= plain ? gap > 0.0f : gap > apart(base, fmaxf(fabsf(b), first));
             ++filled;
           }
         }
@@ -439,7 +449,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
         next = group_max_key<G>(next);
         if (last > kNone && next > kNone && !plain) {
           const float b = value_of(next);
-          sure &= value_of(last) - b > apart(fmaxf(fabsf(b), first));
+          sure &= value_of(last) - b > apart(base, fmaxf(fabsf(b), first));
         }
         // equal values at the end of the slots: more experts than slots
         sure &= group_sum<G>(static_cast<float>(__builtin_popcount(own))) == static_cast<float>(filled);
@@ -483,7 +493,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
           if (l == j && last != 0 && n < p.top_k) slot[h] = KeyF32::expert(last);
           const float b = KeyF32::value(last);
           if (n == 0) first = b;
-          if (!plain && n > 0 && last != 0) sure &= before - b > apart(fmaxf(fabsf(b), fabsf(first)));
+          if (!plain && n > 0 && last != 0) sure &= before - b > apart(base, fmaxf(fabsf(b), fabsf(first)));
           before = b;
         }
       }
@@ -522,13 +532,13 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     }
     high = group_max<G>(high);
     const bool counted = valid && high > none;
-    const float base = !p.renorm ? (a.sigmoid ? 0.0f : top) : a.sigmoid ? fminf(high, 0.0f) : high;
+    const float from = !p.renorm ? (a.sigmoid ? 0.0f : top) : a.sigmoid ? fminf(high, 0.0f) : high;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       e[h] = 0.0f;
       if (slot[h] >= 0)
-        e[h] = a.sigmoid ? exp_of(fminf(xs[h], 0.0f) - base) * inverse(1.0f + low_exp(xs[h]))
-                         : exp_of(xs[h] - base);
+        e[h] = a.sigmoid ? exp_of(fminf(xs[h], 0.0f) - from) * inverse(1.0f + low_exp(xs[h]))
+                         : exp_of(xs[h] - from);
       taken += e[h];
     }
     if (p.renorm) taken = group_sum<G>(taken);

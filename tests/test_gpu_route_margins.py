@@ -122,3 +122,24 @@ def test_gaps_of_a_few_steps(score):
     for k in (1, 4, 8, 10):
         agree(f"k {k}", x, bias, k, score=score)
         agree(f"k {k} in groups", x, bias, k, score=score, groups=8, top_groups=4)
+
+
+@pytest.mark.parametrize("score", ["softmax"])
+def test_a_softmax_total_that_rounds_down_at_every_step(score):
+    """1024 experts, sixteen a lane: what 1 loses in its own lane's fifteen
+    additions and in six steps across lanes, 20.7 steps of 2^-24 in all; the
+    other expert's bias lies between the exact probability and 1."""
+    u, E = 2.0 ** -24, 1024
+    part = torch.empty(E, dtype=torch.float64)
+    part[:16] = 0.99 * u
+    for step in range(6):
+        lanes = 2 ** step
+        part[16 * lanes:32 * lanes] = 0.98 * u / (16 * lanes)
+    x = torch.log(part).float()[None].repeat(4, 1)
+    x[:, 0] = 0.0
+    x[1:, 1:] += torch.tensor([-1e-3, -3e-3, -1e-2])[:, None]
+    for n in range(12, 25):
+        bias = torch.zeros(E)
+        bias[E - 1] = 1.0 - n * u
+        agree(f"total {n}", x, bias, 1, score=score)
+        agree(f"total {n}, two", x, bias, 2, score=score)
