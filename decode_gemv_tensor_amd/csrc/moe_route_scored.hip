@@ -41,7 +41,7 @@ struct ScoredArgs {
   bool sigmoid;
 };
 
-// 1 / v for v >= 1/2 here; and exp(-|x|).
+// exp(-|x|).
 __device__ __forceinline__ float low_exp(float x) { return exp_of(-fabsf(x)); }
 
 // KeyF32's order of any value: rising with it, -0 as +0; NaN and -inf as 0
@@ -52,8 +52,9 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t o = (b ^ neg) + ((neg & 1u) | (~neg & 0x80000000u));
   return v > -__builtin_inff() ? o : 0u;
 }
-// A value's bits as a whole number of the same order, and back. (-0 lies below
-// +0: such a row is not settled, their gap is nothing.) -inf is the least.
+// A value's bits as a whole number of the same order, and back. -0 would lie
+// below +0: values come here as +0 (score + bias is never -0, a logit gets + 0).
+// -inf is the least.
 constexpr int32_t kNone = static_cast<int32_t>(0x807FFFFFu);   // of -inf
 __device__ __forceinline__ int32_t ordered(float v) {
   const int32_t b = __float_as_int(v);
@@ -383,7 +384,7 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     if (special || by_logit) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float xv = x.value(j), w = plain ? xv : __builtin_fmaf(s[j], whole, bias[j]);
+        const float xv = x.value(j), w = plain ? xv + 0.0f : __builtin_fmaf(s[j], whole, bias[j]);
         v[j] = xv > none && w > none ? w : none;
       }
       if (grouped) {

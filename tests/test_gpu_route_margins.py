@@ -143,3 +143,36 @@ def test_a_softmax_total_that_rounds_down_at_every_step(score):
         bias[E - 1] = 1.0 - n * u
         agree(f"total {n}", x, bias, 1, score=score)
         agree(f"total {n}, two", x, bias, 2, score=score)
+
+
+# k up to 8 and above, 8 and 16 experts a lane, every number of lanes
+@pytest.mark.parametrize("k", [1, 2, 4, 8, 9, 12])
+@pytest.mark.parametrize("T,E", [(40, 16), (40, 64), (600, 64), (40, 100), (40, 256), (600, 256), (600, 130),
+                                 (40, 512), (600, 512), (40, 1000)])
+def test_zeros_of_both_signs_are_equal(T, E, k):
+    """Logits of +0 and -0 across the last slot: equal ones by rising expert, with
+    no bias, a bias of zeros and one of numbers, in both types, with and without
+    groups."""
+    g = gen(E + k)
+    signs = torch.where(torch.rand(T, E, generator=g) < 0.5, 0.0, -0.0)
+    x = torch.where(torch.rand(T, E, generator=g) < min(1.0, (k + 3) / E), signs, -1.0)
+    x[0], x[1, :] = -0.0, -1.0
+    x[1, 2], x[1, 5] = -0.0, 0.0
+    x[2, :] = -1.0                        # k of +0, and one of -0 before them
+    x[2, E - k:], x[2, 1] = 0.0, -0.0
+    zeros = torch.where(torch.rand(E, generator=g) < 0.5, 0.0, -0.0)
+    steps = torch.where(torch.rand(E, generator=g) < 0.5, 0.25, 0.5)
+    for dtype in (F32, BF):
+        for score in ("sigmoid", "softmax"):
+            for bias in (None, zeros, steps):
+                want, _ = choice(x, zeros if bias is None else bias, k, score)
+                got = B.moe_route(x.to(dtype).to(DEV), k, score=score, scale=2.0, stats=False,
+                                  bias=None if bias is None else bias.to(DEV)).idx.cpu().long()
+                bad = (got != want).any(1).nonzero().flatten().tolist()
+                assert not bad, (dtype, score, bias is None, bad[:3], got[bad[0]], want[bad[0]])
+                if E % 4 == 0 and k <= E // 2:
+                    want, _ = choice(x, zeros if bias is None else bias, k, score, 4, 2)
+                    got = B.moe_route(x.to(dtype).to(DEV), k, score=score, groups=4, top_groups=2, stats=False,
+                                      bias=None if bias is None else bias.to(DEV)).idx.cpu().long()
+                    bad = (got != want).any(1).nonzero().flatten().tolist()
+                    assert not bad, (dtype, score, "groups", bad[:3], got[bad[0]], want[bad[0]])
