@@ -315,15 +315,17 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
   }
   const bool grouped = a.groups > 1 && a.top_groups < a.groups;
   float bias[V], sums[V];
-  bool zero = true;
+  bool zero = true, number = true;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     bias[j] = a.bias != nullptr && e0 + j < p.n_experts ? a.bias[e0 + j] : 0.0f;
     zero &= bias[j] == 0.0f;
+    number &= bias[j] == bias[j];
     sums[j] = 0.0f;
   }
   // a bias of zeros is none
   const bool by_logit = __ballot(!zero) == 0;
+  const bool nan_bias = __ballot(!number) != 0;
   double* d_row = row_s[wave][mine];
   float* x_row = reinterpret_cast<float*>(d_row);
   float* v_row = x_row + kExperts;
@@ -379,8 +381,9 @@ __global__ __launch_bounds__(64 * kWavesABlock) void scored_kernel(ScoredArgs a)
     const float whole = a.sigmoid ? (shift < 0.0f ? exp_of(shift) : 1.0f) : inv;
     float v[V];
     bool sure = true;
-    // closed experts, or no numbers: each value looked at
-    const bool special = __ballot(!(low > none) || total != total) != 0;
+    // closed experts, or no numbers: each value looked at (a NaN's key would lie
+    // above all others)
+    const bool special = nan_bias || __ballot(!(low > none) || total != total) != 0;
     if (special || by_logit) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {

@@ -176,3 +176,22 @@ def test_zeros_of_both_signs_are_equal(T, E, k):
                                       bias=None if bias is None else bias.to(DEV)).idx.cpu().long()
                     bad = (got != want).any(1).nonzero().flatten().tolist()
                     assert not bad, (dtype, score, "groups", bad[:3], got[bad[0]], want[bad[0]])
+
+
+@pytest.mark.parametrize("k", [1, 3, 8, 10])
+@pytest.mark.parametrize("T,E,groups", [(5, 64, 1), (5, 64, 4), (600, 128, 1), (600, 256, 8), (3, 512, 1)])
+def test_nan_biases_beside_closed_ones(T, E, groups, k):
+    """Biases of -inf for all but a few experts, and NaN of either sign: what is
+    left is taken, a NaN never, also where nothing else is there to be compared."""
+    x = torch.randn(T, E, generator=gen(E))
+    for fine in (0, 1, 2):
+        for score in ("sigmoid", "softmax"):
+            bias = torch.full((E,), -INF)
+            bias[7], bias[20] = math.nan, -math.nan
+            bias[40:40 + fine] = 0.5
+            r = B.moe_route(x.to(DEV), min(k, E // groups), score=score, groups=groups, bias=bias.to(DEV))
+            idx = r.idx.cpu()
+            assert not ((idx == 7) | (idx == 20)).any(), (fine, score)
+            assert ((idx >= 0).sum(1) == min(fine, idx.shape[1])).all()
+            assert (idx[idx >= 0] >= 40).all() and (idx[idx >= 0] < 40 + fine).all()
+            assert int(r.counts[:E].sum()) == T * min(fine, idx.shape[1])
