@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 from dataclasses import dataclass, field
@@ -1426,14 +1427,43 @@ def _f8_arg(w: F8Weight, device):
     return ctypes.byref(w._desc)
 
 
+def _f8_one(w: F8Weight, device, expert: int | None, turned: bool = False):
+    """(descriptor of w, or of one of its experts; what has to outlive the call).
+    An expert's scales start at any multiple of four bytes: where that is none
+    of 16 they are copied, in every call, since w may have been packed again."""
+    whole = _f8_arg(w, device)
+    if expert is None:
+        return whole, None
+    expert = operator.index(expert)
+    if not 0 <= expert < w.count:
+        raise ValueError(f"expert {expert} of {w.count}")
+
+    def part(plane):
+        n = plane.numel() // w.count
+        t = plane[expert * n:(expert + 1) * n]
+        return t.clone() if t.data_ptr() % 16 else t
+
+    if not turned:
+        values, scales = part(w.values), part(w.scales)
+        return ctypes.byref(F8Desc(w.rows, w.cols, 1, w.scale_dtype, values.data_ptr(),
+                                   scales.data_ptr())), (values, scales)
+    values, scales = (w.values, None) if w.values_t is None else (part(w.values_t), part(w.scales_t))
+    # the planes that are not turned are not read by the gradients
+    return ctypes.byref(F8Desc(w.rows, w.cols, 1, w.scale_dtype, w.values.data_ptr(),
+                               w.values.data_ptr(), None if scales is None else values.data_ptr(),
+                               _addr(scales))), (values, scales)
+
+
 @_on_device
 def f8_gemm(x: torch.Tensor, w: F8Weight, out_dtype=torch.float32, y: torch.Tensor | None = None,
-            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+            workspace: torch.Tensor | None = None, stream=None, *,
+            expert: int | None = None) -> torch.Tensor:
     """binade_f8_gemm: Q(x) W^T of bf16 x [m, K], x quantised in blocks of 128
-    along K, summed in fp32; a bf16 result is that sum rounded once."""
+    along K, summed in fp32; a bf16 result is that sum rounded once. Of weights
+    of several experts, expert says which one."""
     code = _dtype_code(out_dtype)
     dev = x.device
-    d = _f8_arg(w, dev)
+    d, held = _f8_one(w, dev, expert)
     x, ldx = _rows16("x", x, w.cols, dev)
     m, n = x.shape[0], w.rows
     y = _out_arg("y", y, _TORCH_DTYPE[code], (m, n), dev)
@@ -1447,12 +1477,13 @@ def f8_gemm(x: torch.Tensor, w: F8Weight, out_dtype=torch.float32, y: torch.Tens
 def f8_gemm_grad(x: torch.Tensor, w: F8Weight, dy: torch.Tensor, grad_dtype=torch.float32,
                  need_dx: bool = True, need_dw: bool = True, dx: torch.Tensor | None = None,
                  dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                 stream=None):
+                 stream=None, *, expert: int | None = None):
     """binade_f8_gemm_grad: (dx bf16 [m, K] or None, dw [N, K] of grad_dtype or
-    None) of f8_gemm from dy bf16 [m, N]; dx needs a weight made with train."""
+    None) of f8_gemm from dy bf16 [m, N]; dx needs a weight made with train. Of
+    f8_moe_gemm: expert by expert, with the rows of its pairs."""
     code = _dtype_code(grad_dtype)
     dev = x.device
-    d = _f8_arg(w, dev)
+    d, held = _f8_one(w, dev, expert, True)
     n, k = w.rows, w.cols
     x, ldx = _rows16("x", x, k, dev)
     m = x.shape[0]

@@ -862,8 +862,11 @@ int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  * 16 (few pairs) to 128 of its pairs; arithmetic as in binade_f8_gemm; a
  * pair's result does not depend on the other pairs' order.
  * top_k in 1..64, count at most 4096, n_tokens * top_k at most 2^24, pairs * N
- * at most 2^36 and 2^23 tiles of outputs, else EUNSUPPORTED. Experts that are
- * trained take binade_f8_gemm_grad of their own rows, expert by expert.
+ * at most 2^36 and 2^23 tiles of outputs, else EUNSUPPORTED. Its gradients:
+ * expert by expert, binade_f8_gemm_grad of the rows of its pairs with a
+ * binade_f8 of count 1 whose planes are expert e's, which begin e / count of
+ * each plane's bytes after its start (scales at a multiple of 4 bytes: where
+ * that is none of 16, copy the expert's first).
  * workspace: binade_f8_moe_workspace_bytes (0 for few pairs). */
 int32_t binade_f8_moe_gemm(const binade_f8 *experts, const uint16_t *x,
                            int64_t ldx, int32_t x_per_slot,
