@@ -1065,14 +1065,19 @@ constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 //   else splits for 256 blocks, or 512 of the tiles of 32 rows, of which four
 //   fit a CU (61 x 3840 x 15360, 30 tiles of 64: 22.5 with 8, 23.3 with 15;
 //   20 x 4096 x 4096: 16.6 with 8, 14.9 with 16).
+int32_t tile_of_rows(int64_t m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+int64_t splits_of(int64_t m, int64_t n, int64_t kb) {
+  const int32_t bm = tile_of_rows(m);
+  const int64_t tiles = ((m + bm - 1) / bm) * blocks_of(n);
+  int64_t splits = tiles >= 128 || (tiles >= 64 && kb <= 8) ? 1 : (bm == 32 ? 512 : 256) / tiles;
+  if (splits > kb / 4) splits = kb / 4;
+  return splits < 1 ? 1 : splits;
+}
 Plan plan_of(int64_t m, int64_t n, int64_t kb) {
   Plan q;
-  q.bm = m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  q.bm = tile_of_rows(m);
   q.bn = 128;
-  const int64_t tiles = ((m + q.bm - 1) / q.bm) * ((n + q.bn - 1) / q.bn);
-  int64_t splits = tiles >= 128 || (tiles >= 64 && kb <= 8) ? 1 : (q.bm == 32 ? 512 : 256) / tiles;
-  if (splits > kb / 4) splits = kb / 4;
-  if (splits < 1) splits = 1;
+  const int64_t splits = splits_of(m, n, kb);
   int64_t per = (kb + splits - 1) / splits;
   per = (per + 3) / 4 * 4;
   q.per_split = static_cast<int32_t>(per);
@@ -1161,9 +1166,28 @@ int32_t run_product(const Side& x, const Side& w, int kind, int64_t m, int64_t n
   return launch_status();
 }
 
+// Of the splits' sums: the most that a product of up to m rows takes (fewer rows
+// may be split more often), so that a workspace for m serves fewer too.
 int64_t part_bytes(int64_t m, int64_t n, int64_t k) {
-  const Plan q = plan_of(m, n, blocks_of(k));
-  return q.splits > 1 ? up16(4 * q.splits * m * n) : 0;
+  const int64_t kb = blocks_of(k);
+  int64_t most = 0;
+  const auto look = [&](int64_t rows) {
+    const Plan q = plan_of(rows, n, kb);
+    const int64_t bytes = q.splits > 1 ? up16(4 * q.splits * rows * n) : 0;
+    most = bytes > most ? bytes : most;
+    return q.splits > 1;
+  };
+  look(m < 32 ? m : 32);
+  if (m > 32) look(m < 64 ? m : 64);
+  if (m > 64)   // from one split on, more tiles have one too
+    for (int64_t rows = 128; look(rows < m ? rows : m) && rows < m;) rows += 128;
+  return most;
+}
+// The same of a sum over up to m rows (k blocks of 128 of them): the most splits,
+// which do not fall as plan_of's own may, a split being whole fours of blocks.
+int64_t part_bytes_of_rows(int64_t m, int64_t n, int64_t k) {
+  const int64_t kb = blocks_of(m), splits = splits_of(n, k, kb);
+  return splits > 1 ? up16(4 * splits * n * k) : 0;
 }
 int64_t side_bytes(int64_t rows, int64_t cols) {
   return tile_rows(rows) * paired(cols) + up16(tile_rows(rows) * codes_of(cols));
@@ -1358,7 +1382,7 @@ extern "C" int64_t binade_f8_gemm_grad_workspace_bytes(int64_t m, int64_t n, int
   }
   if (need_dw) {
     bytes += side_bytes(n, m) + side_bytes(k, m);
-    const int64_t b = part_bytes(n, k, m);
+    const int64_t b = part_bytes_of_rows(m, n, k);
     part = b > part ? b : part;
   }
   return bytes + part;
@@ -1465,7 +1489,15 @@ ExpertSpace expert_space(int64_t rows, int64_t pairs, int64_t k, int32_t experts
   s.share = (pairs / bm + each) / 8 + 2;   // two parts, each rounded up
   s.order = side_bytes(rows, k);
   s.tiles = s.order + up16(4 * pairs);
-  s.total = s.tiles + 16 * 8 * s.share;
+  // with smaller tiles, as fewer pairs have them, there are more: a workspace
+  // for these pairs serves fewer too
+  int64_t most = s.share;
+  for (const int32_t small : {32, 64}) {
+    if (small >= bm) break;
+    const int64_t p = (small + 1ll) * experts - 1, e = experts + 1 < p ? experts + 1 : p;   // the most pairs of them
+    most = (p / small + e) / 8 + 2 > most ? (p / small + e) / 8 + 2 : most;
+  }
+  s.total = s.tiles + 16 * 8 * most;
   return s;
 }
 }  // namespace

@@ -865,7 +865,10 @@ using namespace binade;
 
 extern "C" int64_t binade_moe_route_scored_workspace_bytes(int64_t n_tokens, int32_t n_experts) {
   if (!route_sizes_ok(n_tokens, n_experts)) return 0;
-  return kHead + static_cast<int64_t>(scored_blocks(n_tokens, n_experts)) * (2 * n_experts + 1) * 4;
+  // up to kFewTokens there may be more blocks than for a few tokens more
+  const int64_t few = n_tokens < kFewTokens ? n_tokens : kFewTokens;
+  const int64_t a = scored_blocks(n_tokens, n_experts), b = scored_blocks(few, n_experts);
+  return kHead + (a > b ? a : b) * (2 * n_experts + 1) * 4;
 }
 
 extern "C" int32_t binade_moe_route_scored(const void* logits, int32_t dtype, int64_t ld,

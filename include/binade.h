@@ -656,6 +656,7 @@ int32_t binade_moe_route_scored(const void *logits, int32_t dtype, int64_t ld,
                                 float *prob_sum, float *loss, void *workspace,
                                 int64_t workspace_bytes, void *stream);
 
+/* Serves fewer tokens of as many experts too. */
 int64_t binade_moe_route_scored_workspace_bytes(int64_t n_tokens,
                                                 int32_t n_experts);
 
@@ -827,7 +828,8 @@ int32_t binade_f8_gemm(const binade_f8 *w, const uint16_t *x, int64_t m,
                        void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Workspace bytes of binade_f8_gemm (0 for sizes it refuses). Pure host
- * function. */
+ * function. Here and of the calls below: what serves m rows (tokens) serves
+ * fewer, n and k being the same. */
 int64_t binade_f8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t k,
                                        int32_t y_dtype);
 
