@@ -1338,7 +1338,8 @@ _BYTES_OF_E8M0 = (torch.float8_e8m0fnu, torch.uint8)
 class F8Weight:
     """Weights in 8 bits with a scale for each block of 128 x 128, as f8_pack
     and f8_weight lay them out: count matrices [rows, cols] (experts), and with
-    train their transposed planes, which f8_gemm_grad's dx reads."""
+    train their transposed planes, which f8_gemm_grad's dx reads. The planes
+    are the bytes of binade_f8_sizes_of; the tensors must not be replaced."""
     rows: int
     cols: int
     count: int
@@ -1349,6 +1350,20 @@ class F8Weight:
     scales_t: torch.Tensor | None = None
 
     def __post_init__(self):
+        sizes = F8Sizes()
+        _run("binade_f8_sizes_of", self.rows, self.cols, self.count, self.scale_dtype,
+             ctypes.byref(sizes))
+        if (self.values_t is None) != (self.scales_t is None):
+            raise ValueError("values_t and scales_t: both or none")
+        for name in ("values", "scales", "values_t", "scales_t"):
+            t = getattr(self, name)
+            if t is None and name.endswith("_t"):
+                continue
+            need = getattr(sizes, name + "_bytes")
+            if t.dtype != torch.uint8 or t.numel() != need or not t.is_contiguous():
+                raise ValueError(f"{name}: {need} contiguous bytes (uint8)")
+            if t.device != self.values.device:
+                raise ValueError(f"{name} is on {t.device}, not {self.values.device}")
         self._desc = F8Desc(self.rows, self.cols, self.count, self.scale_dtype,
                             self.values.data_ptr(), self.scales.data_ptr(), _addr(self.values_t),
                             _addr(self.scales_t))
