@@ -818,10 +818,17 @@ __global__ __launch_bounds__(256) void scored_grad_kernel(ScoredGradArgs p) {
 // ------------------------------------------------------------------- hosts
 // Experts a lane, and lanes a row. With few tokens the chain of one row's
 // instructions counts, and eight experts a lane make it shorter; with many
-// their number does: sixteen (more than 512 experts take a whole wave's). In a
-// graph, 8 of 256 fp32 experts in groups, us: one token 7.0 and 8.9, 256 of
-// them 7.8 and 9.7, 2049 9.5 and 15.5 (bf16 13.6 and 10.1), 4096 13.6 and 10.2.
-constexpr int64_t kFewTokens = 512;
+// their number does: sixteen (more than 512 experts take a whole wave's). 8 of
+// 256 experts in groups, in a graph, us with eight and with sixteen, fp32 logits
+// (bf16), of eight sets of logits the least:
+//   512 tokens 7.9 and 9.9 (8.0, 10.1)     1024: 8.0 and 10.0 (8.2, 10.1)
+//   2048: 8.1 and 10.1 (8.3, 10.2)         4096: 10.2 and 10.3 (13.7, 15.7)
+//   16384: 29.8 and 24.7 (29.7, 32.9)
+// With counts 1024: 14.2 and 15.7 (14.1, 15.8); of 512 experts with counts 1024:
+// 15.9 and 17.9 (15.8, 17.6), 2048: 21.4 and 18.6 (21.5, 18.6). So 1024 is where
+// eight are still faster for every number of experts. A row that fp32 does not
+// settle adds 6 us to any of these: one in a few thousand here.
+constexpr int64_t kFewTokens = 1024;
 int32_t scored_each(int64_t n_tokens, int32_t n_experts) {
   return n_experts <= 64 || (n_experts <= 512 && n_tokens <= kFewTokens) ? 8 : 16;
 }

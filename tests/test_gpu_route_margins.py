@@ -195,3 +195,31 @@ def test_nan_biases_beside_closed_ones(T, E, groups, k):
             assert ((idx >= 0).sum(1) == min(fine, idx.shape[1])).all()
             assert (idx[idx >= 0] >= 40).all() and (idx[idx >= 0] < 40 + fine).all()
             assert int(r.counts[:E].sum()) == T * min(fine, idx.shape[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,groups,top_groups,best", [(65, 5, 5, 2, 2), (128, 6, 8, 3, 2), (160, 16, 8, 3, 1),
+                                                        (256, 8, 8, 4, 2), (300, 10, 3, 2, 1), (512, 8, 16, 4, 2),
+                                                        (512, 33, 8, 6, 2), (96, 8, 1, 1, 2)])
+def test_from_1025_tokens_on_as_of_1024(E, k, groups, top_groups, best, score, dtype):
+    """1024 tokens have eight experts a lane, 1025 sixteen: the same choices and
+    counts, weights within the roundings of a total (21 steps of 2^-24) and of two
+    scores and an inverse (5 steps), on both sides."""
+    g = gen(E)
+    x = (torch.randn(1025, E, generator=g) * 2).to(dtype)
+    x[:, torch.randperm(E, generator=g)[:E // 9]] = -INF
+    valid = torch.rand(1025, generator=g) < 0.9
+    bias = torch.randn(E, generator=g) * 0.2
+    for b in (bias, None, (bias * 8).round() / 8):
+        kw = dict(score=score, bias=None if b is None else b.to(DEV), groups=groups, top_groups=top_groups,
+                  group_best=best, scale=2.5)
+        many = B.moe_route(x.to(DEV), k, valid=valid.to(DEV), **kw)
+        few = B.moe_route(x[:1024].to(DEV), k, valid=valid[:1024].to(DEV), **kw)
+        last = B.moe_route(x[1024:].to(DEV), k, valid=valid[1024:].to(DEV), **kw)
+        assert torch.equal(many.idx, torch.cat([few.idx, last.idx]))
+        assert torch.equal(many.counts, few.counts + last.counts)
+        w = torch.cat([few.weights, last.weights])
+        assert torch.all((many.weights - w).abs() <= 52 * 2.0 ** -24 * w)
+        ps = few.prob_sum + last.prob_sum
+        assert torch.all((many.prob_sum - ps).abs() <= (52 + 64) * 2.0 ** -24 * ps)
