@@ -687,7 +687,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(GemmArgs p) {
   }
 }
 
-// The splits' sums, in their order. Only outputs of fewer than 128 tiles are
+// The splits' sums, in their order. Only outputs of up to 128 tiles are
 // split: m * n fits 32 bits. 8 splits of 61 x 3840: 3.0 us, the launch itself.
 template <int kEach>
 __global__ __launch_bounds__(256) void join_kernel(const float* part, int32_t splits, uint32_t total,
@@ -1055,21 +1055,22 @@ struct Plan {
 constexpr int64_t kMaxOutputs = 1ll << 36;   // m * n
 
 // Tiles and splits of a product of m x n outputs over kb blocks. Measured, us
-// for m x n x k with bf16 results (fp32 ones alike):
-//   large tiles from 192 of them on (4096 x 15360 x 3840: 241, 128 x 128 tiles
-//   285; below, more than a quarter of the CUs would stand idle);
-//   one split from 128 tiles on (512 x 4096 x 2048, 128 tiles: 17, four splits
-//   32; 512 x 2048 x 4096, 64 tiles: 28 with one, 26 with four), and with up
-//   to eight blocks from 64 on (256 x 4096 x 1024: 13, with four 17): a step
-//   takes less than joining;
-//   else splits for 256 blocks, or 512 of the tiles of 32 rows, of which four
-//   fit a CU (61 x 3840 x 15360, 30 tiles of 64: 22.5 with 8, 23.3 with 15;
-//   20 x 4096 x 4096: 16.6 with 8, 14.9 with 16).
+// for m x n x k:
+//   one split above 128 tiles (1536 x 2048 x 4096, 192 tiles: 43.7, with two
+//   44.6; 2048 x 2048 x 4096, 256: 44.4 and 49.1), and with no more than a block
+//   for eight tiles from 64 of them on (1024 x 2048 x 2048, 128 tiles: 24.5, with
+//   two 28.0; 512 x 2048 x 1024, 64 tiles: 14.2 and 17.7): the steps saved take
+//   less than joining;
+//   else splits for 256 blocks (1024 x 2048 x 4096, 128 tiles: 33.9 with two, 42.5
+//   with one; 512 x 2048 x 4096, 64 tiles: 26.5 with four, 31.4, 40.6; 61 x 3840 x
+//   15360, 30 tiles of 64 rows: 23.2 with 8, 31.0 with 4, 22.6 with 15), or 512 of
+//   the tiles of 32 rows, of which four fit a CU (20 x 3840 x 15360, 30 tiles: 19.1
+//   with 8, 18.5 with 15, 20.9 with 30).
 int32_t tile_of_rows(int64_t m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 int64_t splits_of(int64_t m, int64_t n, int64_t kb) {
   const int32_t bm = tile_of_rows(m);
   const int64_t tiles = ((m + bm - 1) / bm) * blocks_of(n);
-  int64_t splits = tiles >= 128 || (tiles >= 64 && kb <= 8) ? 1 : (bm == 32 ? 512 : 256) / tiles;
+  int64_t splits = tiles > 128 || (tiles >= 64 && kb <= tiles / 8) ? 1 : (bm == 32 ? 512 : 256) / tiles;
   if (splits > kb / 4) splits = kb / 4;
   return splits < 1 ? 1 : splits;
 }
