@@ -42,11 +42,9 @@ constexpr int kMaxExperts = 4096;        // of an expert product
 constexpr int kSmallRows = 16;           // rows of one few-row pass
 constexpr int kSmallPairs = 256;         // pairs that the few-row kernel sorts by itself
 
-inline int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+__host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
 inline int64_t padded(int64_t n) { return blocks_of(n) * 128; }
 inline int64_t codes_of(int64_t n) { return (blocks_of(n) + 3) / 4 * 4; }   // bytes of a row's codes
-// Columns of an operand that is quantised here: whole pairs of blocks.
-inline int64_t paired(int64_t n) { return (n + 255) / 256 * 256; }
 inline int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------- scales
@@ -141,12 +139,12 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n,
 // of 15360 bytes one below the other meet only four of an L2's sixteen
 // channels: 1.5 times the time of a large product).
 //
-// Rows of v [m, n] as e4m3, paired(n) / 128 blocks of m_pad rows, with a code
+// Rows of v [m, n] as e4m3, blocks_of(n) blocks of m_pad rows, with a code
 // for each block of a row: 16 lanes a block, 8 values a lane.
 __device__ __forceinline__ void quantise_rows(const uint16_t* v, int64_t ld, int64_t m, int64_t n,
                                               bool vec, uint8_t* q, int64_t m_pad, uint8_t* codes,
                                               int64_t ldc, int64_t first, int64_t step) {
-  const int64_t nb = (n + 255) / 256 * 2, units = m * nb;
+  const int64_t nb = blocks_of(n), units = m * nb;
   const int l = threadIdx.x & 15;
 #pragma unroll 2
   for (int64_t u = first; u < units; u += step) {
@@ -449,14 +447,14 @@ __device__ __forceinline__ void expert_tile_of(const GemmArgs& p, int32_t& mt, i
 // side by side in a row of y.
 // Every variant is held to two waves a SIMD (256 registers): the few that took
 // more by themselves lost more from waiting alone than from what they spill
-// (2048 x 4096 x 4096 with fp32 results and scales 108 -> 87 us, experts of
-// 4096 x 8 pairs alike 387 -> 257 us).
+// (2048 x 4096 x 4096 with fp32 results and scales 101 -> 85 us, experts of
+// 4096 x 8 pairs alike 358 -> 256 us; with powers of two 74 -> 72, 229 -> 231).
 // Bound by vector instructions beside the matrix ones: both operands become
 // bf16 here, two conversions for each matrix instruction of a wave's 64 x 64,
 // 3.7 instructions with everything. Two are hidden behind a matrix instruction
 // (7.2 ns a slot of a SIMD with one, 7.8 with two, 11.4 with four). 4096 x
-// 15360 x 3840: 388 us, 1.25 PFLOP/s; 15360 x 3840 x 8192 (a weight's gradient)
-// 0.83 to 0.93 ms, 1.04 to 1.16; a large bf16 library product has 1.6 (tiles of
+// 15360 x 3840: 390 us, 1.24 PFLOP/s; 15360 x 3840 x 8192 (a weight's gradient)
+// 0.83 to 0.95 ms, 1.02 to 1.16; a large bf16 library product has 1.6 (tiles of
 // 256 rows, a wave's 128 or 64 of them: 1.13 and 0.97 ms). With experts and few
 // blocks of K the ends of the tiles count too: runs of two to six tiles a
 // block, the next one's loads under way over an end, spill and gain nothing.
@@ -715,9 +713,12 @@ __global__ __launch_bounds__(256) void zero_kernel(uint32_t* p, int64_t words) {
 }
 
 // ------------------------------------------------------------ few-row product
-// Up to 16 rows of x at a time: what counts is reading the weights (15360 x
-// 3840, one row: 16.3 us, 3.6 TB/s, of which the launch and the ends about 5;
-// 64 pairs of 128 experts, 704 x 2816: 22 us, 5.1 TB/s). A block
+// Up to 16 rows of x at a time: the weights are read once (15360 x 3840, one
+// row: 16.6 us a pass with weights in the cache, 18.2 with ten matrices in turn,
+// 59 MB; 64 pairs of 55 of 128 experts, 704 x 2816: 26.6, and 29.0 from memory,
+// 109 MB). Bound by vector instructions more than by that: 6.9 million for the
+// row, 13 us on 1024 SIMDs at 2.1 GHz; of a step's 239 the weights' conversions
+// are 16, most others find the largest of x and quantise it in each wave. A block
 // has 16 NR rows of w; its waves take blocks of 128 columns in turn, weights
 // and rows of x straight into the operands' registers (lane: row l % 16,
 // columns 16 q .. and 64 + 16 q ..; x in the same order), x quantised there.
@@ -879,10 +880,9 @@ __global__ __launch_bounds__(64 * kWaves) void few_rows_kernel(SmallArgs p) {
 // quantise the rows meanwhile. Tiles lie as the product's blocks take them: an
 // eighth for each XCD, with its share of the tiles that have an expert,
 // connected, then its share of the others (expert -1: zeros), then none (-2).
-// (With tiles numbered through, the last XCDs have few that are in use: 32768
-// pairs of 128 experts 204 us instead of 164.)
-// 32768 pairs take 26 us, a chain of loads, LDS atomics and sums over experts
-// that the rows' quantising (46 MB) hides about half of.
+// (With tiles numbered through, the last XCDs have few that are in use.)
+// 32768 pairs take 27 us, a chain of loads, LDS atomics and sums over experts
+// of one block, beside the rows' quantising (72 MB, 14 us at a copy's rate).
 struct SortArgs {
   const int32_t* idx;
   int32_t pairs, n_experts, bm, share;   // share: places of tiles of an XCD
@@ -1191,7 +1191,7 @@ int64_t part_bytes_of_rows(int64_t m, int64_t n, int64_t k) {
   return splits > 1 ? up16(4 * splits * n * k) : 0;
 }
 int64_t side_bytes(int64_t rows, int64_t cols) {
-  return tile_rows(rows) * paired(cols) + up16(tile_rows(rows) * codes_of(cols));
+  return tile_rows(rows) * padded(cols) + up16(tile_rows(rows) * codes_of(cols));
 }
 
 int32_t check_f8(const binade_f8* w, bool turned) {
@@ -1364,9 +1364,9 @@ extern "C" int32_t binade_f8_gemm(const binade_f8* w, const uint16_t* x, int64_t
     return BINADE_ENOSPACE;
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   uint8_t* q = static_cast<uint8_t*>(workspace);
-  uint8_t* codes = q + tile_rows(m) * paired(k);
+  uint8_t* codes = q + tile_rows(m) * padded(k);
   float* part = reinterpret_cast<float*>(q + side_bytes(m, k));
-  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * paired(k) / 128 + 15) / 16)), dim3(256),
+  hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * blocks_of(k) + 15) / 16)), dim3(256),
                      0, st, x, ldx, m, k, true, q, tile_rows(m), codes, codes_of(k));
   return run_product({q, codes, tile_rows(m), static_cast<int32_t>(codes_of(k))},
                      {w->values, w->scales, n, static_cast<int32_t>(codes_of(k))}, kind_of(w),
@@ -1422,7 +1422,7 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   const auto take = [&](int64_t rows, int64_t cols) {
-    Side s{at, at + tile_rows(rows) * paired(cols), tile_rows(rows), static_cast<int32_t>(codes_of(cols))};
+    Side s{at, at + tile_rows(rows) * padded(cols), tile_rows(rows), static_cast<int32_t>(codes_of(cols))};
     at += side_bytes(rows, cols);
     return s;
   };
@@ -1446,7 +1446,7 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
     p.n_pad = cols_side.rows;
     p.ldct = cols_side.ld_scales;
     p.vec = v8;
-    const dim3 grid(static_cast<uint32_t>(paired(cols) / 128), static_cast<uint32_t>(paired(m) / 128), 1);
+    const dim3 grid(static_cast<uint32_t>(blocks_of(cols)), static_cast<uint32_t>(blocks_of(m)), 1);
     if (rows_side != nullptr) {
       p.q = const_cast<uint8_t*>(rows_side->q);
       p.codes = static_cast<uint8_t*>(const_cast<void*>(rows_side->scales));
@@ -1461,7 +1461,7 @@ extern "C" int32_t binade_f8_gemm_grad(const binade_f8* w, const uint16_t* x, in
     turn(dy, ld_dy, n, vec, need_dx ? &dy_rows : nullptr, dy_cols);
     turn(x, ldx, k, true, nullptr, x_cols);
   } else {
-    hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * paired(n) / 128 + 15) / 16)), dim3(256),
+    hipLaunchKernelGGL(quantise_rows_kernel, dim3(some_blocks((m * blocks_of(n) + 15) / 16)), dim3(256),
                        0, st, dy, ld_dy, m, n, vec, const_cast<uint8_t*>(dy_rows.q), dy_rows.rows,
                        static_cast<uint8_t*>(const_cast<void*>(dy_rows.scales)),
                        static_cast<int64_t>(dy_rows.ld_scales));
@@ -1562,7 +1562,7 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   if (!aligned16(workspace)) return BINADE_EUNSUPPORTED;
   const ExpertSpace space = expert_space(rows, pairs, k, experts->count);
   uint8_t* at = static_cast<uint8_t*>(workspace);
-  uint8_t* codes = at + tile_rows(rows) * paired(k);
+  uint8_t* codes = at + tile_rows(rows) * padded(k);
   Plan q{};
   q.bm = expert_tile(pairs, experts->count);
   q.bn = 128;
@@ -1576,7 +1576,7 @@ extern "C" int32_t binade_f8_moe_gemm(const binade_f8* experts, const uint16_t* 
   if (!launchable(p)) return BINADE_EUNSUPPORTED;
   const SortArgs sort{idx, static_cast<int32_t>(pairs), experts->count, q.bm, p.mt,
                       const_cast<int32_t*>(p.order), const_cast<int4*>(p.tiles), dev_status};
-  const int64_t blocks = (rows * paired(k) / 128 + 127) / 128;   // two blocks of a row a thread
+  const int64_t blocks = (rows * blocks_of(k) + 127) / 128;   // two blocks of a row a thread
   hipLaunchKernelGGL(prepare_experts_kernel, dim3(1 + some_blocks(blocks)), dim3(1024), 0, st, sort, x, ldx,
                      rows, k, at, tile_rows(rows), codes, codes_of(k));
   p.x = at;

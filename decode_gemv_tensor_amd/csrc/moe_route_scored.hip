@@ -13,9 +13,9 @@
 // in the key's other half, so that ties are settled too. The slots' experts
 // are found by their values: a lane looks for its own among the sorted ones.
 //
-// Bound by vector instructions: 1346 for four rows of 256 experts (16 scores, a
+// Bound by vector instructions: 1376 for four rows of 256 experts (16 scores, a
 // sort of 16 and four merges of eight a lane, groups, the checks of gaps);
-// 65536 rows 63 us, of which 71 MB are 14. Three waves a SIMD instead of two
+// 65536 rows 65 us, of which 71 MB are 14. Three waves a SIMD instead of two
 // (168 registers, with spills) take as long.
 //
 // Scores relative to the row's largest: sigmoid(x) = exp(min(x, 0)) / (1 +
