@@ -771,8 +771,10 @@ int64_t binade_lora_grad_workspace_bytes(int64_t m, int64_t n, int64_t k,
  * weight[n, k] = values[n, k] * scales[n / 128, k / 128]. The products take a
  * weight with a power of two as bf16 holds it: under 2^-133 (codes 0 to 2)
  * rounded to its steps, over its largest (codes from 247 on) infinite; and so
- * a quantised x or dy: a value that rounds to 2^128 is infinite. cols % 32 == 0, rows and cols at most 2^22, count at most
- * 65535; planes 16-byte aligned, else BINADE_EUNSUPPORTED. */
+ * a quantised x or dy: a value that rounds to 2^128 is infinite. With fp32
+ * scales a block's 128 products are added before they are scaled: their sum
+ * has to stay in fp32's range. cols % 32 == 0, rows and cols at most 2^22,
+ * count at most 65535; planes 16-byte aligned, else BINADE_EUNSUPPORTED. */
 typedef struct binade_f8 {
   int64_t rows, cols;
   int32_t count, scale_dtype;
@@ -818,8 +820,8 @@ int32_t binade_f8_layout(const uint8_t *values, const void *scales,
  * most 2^36.
  * Arithmetic: exact products of 8-bit values are added in fp32, and a bf16 Y is
  * that sum rounded once. The order depends on m, N and K: the same call gives
- * the same bits, another m may add in another order. A NaN in a row of X, or in a row or a
- * scale of W, gives NaN in that row or column (block) of Y alone.
+ * the same bits, another m may add in another order. A NaN in a row of X, or
+ * in a row or a scale of W, gives NaN in that row or column (block) of Y alone.
  * workspace: device, 16-byte aligned, binade_f8_gemm_workspace_bytes (0 for m
  * <= 16: may be NULL), not read before written; calls that overlap need their
  * own. ENOSPACE: too small. */
